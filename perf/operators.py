@@ -218,7 +218,8 @@ def prepare(case, seed):
         s["freq"], s["scale"] = _frequencies(case)
         if own:
             import test_trained_neural_amd as T
-            s["rotary"] = T.Rotary(case["rot"], base=10000.0, layout=case["layout"], device="cuda", **_scaling(case, T))
+            s["rotary"] = T.Rotary(case["rot"], base=10000.0, device="cuda", **_scaling(case, T),
+                                   layout=T.TM_ROPE_HALF if case["layout"] == "half" else T.TM_ROPE_INTERLEAVED)
         return s
     kv, d = case["kv_heads"], case["dim"]
     if case["op"] == "append":
