@@ -342,7 +342,9 @@ tm_status tm_store_groups_enable(int on);
  * same launch), 5 the per-token read's products,
  * 6 the input side's projection kernel (tm_project; its history kernel is
  * not timed), 7 the memory-as-context window and gate kernels
- * (tm_mac_window, tm_mac_gate).  While bit c of
+ * (tm_mac_window, tm_mac_gate), 8 and 9 tm_backward's state-streaming
+ * launches and its other launches, 10 the attention window's kernels
+ * (tm_attention.h).  While bit c of
  * class_mask is set, every launch of class c is bracketed by a pair of HIP
  * events recorded on its launch stream (mask 0 turns timing off).
  * tm_timing_read waits for the recorded launches and returns, for one class,

@@ -574,3 +574,10 @@ class NeuralMemory:
 
     def check(self, state):
         return tm_state_check(self.ctx, state.buf, state.batch, state.heads)
+
+
+# the attention window's operators (include/tm_attention.h)
+from .attention import (TM_CACHE_BAD_ENTRY, TM_CACHE_BLOCK, TM_CACHE_FULL, TM_CACHE_NO_PAGES,  # noqa: E402,F401
+                        TM_CACHE_NONFINITE, TM_CACHE_PAGE, TM_ROPE_BASE, TM_ROPE_HALF, TM_ROPE_INTERLEAVED,
+                        TM_ROPE_LINEAR, TM_ROPE_NONE, TM_ROPE_PARTS, PagedCache, Rotary, tm_rotary,
+                        tm_rotary_frequencies)

@@ -1,0 +1,357 @@
+"""The attention window's operators: Python binding of ``include/tm_attention.h``.
+
+Rotary positions, a paged key/value cache held in 8 bits, the attention that
+reads it and its pages' housekeeping.  As in the package's other calls, this
+is argument marshalling only: the functions carry the C names and check
+types, shapes and devices before a pointer is passed on.  ``Rotary`` and
+``PagedCache`` keep a frequency table and a cache's blob and allocate
+outputs; ``WindowAttention`` puts them together as the attention of
+``mac_segment``.
+
+Calls run on the current stream of the tensors' device (or on ``stream``).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+import test_trained_neural_amd as T
+
+TM_ROPE_HALF, TM_ROPE_INTERLEAVED = 0, 1
+TM_ROPE_NONE, TM_ROPE_LINEAR, TM_ROPE_BASE, TM_ROPE_PARTS = 0, 1, 2, 3
+TM_CACHE_NONFINITE, TM_CACHE_NO_PAGES, TM_CACHE_FULL, TM_CACHE_BAD_ENTRY = 1, 2, 4, 8
+TM_CACHE_PAGE, TM_CACHE_BLOCK = 64, 16
+
+EXPORTED = ("tm_rotary_frequencies", "tm_rotary", "tm_cache_create", "tm_cache_destroy", "tm_cache_bytes",
+            "tm_cache_layout", "tm_cache_init", "tm_cache_workspace_bytes", "tm_cache_append", "tm_cache_attend",
+            "tm_cache_read", "tm_cache_fork", "tm_cache_free", "tm_cache_compact", "tm_cache_check")
+
+# kernel class of tm_timing_enable / tm_timing_read
+K_ATTENTION = 10
+
+_vp, _i, _l, _d, _f, _z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_double, ctypes.c_float,
+                           ctypes.c_size_t)
+_declared = None
+
+
+def _lib():
+    global _declared
+    if _declared is None:
+        L = T.lib()
+        for name, args in (
+                ("tm_rotary_frequencies", [_i, _d, _i, _d, _d, _d, _d, ctypes.POINTER(_d), ctypes.POINTER(_d)]),
+                ("tm_rotary", [_vp, _l, _l, _vp, _l, _l, _vp, _i, _vp, _d, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
+                ("tm_cache_create", [_i, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
+                ("tm_cache_layout", [_vp, ctypes.POINTER(_z)]),
+                ("tm_cache_init", [_vp, _vp, _vp]),
+                ("tm_cache_append", [_vp, _vp, _vp, _vp, _vp, _l, _l, _vp, _l, _l, _i, _i, _i, _vp, _vp]),
+                ("tm_cache_attend", [_vp, _vp, _vp, _vp, _vp, _l, _l, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _vp, _vp]),
+                ("tm_cache_read", [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp]),
+                ("tm_cache_fork", [_vp, _vp, _vp, _vp, _i, _vp]),
+                ("tm_cache_free", [_vp, _vp, _vp, _vp, _i, _vp]),
+                ("tm_cache_compact", [_vp, _vp, _vp, _vp]),
+                ("tm_cache_check", [_vp, _vp, ctypes.POINTER(_i), ctypes.POINTER(_i), _vp])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = _i, args
+        L.tm_cache_destroy.restype, L.tm_cache_destroy.argtypes = None, [_vp]
+        L.tm_cache_bytes.restype, L.tm_cache_bytes.argtypes = _z, [_vp]
+        L.tm_cache_workspace_bytes.restype, L.tm_cache_workspace_bytes.argtypes = _z, [_vp, _i, _i, _i]
+        _declared = L
+    return _declared
+
+
+# ---------------------------------------------------------------------------
+# argument checks
+
+def _on(device, *named):
+    """Every given tensor is on ``device``, a GPU."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be device tensors")
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, the call is on %s" % (name, t.device, device))
+
+
+def _heads_of(name, t, aligned=True):
+    """(batch distance, token distance) in elements of a [batch][tokens]
+    [heads][dim] tensor whose last two axes are contiguous."""
+    if t.dim() != 4:
+        raise ValueError("%s must be [batch][tokens][heads][dim], got %d axes" % (name, t.dim()))
+    B, N, H, d = t.shape
+    sb, st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError("the last two axes of %s must be contiguous" % name)
+    st, sb = (H * d if N <= 1 else st), (N * H * d if B <= 1 else sb)
+    if aligned and (t.data_ptr() % 16 or sb % 8 or st % 8):
+        raise ValueError("%s must be 16-byte aligned, its distances multiples of 8 elements" % name)
+    return sb, st
+
+
+def _list(name, t, n):
+    if t is not None:
+        if t.dtype != torch.int32:
+            raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+        if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise ValueError("%s must be contiguous and hold %d values, got %s" % (name, n, tuple(t.shape)))
+
+
+class _Device:
+    """The device of a call as the current one, and its stream: ``stream``
+    (then also the one that the call's own buffers are allocated for) or the
+    device's current one."""
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("stream is on %s, the call is on %s" % (stream.device, device))
+            self.guard = torch.cuda.stream(stream)
+        elif device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _vp(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+# ---------------------------------------------------------------------------
+# the C calls, one to one
+
+def tm_rotary_frequencies(rot_dim, base=10000.0, scaling=TM_ROPE_NONE, factor=1.0, original_len=0.0, beta_fast=32.0,
+                          beta_slow=1.0):
+    """(list of rot_dim / 2 frequencies, factor of the result)."""
+    f, s = (_d * max(1, rot_dim // 2))(), _d(1.0)
+    T._check("tm_rotary_frequencies", _lib().tm_rotary_frequencies(rot_dim, base, scaling, factor, original_len,
+                                                                  beta_fast, beta_slow, f, ctypes.byref(s)))
+    return list(f), s.value
+
+
+def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inverse=False, stream=None):
+    """x, y [B][T][H][d] (any distances between tokens and entries; y may be
+    x); positions int32 [B][T], or [B] (the first token's); freq [rot_dim / 2]
+    fp64."""
+    dt = T._dtype_code(x)
+    T._same(x.dtype, ("y", y))
+    T._same(torch.int32, ("positions", positions))
+    T._same(torch.float64, ("freq", freq))
+    T._shape("y", y, x.shape)
+    _on(x.device, ("x", x), ("y", y), ("positions", positions), ("freq", freq))
+    (xb, xt), (yb, yt) = _heads_of("x", x, False), _heads_of("y", y, False)
+    B, N, H, d = x.shape
+    per_token = positions.dim() == 2
+    T._shape("positions", positions, (B, N) if per_token else (B,))
+    if not positions.is_contiguous() or not freq.is_contiguous() or freq.dim() != 1:
+        raise ValueError("positions and freq must be contiguous")
+    with _Device(x.device, stream) as st:
+        T._check("tm_rotary", _lib().tm_rotary(x.data_ptr(), xb, xt, y.data_ptr(), yb, yt, positions.data_ptr(),
+                                               per_token, freq.data_ptr(), result_scale, B, N, H, d,
+                                               2 * freq.shape[0], layout, 1 if inverse else 0, dt, st))
+
+
+def tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages):
+    h = _vp()
+    T._check("tm_cache_create", _lib().tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages,
+                                                       ctypes.byref(h)))
+    return h
+
+
+def tm_cache_destroy(cache):
+    _lib().tm_cache_destroy(cache)
+
+
+def tm_cache_bytes(cache):
+    return _lib().tm_cache_bytes(cache)
+
+
+def tm_cache_layout(cache):
+    """Offsets of meta, scales, keys and values in the blob."""
+    o = (_z * 4)()
+    T._check("tm_cache_layout", _lib().tm_cache_layout(cache, o))
+    return tuple(int(x) for x in o)
+
+
+def tm_cache_workspace_bytes(cache, batch, n_tokens, heads=0):
+    return _lib().tm_cache_workspace_bytes(cache, batch, n_tokens, heads)
+
+
+# ---------------------------------------------------------------------------
+
+class Rotary:
+    """Rotary positions of one table of frequencies: ``y = rotary(x,
+    positions)``; ``inverse=True`` gives the gradient with respect to x."""
+
+    def __init__(self, rot_dim, base=10000.0, layout=TM_ROPE_HALF, scaling=TM_ROPE_NONE, factor=1.0, original_len=0.0,
+                 beta_fast=32.0, beta_slow=1.0, device="cuda"):
+        f, self.result_scale = tm_rotary_frequencies(rot_dim, base, scaling, factor, original_len, beta_fast,
+                                                     beta_slow)
+        self.rot_dim, self.layout = rot_dim, layout
+        self.freq = torch.tensor(f, dtype=torch.float64, device=device)
+
+    def __call__(self, x, positions, inverse=False, out=None, stream=None):
+        _on(x.device, ("x", x))
+        with _Device(x.device, stream):
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            tm_rotary(x, out, positions, self.freq, self.result_scale, self.layout, inverse)
+        return out
+
+
+class PagedCache:
+    """A paged cache in 8 bits: the handle and its blob (``blob``: a uint8
+    tensor of ``tm_cache_bytes`` bytes that already holds a cache; by default
+    a new, empty one).  The views ``meta``, ``lengths``, ``refs``, ``table``,
+    ``scales``, ``k``, ``v`` and ``status`` show its regions."""
+
+    def __init__(self, kv_heads, head_dim, n_pages, n_seqs, seq_pages, device="cuda", blob=None):
+        self.handle = None
+        self.handle = tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages)
+        self.kv_heads, self.head_dim, self.n_pages = kv_heads, head_dim, n_pages
+        self.n_seqs, self.seq_pages = n_seqs, seq_pages
+        need = tm_cache_bytes(self.handle)
+        fresh = blob is None
+        if fresh:
+            blob = torch.empty(need, dtype=torch.uint8, device=device)
+        T._same(torch.uint8, ("blob", blob))
+        T._blob("blob", blob, need)
+        if blob.data_ptr() % 256:
+            raise ValueError("blob must be 256-byte aligned")
+        self.blob, self.device = blob, blob.device
+        o, cells = tm_cache_layout(self.handle), n_pages * kv_heads * TM_CACHE_PAGE * head_dim
+        ints = 64 + n_seqs + n_pages + n_seqs * seq_pages
+        self.meta = blob[:4 * ints].view(torch.int32)
+        self.status, self.lengths = self.meta[:64], self.meta[64:64 + n_seqs]
+        self.refs = self.meta[64 + n_seqs:64 + n_seqs + n_pages]
+        self.table = self.meta[64 + n_seqs + n_pages:].view(n_seqs, seq_pages)
+        self.scales = blob[o[1]:o[1] + n_pages * kv_heads * 8].view(n_pages, kv_heads, 2, 4)
+        self.k = blob[o[2]:o[2] + cells].view(torch.float8_e4m3fn).view(n_pages, kv_heads, TM_CACHE_PAGE, head_dim)
+        self.v = blob[o[3]:o[3] + cells].view(torch.float8_e4m3fn).view(n_pages, kv_heads, head_dim, TM_CACHE_PAGE)
+        self._need = {}
+        if fresh:
+            self.init()
+
+    def __del__(self):
+        try:
+            if self.handle is not None and _declared is not None:
+                tm_cache_destroy(self.handle)
+        except Exception:
+            pass
+
+    def _call(self, name, st, *args):
+        T._check(name, getattr(_declared, name)(self.handle, self.blob.data_ptr(), *args, st))
+
+    def _workspace(self, batch, n_tokens, heads):
+        """Workspace of one call: from torch's allocator, in the stream's
+        order, so that calls on several streams and captured graphs have their
+        own."""
+        key = (batch, n_tokens, heads)
+        need = self._need.get(key)
+        if need is None:
+            if len(self._need) > 4096:
+                self._need.clear()
+            need = self._need[key] = tm_cache_workspace_bytes(self.handle, batch, n_tokens, heads)
+        return torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def init(self, stream=None):
+        with _Device(self.device, stream) as st:
+            self._call("tm_cache_init", st)
+
+    def append(self, seqs, k, v, counts=None, stream=None):
+        """Writes k, v [B][T][kv_heads][d] behind the sequences ``seqs``
+        (int32 [B]; None: 0 ..); counts int32 [B]: tokens of each entry."""
+        dt = T._dtype_code(k)
+        T._same(k.dtype, ("v", v))
+        T._shape("v", v, k.shape)
+        (kb, kt), (vb, vt) = _heads_of("k", k), _heads_of("v", v)
+        B, N, H, d = k.shape
+        T._shape("k", k, (B, N, self.kv_heads, self.head_dim))
+        _list("seqs", seqs, B)
+        _list("counts", counts, B)
+        _on(self.device, ("k", k), ("v", v), ("seqs", seqs), ("counts", counts))
+        with _Device(self.device, stream) as st:
+            ws = self._workspace(B, N, 0)
+            self._call("tm_cache_append", st, T._ptr(seqs), T._ptr(counts), k.data_ptr(), kb, kt, v.data_ptr(), vb,
+                       vt, B, N, dt, ws.data_ptr())
+
+    def attend(self, seqs, q, counts=None, scale=None, window=0, sink=0, max_len=0, out=None, stream=None):
+        """Attention of q [B][T][heads][d], each sequence's last tokens
+        (``counts`` of them), over the cache; scale: 1 / sqrt(d) by default.
+        Returns [B][T][heads][d] of q's type.  Rows behind an entry's count
+        are left as they were: zeros in a new output."""
+        dt = T._dtype_code(q)
+        qb, qt = _heads_of("q", q)
+        B, N, H, d = q.shape
+        T._shape("q", q, (B, N, H, self.head_dim))
+        _list("seqs", seqs, B)
+        _list("counts", counts, B)
+        _on(self.device, ("q", q), ("out", out), ("seqs", seqs), ("counts", counts))
+        if out is not None:
+            T._same(q.dtype, ("out", out))
+            T._shape("out", out, q.shape)
+            if not out.is_contiguous():
+                raise ValueError("out must be contiguous")
+        with _Device(self.device, stream) as st:
+            if out is None:
+                out = (torch.empty if counts is None else torch.zeros)((B, N, H, d), dtype=q.dtype, device=q.device)
+            ws = self._workspace(B, N, H)
+            self._call("tm_cache_attend", st, T._ptr(seqs), T._ptr(counts), q.data_ptr(), qb, qt, out.data_ptr(), B,
+                       N, H, 1.0 / math.sqrt(d) if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
+        return out
+
+    def read(self, seqs, start, n_tokens, dtype=torch.float32, k=None, v=None, stream=None):
+        """(k, v) [B][n_tokens][kv_heads][d]: the values that the tokens
+        start .. of each sequence are held as; rows behind a sequence's end
+        are left as they were (zeros in new outputs)."""
+        B = self.n_seqs if seqs is None else seqs.shape[0]
+        shape = (B, n_tokens, self.kv_heads, self.head_dim)
+        _list("seqs", seqs, B)
+        with _Device(self.device, stream) as st:
+            k = torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
+            v = torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
+            dt = T._dtype_code(k)
+            T._same(k.dtype, ("v", v))
+            T._shape("k", k, shape)
+            T._shape("v", v, shape)
+            if not k.is_contiguous() or not v.is_contiguous():
+                raise ValueError("k and v must be contiguous")
+            _on(self.device, ("k", k), ("v", v), ("seqs", seqs))
+            self._call("tm_cache_read", st, T._ptr(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
+        return k, v
+
+    def fork(self, src, dst, stream=None):
+        """Sequence dst[i] (empty) becomes a copy of src[i] that shares its
+        pages (int32 [n] each)."""
+        _list("src", src, src.shape[0])
+        _list("dst", dst, src.shape[0])
+        _on(self.device, ("src", src), ("dst", dst))
+        with _Device(self.device, stream) as st:
+            self._call("tm_cache_fork", st, src.data_ptr(), dst.data_ptr(), src.shape[0])
+
+    def free(self, seqs, keep=None, stream=None):
+        """Drops all tokens of the sequences, or those behind the first
+        keep[i] (int32 [n] each; seqs None: 0 .. n_seqs - 1)."""
+        n = self.n_seqs if seqs is None else seqs.shape[0]
+        _list("seqs", seqs, n)
+        _list("keep", keep, n)
+        _on(self.device, ("seqs", seqs), ("keep", keep))
+        with _Device(self.device, stream) as st:
+            self._call("tm_cache_free", st, T._ptr(seqs), T._ptr(keep), n)
+
+    def compact(self, stream=None):
+        """Moves the pages in use to the lowest numbers."""
+        with _Device(self.device, stream) as st:
+            ws = self._workspace(0, 0, 0)
+            self._call("tm_cache_compact", st, ws.data_ptr())
+
+    def check(self, stream=None):
+        """(sticky flags, pages in use); waits for the stream."""
+        f, n = _i(0), _i(0)
+        with _Device(self.device, stream) as st:
+            self._call("tm_cache_check", st, ctypes.byref(f), ctypes.byref(n))
+        return int(f.value), int(n.value)

@@ -15,8 +15,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("tm_kernels.hip", "tm_r3.hip", "tm_retrieve.hip", "tm_project.hip",
-                                           "tm_mac.hip", "tm_bwd.hip", "tm_api.hip")]
-HEADERS = [os.path.join(CSRC, "tm_internal.h"), os.path.join(CSRC, "tm_device.h"), os.path.join(ROOT, "include", "tm.h")]
+                                           "tm_mac.hip", "tm_bwd.hip", "tm_rope.hip", "tm_cache.hip",
+                                           "tm_attend.hip", "tm_api.hip")]
+HEADERS = [os.path.join(CSRC, "tm_internal.h"), os.path.join(CSRC, "tm_device.h"), os.path.join(CSRC, "tm_cache.h"),
+           os.path.join(ROOT, "include", "tm.h"), os.path.join(ROOT, "include", "tm_attention.h")]
 LIB = os.path.join(HERE, "libtm.so")
 OBJDIR = os.path.join(ROOT, "_build")
 

@@ -290,7 +290,8 @@ enum {
     K_SCAN = 0, K_FWD = 1, K_BWD = 2, K_FIRST = 4, K_R3 = 5, K_PROJ = 6, K_MAC = 7,
     K_BSTATE = 8,   // tm_backward: the launches that stream the state (recompute's write, adjoint update)
     K_BREST = 9,    // tm_backward: its other products, element-wise steps and coefficients
-    K_CLASSES = 10
+    K_ATTN = 10,    // the attention window's kernels (tm_attention.h)
+    K_CLASSES = 11
 };
 struct Timed {
     hipEvent_t a, b;
@@ -346,6 +347,14 @@ hipError_t timed(int kind, hipStream_t st, F&& launch) {
     g_pending.push_back(Timed{a, b, kind});
     return hipSuccess;
 }
+
+}  // namespace
+
+hipError_t tmk::timed_attn_call(hipStream_t st, hipError_t (*call)(void*), void* arg) {
+    return timed(K_ATTN, st, [&] { return call(arg); });
+}
+
+namespace {
 
 // ---- TM_LOG diagnostics ----
 thread_local bool g_log_plan = false;   // the running launch sequence prints its plan

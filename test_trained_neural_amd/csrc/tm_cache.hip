@@ -1,0 +1,820 @@
+// The paged 8-bit key/value cache (include/tm_attention.h): writing tokens,
+// reading them back, and the bookkeeping of pages (fork, free, compact).
+//
+// Everything that decides which page a token goes to runs on the device, in
+// one workgroup per call (append, compact) or one per entry (fork, free), so
+// no call waits for the host and every call can be captured into a graph.
+// Pages are found by a scan of the reference counts from a lower bound on the
+// first free one, in ascending order: which page an entry gets follows from
+// the bookkeeping alone, and no result depends on the order of atomics.
+#include <new>
+#include <type_traits>
+
+#include "tm_cache.h"
+
+namespace tmk {
+
+constexpr int PLAN_THREADS = 1024;
+constexpr int MAX_SEQS = 8192;
+
+// What the append's plan leaves for its write, per entry of the call.
+struct AppendPlan {
+    int old, n;      // tokens held before, tokens to write
+    int copy_from;   // the shared page that the entry's last page is a copy of, or -1
+    int pad;
+};
+
+struct AppendArgs {
+    CacheView c;
+    const int* seqs;
+    const int* counts;
+    const void* k;
+    const void* v;
+    long kb, kt, vb, vt;
+    int B, T;
+    AppendPlan* plan;
+};
+
+// Inclusive sum over the workgroup; every thread gets the total too.
+template <int THREADS> __device__ __forceinline__ int block_scan(int x, int* wave_sums, int& total) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const int y = __shfl_up(s, o, 64);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();   // the sums of an earlier scan have been read
+    if (lane == 63) wave_sums[w] = s;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) {
+        const int y = wave_sums[i];
+        if (i < w) before += y;
+        all += y;
+    }
+    total = all;
+    return s + before;
+}
+
+// One workgroup decides the whole append: which entries are served, which
+// pages they get, and the lengths and reference counts after it.
+//   1. equal entries: the first one's index wins its sequence (atomicMin in
+//      LDS: the least index, whatever the order);
+//   2. each entry's pages: those its tokens begin, and one for a copy of a
+//      shared last page ("shared" as before the call); an inclusive sum over
+//      the entries gives each its ranks among the free pages;
+//   3. a scan over the reference counts finds the free pages in order; page
+//      of rank r goes to the entry whose ranks hold r (binary search);
+//   4. entries within the free pages take effect.
+// Latency-bound (a handful of dependent round trips); the write that follows
+// has the bytes.
+__global__ __launch_bounds__(PLAN_THREADS) void append_plan_kernel(AppendArgs a) {
+    const CacheView& c = a.c;
+    __shared__ int ranks[MAX_SEQS];   // first the winners of 1, then the inclusive sums of 2
+    __shared__ int wave_sums[PLAN_THREADS / 64];
+    __shared__ int flags, hint;
+    constexpr int PER = MAX_SEQS / PLAN_THREADS;
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        flags = 0;
+        hint = 0x7fffffff;
+    }
+    auto seq_of = [&](int i) { return a.seqs ? a.seqs[i] : i; };
+    for (int i = tid; i < a.B; i += PLAN_THREADS) {
+        const int s = seq_of(i);
+        if ((unsigned)s < (unsigned)c.n_seqs) ranks[s] = 0x7fffffff;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.B; i += PLAN_THREADS) {
+        const int s = seq_of(i);
+        if ((unsigned)s < (unsigned)c.n_seqs) atomicMin(&ranks[s], i);
+    }
+    __syncthreads();
+    unsigned mine = 0;   // bit j: this thread's j-th entry is served so far
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * PLAN_THREADS;
+        if (i >= a.B) break;
+        const int s = seq_of(i);
+        if ((unsigned)s < (unsigned)c.n_seqs && ranks[s] == i) mine |= 1u << j;
+        else atomicOr(&flags, TM_CACHE_BAD_ENTRY);
+    }
+    __syncthreads();
+    int base = 0;
+    for (int j = 0; j * PLAN_THREADS < a.B; ++j) {
+        const int i = tid + j * PLAN_THREADS;
+        int need = 0;
+        if (i < a.B) {
+            AppendPlan p{0, 0, -1, 0};
+            if (mine >> j & 1) {
+                const int s = seq_of(i);
+                p.old = c.length(s);
+                p.n = a.counts ? min(max(a.counts[i], 0), a.T) : a.T;
+                if (p.n > c.seq_pages * PAGE - p.old) {
+                    atomicOr(&flags, TM_CACHE_FULL);
+                    p.n = 0;
+                }
+                if (p.n > 0 && p.old % PAGE) {
+                    const int tail = c.page_at(s, p.old / PAGE);
+                    if (!c.page_ok(tail)) {
+                        atomicOr(&flags, TM_CACHE_BAD_ENTRY);
+                        p.n = 0;
+                    } else if (c.refs[tail] > 1) {
+                        p.copy_from = tail;
+                    }
+                }
+                if (p.n > 0) need = (p.old + p.n + PAGE - 1) / PAGE - (p.old + PAGE - 1) / PAGE + (p.copy_from >= 0);
+            }
+            a.plan[i] = p;
+        }
+        int total;
+        const int incl = base + block_scan<PLAN_THREADS>(need, wave_sums, total);
+        base += total;
+        if (i < a.B) ranks[i] = incl;
+    }
+    const int want = base;   // pages of the whole call
+    __syncthreads();
+    int found = 0;           // free pages seen
+    if (want > 0) {
+        const int from = min(max(c.status[1], 0), c.n_pages) / 4 * 4;
+        for (int p0 = from; p0 < c.n_pages && found < want; p0 += PLAN_THREADS * 4) {
+            const int p = p0 + tid * 4;
+            int free4 = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p + e < c.n_pages && c.refs[p + e] <= 0) free4 |= 1 << e;
+            int total;
+            const int n4 = __popc(free4);
+            int r = found + block_scan<PLAN_THREADS>(n4, wave_sums, total) - n4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!(free4 >> e & 1)) continue;
+                if (r < want) {
+                    int lo = 0, hi = a.B - 1;   // the first entry whose inclusive sum is above r
+                    while (lo < hi) {
+                        const int mid = (lo + hi) / 2;
+                        if (ranks[mid] > r) hi = mid;
+                        else lo = mid + 1;
+                    }
+                    const AppendPlan q = a.plan[lo];
+                    const int first = q.copy_from >= 0 ? q.old / PAGE : (q.old + PAGE - 1) / PAGE;
+                    c.table[(size_t)seq_of(lo) * c.seq_pages + first + r - (lo ? ranks[lo - 1] : 0)] = p + e;
+                    c.refs[p + e] = 1;
+                    if (r == want - 1) hint = p + e + 1;
+                }
+                ++r;
+            }
+            found += total;
+        }
+        __threadfence_block();
+    }
+    __syncthreads();
+    const int have = min(found, want);
+    if (tid == 0 && have < want) hint = c.n_pages;   // every free page was taken (or is given back below)
+    __syncthreads();
+    for (int j = 0; j * PLAN_THREADS < a.B; ++j) {
+        const int i = tid + j * PLAN_THREADS;
+        if (i >= a.B) break;
+        AppendPlan p = a.plan[i];
+        if (p.n == 0) continue;
+        const int s = seq_of(i), before = i ? ranks[i - 1] : 0, incl = ranks[i];
+        if (incl > before && incl > have) {   // not enough pages: those taken so far go back
+            atomicOr(&flags, TM_CACHE_NO_PAGES);
+            const int first = p.copy_from >= 0 ? p.old / PAGE : (p.old + PAGE - 1) / PAGE;
+            for (int r = before; r < have; ++r) {
+                const size_t at = (size_t)s * c.seq_pages + first + r - before;
+                const int page = c.table[at];
+                c.refs[page] = 0;
+                atomicMin(&hint, page);
+            }
+            if (p.copy_from >= 0 && have > before) c.table[(size_t)s * c.seq_pages + first] = p.copy_from;
+            p.n = 0;
+            p.copy_from = -1;
+            a.plan[i] = p;
+            continue;
+        }
+        c.lengths[s] = p.old + p.n;
+        if (p.copy_from >= 0 && atomicSub(&c.refs[p.copy_from], 1) == 1) atomicMin(&hint, p.copy_from);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        if (want > 0) c.status[1] = min(hint, c.n_pages);
+        if (flags) c.status[0] |= flags;
+    }
+}
+
+__device__ __forceinline__ float finite_or_zero(float x, bool& bad) {
+    if (!(fabsf(x) < __builtin_inff())) {
+        bad = true;
+        return 0.f;
+    }
+    return x;
+}
+
+// The least e with amax <= 448 2^e (448 = 1.75 * 2^8), in the stored range.
+__device__ __forceinline__ int block_exponent(float amax) {
+    const unsigned u = __builtin_bit_cast(unsigned, amax);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffff) > 0x600000 ? 1 : 0);
+    return min(max(e, CACHE_E_MIN), CACHE_E_MAX);
+}
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (unsigned)(e + 127) << 23); }
+
+__device__ __forceinline__ float to_range(float x) { return fminf(fmaxf(x, -448.f), 448.f); }
+// four e4m3 codes of values already divided by their scale
+__device__ __forceinline__ unsigned codes4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(a), to_range(b), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(to_range(c), to_range(d), w, true);
+    return (unsigned)w;
+}
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f32x4 values4(unsigned w) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    return f32x4{a[0], a[1], b[0], b[1]};
+}
+// codes of a grown block: times 2^(old exponent - new one), rounded again
+__device__ __forceinline__ unsigned shift4(unsigned w, float by) {
+    const f32x4 x = values4(w);
+    return codes4(x[0] * by, x[1] * by, x[2] * by, x[3] * by);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int o = 32; o > 0; o /= 2) x = fmaxf(x, __shfl_xor(x, o, 64));
+    return x;
+}
+
+// One workgroup writes the tokens of one page and head, each of its four
+// waves one block of 16.  Keys: a lane takes 8 consecutive elements of a
+// token.  Values, whose tokens are innermost: a lane takes two neighbouring
+// dims of all 16 tokens (4 or 8 bytes a lane and token, so a token's row is
+// read whole) and stores the block's 16 codes of a dim at once; the page's
+// 64-byte row of a dim is made of the four waves' pieces.  The block's
+// largest magnitude is a wave reduction between load and store, so the
+// tokens are read once.
+template <class T, int D>
+__global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
+    const CacheView& c = a.c;
+    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const AppendPlan p = a.plan[b];
+    if (p.n == 0) return;
+    const int slot = p.old / PAGE + blockIdx.x;
+    const int b0 = slot * PAGE + w * BLOCK, end = p.old + p.n;   // the block's first token
+    if (slot * PAGE >= end) return;
+    const int lo = max(p.old, b0), hi = min(end, b0 + BLOCK);    // the new tokens in it
+    const bool copied = blockIdx.x == 0 && p.copy_from >= 0;
+    if (lo >= hi && !copied) return;
+    const int s = a.seqs ? a.seqs[b] : b;
+    const int page = c.page_at(s, slot);
+    if (!c.page_ok(page)) return;
+    const int from = copied ? p.copy_from : page;   // where the block's present codes are
+    const bool begun = lo > b0 && lo < hi;          // it holds earlier tokens, and gets new ones
+    const size_t at = c.head_at(page, h), at0 = c.head_at(from, h);
+    const T* kx = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * D;
+    const T* vx = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * D;
+    bool bad = false;
+
+    // ---- keys ----
+    {
+        constexpr int UNITS = BLOCK * D / 8, IT = UNITS / 64;
+        const unsigned char* src = c.k + (at0 * PAGE + w * BLOCK) * D;
+        unsigned char* dst = c.k + (at * PAGE + w * BLOCK) * D;
+        float x[IT][8];
+        float top = 0.f;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int u = it * 64 + lane, t = u / (D / 8), col = u % (D / 8) * 8;
+            if (b0 + t >= lo && b0 + t < hi) {
+                const auto raw = ld8(kx + (long)(b0 + t - p.old) * a.kt + col);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[it][e] = finite_or_zero((float)raw[e], bad);
+                    top = fmaxf(top, fabsf(x[it][e]));
+                }
+            }
+        }
+        const int had = (int)c.scales[at0 * 8 + w] - 127;
+        int e = had;
+        if (lo < hi) {
+            e = block_exponent(wave_max(top));
+            if (begun) e = max(e, had);
+        }
+        const float by = pow2(-e), shift = begun && e > had ? pow2(max(had - e, -126)) : 1.f;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int u = it * 64 + lane, t = u / (D / 8), col = u % (D / 8) * 8;
+            if (b0 + t >= lo && b0 + t < hi) {
+                uint2 o;
+                o.x = codes4(x[it][0] * by, x[it][1] * by, x[it][2] * by, x[it][3] * by);
+                o.y = codes4(x[it][4] * by, x[it][5] * by, x[it][6] * by, x[it][7] * by);
+                *reinterpret_cast<uint2*>(dst + t * D + col) = o;
+            } else if (copied || (shift != 1.f && b0 + t < lo)) {
+                uint2 o = *reinterpret_cast<const uint2*>(src + t * D + col);
+                if (shift != 1.f && b0 + t < lo) {
+                    o.x = shift4(o.x, shift);
+                    o.y = shift4(o.y, shift);
+                }
+                *reinterpret_cast<uint2*>(dst + t * D + col) = o;
+            }
+        }
+        if (lane == 0) c.scales[at * 8 + w] = (unsigned char)(e + 127);
+    }
+    // ---- values ----
+    {
+        constexpr int IT = (D / 2 + 63) / 64;
+        float x[IT][BLOCK][2];
+        float top = 0.f;
+        typedef T Two __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int dim = (it * 64 + lane) * 2;
+#pragma unroll
+            for (int t = 0; t < BLOCK; ++t) {
+                x[it][t][0] = x[it][t][1] = 0.f;
+                if (dim < D && b0 + t >= lo && b0 + t < hi) {
+                    const Two raw = *reinterpret_cast<const Two*>(vx + (long)(b0 + t - p.old) * a.vt + dim);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[it][t][e] = finite_or_zero((float)raw[e], bad);
+                        top = fmaxf(top, fabsf(x[it][t][e]));
+                    }
+                }
+            }
+        }
+        const int had = (int)c.scales[at0 * 8 + 4 + w] - 127;
+        int e = had;
+        if (lo < hi) {
+            e = block_exponent(wave_max(top));
+            if (begun) e = max(e, had);
+        }
+        const float by = pow2(-e), shift = begun && e > had ? pow2(max(had - e, -126)) : 1.f;
+        // bytes of the block's 16 that take new codes
+        const unsigned fresh = lo < hi ? ((1u << (hi - b0)) - 1) & ~((1u << (lo - b0)) - 1) : 0;
+        const bool whole = fresh == 0xffffu;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int dim = (it * 64 + lane) * 2 + z;
+                if (dim >= D) continue;
+                unsigned o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = codes4(x[it][4 * q][z] * by, x[it][4 * q + 1][z] * by, x[it][4 * q + 2][z] * by,
+                                  x[it][4 * q + 3][z] * by);
+                if (!whole) {
+                    const uint4 was = *reinterpret_cast<const uint4*>(c.v + (at0 * D + dim) * PAGE + w * BLOCK);
+                    const unsigned old4[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const unsigned n4 = fresh >> (4 * q) & 15;   // spread to bytes
+                        const unsigned m = (n4 & 1 ? 0xffu : 0u) | (n4 & 2 ? 0xff00u : 0u) | (n4 & 4 ? 0xff0000u : 0u) |
+                                           (n4 & 8 ? 0xff000000u : 0u);
+                        unsigned keep = old4[q];
+                        if (shift != 1.f) {   // the earlier tokens only: bytes below lo
+                            const int n = min(max(lo - b0 - 4 * q, 0), 4);
+                            const unsigned below = n == 4 ? ~0u : (1u << (8 * n)) - 1;
+                            keep = (shift4(keep, shift) & below) | (keep & ~below);
+                        }
+                        o[q] = (o[q] & m) | (keep & ~m);
+                    }
+                }
+                *reinterpret_cast<uint4*>(c.v + (at * D + dim) * PAGE + w * BLOCK) = uint4{o[0], o[1], o[2], o[3]};
+            }
+        }
+        if (lane == 0) c.scales[at * 8 + 4 + w] = (unsigned char)(e + 127);
+    }
+    if (__any(bad) && lane == 0) atomicOr(&c.status[0], TM_CACHE_NONFINITE);
+}
+
+struct ReadArgs {
+    CacheView c;
+    const int* seqs;
+    void* k;
+    void* v;
+    int start, B, T;
+};
+
+// The append's mapping backwards: one workgroup per page and head, a wave
+// per block.
+template <class T, int D>
+__global__ __launch_bounds__(256) void cache_read_kernel(ReadArgs a) {
+    const CacheView& c = a.c;
+    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int s = a.seqs ? a.seqs[b] : b;
+    if ((unsigned)s >= (unsigned)c.n_seqs) return;
+    const int slot = a.start / PAGE + blockIdx.x;
+    const int b0 = slot * PAGE + w * BLOCK;
+    const int lo = max(a.start, b0), hi = (int)min((long)min(c.length(s), b0 + BLOCK), (long)a.start + a.T);
+    if (lo >= hi) return;
+    const int page = c.page_at(s, slot);
+    if (!c.page_ok(page)) return;
+    const size_t at = c.head_at(page, h);
+    const long row = (long)c.H * D;   // elements between tokens
+    T* ko = reinterpret_cast<T*>(a.k) + ((long)b * a.T - a.start) * row + (long)h * D;
+    T* vo = reinterpret_cast<T*>(a.v) + ((long)b * a.T - a.start) * row + (long)h * D;
+    const float sk = scale_of(c.scales[at * 8 + w]), sv = scale_of(c.scales[at * 8 + 4 + w]);
+    typedef T Four __attribute__((ext_vector_type(4)));
+    constexpr int IT = BLOCK * D / 4 / 64;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int u = it * 64 + lane, t = u / (D / 4), col = u % (D / 4) * 4;
+        if (b0 + t < lo || b0 + t >= hi) continue;
+        const f32x4 x = values4(*reinterpret_cast<const unsigned*>(c.k + (at * PAGE + w * BLOCK + t) * D + col));
+        Four o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (T)(x[e] * sk);
+        *reinterpret_cast<Four*>(ko + (b0 + t) * row + col) = o;
+    }
+    typedef T Two __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int it = 0; it < (D / 2 + 63) / 64; ++it) {
+        const int dim = (it * 64 + lane) * 2;
+        if (dim >= D) continue;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(c.v + (at * D + dim) * PAGE + w * BLOCK);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(c.v + (at * D + dim + 1) * PAGE + w * BLOCK);
+        const unsigned w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 f0 = values4(w0[q]), f1 = values4(w1[q]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = b0 + 4 * q + e;
+                if (t < lo || t >= hi) continue;
+                *reinterpret_cast<Two*>(vo + t * row + dim) = Two{(T)(f0[e] * sv), (T)(f1[e] * sv)};
+            }
+        }
+    }
+}
+
+struct ForkArgs {
+    CacheView c;
+    const int* src;
+    const int* dst;
+    int n;
+};
+
+// One workgroup per fork.  Which forks are served follows from the lists and
+// the lengths before the call alone: a destination must be empty, not listed
+// before, and no source; then no workgroup writes what another reads.
+__global__ __launch_bounds__(256) void fork_kernel(ForkArgs a) {
+    const CacheView& c = a.c;
+    const int i = blockIdx.x, tid = threadIdx.x;
+    __shared__ int refused;
+    if (tid == 0) refused = 0;
+    __syncthreads();
+    const int src = a.src[i], dst = a.dst[i];
+    if ((unsigned)src >= (unsigned)c.n_seqs || (unsigned)dst >= (unsigned)c.n_seqs) {
+        if (tid == 0) atomicOr(&c.status[0], TM_CACHE_BAD_ENTRY);
+        return;
+    }
+    bool no = false;
+    for (int j = tid; j < a.n; j += 256) {
+        const int d = a.dst[j];
+        no |= (j < i && d == dst) || d == src;
+    }
+    if (tid == 0) no |= c.lengths[dst] != 0;
+    if (no) refused = 1;
+    __syncthreads();
+    if (refused) {
+        if (tid == 0) atomicOr(&c.status[0], TM_CACHE_BAD_ENTRY);
+        return;
+    }
+    const int len = c.length(src), held = (len + PAGE - 1) / PAGE;
+    for (int p = tid; p < held; p += 256) {
+        const int page = c.page_at(src, p);
+        c.table[(size_t)dst * c.seq_pages + p] = page;
+        if (c.page_ok(page)) atomicAdd(&c.refs[page], 1);
+    }
+    if (tid == 0) c.lengths[dst] = len;
+}
+
+struct FreeArgs {
+    CacheView c;
+    const int* seqs;
+    const int* keep;
+    int n;
+};
+
+// One workgroup per entry; an entry whose sequence stands earlier in the list
+// is refused, so each sequence's length has one reader and writer.
+__global__ __launch_bounds__(256) void free_kernel(FreeArgs a) {
+    const CacheView& c = a.c;
+    const int i = blockIdx.x, tid = threadIdx.x;
+    const int s = a.seqs ? a.seqs[i] : i;
+    __shared__ int twice;
+    if (tid == 0) twice = 0;
+    __syncthreads();
+    bool no = (unsigned)s >= (unsigned)c.n_seqs;
+    if (a.seqs)
+        for (int j = tid; j < i; j += 256) no |= a.seqs[j] == s;
+    if (no) twice = 1;
+    __syncthreads();
+    if (twice) {
+        if (tid == 0) atomicOr(&c.status[0], TM_CACHE_BAD_ENTRY);
+        return;
+    }
+    const int old = c.length(s), keep = a.keep ? min(max(a.keep[i], 0), old) : 0;
+    __syncthreads();   // every thread has read the length
+    if (tid == 0) c.lengths[s] = keep;
+    for (int p = (keep + PAGE - 1) / PAGE + tid; p < (old + PAGE - 1) / PAGE; p += 256) {
+        const int page = c.page_at(s, p);
+        if (c.page_ok(page) && atomicSub(&c.refs[page], 1) == 1) atomicMin(&c.status[1], page);
+    }
+}
+
+struct CompactArgs {
+    CacheView c;
+    int* count;   // [0] pages to move, [1] pages in use
+    int* from;    // the i-th used page at or above [1]
+    int* to;      // the i-th free page below [1]
+    int* map;     // page -> where it goes (used pages at or above [1])
+    int d;
+};
+
+// One workgroup: the number of pages in use, then the lists of those that
+// move and of the holes they move to, both ascending.
+__global__ __launch_bounds__(PLAN_THREADS) void compact_plan_kernel(CompactArgs a) {
+    const CacheView& c = a.c;
+    __shared__ int wave_sums[PLAN_THREADS / 64];
+    const int tid = threadIdx.x;
+    int mine = 0, used;
+    for (int p = tid; p < c.n_pages; p += PLAN_THREADS) mine += c.refs[p] > 0;
+    block_scan<PLAN_THREADS>(mine, wave_sums, used);
+    int moved = 0, holes = 0;
+    for (int p0 = 0; p0 < c.n_pages; p0 += PLAN_THREADS * 4) {
+        const int p = p0 + tid * 4;
+        int pick4 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (p + e < c.n_pages && (c.refs[p + e] > 0) == (p + e >= used)) pick4 |= 1 << e;
+        // free pages below `used` and used pages above it: a group of four may
+        // hold both, so both are counted in one sum (16 bits each: at most
+        // 4096 in a pass)
+        int nh = 0, nm = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            nh += (pick4 >> e & 1) && p + e < used;
+            nm += (pick4 >> e & 1) && p + e >= used;
+        }
+        int total;
+        const int sum = block_scan<PLAN_THREADS>(nh | nm << 16, wave_sums, total);
+        int rh = holes + (sum & 0xffff) - nh, rm = moved + (sum >> 16) - nm;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!(pick4 >> e & 1)) continue;
+            if (p + e < used) a.to[rh++] = p + e;
+            else a.from[rm++] = p + e;
+        }
+        holes += total & 0xffff;
+        moved += total >> 16;
+    }
+    __threadfence_block();
+    __syncthreads();
+    for (int i = tid; i < moved; i += PLAN_THREADS) a.map[a.from[i]] = a.to[i];
+    if (tid == 0) {
+        a.count[0] = moved;
+        a.count[1] = used;
+        c.status[1] = used;
+    }
+}
+
+// Workgroups below `seq_blocks` rewrite the tables, the others copy pages (a
+// page's keys, values and scales; 16 bytes a thread and step).
+__global__ __launch_bounds__(256) void compact_move_kernel(CompactArgs a, int seq_blocks) {
+    const CacheView& c = a.c;
+    const int tid = threadIdx.x, moved = a.count[0], used = a.count[1];
+    if ((int)blockIdx.x < seq_blocks) {
+        for (int s = blockIdx.x; s < c.n_seqs; s += seq_blocks) {
+            const int held = (c.length(s) + PAGE - 1) / PAGE;
+            for (int p = tid; p < held; p += 256) {
+                int* at = c.table + (size_t)s * c.seq_pages + p;
+                const int page = *at;
+                if (page < used || !c.page_ok(page)) continue;
+                const int to = a.map[page];
+                if (c.page_ok(to)) *at = to;
+            }
+        }
+        return;
+    }
+    const long half = (long)c.H * PAGE * c.d;   // bytes of a page's keys
+    const int pieces = (int)(half / 16);        // and as many of its values
+    for (int i = blockIdx.x - seq_blocks; i < moved; i += gridDim.x - seq_blocks) {
+        const int from = a.from[i], to = a.to[i];
+        const uint4* ks = reinterpret_cast<const uint4*>(c.k + from * half);
+        const uint4* vs = reinterpret_cast<const uint4*>(c.v + from * half);
+        uint4* kd = reinterpret_cast<uint4*>(c.k + to * half);
+        uint4* vd = reinterpret_cast<uint4*>(c.v + to * half);
+#pragma unroll 4
+        for (int p = tid; p < pieces; p += 256) {
+            kd[p] = ks[p];
+            vd[p] = vs[p];
+        }
+        const uint2* ss = reinterpret_cast<const uint2*>(c.scales + (size_t)from * c.H * 8);
+        uint2* sd = reinterpret_cast<uint2*>(c.scales + (size_t)to * c.H * 8);
+        for (int p = tid; p < c.H; p += 256) sd[p] = ss[p];
+        if (tid == 0) {
+            c.refs[to] = c.refs[from];
+            c.refs[from] = 0;
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void cache_init_kernel(CacheView c) {
+    const long n = 64L + c.n_seqs + c.n_pages;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) c.status[i] = 0;
+}
+
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+static tm_status status_of(hipError_t e) { return e == hipSuccess ? TM_OK : TM_ERR_HIP; }
+
+static bool blob_ok(const tm_cache* c, const void* blob) { return c && ptr_ok(blob, 256); }
+static bool list_ok(const int* p) { return (uintptr_t)p % 4 == 0; }
+
+}  // namespace tmk
+
+using namespace tmk;
+
+extern "C" {
+
+tm_status tm_cache_create(int kv_heads, int head_dim, int n_pages, int n_seqs, int seq_pages, tm_cache** out) {
+    if (!out) return TM_ERR_INVALID;
+    *out = nullptr;
+    if (kv_heads < 1 || kv_heads > 1024 || head_dim < 32 || head_dim > 256 || head_dim % 32 != 0 || n_pages < 1 ||
+        n_pages > 1 << 24 || n_seqs < 1 || n_seqs > MAX_SEQS || seq_pages < 1 || seq_pages > 1 << 20 ||
+        (long)n_seqs * seq_pages > 1L << 30)
+        return TM_ERR_INVALID;
+    tm_cache* c = new (std::nothrow) tm_cache;
+    if (!c) return TM_ERR_INVALID;
+    c->H = kv_heads;
+    c->d = head_dim;
+    c->n_pages = n_pages;
+    c->n_seqs = n_seqs;
+    c->seq_pages = seq_pages;
+    const size_t cells = (size_t)n_pages * kv_heads * PAGE * head_dim;
+    c->off[0] = 0;
+    c->off[1] = up256(4 * (64 + (size_t)n_seqs + n_pages + (size_t)n_seqs * seq_pages));
+    c->off[2] = c->off[1] + up256((size_t)n_pages * kv_heads * 8);
+    c->off[3] = c->off[2] + up256(cells);
+    c->bytes = c->off[3] + up256(cells);
+    *out = c;
+    return TM_OK;
+}
+
+void tm_cache_destroy(tm_cache* c) { delete c; }
+
+size_t tm_cache_bytes(const tm_cache* c) { return c ? c->bytes : 0; }
+
+tm_status tm_cache_layout(const tm_cache* c, size_t offsets[4]) {
+    if (!c || !offsets) return TM_ERR_INVALID;
+    for (int i = 0; i < 4; ++i) offsets[i] = c->off[i];
+    return TM_OK;
+}
+
+size_t tm_cache_workspace_bytes(const tm_cache* c, int batch, int n_tokens, int heads) {
+    if (!c || batch < 0 || n_tokens < 0 || heads < 0) return 0;
+    size_t n = up256((size_t)batch * sizeof(AppendPlan));
+    const size_t compact = 256 + up256((size_t)c->n_pages * 12);
+    if (compact > n) n = compact;
+    if (heads > 0) {
+        const size_t at = attend_workspace(c, batch, n_tokens, heads);
+        if (at > n) n = at;
+    }
+    return n;
+}
+
+tm_status tm_cache_init(const tm_cache* c, void* blob, void* stream) {
+    if (!blob_ok(c, blob)) return TM_ERR_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const long n = 64L + c->n_seqs + c->n_pages;
+    const unsigned blocks = (unsigned)((n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024);
+    return status_of(timed_attn(st, [&] {
+        launch_k(cache_init_kernel, dim3(blocks), dim3(256), 0, st, cache_view(c, blob));
+        return hipGetLastError();
+    }));
+}
+
+tm_status tm_cache_append(const tm_cache* c, void* blob, const int* seqs, const int* counts, const void* k,
+                          long k_batch, long k_token, const void* v, long v_batch, long v_token, int batch,
+                          int n_tokens, tm_dtype dtype, void* workspace, void* stream) {
+    if (dtype != TM_F32 && dtype != TM_BF16) return TM_ERR_DTYPE;
+    if (!blob_ok(c, blob) || batch < 0 || n_tokens < 0) return TM_ERR_INVALID;
+    if (batch == 0 || n_tokens == 0) return TM_OK;
+    if (batch > c->n_seqs || !list_ok(seqs) || !list_ok(counts) || !ptr_ok(k, 16) || !ptr_ok(v, 16) ||
+        !ptr_ok(workspace, 256) || !strides_ok(k_batch, k_token) || !strides_ok(v_batch, v_token))
+        return TM_ERR_INVALID;
+    // a longer call could not be served by any sequence
+    const long most = (long)c->seq_pages * PAGE;
+    if (n_tokens > most && !counts) return TM_ERR_INVALID;
+    AppendArgs a{cache_view(c, blob), seqs, counts, k, v, k_batch, k_token, v_batch, v_token, batch, n_tokens,
+                 static_cast<AppendPlan*>(workspace)};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = timed_attn(st, [&] {
+        launch_k(append_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, a);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return TM_ERR_HIP;
+    const long tokens = n_tokens < most ? n_tokens : most;
+    const dim3 grid((unsigned)((tokens + PAGE - 2) / PAGE + 1), (unsigned)c->H, (unsigned)batch);
+    return status_of(timed_attn(st, [&] {
+        return for_head_dim(c->d, [&](auto D) {
+            if (dtype == TM_F32) launch_k(append_write_kernel<float, D()>, grid, dim3(256), 0, st, a);
+            else launch_k(append_write_kernel<bf16, D()>, grid, dim3(256), 0, st, a);
+            return hipGetLastError();
+        });
+    }));
+}
+
+tm_status tm_cache_read(const tm_cache* c, const void* blob, const int* seqs, int start, void* k, void* v, int batch,
+                        int n_tokens, tm_dtype dtype, void* stream) {
+    if (dtype != TM_F32 && dtype != TM_BF16) return TM_ERR_DTYPE;
+    if (!blob_ok(c, blob) || batch < 0 || n_tokens < 0 || start < 0) return TM_ERR_INVALID;
+    if (batch == 0 || n_tokens == 0) return TM_OK;
+    const long most = (long)c->seq_pages * PAGE;
+    if (batch > 65535 || (!seqs && batch > c->n_seqs) || !list_ok(seqs) || !ptr_ok(k, 16) || !ptr_ok(v, 16))
+        return TM_ERR_INVALID;
+    if (start >= most) return TM_OK;
+    ReadArgs a{cache_view(c, const_cast<void*>(blob)), seqs, k, v, start, batch, n_tokens};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const long last = (long)start + n_tokens < most ? (long)start + n_tokens : most;
+    const dim3 grid((unsigned)((last + PAGE - 1) / PAGE - start / PAGE), (unsigned)c->H, (unsigned)batch);
+    return status_of(timed_attn(st, [&] {
+        return for_head_dim(c->d, [&](auto D) {
+            if (dtype == TM_F32) launch_k(cache_read_kernel<float, D()>, grid, dim3(256), 0, st, a);
+            else launch_k(cache_read_kernel<bf16, D()>, grid, dim3(256), 0, st, a);
+            return hipGetLastError();
+        });
+    }));
+}
+
+tm_status tm_cache_fork(const tm_cache* c, void* blob, const int* src, const int* dst, int n, void* stream) {
+    if (!blob_ok(c, blob) || n < 0) return TM_ERR_INVALID;
+    if (n == 0) return TM_OK;
+    if (n > c->n_seqs || !ptr_ok(src, 4) || !ptr_ok(dst, 4)) return TM_ERR_INVALID;
+    ForkArgs a{cache_view(c, blob), src, dst, n};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return status_of(timed_attn(st, [&] {
+        launch_k(fork_kernel, dim3((unsigned)n), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }));
+}
+
+tm_status tm_cache_free(const tm_cache* c, void* blob, const int* seqs, const int* keep, int n, void* stream) {
+    if (!blob_ok(c, blob) || n < 0) return TM_ERR_INVALID;
+    if (n == 0) return TM_OK;
+    if (n > c->n_seqs || !list_ok(seqs) || !list_ok(keep)) return TM_ERR_INVALID;
+    FreeArgs a{cache_view(c, blob), seqs, keep, n};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return status_of(timed_attn(st, [&] {
+        launch_k(free_kernel, dim3((unsigned)n), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }));
+}
+
+tm_status tm_cache_compact(const tm_cache* c, void* blob, void* workspace, void* stream) {
+    if (!blob_ok(c, blob) || !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
+    int* ws = static_cast<int*>(workspace);
+    CompactArgs a{cache_view(c, blob), ws, ws + 64, ws + 64 + (size_t)c->n_pages, ws + 64 + 2 * (size_t)c->n_pages, c->d};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = timed_attn(st, [&] {
+        launch_k(compact_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, a);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return TM_ERR_HIP;
+    const int seq_blocks = c->n_seqs < 256 ? c->n_seqs : 256;
+    const int movers = c->n_pages < 4096 ? c->n_pages : 4096;
+    return status_of(timed_attn(st, [&] {
+        launch_k(compact_move_kernel, dim3((unsigned)(seq_blocks + movers)), dim3(256), 0, st, a, seq_blocks);
+        return hipGetLastError();
+    }));
+}
+
+tm_status tm_cache_check(const tm_cache* c, const void* blob, int* flags, int* pages_used, void* stream) {
+    if (!blob_ok(c, blob)) return TM_ERR_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const CacheView v = cache_view(c, const_cast<void*>(blob));
+    int f = 0;
+    if (hipMemcpyAsync(&f, v.status, 4, hipMemcpyDeviceToHost, st) != hipSuccess) return TM_ERR_HIP;
+    int* refs = nullptr;
+    if (pages_used) {
+        refs = new (std::nothrow) int[c->n_pages];
+        if (!refs) return TM_ERR_HIP;
+        if (hipMemcpyAsync(refs, v.refs, 4 * (size_t)c->n_pages, hipMemcpyDeviceToHost, st) != hipSuccess) {
+            (void)hipStreamSynchronize(st);
+            delete[] refs;
+            return TM_ERR_HIP;
+        }
+    }
+    const bool ok = hipStreamSynchronize(st) == hipSuccess;
+    if (ok && flags) *flags = f;
+    if (ok && pages_used) {
+        int n = 0;
+        for (int i = 0; i < c->n_pages; ++i) n += refs[i] > 0;
+        *pages_used = n;
+    }
+    delete[] refs;
+    return ok ? TM_OK : TM_ERR_HIP;
+}
+
+}  // extern "C"

@@ -521,6 +521,13 @@ struct MacArgs {
 hipError_t launch_mac_window(const MacArgs& a, int f32, hipStream_t st);
 hipError_t launch_mac_gate(const MacArgs& a, int f32, hipStream_t st);
 
+// One launch of the attention window's kernels (tm_rope.hip, tm_cache.hip,
+// tm_attend.hip), timed under their class when that is on (tm_api.hip).
+hipError_t timed_attn_call(hipStream_t st, hipError_t (*call)(void*), void* arg);
+template <class F> inline hipError_t timed_attn(hipStream_t st, F launch) {
+    return timed_attn_call(st, [](void* f) { return (*static_cast<F*>(f))(); }, &launch);
+}
+
 // ---- launchers (tm_project.hip) ----
 hipError_t launch_project(const ProjArgs& p, int f32, hipStream_t st);
 

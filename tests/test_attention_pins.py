@@ -1,0 +1,251 @@
+"""Pins of the attention window's oracle (oracle/attention.py) against hand
+values and torch's own conversions, and the host side of its C calls: the
+library exports what include/tm_attention.h declares and refuses bad
+arguments before anything is launched.  No GPU needed."""
+import ctypes
+import math
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import test_trained_neural_amd as T
+from oracle import attention as O
+from test_trained_neural_amd import attention as A
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+# ---- the oracle ----
+
+def test_e4m3_rounding_matches_torch():
+    rng = np.random.default_rng(3)
+    x = np.concatenate([rng.standard_normal(4096) * 10.0 ** rng.integers(-4, 3, 4096),
+                        np.arange(0, 449, 0.25), 2.0 ** -9 * np.arange(-40, 40) / 4]).astype(np.float32)
+    x = np.clip(x, -448, 448)
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).to(torch.float64).numpy()
+    assert np.array_equal(O.round_e4m3(x), want)
+
+
+def test_exponent_by_hand():
+    assert O.exponent(448.0) == 0 and O.exponent(448.0001) == 1 and O.exponent(224.0) == -1
+    assert O.exponent(0.0) == O.E_MIN and O.exponent(3e38) == O.E_MAX
+
+
+def test_rotation_by_hand():
+    x = np.zeros((1, 1, 1, 5))
+    x[..., :] = [1.0, 2.0, 3.0, 4.0, 5.0]
+    f = [math.pi / 2, math.pi]     # position 1: a quarter turn, half a turn
+    assert np.allclose(O.rotate(x, [[1]], f)[0, 0, 0], [-3, -2, 1, -4, 5])
+    assert np.allclose(O.rotate(x, [[1]], f, interleaved=True)[0, 0, 0], [-2, 1, -3, -4, 5])
+    y = O.rotate(x, [[7]], [0.3, 0.01], scale=1.5)
+    assert np.allclose(O.rotate(y, [[7]], [0.3, 0.01], scale=1 / 1.5, inverse=True), x)
+
+
+def test_rotation_gradient_by_differences():
+    rng = np.random.default_rng(0)
+    x, dy = rng.standard_normal((2, 3, 2, 8)), rng.standard_normal((2, 3, 2, 8))
+    pos, f = rng.integers(0, 1000, (2, 3)), [0.7, 0.1, 0.02]
+    g = O.rotate(dy, pos, f, 1.25, inverse=True)
+    g[..., 6:] = dy[..., 6:]
+    for at in ((0, 0, 0, 0), (1, 2, 1, 4), (0, 1, 0, 7)):
+        e = np.zeros_like(x)
+        e[at] = 1e-5
+        d = ((O.rotate(x + e, pos, f, 1.25) - O.rotate(x - e, pos, f, 1.25)) * dy).sum() / 2e-5
+        assert abs(d - g[at]) < 1e-8
+
+
+def test_cache_model_rules():
+    rng = np.random.default_rng(1)
+    c = O.Cache(1, 32, 6, 4, 3)
+    x = lambda n: rng.standard_normal((1, n, 1, 32))  # noqa: E731
+    c.append([0], [70], x(70), x(70))
+    assert c.pages[0] == [0, 1] and c.lengths[0] == 70
+    k0 = c.held(0)[0].copy()
+    assert np.abs(k0 - c.held(0)[0]).max() == 0
+    c.fork([0, 0], [1, 2])
+    assert c.refs[:2] == [3, 3]
+    c.append([1], [1], x(1), x(1))                       # copies the shared last page
+    assert c.pages[1] == [0, 2] and c.refs[:3] == [3, 2, 1]
+    assert np.array_equal(c.held(0)[0], k0) and np.array_equal(c.held(2)[0], k0)
+    assert np.allclose(c.held(1)[0][:64], k0[:64])
+    c.free([0, 2])
+    assert c.refs[:3] == [1, 0, 1] and c.used() == 2
+    c.compact()
+    assert c.pages[1] == [0, 1] and c.used() == 2 and c.flags == 0
+    c.append([1], [200], x(200), x(200))
+    assert c.flags == O.FULL and c.lengths[1] == 71
+    c.append([1, 1, 9], [1, 1, 1], np.repeat(x(1), 3, 0), np.repeat(x(1), 3, 0))
+    assert c.flags == O.FULL | O.BAD_ENTRY and c.lengths[1] == 72
+
+
+def test_attention_by_hand():
+    k = np.zeros((3, 1, 2))
+    k[:, 0] = [[0, 0], [math.log(3), 0], [0, 5]]
+    v = np.array([[[1.0, 0]], [[5.0, 2.0]], [[7.0, 1.0]]])
+    q = np.array([[[1.0, 0]], [[1.0, 0]]])               # positions 1 and 2
+    out, _, _ = O.attend(k, v, q, 1.0)
+    assert np.allclose(out[0, 0], [4.0, 1.5])            # weights 1/4, 3/4
+    assert np.allclose(out[1, 0], [(1 + 15 + 7) / 5, (6 + 1) / 5])
+    out, _, _ = O.attend(k, v, q, 1.0, window=1)
+    assert np.allclose(out[:, 0], v[1:, 0])
+    out, _, _ = O.attend(k, v, q, 1.0, window=1, sink=1)
+    assert np.allclose(out[1, 0], [4.0, 0.5])
+    out, _, _ = O.attend(k[:1], v[:1], q, 1.0)           # the first query stands before the sequence
+    assert np.allclose(out[:, 0], [[0, 0], [1, 0]])
+
+
+# ---- the library, on the host ----
+
+def declared():
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "tm_attention.h")).read(), flags=re.S)
+    return set(re.findall(r"\b(tm_[a-z0-9_]+)\s*\(", src))
+
+
+def test_library_exports_every_declared_symbol():
+    assert declared() == set(A.EXPORTED)
+    L = ctypes.CDLL(T.LIB_PATH)
+    for s in A.EXPORTED:
+        assert hasattr(L, s), s
+
+
+def test_frequencies():
+    f, s = T.tm_rotary_frequencies(8)
+    assert s == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001], rtol=1e-15)
+    f, s = T.tm_rotary_frequencies(8, scaling=T.TM_ROPE_LINEAR, factor=4.0)
+    assert s == 1.0 and np.allclose(f, [0.25, 0.025, 0.0025, 0.00025], rtol=1e-15)
+    f, _ = T.tm_rotary_frequencies(8, scaling=T.TM_ROPE_BASE, factor=4.0)
+    assert np.allclose(f, (10000.0 * 4.0 ** (8 / 6)) ** (-np.arange(4) / 4), rtol=1e-13)
+    f, s = T.tm_rotary_frequencies(64, scaling=T.TM_ROPE_PARTS, factor=16.0, original_len=4096)
+    plain = 10000.0 ** (-np.arange(32) / 32)
+    turns = 4096 * plain / (2 * math.pi)
+    assert abs(s - (0.1 * math.log(16) + 1)) < 1e-15
+    fast, slow = turns > 32 * 1.4, turns < 0.7
+    assert fast.any() and slow.any()
+    assert np.allclose(np.array(f)[fast], plain[fast], rtol=1e-15)
+    assert np.allclose(np.array(f)[slow], plain[slow] / 16, rtol=1e-15)
+    assert np.all(np.diff(np.array(f) / plain) <= 1e-15)
+
+
+@pytest.mark.parametrize("args", [dict(rot_dim=0), dict(rot_dim=7), dict(rot_dim=1026), dict(rot_dim=8, base=1.0),
+                                  dict(rot_dim=8, base=math.inf), dict(rot_dim=8, base=math.nan),
+                                  dict(rot_dim=8, scaling=7), dict(rot_dim=8, scaling=1, factor=0.0),
+                                  dict(rot_dim=2, scaling=2, factor=2.0), dict(rot_dim=8, scaling=3, factor=2.0),
+                                  dict(rot_dim=8, scaling=3, factor=2.0, original_len=64, beta_fast=1.0, beta_slow=1.0)])
+def test_frequencies_refusals(args):
+    with pytest.raises(T.TMError) as e:
+        T.tm_rotary_frequencies(**args)
+    assert e.value.code == T.TM_ERR_INVALID
+
+
+def test_create_refusals_and_sizes():
+    for args in [(0, 64, 4, 1, 1), (1025, 64, 4, 1, 1), (2, 48, 4, 1, 1), (2, 288, 4, 1, 1), (2, 0, 4, 1, 1),
+                 (2, 64, 0, 1, 1), (2, 64, (1 << 24) + 1, 1, 1), (2, 64, 4, 0, 1), (2, 64, 4, 8193, 1), (2, 64, 4, 1, 0),
+                 (2, 64, 4, 1, (1 << 20) + 1), (2, 64, 4, 8192, 1 << 20)]:
+        with pytest.raises(T.TMError) as e:
+            A.tm_cache_create(*args)
+        assert e.value.code == T.TM_ERR_INVALID
+    assert A._lib().tm_cache_create(2, 64, 4, 1, 1, None) == T.TM_ERR_INVALID
+    h = A.tm_cache_create(2, 96, 5, 3, 4)
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    meta, scales, cells = up(4 * (64 + 3 + 5 + 12)), up(5 * 2 * 8), up(5 * 2 * 64 * 96)
+    assert A.tm_cache_layout(h) == (0, meta, meta + scales, meta + scales + cells)
+    assert A.tm_cache_bytes(h) == meta + scales + 2 * cells
+    assert A.tm_cache_workspace_bytes(h, 3, 10) > 0 and A.tm_cache_bytes(None) == 0
+    A.tm_cache_destroy(h)
+
+
+def test_calls_refuse_before_launch():
+    # fake, aligned "device" addresses: every call below must be refused on
+    # the host, so nothing is dereferenced or launched
+    L, INV, DT, OK = A._lib(), T.TM_ERR_INVALID, T.TM_ERR_DTYPE, T.TM_OK
+    h = A.tm_cache_create(2, 64, 8, 4, 4)
+    P = 1 << 20
+    bf, f32 = T.TM_BF16, T.TM_F32
+
+    def append(cache=h, blob=P, seqs=None, counts=None, k=P, kb=128, kt=128, v=P, vb=128, vt=128, batch=1, n=1, dt=bf,
+               ws=P):
+        return L.tm_cache_append(cache, blob, seqs, counts, k, kb, kt, v, vb, vt, batch, n, dt, ws, None)
+
+    for bad in (dict(cache=None), dict(blob=None), dict(blob=P + 16), dict(k=None), dict(k=P + 8), dict(v=None),
+                dict(v=P + 2), dict(kb=4), dict(kt=-8), dict(vb=1), dict(vt=12), dict(batch=-1), dict(batch=5),
+                dict(n=-1), dict(n=257), dict(ws=None), dict(ws=P + 64), dict(seqs=P + 1), dict(counts=P + 2),
+                dict(kb=1 << 41)):
+        assert append(**bad) == INV, bad
+    assert append(dt=7) == DT
+    assert append(batch=0) == OK and append(n=0) == OK and append(n=0, k=None, v=None) == OK
+
+    def attend(cache=h, blob=P, seqs=None, counts=None, q=P, qb=256, qt=256, out=P, batch=1, n=1, heads=4, scale=0.125,
+               window=0, sink=0, max_len=0, dt=bf, ws=P):
+        return L.tm_cache_attend(cache, blob, seqs, counts, q, qb, qt, out, batch, n, heads, scale, window, sink,
+                                 max_len, dt, ws, None)
+
+    for bad in (dict(cache=None), dict(blob=None), dict(blob=P + 128), dict(q=None), dict(q=P + 4), dict(qb=12),
+                dict(qt=-8), dict(out=None), dict(out=P + 8), dict(batch=-1), dict(batch=5), dict(batch=65536, seqs=P),
+                dict(n=-1), dict(n=(1 << 24) + 1), dict(heads=0), dict(heads=3), dict(heads=130), dict(scale=math.nan),
+                dict(scale=math.inf), dict(window=-1), dict(sink=-1), dict(max_len=-1), dict(seqs=P + 1),
+                dict(counts=P + 3)):
+        assert attend(**bad) == INV, bad
+    assert attend(dt=2) == DT
+    assert attend(batch=0) == OK and attend(n=0, q=None, out=None) == OK
+
+    def read(cache=h, blob=P, seqs=None, start=0, k=P, v=P, batch=1, n=1, dt=bf):
+        return L.tm_cache_read(cache, blob, seqs, start, k, v, batch, n, dt, None)
+
+    for bad in (dict(cache=None), dict(blob=P + 4), dict(start=-1), dict(k=None), dict(v=P + 8), dict(batch=5),
+                dict(n=-1), dict(seqs=P + 2)):
+        assert read(**bad) == INV, bad
+    assert read(dt=5) == DT and read(n=0) == OK and read(start=256) == OK
+    assert L.tm_cache_fork(h, P, P, None, 1, None) == INV and L.tm_cache_fork(h, P, P, P, 5, None) == INV
+    assert L.tm_cache_fork(h, P, P + 2, P, 1, None) == INV and L.tm_cache_fork(h, P, P, P, -1, None) == INV
+    assert L.tm_cache_fork(h, None, P, P, 1, None) == INV and L.tm_cache_fork(h, P, None, None, 0, None) == OK
+    assert L.tm_cache_free(h, P, None, None, 5, None) == INV and L.tm_cache_free(h, P, P + 1, None, 1, None) == INV
+    assert L.tm_cache_free(None, P, None, None, 1, None) == INV and L.tm_cache_free(h, P, None, None, 0, None) == OK
+    assert L.tm_cache_compact(h, P, None, None) == INV and L.tm_cache_compact(h, P + 8, P, None) == INV
+    assert L.tm_cache_init(h, None, None) == INV and L.tm_cache_init(None, P, None) == INV
+    assert L.tm_cache_check(h, None, None, None, None) == INV
+
+    def rotary(x=P, xb=0, xt=64, y=P, yb=0, yt=64, pos=P, freq=P, scale=1.0, batch=1, n=2, heads=1, d=64, r=64,
+               layout=0, dt=f32):
+        return L.tm_rotary(x, xb, xt, y, yb, yt, pos, 1, freq, scale, batch, n, heads, d, r, layout, 0, dt, None)
+
+    for bad in (dict(x=None), dict(x=P + 2), dict(y=None), dict(pos=None), dict(pos=P + 2), dict(freq=P + 4),
+                dict(freq=None), dict(scale=math.nan), dict(batch=-1), dict(n=-1), dict(heads=0), dict(d=0), dict(d=1025),
+                dict(r=3), dict(r=66), dict(r=0), dict(layout=2), dict(yt=32, y=P + 4096), dict(xt=-1), dict(xt=128),
+                dict(batch=2, yb=64, xb=64)):
+        assert rotary(**bad) == INV, bad
+    assert rotary(dt=9) == DT and rotary(n=0) == OK and rotary(batch=0, x=None) == OK
+    A.tm_cache_destroy(h)
+
+
+def test_binding_checks():
+    bf, f32 = torch.bfloat16, torch.float32
+    x = torch.zeros((1, 2, 3, 8))
+    pos, f = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(4, dtype=torch.float64)
+    with pytest.raises(ValueError, match="device"):
+        T.tm_rotary(x, x, pos, f)
+    with pytest.raises(TypeError, match="positions"):
+        T.tm_rotary(x, x, pos.long(), f)
+    with pytest.raises(TypeError, match="freq"):
+        T.tm_rotary(x, x, pos, f.float())
+    with pytest.raises(TypeError, match="y"):
+        T.tm_rotary(x, x.to(bf), pos, f)
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        T.tm_rotary(x.half(), x.half(), pos, f)
+    with pytest.raises(ValueError, match="shape"):
+        T.tm_rotary(x, x[:, :1], pos, f)
+    with pytest.raises(ValueError, match="blob"):
+        T.PagedCache(1, 32, 2, 1, 2, blob=torch.zeros(1 << 20, dtype=torch.uint8))
+    for t in (x.transpose(2, 3), x[..., ::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            A._heads_of("q", t)
+    with pytest.raises(ValueError, match="16-byte"):
+        A._heads_of("q", torch.zeros((1, 2, 1, 12), dtype=f32))
+    with pytest.raises(ValueError, match="axes"):
+        A._heads_of("q", x[0])
+    with pytest.raises(TypeError, match="int32"):
+        A._list("seqs", torch.zeros(2, dtype=torch.int64), 2)
+    with pytest.raises(ValueError, match="hold 2"):
+        A._list("seqs", torch.zeros(3, dtype=torch.int32), 2)
