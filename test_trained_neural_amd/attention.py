@@ -64,6 +64,29 @@ def _lib():
 
 # ---------------------------------------------------------------------------
 # argument checks
+#
+# What a call checks of its tensors' types, shapes, distances and devices
+# follows from those alone, so each call keeps, per combination that has
+# passed, what it read off them (a step of a few microseconds would otherwise
+# spend most of them here).  Addresses are checked on every call.
+
+_passed = {}
+
+
+def _once(key, check):
+    """check()'s result, remembered under ``key``."""
+    v = _passed.get(key)
+    if v is None:
+        if len(_passed) > 4096:
+            _passed.clear()
+        v = _passed[key] = check()
+    return v
+
+
+def _look(t):
+    """What a check sees of a tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
 
 def _on(device, *named):
     """Every given tensor is on ``device``, a GPU."""
@@ -84,9 +107,15 @@ def _heads_of(name, t, aligned=True):
     if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError("the last two axes of %s must be contiguous" % name)
     st, sb = (H * d if N <= 1 else st), (N * H * d if B <= 1 else sb)
-    if aligned and (t.data_ptr() % 16 or sb % 8 or st % 8):
+    if aligned and (sb % 8 or st % 8):
         raise ValueError("%s must be 16-byte aligned, its distances multiples of 8 elements" % name)
     return sb, st
+
+
+def _aligned(name, ptr):
+    if ptr % 16:
+        raise ValueError("%s must be 16-byte aligned" % name)
+    return ptr
 
 
 def _list(name, t, n):
@@ -97,24 +126,30 @@ def _list(name, t, n):
             raise ValueError("%s must be contiguous and hold %d values, got %s" % (name, n, tuple(t.shape)))
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 class _Device:
     """The device of a call as the current one, and its stream: ``stream``
     (then also the one that the call's own buffers are allocated for) or the
     device's current one."""
 
+    __slots__ = ("guard", "index")
+
     def __init__(self, device, stream):
-        self.guard = None
+        self.guard, self.index = None, device.index
         if stream is not None:
             if stream.device != device:
                 raise ValueError("stream is on %s, the call is on %s" % (stream.device, device))
             self.guard = torch.cuda.stream(stream)
-        elif device.index is not None and device.index != torch.cuda.current_device():
+        elif self.index != torch._C._cuda_getDevice():
             self.guard = torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return _vp(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *e):
         if self.guard is not None:
@@ -133,10 +168,7 @@ def tm_rotary_frequencies(rot_dim, base=10000.0, scaling=TM_ROPE_NONE, factor=1.
     return list(f), s.value
 
 
-def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inverse=False, stream=None):
-    """x, y [B][T][H][d] (any distances between tokens and entries; y may be
-    x); positions int32 [B][T], or [B] (the first token's); freq [rot_dim / 2]
-    fp64."""
+def _rotary_geometry(x, y, positions, freq):
     dt = T._dtype_code(x)
     T._same(x.dtype, ("y", y))
     T._same(torch.int32, ("positions", positions))
@@ -149,10 +181,20 @@ def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inve
     T._shape("positions", positions, (B, N) if per_token else (B,))
     if not positions.is_contiguous() or not freq.is_contiguous() or freq.dim() != 1:
         raise ValueError("positions and freq must be contiguous")
+    return xb, xt, yb, yt, 1 if per_token else 0, (B, N, H, d, 2 * freq.shape[0]), dt
+
+
+def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inverse=False, stream=None):
+    """x, y [B][T][H][d] (any distances between tokens and entries; y may be
+    x); positions int32 [B][T], or [B] (the first token's); freq [rot_dim / 2]
+    fp64."""
+    xb, xt, yb, yt, per_token, sizes, dt = _once(
+        ("rotary", _look(x), _look(y), _look(positions), _look(freq)), lambda: _rotary_geometry(x, y, positions, freq))
     with _Device(x.device, stream) as st:
-        T._check("tm_rotary", _lib().tm_rotary(x.data_ptr(), xb, xt, y.data_ptr(), yb, yt, positions.data_ptr(),
-                                               per_token, freq.data_ptr(), result_scale, B, N, H, d,
-                                               2 * freq.shape[0], layout, 1 if inverse else 0, dt, st))
+        rc = _lib().tm_rotary(x.data_ptr(), xb, xt, y.data_ptr(), yb, yt, positions.data_ptr(), per_token,
+                              freq.data_ptr(), result_scale, *sizes, layout, 1 if inverse else 0, dt, st)
+    if rc:
+        T._check("tm_rotary", rc)
 
 
 def tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages):
@@ -195,11 +237,13 @@ class Rotary:
         self.freq = torch.tensor(f, dtype=torch.float64, device=device)
 
     def __call__(self, x, positions, inverse=False, out=None, stream=None):
-        _on(x.device, ("x", x))
-        with _Device(x.device, stream):
-            if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            tm_rotary(x, out, positions, self.freq, self.result_scale, self.layout, inverse)
+        if stream is not None:
+            _on(x.device, ("x", x))
+            with _Device(x.device, stream):
+                return self(x, positions, inverse, out)
+        if out is None:
+            out = x.new_empty(x.shape)
+        tm_rotary(x, out, positions, self.freq, self.result_scale, self.layout, inverse)
         return out
 
 
@@ -223,6 +267,7 @@ class PagedCache:
         if blob.data_ptr() % 256:
             raise ValueError("blob must be 256-byte aligned")
         self.blob, self.device = blob, blob.device
+        self._h, self._b = self.handle.value, blob.data_ptr()
         o, cells = tm_cache_layout(self.handle), n_pages * kv_heads * TM_CACHE_PAGE * head_dim
         ints = 64 + n_seqs + n_pages + n_seqs * seq_pages
         self.meta = blob[:4 * ints].view(torch.int32)
@@ -232,7 +277,8 @@ class PagedCache:
         self.scales = blob[o[1]:o[1] + n_pages * kv_heads * 8].view(n_pages, kv_heads, 2, 4)
         self.k = blob[o[2]:o[2] + cells].view(torch.float8_e4m3fn).view(n_pages, kv_heads, TM_CACHE_PAGE, head_dim)
         self.v = blob[o[3]:o[3] + cells].view(torch.float8_e4m3fn).view(n_pages, kv_heads, head_dim, TM_CACHE_PAGE)
-        self._need = {}
+        self._need, self._kind = {}, (kv_heads, head_dim, blob.device)   # what a call's checks go by
+        self._scale = 1.0 / math.sqrt(head_dim)
         if fresh:
             self.init()
 
@@ -244,7 +290,9 @@ class PagedCache:
             pass
 
     def _call(self, name, st, *args):
-        T._check(name, getattr(_declared, name)(self.handle, self.blob.data_ptr(), *args, st))
+        rc = getattr(_declared, name)(self._h, self._b, *args, st)
+        if rc:
+            T._check(name, rc)
 
     def _workspace(self, batch, n_tokens, heads):
         """Workspace of one call: from torch's allocator, in the stream's
@@ -256,7 +304,7 @@ class PagedCache:
             if len(self._need) > 4096:
                 self._need.clear()
             need = self._need[key] = tm_cache_workspace_bytes(self.handle, batch, n_tokens, heads)
-        return torch.empty(need, dtype=torch.uint8, device=self.device)
+        return self.blob.new_empty(need)
 
     def init(self, stream=None):
         with _Device(self.device, stream) as st:
@@ -265,43 +313,52 @@ class PagedCache:
     def append(self, seqs, k, v, counts=None, stream=None):
         """Writes k, v [B][T][kv_heads][d] behind the sequences ``seqs``
         (int32 [B]; None: 0 ..); counts int32 [B]: tokens of each entry."""
-        dt = T._dtype_code(k)
-        T._same(k.dtype, ("v", v))
-        T._shape("v", v, k.shape)
-        (kb, kt), (vb, vt) = _heads_of("k", k), _heads_of("v", v)
-        B, N, H, d = k.shape
-        T._shape("k", k, (B, N, self.kv_heads, self.head_dim))
-        _list("seqs", seqs, B)
-        _list("counts", counts, B)
-        _on(self.device, ("k", k), ("v", v), ("seqs", seqs), ("counts", counts))
+        def check():
+            dt = T._dtype_code(k)
+            T._same(k.dtype, ("v", v))
+            T._shape("v", v, k.shape)
+            d_k, d_v = _heads_of("k", k), _heads_of("v", v)
+            B, N = k.shape[:2]
+            T._shape("k", k, (B, N, self.kv_heads, self.head_dim))
+            _list("seqs", seqs, B)
+            _list("counts", counts, B)
+            _on(self.device, ("k", k), ("v", v), ("seqs", seqs), ("counts", counts))
+            return d_k, d_v, B, N, dt
+
+        d_k, d_v, B, N, dt = _once((self._kind, "append", _look(k), _look(v), _look(seqs), _look(counts)), check)
+        pk, pv = _aligned("k", k.data_ptr()), _aligned("v", v.data_ptr())
         with _Device(self.device, stream) as st:
             ws = self._workspace(B, N, 0)
-            self._call("tm_cache_append", st, T._ptr(seqs), T._ptr(counts), k.data_ptr(), kb, kt, v.data_ptr(), vb,
-                       vt, B, N, dt, ws.data_ptr())
+            self._call("tm_cache_append", st, _at(seqs), _at(counts), pk, *d_k, pv, *d_v, B, N, dt, ws.data_ptr())
 
     def attend(self, seqs, q, counts=None, scale=None, window=0, sink=0, max_len=0, out=None, stream=None):
         """Attention of q [B][T][heads][d], each sequence's last tokens
         (``counts`` of them), over the cache; scale: 1 / sqrt(d) by default.
         Returns [B][T][heads][d] of q's type.  Rows behind an entry's count
         are left as they were: zeros in a new output."""
-        dt = T._dtype_code(q)
-        qb, qt = _heads_of("q", q)
-        B, N, H, d = q.shape
-        T._shape("q", q, (B, N, H, self.head_dim))
-        _list("seqs", seqs, B)
-        _list("counts", counts, B)
-        _on(self.device, ("q", q), ("out", out), ("seqs", seqs), ("counts", counts))
-        if out is not None:
-            T._same(q.dtype, ("out", out))
-            T._shape("out", out, q.shape)
-            if not out.is_contiguous():
-                raise ValueError("out must be contiguous")
+        def check():
+            dt = T._dtype_code(q)
+            d_q = _heads_of("q", q)
+            B, N, H, d = q.shape
+            T._shape("q", q, (B, N, H, self.head_dim))
+            _list("seqs", seqs, B)
+            _list("counts", counts, B)
+            _on(self.device, ("q", q), ("out", out), ("seqs", seqs), ("counts", counts))
+            if out is not None:
+                T._same(q.dtype, ("out", out))
+                T._shape("out", out, q.shape)
+                if not out.is_contiguous():
+                    raise ValueError("out must be contiguous")
+            return d_q, B, N, H, dt
+
+        d_q, B, N, H, dt = _once((self._kind, "attend", _look(q), _look(seqs), _look(counts), _look(out)), check)
+        pq = _aligned("q", q.data_ptr())
         with _Device(self.device, stream) as st:
             if out is None:
-                out = (torch.empty if counts is None else torch.zeros)((B, N, H, d), dtype=q.dtype, device=q.device)
+                out = q.new_empty(q.shape) if counts is None else q.new_zeros(q.shape)
             ws = self._workspace(B, N, H)
-            self._call("tm_cache_attend", st, T._ptr(seqs), T._ptr(counts), q.data_ptr(), qb, qt, out.data_ptr(), B,
-                       N, H, 1.0 / math.sqrt(d) if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
+            self._call("tm_cache_attend", st, _at(seqs), _at(counts), pq, *d_q, out.data_ptr(), B, N, H,
+                       self._scale if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
         return out
 
     def read(self, seqs, start, n_tokens, dtype=torch.float32, k=None, v=None, stream=None):
@@ -321,27 +378,38 @@ class PagedCache:
             if not k.is_contiguous() or not v.is_contiguous():
                 raise ValueError("k and v must be contiguous")
             _on(self.device, ("k", k), ("v", v), ("seqs", seqs))
-            self._call("tm_cache_read", st, T._ptr(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
+            self._call("tm_cache_read", st, _at(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
         return k, v
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] (empty) becomes a copy of src[i] that shares its
         pages (int32 [n] each)."""
-        _list("src", src, src.shape[0])
-        _list("dst", dst, src.shape[0])
-        _on(self.device, ("src", src), ("dst", dst))
+        n = src.shape[0]
+
+        def check():
+            _list("src", src, n)
+            _list("dst", dst, n)
+            _on(self.device, ("src", src), ("dst", dst))
+            return True
+
+        _once((self._kind, "fork", _look(src), _look(dst)), check)
         with _Device(self.device, stream) as st:
-            self._call("tm_cache_fork", st, src.data_ptr(), dst.data_ptr(), src.shape[0])
+            self._call("tm_cache_fork", st, src.data_ptr(), dst.data_ptr(), n)
 
     def free(self, seqs, keep=None, stream=None):
         """Drops all tokens of the sequences, or those behind the first
         keep[i] (int32 [n] each; seqs None: 0 .. n_seqs - 1)."""
         n = self.n_seqs if seqs is None else seqs.shape[0]
-        _list("seqs", seqs, n)
-        _list("keep", keep, n)
-        _on(self.device, ("seqs", seqs), ("keep", keep))
+
+        def check():
+            _list("seqs", seqs, n)
+            _list("keep", keep, n)
+            _on(self.device, ("seqs", seqs), ("keep", keep))
+            return True
+
+        _once((self._kind, "free", n, _look(seqs), _look(keep)), check)
         with _Device(self.device, stream) as st:
-            self._call("tm_cache_free", st, T._ptr(seqs), T._ptr(keep), n)
+            self._call("tm_cache_free", st, _at(seqs), _at(keep), n)
 
     def compact(self, stream=None):
         """Moves the pages in use to the lowest numbers."""
