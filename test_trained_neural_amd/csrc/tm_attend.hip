@@ -43,6 +43,9 @@ struct AttendArgs {
 };
 
 constexpr float NEG_INF = -__builtin_inff();
+// A row's running maximum moves when it grows by more than this: weights up
+// to 2^8 are as exact, and the accumulators are rarely rescaled.
+constexpr float SLACK = 8.f;
 
 // What the row r = i G + g of entry b sees: tokens lo .. pos and 0 .. sink-1.
 struct RowSpan {
@@ -126,39 +129,40 @@ __device__ __forceinline__ float group_sum(float x) {
     return x + __shfl_xor(x, 32, 64);
 }
 
-// Rows of one kv head against its sequence, RT tiles of 16 rows per
-// workgroup (row r = i G + g: query token i, head g of the group).  The four
-// waves take every fourth page of the workgroup's range; their accumulators
-// are joined in LDS at the end.  With one range the workgroup writes the
-// output, otherwise its accumulators, maxima and sums for combine_kernel.
-template <class T, int D, int RT>
+// Few rows of one kv head against its sequence (single tokens, drafts): WR
+// tiles of 16 rows per workgroup (row r = i G + g: query token i, head g of
+// the group).  Wave w takes row tile w % WR and every (4 / WR)-th page of the
+// workgroup's range; the waves of a tile are joined in LDS at the end.  With
+// one range the workgroup writes the output, otherwise its accumulators,
+// maxima and sums for combine_kernel.  Bound by reading the pages: a wave's
+// next keys and present values are in flight while it computes.
+template <class T, int D, int WR>
 __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
     constexpr int NP = sizeof(T) == 4 ? 3 : 1;
-    constexpr int WAVES = 4;
+    constexpr int WAVES = 4, WP = WAVES / WR;   // waves that share a row tile
     const CacheView& c = a.c;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    const int wr = w % WR, wp = w / WR;
     const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, h = blockIdx.y, b = blockIdx.z;
     const int s = a.seqs ? a.seqs[b] : b;
     const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
-    const int rows = count * a.G, row0 = tile * 16 * RT;
-    if (row0 >= rows) return;
-    const bool known = (unsigned)s < (unsigned)c.n_seqs;
-    const int len = known ? c.length(s) : 0;
-    const int i_min = row0 / a.G, i_max = (min(rows, row0 + 16 * RT) - 1) / a.G;
-    const int pos_min = len - count + i_min, pos_max = len - count + i_max;
+    const int rows = count * a.G, row0 = (tile * WR + wr) * 16;
+    if (tile * WR * 16 >= rows) return;
+    const int len = (unsigned)s < (unsigned)c.n_seqs ? c.length(s) : 0;
+    // the workgroup's pages are those that any of its rows sees
+    const int pos_min = len - count + tile * WR * 16 / a.G;
+    const int pos_max = len - count + (min(rows, (tile + 1) * WR * 16) - 1) / a.G;
     const PageSpan span = page_span(a, pos_min, pos_max);
     const int per = (span.n + a.splits - 1) / a.splits;
     const int p_begin = min(split * per, span.n), p_end = min(p_begin + per, span.n);
+    const bool full = row0 + 16 <= rows;
 
-    // this lane's row of each tile: its queries as matrix operands, its span
-    bf16x8 qf[RT][D / 32][NP];
-    int pos[RT];
-    const int HG = c.H * a.G;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = row0 + rt * 16 + m, i = r / a.G, hg = h * a.G + r % a.G;
-        pos[rt] = r < rows ? len - count + i : -1;
-        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + i * a.qt + (long)hg * D;
+    // this lane's row: its queries as matrix operands, its position
+    bf16x8 qf[D / 32][NP];
+    const int HG = c.H * a.G, r = row0 + m, hg = h * a.G + r % a.G;
+    const int pos = r < rows ? len - count + r / a.G : -1;
+    {
+        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)hg * D;
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
             if (r < rows) {
@@ -168,47 +172,40 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
                     bf16 parts[NP];
                     split_bf16<NP>((float)x[j], parts);
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) qf[rt][st][p][j] = parts[p];
+                    for (int p = 0; p < NP; ++p) qf[st][p][j] = parts[p];
                 }
             } else {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) qf[rt][st][p] = zero_frag<bf16>();
+                for (int p = 0; p < NP; ++p) qf[st][p] = zero_frag<bf16>();
             }
         }
     }
 
-    f32x4 o[RT][D / 16];
-    float mx[RT], sum[RT];
+    f32x4 o[D / 16];
+    float mx = NEG_INF, sum = 0.f;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        mx[rt] = NEG_INF;
-        sum[rt] = 0.f;
-#pragma unroll
-        for (int u = 0; u < D / 16; ++u) o[rt][u] = f32x4{0, 0, 0, 0};
-    }
+    for (int u = 0; u < D / 16; ++u) o[u] = f32x4{0, 0, 0, 0};
 
     auto page_of = [&](int i) {   // table entry of the range's page i, or -1
         const int page = i < p_end ? c.page_at(s, span.at(i)) : -1;
-        return c.page_ok(page) ? page : -1;
+        return __builtin_amdgcn_readfirstlane(c.page_ok(page) ? page : -1);
     };
     KeyRegs<D> kr;
     ValueRegs<D> vr;
-    float ks, vs;
+    float ks = 1.f, vs = 1.f;
     auto base = [&](int page) { return c.head_at(max(page, 0), h); };
-    int page = page_of(p_begin + w), next = page_of(p_begin + w + WAVES);
-    if (p_begin + w < p_end) {
+    int page = page_of(p_begin + wp), next = page_of(p_begin + wp + WP);
+    if (p_begin + wp < p_end) {
         load_keys<D>(kr, c.k + base(page) * PAGE * D, lane);
         ks = scale_of(c.scales[base(page) * 8 + (m >> 2)]);
     }
-    for (int i = p_begin + w; i < p_end; i += WAVES) {
+    for (int i = p_begin + wp; i < p_end; i += WP) {
         load_values<D>(vr, c.v + base(page) * PAGE * D, lane);
         vs = scale_of(c.scales[base(page) * 8 + 4 + g]);
         // scores, transposed: lane's row m, tokens 16 g + 4 t + e
-        f32x4 sc[RT][4];
+        f32x4 sc[4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) sc[rt][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < 4; ++t) sc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -216,61 +213,56 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
                 const uint4 x = kr.w[t][st / 2];
                 const bf16x8 kf = st & 1 ? operand8(x.z, x.w, ks) : operand8(x.x, x.y, ks);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) mma(sc[rt][t], kf, qf[rt][st][p]);
+                for (int p = 0; p < NP; ++p) mma(sc[t], kf, qf[st][p]);
             }
         }
         const int tok = span.at(i) * PAGE;
         const int here = page;
         page = next;
-        if (i + WAVES < p_end) {   // the next page's keys, in flight over what follows
+        if (i + WP < p_end) {   // the next page's keys, in flight over what follows
             load_keys<D>(kr, c.k + base(page) * PAGE * D, lane);
             ks = scale_of(c.scales[base(page) * 8 + (m >> 2)]);
-            next = page_of(i + 2 * WAVES);
+            next = page_of(i + 2 * WP);
         }
-        // a page that every row of the workgroup sees whole needs no mask
-        const bool whole = here >= 0 && tok + PAGE - 1 <= pos_min &&
-                           (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink) && row0 + 16 * RT <= rows;
-        bf16x8 pf[RT][2][NP];
+        // a page that every row sees whole needs no mask
+        const bool whole = full && here >= 0 && tok + PAGE - 1 <= pos_min &&
+                           (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
+        float top = NEG_INF;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float top = NEG_INF;
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[rt][t][e] * a.scale2;
-                    if (!whole) {
-                        const int j = tok + 16 * g + 4 * t + e;
-                        const bool see = here >= 0 && j <= pos[rt] &&
-                                         (a.window == 0 || j > pos[rt] - a.window || j < a.sink);
-                        x = see ? x : NEG_INF;
-                    }
-                    sc[rt][t][e] = x;
-                    top = fmaxf(top, x);
+            for (int e = 0; e < 4; ++e) {
+                float x = sc[t][e] * a.scale2;
+                if (!whole) {
+                    const int j = tok + 16 * g + 4 * t + e;
+                    const bool see = here >= 0 && j <= pos && (a.window == 0 || j > pos - a.window || j < a.sink);
+                    x = see ? x : NEG_INF;
                 }
-            top = fmaxf(mx[rt], group_max(top));
-            if (__any(top > mx[rt])) {
-                const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - top);
-                sum[rt] *= by;
-#pragma unroll
-                for (int u = 0; u < D / 16; ++u) o[rt][u] *= by;
-                mx[rt] = top;
+                sc[t][e] = x;
+                top = fmaxf(top, x);
             }
-            const float ref = top == NEG_INF ? 0.f : top;   // nothing seen yet: every weight 2^-inf = 0
+        top = group_max(top);
+        if (__any(top > mx + SLACK)) {
+            top = fmaxf(top, mx);
+            const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
+            sum *= by;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(sc[rt][t][e] - ref);
-                    sum[rt] += p;
-                    bf16 parts[NP];
-                    split_bf16<NP>(p, parts);
-#pragma unroll
-                    for (int z = 0; z < NP; ++z) pf[rt][t >> 1][z][(t & 1) * 4 + e] = parts[z];
-                }
+            for (int u = 0; u < D / 16; ++u) o[u] *= by;
+            mx = top;
         }
+        const float ref = mx == NEG_INF ? 0.f : mx;   // nothing seen yet: every weight 2^-inf = 0
+        bf16x8 pf[2][NP];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = __builtin_amdgcn_exp2f(sc[t][e] - ref);
+                sum += p;
+                bf16 parts[NP];
+                split_bf16<NP>(p, parts);
+#pragma unroll
+                for (int z = 0; z < NP; ++z) pf[t >> 1][z][(t & 1) * 4 + e] = parts[z];
+            }
         // behind the sequence's end the page holds anything, NaN codes too
         const int live = len - tok - 16 * g;   // tokens of this lane's block
         const bool cut = tok + PAGE > len;
@@ -288,146 +280,370 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
             }
             const bf16x8 v0 = operand8(x.x, x.y, vs), v1 = operand8(x.z, x.w, vs);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int z = 0; z < NP; ++z) {
-                    mma(o[rt][u], v0, pf[rt][0][z]);
-                    mma(o[rt][u], v1, pf[rt][1][z]);
-                }
+            for (int z = 0; z < NP; ++z) {
+                mma(o[u], v0, pf[0][z]);
+                mma(o[u], v1, pf[1][z]);
+            }
         }
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
+    sum = group_sum(sum);
 
-    // join the waves: common maximum, then sums in a tree
-    __shared__ float ml[WAVES][RT * 16][2];
-    __shared__ float acc[WAVES / 2][RT * 16][D + 4];
-    if (g == 0) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            ml[w][rt * 16 + m][0] = mx[rt];
-            ml[w][rt * 16 + m][1] = sum[rt];
+    // join the waves of a row tile: common maximum, then sums in a tree
+    __shared__ float ml[WAVES][16][2];
+    __shared__ float acc[WP > 1 ? WAVES / 2 : 1][16][D + 4];
+    if constexpr (WP > 1) {
+        if (g == 0) {
+            ml[w][m][0] = mx;
+            ml[w][m][1] = sum;
         }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
         float top = NEG_INF, total = 0.f;
 #pragma unroll
-        for (int z = 0; z < WAVES; ++z) top = fmaxf(top, ml[z][rt * 16 + m][0]);
+        for (int z = 0; z < WP; ++z) top = fmaxf(top, ml[z * WR + wr][m][0]);
         const float ref = top == NEG_INF ? 0.f : top;
 #pragma unroll
-        for (int z = 0; z < WAVES; ++z)
-            total += ml[z][rt * 16 + m][1] * __builtin_amdgcn_exp2f(ml[z][rt * 16 + m][0] - ref);
-        const float by = __builtin_amdgcn_exp2f(mx[rt] - ref);
+        for (int z = 0; z < WP; ++z) total += ml[z * WR + wr][m][1] * __builtin_amdgcn_exp2f(ml[z * WR + wr][m][0] - ref);
+        const float by = __builtin_amdgcn_exp2f(mx - ref);
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) o[rt][u] *= by;
-        mx[rt] = top;
-        sum[rt] = total;
-    }
+        for (int u = 0; u < D / 16; ++u) o[u] *= by;
+        mx = top;
+        sum = total;
 #pragma unroll
-    for (int half = WAVES / 2; half >= 1; half /= 2) {
-        if (w >= half && w < 2 * half) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+        for (int half = WP / 2; half >= 1; half /= 2) {
+            if (wp >= half && wp < 2 * half) {
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u)
-                    *reinterpret_cast<f32x4*>(&acc[w - half][rt * 16 + m][16 * u + 4 * g]) = o[rt][u];
-        }
-        __syncthreads();
-        if (w < half) {
+                    *reinterpret_cast<f32x4*>(&acc[w - half * WR][m][16 * u + 4 * g]) = o[u];
+            }
+            __syncthreads();
+            if (wp < half) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int u = 0; u < D / 16; ++u)
-                    o[rt][u] += *reinterpret_cast<const f32x4*>(&acc[w][rt * 16 + m][16 * u + 4 * g]);
+                for (int u = 0; u < D / 16; ++u) o[u] += *reinterpret_cast<const f32x4*>(&acc[w][m][16 * u + 4 * g]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
-    if (w != 0) return;
-    typedef T Four __attribute__((ext_vector_type(4)));
+    if (wp != 0 || r >= rows) return;
+    if (a.splits == 1) {
+        typedef T Four __attribute__((ext_vector_type(4)));
+        const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + hg) * D;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = row0 + rt * 16 + m;
-        if (r >= rows) continue;
-        if (a.splits == 1) {
-            const float by = sum[rt] > 0.f ? 1.f / sum[rt] : (sum[rt] == 0.f ? 0.f : sum[rt]);
-            T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + h * a.G + r % a.G) * D;
+        for (int u = 0; u < D / 16; ++u) {
+            Four y;
 #pragma unroll
-            for (int u = 0; u < D / 16; ++u) {
-                Four y;
+            for (int e = 0; e < 4; ++e) y[e] = (T)(o[u][e] * by);
+            *reinterpret_cast<Four*>(out + 16 * u + 4 * g) = y;
+        }
+    } else {
+        const size_t at = (((size_t)b * c.H + h) * a.splits + split) * ((size_t)a.T * a.G) + r;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = (T)(o[rt][u][e] * by);
-                *reinterpret_cast<Four*>(out + 16 * u + 4 * g) = y;
-            }
-        } else {
-            const size_t at = (((size_t)b * c.H + h) * a.splits + split) * ((size_t)a.T * a.G) + r;
-#pragma unroll
-            for (int u = 0; u < D / 16; ++u) *reinterpret_cast<f32x4*>(a.part + at * D + 16 * u + 4 * g) = o[rt][u];
-            if (g == 0) {
-                a.ml[2 * at] = mx[rt];
-                a.ml[2 * at + 1] = sum[rt];
-            }
+        for (int u = 0; u < D / 16; ++u) *reinterpret_cast<f32x4*>(a.part + at * D + 16 * u + 4 * g) = o[u];
+        if (g == 0) {
+            a.ml[2 * at] = mx;
+            a.ml[2 * at + 1] = sum;
         }
     }
 }
 
-// Joins the ranges of a row: a wave per row.
+// Many rows of one kv head against its sequence (a segment or a prompt):
+// 128 rows per workgroup, 32 per wave, on the 32x32x16 matrix instruction.
+// Every wave needs every page, so the page's codes are converted to bf16 once
+// per workgroup, into LDS (two buffers: the next page is loaded over the
+// present one's products and stored into the other buffer, one barrier per
+// page); rows of D + 8 and 64 + 8 elements keep the 16-byte operand reads off
+// each other's banks.  The transposed scores' layout (lane group h of 2 holds
+// rows 8 a + 4 h + b) is again made the second product's operand by the order
+// in which rows of K are fed: row 8 a + 4 h + b of a 32-token tile is token
+// 16 (a / 2) + 8 h + 4 (a % 2) + b, so a lane ends up with runs of 8 tokens.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int TILE_ROWS = 128;
+
+template <class T, int D>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attend_tiles_kernel(AttendArgs a) {
+    constexpr int NP = sizeof(T) == 4 ? 3 : 1;
+    constexpr int KS = D + 8, VS = PAGE + 8;            // LDS row distances
+    constexpr int PIECES = 4 * D, NK = (PIECES + 255) / 256;   // 16-byte pieces of a page's keys (and of its values)
+    __shared__ __align__(16) bf16 kb[2][PAGE * KS];
+    __shared__ __align__(16) bf16 vb[2][D * VS];
+    const CacheView& c = a.c;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 31, g = lane >> 5;
+    // heads innermost: with a multiple of 8 of them, the workgroups that read
+    // the same pages stand on one XCD and share its L2
+    const int h = blockIdx.x % c.H, x = blockIdx.x / c.H, b = blockIdx.z;
+    const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
+    const int rows = count * a.G;
+    // the last rows first: they see the most
+    const int tiles = (rows + TILE_ROWS - 1) / TILE_ROWS, split = x % a.splits;
+    const int tile = tiles - 1 - x / a.splits;
+    if (tile < 0) return;
+    const int row0 = tile * TILE_ROWS, s = a.seqs ? a.seqs[b] : b;
+    const int len = (unsigned)s < (unsigned)c.n_seqs ? c.length(s) : 0;
+    const int first = len - count;                       // position of query 0
+    const int pos_max = first + (min(rows, row0 + TILE_ROWS) - 1) / a.G;
+    const PageSpan span = page_span(a, first + row0 / a.G, pos_max);
+    const int per = (span.n + a.splits - 1) / a.splits;
+    const int p_begin = min(split * per, span.n), p_end = min(p_begin + per, span.n);
+
+    // this wave's rows, and what all of them and any of them see
+    const int wr0 = row0 + 32 * w, r = wr0 + m, HG = c.H * a.G;
+    const bool live_row = r < rows;
+    const int pos = live_row ? first + r / a.G : -1;
+    const int w_min = first + wr0 / a.G, w_max = wr0 < rows ? first + (min(rows, wr0 + 32) - 1) / a.G : -1;
+    const bool full = wr0 + 32 <= rows;
+
+    bf16x8 qf[D / 16][NP];
+    {
+        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)(h * a.G + r % a.G) * D;
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {
+            if (live_row) {
+                const auto x = ld8(q + 16 * st + 8 * g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    bf16 parts[NP];
+                    split_bf16<NP>((float)x[j], parts);
+#pragma unroll
+                    for (int z = 0; z < NP; ++z) qf[st][z][j] = parts[z];
+                }
+            } else {
+#pragma unroll
+                for (int z = 0; z < NP; ++z) qf[st][z] = zero_frag<bf16>();
+            }
+        }
+    }
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[u][e] = 0.f;
+    float mx = NEG_INF, sum = 0.f;
+
+    uint4 kr[NK], vr[NK];
+    uint2 scales = {0, 0};
+    auto page_of = [&](int i) {
+        const int page = i < p_end ? c.page_at(s, span.at(i)) : -1;
+        return __builtin_amdgcn_readfirstlane(c.page_ok(page) ? page : -1);
+    };
+    auto load = [&](int page) {
+        if (page < 0) return;
+        const size_t at = c.head_at(page, h);
+        const uint4* k = reinterpret_cast<const uint4*>(c.k + at * PAGE * D);
+        const uint4* v = reinterpret_cast<const uint4*>(c.v + at * PAGE * D);
+        scales = *reinterpret_cast<const uint2*>(c.scales + at * 8);
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            const int p = tid + 256 * n;
+            if (PIECES % 256 == 0 || p < PIECES) {
+                kr[n] = k[p];
+                vr[n] = v[p];
+            }
+        }
+    };
+    auto stage = [&](int buf, int tok) {
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+            const int p = tid + 256 * n;
+            if (PIECES % 256 != 0 && p >= PIECES) continue;
+            const int t = p / (D / 16), col = p % (D / 16) * 16;
+            const float ks = scale_of((unsigned char)(scales.x >> (8 * (t >> 4))));
+            bf16* kd = &kb[buf][t * KS + col];
+            *reinterpret_cast<bf16x8*>(kd) = operand8(kr[n].x, kr[n].y, ks);
+            *reinterpret_cast<bf16x8*>(kd + 8) = operand8(kr[n].z, kr[n].w, ks);
+            const int dim = p >> 2, quarter = p & 3;
+            const int live = len - tok - 16 * quarter;   // tokens of the piece within the sequence
+            float vs = scale_of((unsigned char)(scales.y >> (8 * quarter)));
+            uint4 x = vr[n];
+            if (live < 16) {   // behind the end the page holds anything, NaN codes too
+                unsigned* xw = reinterpret_cast<unsigned*>(&x);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int k4 = min(max(live - 4 * z, 0), 4);
+                    xw[z] &= k4 == 4 ? ~0u : (1u << (8 * k4)) - 1;
+                }
+                if (live <= 0) vs = 1.f;
+            }
+            bf16* vd = &vb[buf][dim * VS + quarter * 16];
+            *reinterpret_cast<bf16x8*>(vd) = operand8(x.x, x.y, vs);
+            *reinterpret_cast<bf16x8*>(vd + 8) = operand8(x.z, x.w, vs);
+        }
+    };
+    const int tau = 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);   // token of row m of a tile
+
+    int page = page_of(p_begin);
+    load(page);
+    if (page >= 0) stage(0, span.at(p_begin) * PAGE);
+    __syncthreads();
+    for (int i = p_begin; i < p_end; ++i) {
+        const int buf = (i - p_begin) & 1, tok = span.at(i) * PAGE;
+        const int next = page_of(i + 1);
+        load(next);
+        // nothing of the page in sight of the wave's rows: its products are skipped
+        const bool seen = page >= 0 && tok <= w_max &&
+                          (a.window == 0 || tok + PAGE - 1 > w_min - a.window || tok < a.sink);
+        if (seen) {
+            f32x16 sc[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sc[t][e] = 0.f;
+#pragma unroll
+            for (int st = 0; st < D / 16; ++st)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&kb[buf][(t * 32 + tau) * KS + 16 * st + 8 * g]);
+#pragma unroll
+                    for (int z = 0; z < NP; ++z)
+                        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st][z], sc[t], 0, 0, 0);
+                }
+            const bool whole = full && tok + PAGE - 1 <= w_min &&
+                               (a.window == 0 || tok > w_max - a.window || tok + PAGE <= a.sink);
+            float top = NEG_INF;
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = tok + 32 * t + 16 * (e >> 3) + 8 * g + (e & 7);
+                        const bool see = j <= pos && (a.window == 0 || j > pos - a.window || j < a.sink);
+                        sc[t][e] = see ? sc[t][e] * a.scale2 : NEG_INF;
+                        top = fmaxf(top, sc[t][e]);
+                    }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        sc[t][e] *= a.scale2;
+                        top = fmaxf(top, sc[t][e]);
+                    }
+            }
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            if (__any(top > mx + SLACK)) {
+                top = fmaxf(top, mx);
+                const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
+                sum *= by;
+#pragma unroll
+                for (int u = 0; u < D / 32; ++u) o[u] *= by;
+                mx = top;
+            }
+            const float ref = mx == NEG_INF ? 0.f : mx;
+            bf16x8 pf[4][NP];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(sc[t][e] - ref);
+                    sum += p;
+                    bf16 parts[NP];
+                    split_bf16<NP>(p, parts);
+#pragma unroll
+                    for (int z = 0; z < NP; ++z) pf[2 * t + (e >> 3)][z][e & 7] = parts[z];
+                }
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const bf16x8 vf = *reinterpret_cast<const bf16x8*>(&vb[buf][(32 * u + m) * VS + 16 * k4 + 8 * g]);
+#pragma unroll
+                    for (int z = 0; z < NP; ++z)
+                        o[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[k4][z], o[u], 0, 0, 0);
+                }
+        }
+        if (next >= 0) stage(buf ^ 1, span.at(i + 1) * PAGE);
+        __syncthreads();
+        page = next;
+    }
+    if (!live_row) return;
+    sum += __shfl_xor(sum, 32, 64);
+    if (a.splits == 1) {
+        const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        typedef T Four __attribute__((ext_vector_type(4)));
+        T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + h * a.G + r % a.G) * D + 4 * g;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                Four y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = (T)(o[u][4 * z + e] * by);
+                *reinterpret_cast<Four*>(out + 32 * u + 8 * z) = y;
+            }
+    } else {
+        const size_t at = (((size_t)b * c.H + h) * a.splits + split) * ((size_t)a.T * a.G) + r;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                *reinterpret_cast<f32x4*>(a.part + at * D + 32 * u + 8 * z + 4 * g) =
+                    f32x4{o[u][4 * z], o[u][4 * z + 1], o[u][4 * z + 2], o[u][4 * z + 3]};
+        if (g == 0) {
+            a.ml[2 * at] = mx;
+            a.ml[2 * at + 1] = sum;
+        }
+    }
+}
+
+// Joins the ranges of a row: a workgroup per row, D / 4 lanes per range, so
+// that several ranges are read at a time.
 template <class T, int D>
 __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
+    constexpr int LP = D / 4, GW = 64 / LP, GROUPS = 4 * GW;   // lanes of a range, ranges at a time
     const CacheView& c = a.c;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = blockIdx.y, b = blockIdx.z;
     const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
-    const int r = blockIdx.x * 4 + w;
+    const int r = blockIdx.x;
     if (r >= count * a.G) return;
     const size_t rows = (size_t)a.T * a.G, at0 = ((size_t)b * c.H + h) * a.splits * rows + r;
+    __shared__ float acc[GROUPS][D + 4];
+    __shared__ float sums[GROUPS];
     float top = NEG_INF;
     for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.ml[2 * (at0 + s * rows)]);
 #pragma unroll
     for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
     const float ref = top == NEG_INF ? 0.f : top;
-    constexpr int IT = (D + 127) / 128;
-    float o[IT][2], total = 0.f;
-#pragma unroll
-    for (int it = 0; it < IT; ++it) o[it][0] = o[it][1] = 0.f;
+    const int grp = w * GW + lane / LP, col = lane % LP * 4;
+    if (lane < GW * LP) {
+        f32x4 o = {0, 0, 0, 0};
+        float total = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const size_t at = at0 + s * rows;
-        const float by = __builtin_amdgcn_exp2f(a.ml[2 * at] - ref);
-        total += a.ml[2 * at + 1] * by;
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int dim = it * 128 + 2 * lane;
-            if (dim < D) {
-                const float2 x = *reinterpret_cast<const float2*>(a.part + at * D + dim);
-                o[it][0] += x.x * by;
-                o[it][1] += x.y * by;
-            }
+        for (int s = grp; s < a.splits; s += GROUPS) {
+            const size_t at = at0 + s * rows;
+            const float by = __builtin_amdgcn_exp2f(a.ml[2 * at] - ref);
+            total += a.ml[2 * at + 1] * by;
+            o += *reinterpret_cast<const f32x4*>(a.part + at * D + col) * by;
         }
+        *reinterpret_cast<f32x4*>(&acc[grp][col]) = o;
+        if (col == 0) sums[grp] = total;
+    }
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    float y = 0.f, total = 0.f;
+#pragma unroll
+    for (int z = 0; z < GROUPS; ++z) {
+        y += acc[z][threadIdx.x];
+        total += sums[z];
     }
     const float by = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
-    typedef T Two __attribute__((ext_vector_type(2)));
-    T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * c.H * a.G + h * a.G + r % a.G) * D;
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-        const int dim = it * 128 + 2 * lane;
-        if (dim < D) *reinterpret_cast<Two*>(out + dim) = Two{(T)(o[it][0] * by), (T)(o[it][1] * by)};
-    }
+    reinterpret_cast<T*>(a.out)[(((long)b * a.T + r / a.G) * c.H * a.G + h * a.G + r % a.G) * D + threadIdx.x] = (T)(y * by);
 }
 
-// How a call is launched: tiles of 16 or 32 rows, and into how many ranges
-// the sequences are divided.
+// How a call is launched: which kernel, how many tiles of rows, and into how
+// many ranges the sequences are divided.
 struct AttendPlan {
-    int rt, tiles, splits;
+    bool wide;   // attend_tiles_kernel (128 rows a tile), else attend_rows_kernel (16 wr)
+    int wr, tiles, splits;
 };
 static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len) {
     AttendPlan p;
     const long rows = (long)n_tokens * (heads / c->H);
-    p.rt = rows > 16 ? 2 : 1;
-    p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    p.wide = rows > 64;
+    p.wr = rows > 32 ? 4 : rows > 16 ? 2 : 1;
+    const int tile = p.wide ? TILE_ROWS : 16 * p.wr;
+    p.tiles = (int)((rows + tile - 1) / tile);
     const long pages = (max_len + PAGE - 1) / PAGE, groups = (long)batch * c->H * p.tiles;
-    long s = 1024 / groups;
-    const long most = (pages + 7) / 8;   // two pages a wave at least
+    long s = p.wide ? 512 / groups : 1024 / groups;
+    const long most = p.wide ? (pages + 3) / 4 : (pages + 7) / 8;   // four pages a range, or two a wave, at least
     if (s > most) s = most;
     if (s > 256) s = 256;
     p.splits = s < 1 ? 1 : (int)s;
@@ -447,16 +663,22 @@ template <class T>
 static hipError_t launch_attend(const tm_cache* c, const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
     hipError_t e = timed_attn(st, [&] {
         return for_head_dim(c->d, [&](auto D) {
+            if (p.wide) {
+                const dim3 grid((unsigned)(p.tiles * p.splits * c->H), 1, (unsigned)a.B);
+                launch_k(attend_tiles_kernel<T, D()>, grid, dim3(256), 0, st, a);
+                return hipGetLastError();
+            }
             const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c->H, (unsigned)a.B);
-            if (p.rt == 1) launch_k(attend_rows_kernel<T, D(), 1>, grid, dim3(256), 0, st, a);
-            else launch_k(attend_rows_kernel<T, D(), 2>, grid, dim3(256), 0, st, a);
+            if (p.wr == 1) launch_k(attend_rows_kernel<T, D(), 1>, grid, dim3(256), 0, st, a);
+            else if (p.wr == 2) launch_k(attend_rows_kernel<T, D(), 2>, grid, dim3(256), 0, st, a);
+            else launch_k(attend_rows_kernel<T, D(), 4>, grid, dim3(256), 0, st, a);
             return hipGetLastError();
         });
     });
     if (e != hipSuccess || p.splits == 1) return e;
     return timed_attn(st, [&] {
         return for_head_dim(c->d, [&](auto D) {
-            const dim3 grid((unsigned)(((long)a.T * a.G + 3) / 4), (unsigned)c->H, (unsigned)a.B);
+            const dim3 grid((unsigned)(a.T * a.G), (unsigned)c->H, (unsigned)a.B);
             launch_k(combine_kernel<T, D()>, grid, dim3(256), 0, st, a);
             return hipGetLastError();
         });
@@ -481,6 +703,7 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
     const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most);
+    if ((long)p.tiles * p.splits * c->H > 0x7fffffffL) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
     const int G = heads / c->H;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * G;
