@@ -37,20 +37,19 @@ struct AttendArgs {
     int B, T, G;         // entries, query tokens, query heads per kv head
     float scale2;        // score_scale log2(e)
     int window, sink;
-    int splits;          // key ranges that the sequence is divided into
+    int splits;          // the most key ranges that a tile's pages are divided into
+    int least;           // pages of a range, at least
+    int tile_rows;       // rows of a workgroup
     float* part;         // [B][H][splits][rows][D]: accumulators
     float* ml;           // [B][H][splits][rows][2]: maximum and sum
 };
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 constexpr float NEG_INF = -__builtin_inff();
 // A row's running maximum moves when it grows by more than this: weights up
 // to 2^8 are as exact, and the accumulators are rarely rescaled.
 constexpr float SLACK = 8.f;
-
-// What the row r = i G + g of entry b sees: tokens lo .. pos and 0 .. sink-1.
-struct RowSpan {
-    int pos, lo;
-};
 
 // The pages a range of rows sees: `first` pages of the sequence's beginning
 // (the sink), then lo_page ..; n in all.
@@ -65,6 +64,28 @@ __device__ __forceinline__ PageSpan page_span(const AttendArgs& a, int pos_min, 
     const int lo_page = lo / PAGE;
     const int first = a.window > 0 ? min((a.sink + PAGE - 1) / PAGE, lo_page) : 0;
     return PageSpan{first, lo_page, first + pos_max / PAGE + 1 - lo_page};
+}
+
+// One workgroup's part of a call: a tile of rows of entry b.  Wave-uniform.
+struct Tile {
+    int len, rows;          // tokens of the sequence; rows of the entry
+    int first;              // position of query 0
+    int pos_min, pos_max;   // positions of the tile's first and last row
+    PageSpan span;          // the pages its rows see
+    int ranges, per;        // how many ranges they are divided into, pages of each
+};
+__device__ __forceinline__ Tile tile_of(const AttendArgs& a, int b, int s, int tile) {
+    Tile t;
+    const int count = uniform(a.counts ? min(max(a.counts[b], 0), a.T) : a.T);
+    t.len = uniform((unsigned)s < (unsigned)a.c.n_seqs ? a.c.length(s) : 0);
+    t.rows = count * a.G;
+    t.first = t.len - count;
+    t.pos_min = t.first + tile * a.tile_rows / a.G;
+    t.pos_max = t.first + (min(t.rows, (tile + 1) * a.tile_rows) - 1) / a.G;
+    t.span = page_span(a, t.pos_min, t.pos_max);
+    t.ranges = min(a.splits, max(1, (t.span.n + a.least - 1) / a.least));
+    t.per = (t.span.n + t.ranges - 1) / t.ranges;
+    return t;
 }
 
 // Three bf16 values whose sum is x to 24 bits (NP parts of it).
@@ -131,40 +152,41 @@ __device__ __forceinline__ float group_sum(float x) {
 
 // Few rows of one kv head against its sequence (single tokens, drafts): WR
 // tiles of 16 rows per workgroup (row r = i G + g: query token i, head g of
-// the group).  Wave w takes row tile w % WR and every (4 / WR)-th page of the
-// workgroup's range; the waves of a tile are joined in LDS at the end.  With
+// the group).  Wave w takes row tile w % WR and every (WAVES / WR)-th page of
+// the workgroup's range; the waves of a tile are joined in LDS at the end.  With
 // one range the workgroup writes the output, otherwise its accumulators,
 // maxima and sums for combine_kernel.  Bound by reading the pages: a wave's
 // next keys and present values are in flight while it computes.
-template <class T, int D, int WR>
-__global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
+template <class T, int D, int WR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
     constexpr int NP = sizeof(T) == 4 ? 3 : 1;
-    constexpr int WAVES = 4, WP = WAVES / WR;   // waves that share a row tile
+    constexpr int WP = WAVES / WR;   // waves that share a row tile
     const CacheView& c = a.c;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
     const int wr = w % WR, wp = w / WR;
     const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, h = blockIdx.y, b = blockIdx.z;
-    const int s = a.seqs ? a.seqs[b] : b;
-    const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
-    const int rows = count * a.G, row0 = (tile * WR + wr) * 16;
-    if (tile * WR * 16 >= rows) return;
-    const int len = (unsigned)s < (unsigned)c.n_seqs ? c.length(s) : 0;
-    // the workgroup's pages are those that any of its rows sees
-    const int pos_min = len - count + tile * WR * 16 / a.G;
-    const int pos_max = len - count + (min(rows, (tile + 1) * WR * 16) - 1) / a.G;
-    const PageSpan span = page_span(a, pos_min, pos_max);
-    const int per = (span.n + a.splits - 1) / a.splits;
-    const int p_begin = min(split * per, span.n), p_end = min(p_begin + per, span.n);
+    const int s = uniform(a.seqs ? a.seqs[b] : b), row0 = (tile * WR + wr) * 16;
+    const Tile tl = tile_of(a, b, s, tile);
+    const int rows = tl.rows, len = tl.len, pos_min = tl.pos_min, pos_max = tl.pos_max;
+    if (tile * WR * 16 >= rows || split >= tl.ranges) return;
+    const PageSpan span = tl.span;
+    const int p_begin = min(split * tl.per, span.n), p_end = min(p_begin + tl.per, span.n);
     const bool full = row0 + 16 <= rows;
 
     // this lane's row: its queries as matrix operands, its position
-    bf16x8 qf[D / 32][NP];
+    // (three parts of them would take too many registers: in LDS, per row tile)
+    constexpr bool Q_LDS = NP > 1;
+    __shared__ bf16x8 ql[Q_LDS ? WR : 1][Q_LDS ? D / 32 * NP : 1][64];
+    bf16x8 qf[Q_LDS ? 1 : D / 32];
     const int HG = c.H * a.G, r = row0 + m, hg = h * a.G + r % a.G;
-    const int pos = r < rows ? len - count + r / a.G : -1;
+    const int pos = r < rows ? tl.first + r / a.G : -1;
     {
         const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)hg * D;
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
+            bf16x8 f[NP];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) f[p] = zero_frag<bf16>();
             if (r < rows) {
                 const auto x = ld8(q + key_dim<D>(st, g));
 #pragma unroll
@@ -172,13 +194,19 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
                     bf16 parts[NP];
                     split_bf16<NP>((float)x[j], parts);
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) qf[st][p][j] = parts[p];
+                    for (int p = 0; p < NP; ++p) f[p][j] = parts[p];
+                }
+            }
+            if constexpr (Q_LDS) {
+                if (wp == 0) {
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) ql[wr][st * NP + p][lane] = f[p];
                 }
             } else {
-#pragma unroll
-                for (int p = 0; p < NP; ++p) qf[st][p] = zero_frag<bf16>();
+                qf[st] = f[0];
             }
         }
+        if constexpr (Q_LDS) __syncthreads();
     }
 
     f32x4 o[D / 16];
@@ -186,44 +214,59 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
 #pragma unroll
     for (int u = 0; u < D / 16; ++u) o[u] = f32x4{0, 0, 0, 0};
 
-    auto page_of = [&](int i) {   // table entry of the range's page i, or -1
-        const int page = i < p_end ? c.page_at(s, span.at(i)) : -1;
-        return __builtin_amdgcn_readfirstlane(c.page_ok(page) ? page : -1);
+    // Table entries of this wave's next 64 pages, one a lane, read ahead of the
+    // codes: a load behind them would be waited for together with them.
+    const int i0 = p_begin + wp;
+    int ids = -1;
+    auto page_of = [&](int n) {   // the wave's n-th page, or -1; called in order
+        if ((n & 63) == 0) {
+            const int i = i0 + (n + lane) * WP;
+            ids = i < p_end ? c.page_at(s, span.at(i)) : -1;
+        }
+        const int page = __builtin_amdgcn_readlane(ids, n & 63);
+        return c.page_ok(page) ? page : -1;
     };
-    KeyRegs<D> kr;
-    ValueRegs<D> vr;
-    float ks = 1.f, vs = 1.f;
+    struct Codes {
+        KeyRegs<D> k;
+        ValueRegs<D> v;
+        unsigned char ks, vs;   // the scales of the lane's rows, as stored: made numbers where they are used, not
+                                // where they are loaded, which would wait for the codes loaded before them
+    };
     auto base = [&](int page) { return c.head_at(max(page, 0), h); };
-    int page = page_of(p_begin + wp), next = page_of(p_begin + wp + WP);
-    if (p_begin + wp < p_end) {
-        load_keys<D>(kr, c.k + base(page) * PAGE * D, lane);
-        ks = scale_of(c.scales[base(page) * 8 + (m >> 2)]);
-    }
-    for (int i = p_begin + wp; i < p_end; i += WP) {
-        load_values<D>(vr, c.v + base(page) * PAGE * D, lane);
-        vs = scale_of(c.scales[base(page) * 8 + 4 + g]);
+    auto load_k = [&](Codes& x, int page) {
+        load_keys<D>(x.k, c.k + base(page) * PAGE * D, lane);
+        x.ks = c.scales[base(page) * 8 + (m >> 2)];
+    };
+    auto load_v = [&](Codes& x, int page) {
+        load_values<D>(x.v, c.v + base(page) * PAGE * D, lane);
+        x.vs = c.scales[base(page) * 8 + 4 + g];
+    };
+    // one page's step; `then` starts loads as soon as the keys are used up
+    auto step = [&](Codes& x, int i, int here, auto&& then) {
         // scores, transposed: lane's row m, tokens 16 g + 4 t + e
         f32x4 sc[4];
+        const float ks = scale_of(x.ks);
 #pragma unroll
         for (int t = 0; t < 4; ++t) sc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int st = 0; st < D / 32; ++st) {
+            bf16x8 kf[4];
 #pragma unroll
-            for (int st = 0; st < D / 32; ++st) {
-                const uint4 x = kr.w[t][st / 2];
-                const bf16x8 kf = st & 1 ? operand8(x.z, x.w, ks) : operand8(x.x, x.y, ks);
+            for (int t = 0; t < 4; ++t) {
+                const uint4 y = x.k.w[t][st / 2];
+                kf[t] = st & 1 ? operand8(y.z, y.w, ks) : operand8(y.x, y.y, ks);
+            }
 #pragma unroll
-                for (int p = 0; p < NP; ++p) mma(sc[t], kf, qf[st][p]);
+            for (int p = 0; p < NP; ++p) {
+                bf16x8 f;
+                if constexpr (Q_LDS) f = ql[wr][st * NP + p][lane];
+                else f = qf[st];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) mma(sc[t], kf[t], f);
             }
         }
+        then();
         const int tok = span.at(i) * PAGE;
-        const int here = page;
-        page = next;
-        if (i + WP < p_end) {   // the next page's keys, in flight over what follows
-            load_keys<D>(kr, c.k + base(page) * PAGE * D, lane);
-            ks = scale_of(c.scales[base(page) * 8 + (m >> 2)]);
-            next = page_of(i + 2 * WP);
-        }
         // a page that every row sees whole needs no mask
         const bool whole = full && here >= 0 && tok + PAGE - 1 <= pos_min &&
                            (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
@@ -232,14 +275,14 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = sc[t][e] * a.scale2;
+                float y = sc[t][e] * a.scale2;
                 if (!whole) {
                     const int j = tok + 16 * g + 4 * t + e;
-                    const bool see = here >= 0 && j <= pos && (a.window == 0 || j > pos - a.window || j < a.sink);
-                    x = see ? x : NEG_INF;
+                    const bool see = (here >= 0) & (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
+                    y = see ? y : NEG_INF;
                 }
-                sc[t][e] = x;
-                top = fmaxf(top, x);
+                sc[t][e] = y;
+                top = fmaxf(top, y);
             }
         top = group_max(top);
         if (__any(top > mx + SLACK)) {
@@ -263,27 +306,60 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
 #pragma unroll
                 for (int z = 0; z < NP; ++z) pf[t >> 1][z][(t & 1) * 4 + e] = parts[z];
             }
+        float vs = scale_of(x.vs);
         // behind the sequence's end the page holds anything, NaN codes too
-        const int live = len - tok - 16 * g;   // tokens of this lane's block
-        const bool cut = tok + PAGE > len;
-        if (cut && live <= 0) vs = 1.f;
+        if (tok + PAGE > len) {
+            const int live = len - tok - 16 * g;   // tokens of this lane's block
+            if (live <= 0) vs = 1.f;
+            unsigned keep[4];
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            uint4 x = vr.w[u];
-            if (cut) {
-                unsigned* xw = reinterpret_cast<unsigned*>(&x);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int n = min(max(live - 4 * z, 0), 4);
-                    xw[z] &= n == 4 ? ~0u : (1u << (8 * n)) - 1;
-                }
+            for (int z = 0; z < 4; ++z) {
+                const int n = min(max(live - 4 * z, 0), 4);
+                keep[z] = n == 4 ? ~0u : (1u << (8 * n)) - 1;
             }
-            const bf16x8 v0 = operand8(x.x, x.y, vs), v1 = operand8(x.z, x.w, vs);
 #pragma unroll
-            for (int z = 0; z < NP; ++z) {
-                mma(o[u], v0, pf[0][z]);
-                mma(o[u], v1, pf[1][z]);
+            for (int u = 0; u < D / 16; ++u) {
+                x.v.w[u].x &= keep[0];
+                x.v.w[u].y &= keep[1];
+                x.v.w[u].z &= keep[2];
+                x.v.w[u].w &= keep[3];
             }
+        }
+        // two dim tiles at a time: products that do not wait for each other
+#pragma unroll
+        for (int u = 0; u < D / 16; u += 2) {
+            bf16x8 vf[2][2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                vf[y][0] = operand8(x.v.w[u + y].x, x.v.w[u + y].y, vs);
+                vf[y][1] = operand8(x.v.w[u + y].z, x.v.w[u + y].w, vs);
+            }
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                for (int z = 0; z < NP; ++z)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) mma(o[u + y], vf[y][k2], pf[k2][z]);
+        }
+    };
+    const int pages = i0 < p_end ? (p_end - i0 + WP - 1) / WP : 0;
+    // A page's values are loaded over its first product, the next page's keys
+    // over the rest.  The loads of what comes next are issued on every path
+    // (the last page's keys again behind the end): behind a branch, every wait
+    // would have to be for all that may be in flight.  (Loading both a whole
+    // page ahead, with twice the registers, measured no faster: 2-3% slower
+    // for 48 sequences of 2000 to 30000 tokens.)
+    if (pages > 0) {
+        Codes x;
+        int page = page_of(0);
+        load_k(x, page);
+        for (int n = 0; n < pages; ++n) {
+            const int here = page;
+            load_v(x, here);
+            step(x, i0 + n * WP, here, [&] {
+                if (n + 1 < pages) page = page_of(n + 1);
+                load_k(x, page);
+            });
         }
     }
     sum = group_sum(sum);
@@ -324,7 +400,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
         }
     }
     if (wp != 0 || r >= rows) return;
-    if (a.splits == 1) {
+    if (tl.ranges == 1) {
         typedef T Four __attribute__((ext_vector_type(4)));
         const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + hg) * D;
@@ -371,19 +447,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
     // heads innermost: with a multiple of 8 of them, the workgroups that read
     // the same pages stand on one XCD and share its L2
     const int h = blockIdx.x % c.H, x = blockIdx.x / c.H, b = blockIdx.z;
-    const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
-    const int rows = count * a.G;
+    const int s = uniform(a.seqs ? a.seqs[b] : b);
     // the last rows first: they see the most
-    const int tiles = (rows + TILE_ROWS - 1) / TILE_ROWS, split = x % a.splits;
-    const int tile = tiles - 1 - x / a.splits;
-    if (tile < 0) return;
-    const int row0 = tile * TILE_ROWS, s = a.seqs ? a.seqs[b] : b;
-    const int len = (unsigned)s < (unsigned)c.n_seqs ? c.length(s) : 0;
-    const int first = len - count;                       // position of query 0
-    const int pos_max = first + (min(rows, row0 + TILE_ROWS) - 1) / a.G;
-    const PageSpan span = page_span(a, first + row0 / a.G, pos_max);
-    const int per = (span.n + a.splits - 1) / a.splits;
-    const int p_begin = min(split * per, span.n), p_end = min(p_begin + per, span.n);
+    const int split = x % a.splits, tile = (a.T * a.G + TILE_ROWS - 1) / TILE_ROWS - 1 - x / a.splits;
+    const Tile tl = tile_of(a, b, s, tile);
+    const int rows = tl.rows, len = tl.len, first = tl.first, row0 = tile * TILE_ROWS;
+    if (row0 >= rows || split >= tl.ranges) return;
+    const PageSpan span = tl.span;
+    const int p_begin = min(split * tl.per, span.n), p_end = min(p_begin + tl.per, span.n);
 
     // this wave's rows, and what all of them and any of them see
     const int wr0 = row0 + 32 * w, r = wr0 + m, HG = c.H * a.G;
@@ -421,9 +492,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
 
     uint4 kr[NK], vr[NK];
     uint2 scales = {0, 0};
+    int ids = -1;   // table entries of 64 of the range's pages, one a lane
     auto page_of = [&](int i) {
-        const int page = i < p_end ? c.page_at(s, span.at(i)) : -1;
-        return __builtin_amdgcn_readfirstlane(c.page_ok(page) ? page : -1);
+        const int k = (i - p_begin) & 63;
+        if (k == 0) ids = i + lane < p_end ? c.page_at(s, span.at(i + lane)) : -1;
+        const int page = i < p_end ? __builtin_amdgcn_readlane(ids, k) : -1;
+        return c.page_ok(page) ? page : -1;
     };
     auto load = [&](int page) {
         if (page < 0) return;
@@ -505,7 +579,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int j = tok + 32 * t + 16 * (e >> 3) + 8 * g + (e & 7);
-                        const bool see = j <= pos && (a.window == 0 || j > pos - a.window || j < a.sink);
+                        const bool see = (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
                         sc[t][e] = see ? sc[t][e] * a.scale2 : NEG_INF;
                         top = fmaxf(top, sc[t][e]);
                     }
@@ -556,7 +630,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
     }
     if (!live_row) return;
     sum += __shfl_xor(sum, 32, 64);
-    if (a.splits == 1) {
+    if (tl.ranges == 1) {
         const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         typedef T Four __attribute__((ext_vector_type(4)));
         T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + h * a.G + r % a.G) * D + 4 * g;
@@ -584,66 +658,87 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
     }
 }
 
-// Joins the ranges of a row: a workgroup per row, D / 4 lanes per range, so
-// that several ranges are read at a time.
-template <class T, int D>
+// Joins the ranges of a row, D / 4 lanes per range so that several are read
+// at a time: a workgroup per row where there are many ranges, else a wave.
+template <class T, int D, int ROWS>
 __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
-    constexpr int LP = D / 4, GW = 64 / LP, GROUPS = 4 * GW;   // lanes of a range, ranges at a time
-    const CacheView& c = a.c;
+    constexpr int LP = D / 4, GW = 64 / LP, GROUPS = 4 / ROWS * GW;   // lanes of a range, ranges at a time
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = blockIdx.y, b = blockIdx.z;
-    const int count = a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
-    const int r = blockIdx.x;
-    if (r >= count * a.G) return;
-    const size_t rows = (size_t)a.T * a.G, at0 = ((size_t)b * c.H + h) * a.splits * rows + r;
-    __shared__ float acc[GROUPS][D + 4];
-    __shared__ float sums[GROUPS];
+    const int r = blockIdx.x * ROWS + (ROWS > 1 ? w : 0);
+    const Tile tl = tile_of(a, b, uniform(a.seqs ? a.seqs[b] : b), r / a.tile_rows);
+    const bool out_of = r >= tl.rows || tl.ranges == 1;
+    if (ROWS == 1 && out_of) return;
+    const int ranges = out_of ? 0 : tl.ranges;
+    const size_t rows = (size_t)a.T * a.G, at0 = ((size_t)b * a.c.H + h) * a.splits * rows + r;
+    __shared__ __align__(16) float acc[4 * GW][D + 4];
+    __shared__ float sums[4 * GW];
     float top = NEG_INF;
-    for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.ml[2 * (at0 + s * rows)]);
+    for (int s = lane; s < ranges; s += 64) top = fmaxf(top, a.ml[2 * (at0 + s * rows)]);
 #pragma unroll
     for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
     const float ref = top == NEG_INF ? 0.f : top;
-    const int grp = w * GW + lane / LP, col = lane % LP * 4;
+    const int grp = (ROWS > 1 ? 0 : w * GW) + lane / LP, col = lane % LP * 4;
     if (lane < GW * LP) {
         f32x4 o = {0, 0, 0, 0};
         float total = 0.f;
 #pragma unroll 4
-        for (int s = grp; s < a.splits; s += GROUPS) {
+        for (int s = grp; s < ranges; s += GROUPS) {
             const size_t at = at0 + s * rows;
             const float by = __builtin_amdgcn_exp2f(a.ml[2 * at] - ref);
             total += a.ml[2 * at + 1] * by;
             o += *reinterpret_cast<const f32x4*>(a.part + at * D + col) * by;
         }
-        *reinterpret_cast<f32x4*>(&acc[grp][col]) = o;
-        if (col == 0) sums[grp] = total;
+        *reinterpret_cast<f32x4*>(&acc[w * GW + lane / LP][col]) = o;
+        if (col == 0) sums[w * GW + lane / LP] = total;
     }
     __syncthreads();
-    if (threadIdx.x >= D) return;
-    float y = 0.f, total = 0.f;
+    if (out_of) return;
+    T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * a.c.H * a.G + h * a.G + r % a.G) * D;
+    const int z0 = ROWS > 1 ? w * GW : 0, step = ROWS > 1 ? 64 : 256;
+    for (int dim = ROWS > 1 ? lane : threadIdx.x; dim < D; dim += step) {
+        float y = 0.f, total = 0.f;
 #pragma unroll
-    for (int z = 0; z < GROUPS; ++z) {
-        y += acc[z][threadIdx.x];
-        total += sums[z];
+        for (int z = 0; z < GROUPS; ++z) {
+            y += acc[z0 + z][dim];
+            total += sums[z0 + z];
+        }
+        out[dim] = (T)(y * (total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total)));
     }
-    const float by = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
-    reinterpret_cast<T*>(a.out)[(((long)b * a.T + r / a.G) * c.H * a.G + h * a.G + r % a.G) * D + threadIdx.x] = (T)(y * by);
 }
 
+constexpr int ONE_DIM = 128, ONE_PAGES = 24;
 // How a call is launched: which kernel, how many tiles of rows, and into how
 // many ranges the sequences are divided.
 struct AttendPlan {
     bool wide;   // attend_tiles_kernel (128 rows a tile), else attend_rows_kernel (16 wr)
-    int wr, tiles, splits;
+    int wr, waves, tile_rows, tiles, splits, least;
 };
-static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len) {
+static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool f32) {
     AttendPlan p;
     const long rows = (long)n_tokens * (heads / c->H);
     p.wide = rows > 64;
     p.wr = rows > 32 ? 4 : rows > 16 ? 2 : 1;
-    const int tile = p.wide ? TILE_ROWS : 16 * p.wr;
-    p.tiles = (int)((rows + tile - 1) / tile);
+    p.tile_rows = p.wide ? TILE_ROWS : 16 * p.wr;
+    p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     const long pages = (max_len + PAGE - 1) / PAGE, groups = (long)batch * c->H * p.tiles;
-    long s = p.wide ? 512 / groups : 1024 / groups;
-    const long most = p.wide ? (pages + 3) / 4 : (pages + 7) / 8;   // four pages a range, or two a wave, at least
+    // Short sequences (a window's) in one range of eight waves, where the
+    // registers allow eight: one launch instead of two
+    p.waves = 4;
+    if (!p.wide && p.wr == 1 && c->d <= ONE_DIM && pages <= ONE_PAGES) {
+        p.waves = 8;
+        p.splits = 1;
+        p.least = 1 << 20;
+        return p;
+    }
+    // workgroups in flight: as many as the registers and LDS of a compute unit
+    // take (tiles), or several rounds of them, which even out ragged lengths
+    const int slots = 256 * (c->d <= 64 ? (f32 ? 2 : 3) : c->d <= 128 && !f32 ? 2 : 1);
+    // pages of a range: two a wave while the chip is not full, more as soon as
+    // it is (every range costs a start and a place in the join)
+    const long eights = groups * ((pages + 7) / 8);
+    p.least = p.wide ? 4 : eights <= 1024 ? 8 : eights <= 4096 ? 16 : 32;
+    long s = (p.wide ? slots : 8192) / groups;
+    const long most = (pages + p.least - 1) / p.least;
     if (s > most) s = most;
     if (s > 256) s = 256;
     p.splits = s < 1 ? 1 : (int)s;
@@ -652,8 +747,8 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
 
 size_t attend_workspace(const tm_cache* c, int batch, int n_tokens, int heads) {
     if (heads % c->H != 0 || batch == 0 || n_tokens == 0) return 0;
-    // the most ranges that any max_len leads to
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, (long)c->seq_pages * PAGE);
+    // the most ranges that any max_len and either type lead to
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, (long)c->seq_pages * PAGE, false);
     if (p.splits == 1) return 0;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * (heads / c->H);
     return (rows * (c->d + 2) * 4 + 511) / 256 * 256;
@@ -669,17 +764,27 @@ static hipError_t launch_attend(const tm_cache* c, const AttendArgs& a, const At
                 return hipGetLastError();
             }
             const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c->H, (unsigned)a.B);
-            if (p.wr == 1) launch_k(attend_rows_kernel<T, D(), 1>, grid, dim3(256), 0, st, a);
-            else if (p.wr == 2) launch_k(attend_rows_kernel<T, D(), 2>, grid, dim3(256), 0, st, a);
-            else launch_k(attend_rows_kernel<T, D(), 4>, grid, dim3(256), 0, st, a);
+            if constexpr (D() <= ONE_DIM) {
+                if (p.waves == 8) {
+                    launch_k(attend_rows_kernel<T, D(), 1, 8>, grid, dim3(512), 0, st, a);
+                    return hipGetLastError();
+                }
+            }
+            if (p.wr == 1) launch_k(attend_rows_kernel<T, D(), 1, 4>, grid, dim3(256), 0, st, a);
+            else if (p.wr == 2) launch_k(attend_rows_kernel<T, D(), 2, 4>, grid, dim3(256), 0, st, a);
+            else launch_k(attend_rows_kernel<T, D(), 4, 4>, grid, dim3(256), 0, st, a);
             return hipGetLastError();
         });
     });
     if (e != hipSuccess || p.splits == 1) return e;
     return timed_attn(st, [&] {
         return for_head_dim(c->d, [&](auto D) {
-            const dim3 grid((unsigned)(a.T * a.G), (unsigned)c->H, (unsigned)a.B);
-            launch_k(combine_kernel<T, D()>, grid, dim3(256), 0, st, a);
+            const int rows = a.T * a.G;
+            if (p.splits > 16)
+                launch_k(combine_kernel<T, D(), 1>, dim3((unsigned)rows, (unsigned)c->H, (unsigned)a.B), dim3(256), 0, st, a);
+            else
+                launch_k(combine_kernel<T, D(), 4>, dim3((unsigned)((rows + 3) / 4), (unsigned)c->H, (unsigned)a.B), dim3(256),
+                         0, st, a);
             return hipGetLastError();
         });
     });
@@ -702,14 +807,14 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
     if (batch > 65535 || (!seqs && batch > c->n_seqs) || n_tokens > 1 << 24 || (uintptr_t)seqs % 4 || (uintptr_t)counts % 4 ||
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most);
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most, dtype == TM_F32);
     if ((long)p.tiles * p.splits * c->H > 0x7fffffffL) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
     const int G = heads / c->H;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * G;
     float* part = static_cast<float*>(workspace);
     AttendArgs a{cache_view(c, const_cast<void*>(blob)), seqs, counts, q, q_batch, q_token, out, batch, n_tokens, G,
-                 score_scale * 1.44269504088896340736f, window, sink < most ? sink : (int)most, p.splits, part, part + rows * c->d};
+                 score_scale * 1.44269504088896340736f, window, sink < most ? sink : (int)most, p.splits, p.least, p.tile_rows, part, part + rows * c->d};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == TM_F32 ? launch_attend<float>(c, a, p, st) : launch_attend<bf16>(c, a, p, st);
     return e == hipSuccess ? TM_OK : TM_ERR_HIP;
