@@ -26,10 +26,28 @@ struct RopeArgs {
     int units, hgroup;     // work units of a head vector; heads per thread
 };
 
+// 16-byte loads and stores past the caches (STREAM) or through them.
+template <bool STREAM, class V> __device__ __forceinline__ V get(const V* p) {
+    if constexpr (STREAM) {
+        typedef unsigned U __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(V, __builtin_nontemporal_load(reinterpret_cast<const U*>(p)));
+    } else {
+        return *p;
+    }
+}
+template <bool STREAM, class V> __device__ __forceinline__ void put(V* p, V v) {
+    if constexpr (STREAM) {
+        typedef unsigned U __attribute__((ext_vector_type(4)));
+        __builtin_nontemporal_store(__builtin_bit_cast(U, v), reinterpret_cast<U*>(p));
+    } else {
+        *p = v;
+    }
+}
+
 // One unit is V consecutive elements (16 bytes at most).  Half layout: V
 // pairs (V elements of each half); interleaved: V / 2 pairs (one where V is
 // 1); the elements behind the rotated ones are units of their own, copied.
-template <class T, int V, bool HALF>
+template <class T, int V, bool HALF, bool STREAM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     struct __align__(sizeof(T) * V) Vec { T e[V]; };
     constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);
@@ -47,7 +65,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
         if (x == y) return;
         const int c = a.r + (u - rot_units) * V;
         for (int h = h0; h < h1; ++h)
-            *reinterpret_cast<Vec*>(y + (long)h * a.d + c) = *reinterpret_cast<const Vec*>(x + (long)h * a.d + c);
+            *reinterpret_cast<Vec*>(y + (long)h * a.d + c) = get<STREAM>(reinterpret_cast<const Vec*>(x + (long)h * a.d + c));
         return;
     }
     const double p = (double)a.pos[a.per_token ? bt : b] + (a.per_token ? 0 : t);
@@ -66,8 +84,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
         const int c = u * V;
 #pragma unroll 4
         for (int h = h0; h < h1; ++h) {
-            const Vec lo = *reinterpret_cast<const Vec*>(x + (long)h * a.d + c);
-            const Vec hi = *reinterpret_cast<const Vec*>(x + (long)h * a.d + a.r / 2 + c);
+            const Vec lo = get<STREAM>(reinterpret_cast<const Vec*>(x + (long)h * a.d + c));
+            const Vec hi = get<STREAM>(reinterpret_cast<const Vec*>(x + (long)h * a.d + a.r / 2 + c));
             Vec ol, oh;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -75,15 +93,15 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
                 ol.e[j] = (T)(p0 * cs[j] - p1 * sn[j]);
                 oh.e[j] = (T)(p0 * sn[j] + p1 * cs[j]);
             }
-            *reinterpret_cast<Vec*>(y + (long)h * a.d + c) = ol;
-            *reinterpret_cast<Vec*>(y + (long)h * a.d + a.r / 2 + c) = oh;
+            put<STREAM>(reinterpret_cast<Vec*>(y + (long)h * a.d + c), ol);
+            put<STREAM>(reinterpret_cast<Vec*>(y + (long)h * a.d + a.r / 2 + c), oh);
         }
     } else {
         struct __align__(sizeof(T) * V) Pairs { T e[2 * NP]; };
         const int c = u * 2 * NP;
 #pragma unroll 4
         for (int h = h0; h < h1; ++h) {
-            const Pairs v = *reinterpret_cast<const Pairs*>(x + (long)h * a.d + c);
+            const Pairs v = get<STREAM>(reinterpret_cast<const Pairs*>(x + (long)h * a.d + c));
             Pairs o;
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -91,7 +109,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
                 o.e[2 * j] = (T)(p0 * cs[j] - p1 * sn[j]);
                 o.e[2 * j + 1] = (T)(p0 * sn[j] + p1 * cs[j]);
             }
-            *reinterpret_cast<Pairs*>(y + (long)h * a.d + c) = o;
+            put<STREAM>(reinterpret_cast<Pairs*>(y + (long)h * a.d + c), o);
         }
     }
 }
@@ -102,14 +120,27 @@ static hipError_t launch_v(RopeArgs a, bool half, hipStream_t st) {
     const long threads = (long)a.B * a.T * a.units;
     const long blocks = (threads + 255) / 256;
     if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    // What does not fit the 256 MB of the last-level cache goes past the
+    // caches, with more workgroups (2 x 16384 tokens of 40 heads of 128 in
+    // bf16, 671 MB: 131 us against 138; 4 x 8192 of 10 heads of 64, 84 MB:
+    // through the caches 17 us, past them 24).
+    const bool stream = (long)a.B * a.T * a.H * a.d * (long)sizeof(T) * 2 > 256L << 20;
     // heads per thread: all of them where the tokens alone fill the chip,
-    // fewer until about 4 workgroups stand on each of 256 compute units
+    // fewer until about 4 workgroups (64 in a stream) stand on each of 256
+    // compute units
     int groups = 1;
-    while (groups < a.H && blocks * groups < 1024) groups *= 2;
+    while (groups < a.H && blocks * groups < (stream ? 16384 : 1024)) groups *= 2;
     a.hgroup = (a.H + groups - 1) / groups;
     const dim3 grid((unsigned)blocks, (unsigned)((a.H + a.hgroup - 1) / a.hgroup));
-    if (half) launch_k(rope_kernel<T, V, true>, grid, dim3(256), 0, st, a);
-    else launch_k(rope_kernel<T, V, false>, grid, dim3(256), 0, st, a);
+    if constexpr (V * sizeof(T) == 16) {
+        if (stream) {
+            if (half) launch_k(rope_kernel<T, V, true, true>, grid, dim3(256), 0, st, a);
+            else launch_k(rope_kernel<T, V, false, true>, grid, dim3(256), 0, st, a);
+            return hipGetLastError();
+        }
+    }
+    if (half) launch_k(rope_kernel<T, V, true, false>, grid, dim3(256), 0, st, a);
+    else launch_k(rope_kernel<T, V, false, false>, grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
