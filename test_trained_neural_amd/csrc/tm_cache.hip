@@ -21,7 +21,7 @@ constexpr int MAX_SEQS = 8192;
 struct AppendPlan {
     int old, n;      // tokens held before, tokens to write
     int copy_from;   // the shared page that the entry's last page is a copy of, or -1
-    int pad;
+    int page;        // the page of token `old`
 };
 
 struct AppendArgs {
@@ -68,85 +68,104 @@ template <int THREADS> __device__ __forceinline__ int block_scan(int x, int* wav
 //   3. a scan over the reference counts finds the free pages in order; page
 //      of rank r goes to the entry whose ranks hold r (binary search);
 //   4. entries within the free pages take effect.
-// Latency-bound (a handful of dependent round trips); the write that follows
-// has the bytes.
-__global__ __launch_bounds__(PLAN_THREADS) void append_plan_kernel(AppendArgs a) {
+// Bound by the latency of its dependent reads (list, length, last page, its
+// references); the first reference counts of the scan are read beside them.
+// The write that follows has the bytes.
+template <int THREADS, int ENTRIES>
+__global__ __launch_bounds__(THREADS) void append_plan_kernel(AppendArgs a) {
     const CacheView& c = a.c;
+    constexpr int PER = ENTRIES / THREADS, STEP = THREADS * 4;
     __shared__ int ranks[MAX_SEQS];   // first the winners of 1, then the inclusive sums of 2
-    __shared__ int wave_sums[PLAN_THREADS / 64];
+    __shared__ short copies[ENTRIES]; // 1: the entry's first page is a copy; 2: its first page is new
+    __shared__ int olds[ENTRIES <= 256 ? ENTRIES : 1];
+    __shared__ int wave_sums[THREADS / 64];
     __shared__ int flags, hint;
-    constexpr int PER = MAX_SEQS / PLAN_THREADS;
     const int tid = threadIdx.x;
+    const int from = min(max(c.status[1], 0), c.n_pages) / 4 * 4;
+    auto free_of = [&](int p) {   // bit e: page p + e is free
+        int r[4], f = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = p + e < c.n_pages ? c.refs[p + e] : 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f |= (r[e] <= 0) << e;
+        return f;
+    };
+    int free4 = free_of(from + tid * 4);
     if (tid == 0) {
         flags = 0;
         hint = 0x7fffffff;
     }
     auto seq_of = [&](int i) { return a.seqs ? a.seqs[i] : i; };
-    for (int i = tid; i < a.B; i += PLAN_THREADS) {
-        const int s = seq_of(i);
-        if ((unsigned)s < (unsigned)c.n_seqs) ranks[s] = 0x7fffffff;
-    }
-    __syncthreads();
-    for (int i = tid; i < a.B; i += PLAN_THREADS) {
-        const int s = seq_of(i);
-        if ((unsigned)s < (unsigned)c.n_seqs) atomicMin(&ranks[s], i);
-    }
-    __syncthreads();
-    unsigned mine = 0;   // bit j: this thread's j-th entry is served so far
+    int seq[PER];
+#pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int i = tid + j * PLAN_THREADS;
-        if (i >= a.B) break;
-        const int s = seq_of(i);
-        if ((unsigned)s < (unsigned)c.n_seqs && ranks[s] == i) mine |= 1u << j;
-        else atomicOr(&flags, TM_CACHE_BAD_ENTRY);
+        const int i = tid + j * THREADS;
+        seq[j] = i < a.B ? seq_of(i) : -1;
+        if ((unsigned)seq[j] < (unsigned)c.n_seqs) ranks[seq[j]] = 0x7fffffff;
+        else seq[j] = -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (seq[j] >= 0) atomicMin(&ranks[seq[j]], tid + j * THREADS);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * THREADS;
+        if (i < a.B && (seq[j] < 0 || ranks[seq[j]] != i)) {
+            atomicOr(&flags, TM_CACHE_BAD_ENTRY);
+            seq[j] = -1;
+        }
     }
     __syncthreads();
     int base = 0;
-    for (int j = 0; j * PLAN_THREADS < a.B; ++j) {
-        const int i = tid + j * PLAN_THREADS;
+    AppendPlan plan[PER];
+    int before[PER], incl[PER];   // an entry's ranks: before .. incl - 1
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * THREADS, s = seq[j];
+        AppendPlan p{0, 0, -1, -1};
         int need = 0;
-        if (i < a.B) {
-            AppendPlan p{0, 0, -1, 0};
-            if (mine >> j & 1) {
-                const int s = seq_of(i);
-                p.old = c.length(s);
-                p.n = a.counts ? min(max(a.counts[i], 0), a.T) : a.T;
-                if (p.n > c.seq_pages * PAGE - p.old) {
-                    atomicOr(&flags, TM_CACHE_FULL);
-                    p.n = 0;
-                }
-                if (p.n > 0 && p.old % PAGE) {
-                    const int tail = c.page_at(s, p.old / PAGE);
-                    if (!c.page_ok(tail)) {
-                        atomicOr(&flags, TM_CACHE_BAD_ENTRY);
-                        p.n = 0;
-                    } else if (c.refs[tail] > 1) {
-                        p.copy_from = tail;
-                    }
-                }
-                if (p.n > 0) need = (p.old + p.n + PAGE - 1) / PAGE - (p.old + PAGE - 1) / PAGE + (p.copy_from >= 0);
+        if (s >= 0) {
+            p.old = c.length(s);
+            p.n = a.counts ? min(max(a.counts[i], 0), a.T) : a.T;
+            if (p.n > c.seq_pages * PAGE - p.old) {
+                atomicOr(&flags, TM_CACHE_FULL);
+                p.n = 0;
             }
-            a.plan[i] = p;
+            if (p.n > 0 && p.old % PAGE) {
+                p.page = c.page_at(s, p.old / PAGE);
+                if (!c.page_ok(p.page)) {
+                    atomicOr(&flags, TM_CACHE_BAD_ENTRY);
+                    p.n = 0;
+                } else if (c.refs[p.page] > 1) {
+                    p.copy_from = p.page;
+                }
+            }
+            if (p.n > 0) need = (p.old + p.n + PAGE - 1) / PAGE - (p.old + PAGE - 1) / PAGE + (p.copy_from >= 0);
         }
         int total;
-        const int incl = base + block_scan<PLAN_THREADS>(need, wave_sums, total);
+        incl[j] = base + block_scan<THREADS>(need, wave_sums, total);
+        before[j] = incl[j] - need;
         base += total;
-        if (i < a.B) ranks[i] = incl;
+        plan[j] = p;
+        if (i < a.B) {
+            ranks[i] = incl[j];
+            copies[i] = p.copy_from >= 0 ? 1 : p.n > 0 && p.old % PAGE == 0 ? 2 : 0;
+            if constexpr (ENTRIES <= 256) olds[i] = p.old;
+            a.plan[i] = p;
+        }
     }
     const int want = base;   // pages of the whole call
     __syncthreads();
     int found = 0;           // free pages seen
     if (want > 0) {
-        const int from = min(max(c.status[1], 0), c.n_pages) / 4 * 4;
-        for (int p0 = from; p0 < c.n_pages && found < want; p0 += PLAN_THREADS * 4) {
+        for (int p0 = from; p0 < c.n_pages && found < want; p0 += STEP) {
             const int p = p0 + tid * 4;
-            int free4 = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (p + e < c.n_pages && c.refs[p + e] <= 0) free4 |= 1 << e;
+            if (p0 != from) free4 = free_of(p);
             int total;
             const int n4 = __popc(free4);
-            int r = found + block_scan<PLAN_THREADS>(n4, wave_sums, total) - n4;
+            int r = found + block_scan<THREADS>(n4, wave_sums, total) - n4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (!(free4 >> e & 1)) continue;
@@ -157,10 +176,14 @@ __global__ __launch_bounds__(PLAN_THREADS) void append_plan_kernel(AppendArgs a)
                         if (ranks[mid] > r) hi = mid;
                         else lo = mid + 1;
                     }
-                    const AppendPlan q = a.plan[lo];
-                    const int first = q.copy_from >= 0 ? q.old / PAGE : (q.old + PAGE - 1) / PAGE;
-                    c.table[(size_t)seq_of(lo) * c.seq_pages + first + r - (lo ? ranks[lo - 1] : 0)] = p + e;
+                    int old;
+                    if constexpr (ENTRIES <= 256) old = olds[lo];
+                    else old = a.plan[lo].old;
+                    const int nth = r - (lo ? ranks[lo - 1] : 0), kind = copies[lo];
+                    const int slot = (kind == 1 ? old / PAGE : (old + PAGE - 1) / PAGE) + nth;
+                    c.table[(size_t)seq_of(lo) * c.seq_pages + slot] = p + e;
                     c.refs[p + e] = 1;
+                    if (kind && nth == 0) a.plan[lo].page = p + e;
                     if (r == want - 1) hint = p + e + 1;
                 }
                 ++r;
@@ -173,25 +196,21 @@ __global__ __launch_bounds__(PLAN_THREADS) void append_plan_kernel(AppendArgs a)
     const int have = min(found, want);
     if (tid == 0 && have < want) hint = c.n_pages;   // every free page was taken (or is given back below)
     __syncthreads();
-    for (int j = 0; j * PLAN_THREADS < a.B; ++j) {
-        const int i = tid + j * PLAN_THREADS;
-        if (i >= a.B) break;
-        AppendPlan p = a.plan[i];
-        if (p.n == 0) continue;
-        const int s = seq_of(i), before = i ? ranks[i - 1] : 0, incl = ranks[i];
-        if (incl > before && incl > have) {   // not enough pages: those taken so far go back
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * THREADS, s = seq[j];
+        AppendPlan& p = plan[j];
+        if (i >= a.B || p.n == 0) continue;
+        if (incl[j] > before[j] && incl[j] > have) {   // not enough pages: those taken so far go back
             atomicOr(&flags, TM_CACHE_NO_PAGES);
             const int first = p.copy_from >= 0 ? p.old / PAGE : (p.old + PAGE - 1) / PAGE;
-            for (int r = before; r < have; ++r) {
-                const size_t at = (size_t)s * c.seq_pages + first + r - before;
-                const int page = c.table[at];
+            for (int r = before[j]; r < have; ++r) {
+                const int page = c.table[(size_t)s * c.seq_pages + first + r - before[j]];
                 c.refs[page] = 0;
                 atomicMin(&hint, page);
             }
-            if (p.copy_from >= 0 && have > before) c.table[(size_t)s * c.seq_pages + first] = p.copy_from;
-            p.n = 0;
-            p.copy_from = -1;
-            a.plan[i] = p;
+            if (p.copy_from >= 0 && have > before[j]) c.table[(size_t)s * c.seq_pages + first] = p.copy_from;
+            a.plan[i].n = 0;
             continue;
         }
         c.lengths[s] = p.old + p.n;
@@ -249,9 +268,9 @@ __device__ __forceinline__ float wave_max(float x) {
 // token.  Values, whose tokens are innermost: a lane takes two neighbouring
 // dims of all 16 tokens (4 or 8 bytes a lane and token, so a token's row is
 // read whole) and stores the block's 16 codes of a dim at once; the page's
-// 64-byte row of a dim is made of the four waves' pieces.  The block's
-// largest magnitude is a wave reduction between load and store, so the
-// tokens are read once.
+// 64-byte row of a dim is made of the four waves' pieces.  All tokens are
+// read up front, once, and stay as they are in registers through the wave's
+// reduction to the block's largest magnitude.
 template <class T, int D>
 __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
     const CacheView& c = a.c;
@@ -264,52 +283,87 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
     const int lo = max(p.old, b0), hi = min(end, b0 + BLOCK);    // the new tokens in it
     const bool copied = blockIdx.x == 0 && p.copy_from >= 0;
     if (lo >= hi && !copied) return;
-    const int s = a.seqs ? a.seqs[b] : b;
-    const int page = c.page_at(s, slot);
+    const T* kx = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * D;
+    const T* vx = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * D;
+
+    typedef T Two __attribute__((ext_vector_type(2)));
+    constexpr int KI = BLOCK * D / 8 / 64, VI = (D / 2 + 63) / 64;
+    decltype(ld8(kx)) kr[KI];
+    Two vr[VI][BLOCK];
+#pragma unroll
+    for (int it = 0; it < KI; ++it) {
+        const int u = it * 64 + lane, t = u / (D / 8), col = u % (D / 8) * 8;
+        kr[it] = {};
+        if (b0 + t >= lo && b0 + t < hi) kr[it] = ld8(kx + (long)(b0 + t - p.old) * a.kt + col);
+    }
+#pragma unroll
+    for (int it = 0; it < VI; ++it) {
+        const int dim = (it * 64 + lane) * 2;
+#pragma unroll
+        for (int t = 0; t < BLOCK; ++t) {
+            vr[it][t] = Two{(T)0.f, (T)0.f};
+            if (dim < D && b0 + t >= lo && b0 + t < hi)
+                vr[it][t] = *reinterpret_cast<const Two*>(vx + (long)(b0 + t - p.old) * a.vt + dim);
+        }
+    }
+    const int page = blockIdx.x == 0 ? p.page : c.page_at(a.seqs ? a.seqs[b] : b, slot);
     if (!c.page_ok(page)) return;
     const int from = copied ? p.copy_from : page;   // where the block's present codes are
     const bool begun = lo > b0 && lo < hi;          // it holds earlier tokens, and gets new ones
     const size_t at = c.head_at(page, h), at0 = c.head_at(from, h);
-    const T* kx = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * D;
-    const T* vx = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * D;
-    bool bad = false;
-
-    // ---- keys ----
-    {
-        constexpr int UNITS = BLOCK * D / 8, IT = UNITS / 64;
-        const unsigned char* src = c.k + (at0 * PAGE + w * BLOCK) * D;
-        unsigned char* dst = c.k + (at * PAGE + w * BLOCK) * D;
-        float x[IT][8];
-        float top = 0.f;
+    const bool use = begun || lo >= hi;             // the present scales matter
+    const int had_k = use ? (int)c.scales[at0 * 8 + w] - 127 : 0, had_v = use ? (int)c.scales[at0 * 8 + 4 + w] - 127 : 0;
+    // bytes of the block's 16 that take new codes; around them the present ones
+    // stay, so a block that is not written whole is read first
+    const unsigned fresh = lo < hi ? ((1u << (hi - b0)) - 1) & ~((1u << (lo - b0)) - 1) : 0;
+    const bool whole = fresh == 0xffffu;
+    uint4 was[VI][2];
+    if (!whole) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int u = it * 64 + lane, t = u / (D / 8), col = u % (D / 8) * 8;
-            if (b0 + t >= lo && b0 + t < hi) {
-                const auto raw = ld8(kx + (long)(b0 + t - p.old) * a.kt + col);
+        for (int it = 0; it < VI; ++it)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[it][e] = finite_or_zero((float)raw[e], bad);
-                    top = fmaxf(top, fabsf(x[it][e]));
-                }
+            for (int z = 0; z < 2; ++z) {
+                const int dim = (it * 64 + lane) * 2 + z;
+                if (dim < D) was[it][z] = *reinterpret_cast<const uint4*>(c.v + (at0 * D + dim) * PAGE + w * BLOCK);
             }
-        }
-        const int had = (int)c.scales[at0 * 8 + w] - 127;
+    }
+    bool bad = false;
+    // the block's new exponent, and what its present codes are multiplied by
+    auto settle = [&](float top, int had, float& by, float& shift) {
         int e = had;
         if (lo < hi) {
             e = block_exponent(wave_max(top));
             if (begun) e = max(e, had);
         }
-        const float by = pow2(-e), shift = begun && e > had ? pow2(max(had - e, -126)) : 1.f;
+        by = pow2(-e);
+        shift = begun && e > had ? pow2(max(had - e, -126)) : 1.f;
+        return (unsigned char)(e + 127);
+    };
+
+    // ---- keys ----
+    {
+        const unsigned char* src = c.k + (at0 * PAGE + w * BLOCK) * D;
+        unsigned char* dst = c.k + (at * PAGE + w * BLOCK) * D;
+        float top = 0.f;
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
+        for (int it = 0; it < KI; ++it)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(finite_or_zero((float)kr[it][e], bad)));
+        float by, shift;
+        const unsigned char scale = settle(top, had_k, by, shift);
+#pragma unroll
+        for (int it = 0; it < KI; ++it) {
             const int u = it * 64 + lane, t = u / (D / 8), col = u % (D / 8) * 8;
+            uint2 o;
             if (b0 + t >= lo && b0 + t < hi) {
-                uint2 o;
-                o.x = codes4(x[it][0] * by, x[it][1] * by, x[it][2] * by, x[it][3] * by);
-                o.y = codes4(x[it][4] * by, x[it][5] * by, x[it][6] * by, x[it][7] * by);
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = finite_or_zero((float)kr[it][e], bad) * by;
+                o.x = codes4(x[0], x[1], x[2], x[3]);
+                o.y = codes4(x[4], x[5], x[6], x[7]);
                 *reinterpret_cast<uint2*>(dst + t * D + col) = o;
             } else if (copied || (shift != 1.f && b0 + t < lo)) {
-                uint2 o = *reinterpret_cast<const uint2*>(src + t * D + col);
+                o = *reinterpret_cast<const uint2*>(src + t * D + col);
                 if (shift != 1.f && b0 + t < lo) {
                     o.x = shift4(o.x, shift);
                     o.y = shift4(o.y, shift);
@@ -317,54 +371,35 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
                 *reinterpret_cast<uint2*>(dst + t * D + col) = o;
             }
         }
-        if (lane == 0) c.scales[at * 8 + w] = (unsigned char)(e + 127);
+        if (lane == 0) c.scales[at * 8 + w] = scale;
     }
     // ---- values ----
     {
-        constexpr int IT = (D / 2 + 63) / 64;
-        float x[IT][BLOCK][2];
         float top = 0.f;
-        typedef T Two __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int dim = (it * 64 + lane) * 2;
+        for (int it = 0; it < VI; ++it)
 #pragma unroll
-            for (int t = 0; t < BLOCK; ++t) {
-                x[it][t][0] = x[it][t][1] = 0.f;
-                if (dim < D && b0 + t >= lo && b0 + t < hi) {
-                    const Two raw = *reinterpret_cast<const Two*>(vx + (long)(b0 + t - p.old) * a.vt + dim);
+            for (int t = 0; t < BLOCK; ++t)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[it][t][e] = finite_or_zero((float)raw[e], bad);
-                        top = fmaxf(top, fabsf(x[it][t][e]));
-                    }
-                }
-            }
-        }
-        const int had = (int)c.scales[at0 * 8 + 4 + w] - 127;
-        int e = had;
-        if (lo < hi) {
-            e = block_exponent(wave_max(top));
-            if (begun) e = max(e, had);
-        }
-        const float by = pow2(-e), shift = begun && e > had ? pow2(max(had - e, -126)) : 1.f;
-        // bytes of the block's 16 that take new codes
-        const unsigned fresh = lo < hi ? ((1u << (hi - b0)) - 1) & ~((1u << (lo - b0)) - 1) : 0;
-        const bool whole = fresh == 0xffffu;
+                for (int z = 0; z < 2; ++z) top = fmaxf(top, fabsf(finite_or_zero((float)vr[it][t][z], bad)));
+        float by, shift;
+        const unsigned char scale = settle(top, had_v, by, shift);
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
+        for (int it = 0; it < VI; ++it) {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int dim = (it * 64 + lane) * 2 + z;
                 if (dim >= D) continue;
                 unsigned o[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    o[q] = codes4(x[it][4 * q][z] * by, x[it][4 * q + 1][z] * by, x[it][4 * q + 2][z] * by,
-                                  x[it][4 * q + 3][z] * by);
+                for (int q = 0; q < 4; ++q) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = finite_or_zero((float)vr[it][4 * q + e][z], bad) * by;
+                    o[q] = codes4(x[0], x[1], x[2], x[3]);
+                }
                 if (!whole) {
-                    const uint4 was = *reinterpret_cast<const uint4*>(c.v + (at0 * D + dim) * PAGE + w * BLOCK);
-                    const unsigned old4[4] = {was.x, was.y, was.z, was.w};
+                    const unsigned old4[4] = {was[it][z].x, was[it][z].y, was[it][z].z, was[it][z].w};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const unsigned n4 = fresh >> (4 * q) & 15;   // spread to bytes
@@ -382,7 +417,7 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
                 *reinterpret_cast<uint4*>(c.v + (at * D + dim) * PAGE + w * BLOCK) = uint4{o[0], o[1], o[2], o[3]};
             }
         }
-        if (lane == 0) c.scales[at * 8 + 4 + w] = (unsigned char)(e + 127);
+        if (lane == 0) c.scales[at * 8 + 4 + w] = scale;
     }
     if (__any(bad) && lane == 0) atomicOr(&c.status[0], TM_CACHE_NONFINITE);
 }
@@ -724,7 +759,8 @@ tm_status tm_cache_append(const tm_cache* c, void* blob, const int* seqs, const 
                  static_cast<AppendPlan*>(workspace)};
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = timed_attn(st, [&] {
-        launch_k(append_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, a);
+        if (batch <= 256) launch_k(append_plan_kernel<256, 256>, dim3(1), dim3(256), 0, st, a);
+        else launch_k(append_plan_kernel<PLAN_THREADS, MAX_SEQS>, dim3(1), dim3(PLAN_THREADS), 0, st, a);
         return hipGetLastError();
     });
     if (e != hipSuccess) return TM_ERR_HIP;
