@@ -1,8 +1,11 @@
 // Attention over the paged 8-bit cache (include/tm_attention.h,
 // tm_cache_attend).
 //
-//   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c (q . k_j) - m),
-//   c = score_scale log2(e), m the row's running maximum of c (q . k_j)
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c s_j - m),   s_j = +-q . k_j,
+//   c = |score_scale| log2(e), m the row's running maximum of c s_j
+//
+// (the sign of score_scale goes into q, so that the largest s_j has the
+// largest weight and c is applied in the exponent's fused multiply-add).
 //
 // One pass over the keys and values: a wave takes a page of 64 tokens at a
 // time, keeps each row's maximum and sum in fp32, and rescales what it has
@@ -35,7 +38,7 @@ struct AttendArgs {
     long qb, qt;
     void* out;
     int B, T, G;         // entries, query tokens, query heads per kv head
-    float scale2;        // score_scale log2(e)
+    float scale2, sign;  // |score_scale| log2(e), above 0 (a masked score is -inf times it), and score_scale's sign
     int window, sink;
     int splits;          // the most key ranges that a tile's pages are divided into
     int least;           // pages of a range, at least
@@ -192,7 +195,7 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     bf16 parts[NP];
-                    split_bf16<NP>((float)x[j], parts);
+                    split_bf16<NP>((float)x[j] * a.sign, parts);
 #pragma unroll
                     for (int p = 0; p < NP; ++p) f[p][j] = parts[p];
                 }
@@ -271,20 +274,21 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
         const bool whole = full && here >= 0 && tok + PAGE - 1 <= pos_min &&
                            (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
         float top = NEG_INF;
+        if (!whole) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = tok + 16 * g + 4 * t + e;
+                    const bool see = (here >= 0) & (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
+                    sc[t][e] = see ? sc[t][e] : NEG_INF;
+                }
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float y = sc[t][e] * a.scale2;
-                if (!whole) {
-                    const int j = tok + 16 * g + 4 * t + e;
-                    const bool see = (here >= 0) & (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
-                    y = see ? y : NEG_INF;
-                }
-                sc[t][e] = y;
-                top = fmaxf(top, y);
-            }
-        top = group_max(top);
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][e]);
+        top = group_max(top) * a.scale2;
         if (__any(top > mx + SLACK)) {
             top = fmaxf(top, mx);
             const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
@@ -299,7 +303,7 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float p = __builtin_amdgcn_exp2f(sc[t][e] - ref);
+                const float p = __builtin_amdgcn_exp2f(fmaf(sc[t][e], a.scale2, -ref));
                 sum += p;
                 bf16 parts[NP];
                 split_bf16<NP>(p, parts);
@@ -422,28 +426,32 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
     }
 }
 
-// Many rows of one kv head against its sequence (a segment or a prompt):
-// 128 rows per workgroup, 32 per wave, on the 32x32x16 matrix instruction.
-// Every wave needs every page, so the page's codes are converted to bf16 once
-// per workgroup, into LDS (two buffers: the next page is loaded over the
-// present one's products and stored into the other buffer, one barrier per
-// page); rows of D + 8 and 64 + 8 elements keep the 16-byte operand reads off
+// Many rows of one kv head against its sequence (a segment or a prompt): 32
+// rows per wave, on the 32x32x16 matrix instruction.  Every row tile needs
+// every page, so the pages' codes are converted to bf16 once per workgroup,
+// into LDS (two buffers: the next pages are loaded over the present ones'
+// products and stored into the other buffer, one barrier per step); rows of D + 8 and 64 + 8 elements keep the 16-byte operand reads off
 // each other's banks.  The transposed scores' layout (lane group h of 2 holds
 // rows 8 a + 4 h + b) is again made the second product's operand by the order
 // in which rows of K are fed: row 8 a + 4 h + b of a 32-token tile is token
 // 16 (a / 2) + 8 h + 4 (a % 2) + b, so a lane ends up with runs of 8 tokens.
+//
+// KW waves share a row tile and take a page each of the KW that a step holds;
+// they are joined in LDS at the end.  Large calls take KW = 1 (128 rows of
+// four waves; the sequence in several ranges where the tiles do not fill the
+// chip); a window's few tiles take eight waves and KW = 2 or 4, which walks
+// the sequence in fewer steps without a second launch.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr int TILE_ROWS = 128;
-
-template <class T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attend_tiles_kernel(AttendArgs a) {
+template <class T, int D, int WAVES, int KW>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attend_tiles_kernel(AttendArgs a) {
     constexpr int NP = sizeof(T) == 4 ? 3 : 1;
-    constexpr int KS = D + 8, VS = PAGE + 8;            // LDS row distances
-    constexpr int PIECES = 4 * D, NK = (PIECES + 255) / 256;   // 16-byte pieces of a page's keys (and of its values)
-    __shared__ __align__(16) bf16 kb[2][PAGE * KS];
-    __shared__ __align__(16) bf16 vb[2][D * VS];
+    constexpr int THREADS = 64 * WAVES, TILE_ROWS = 32 * WAVES / KW;
+    constexpr int KS = D + 8, VS = PAGE + 8, KB = PAGE * KS, VB = D * VS;   // LDS row and page distances
+    constexpr int PP = 4 * D, PIECES = KW * PP, NK = (PIECES + THREADS - 1) / THREADS;   // 16-byte pieces of the keys
+    __shared__ __align__(16) bf16 kv[2][KW * (KB + VB)];
     const CacheView& c = a.c;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 31, g = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, g = lane >> 5;
+    const int w = uniform(tid >> 6), kw = w % KW;
     // heads innermost: with a multiple of 8 of them, the workgroups that read
     // the same pages stand on one XCD and share its L2
     const int h = blockIdx.x % c.H, x = blockIdx.x / c.H, b = blockIdx.z;
@@ -457,7 +465,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
     const int p_begin = min(split * tl.per, span.n), p_end = min(p_begin + tl.per, span.n);
 
     // this wave's rows, and what all of them and any of them see
-    const int wr0 = row0 + 32 * w, r = wr0 + m, HG = c.H * a.G;
+    const int wr0 = row0 + 32 * (w / KW), r = wr0 + m, HG = c.H * a.G;
     const bool live_row = r < rows;
     const int pos = live_row ? first + r / a.G : -1;
     const int w_min = first + wr0 / a.G, w_max = wr0 < rows ? first + (min(rows, wr0 + 32) - 1) / a.G : -1;
@@ -473,7 +481,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     bf16 parts[NP];
-                    split_bf16<NP>((float)x[j], parts);
+                    split_bf16<NP>((float)x[j] * a.sign, parts);
 #pragma unroll
                     for (int z = 0; z < NP; ++z) qf[st][z][j] = parts[z];
                 }
@@ -491,67 +499,73 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
     float mx = NEG_INF, sum = 0.f;
 
     uint4 kr[NK], vr[NK];
-    uint2 scales = {0, 0};
+    uint2 scales[NK];
     int ids = -1;   // table entries of 64 of the range's pages, one a lane
-    auto page_of = [&](int i) {
-        const int k = (i - p_begin) & 63;
-        if (k == 0) ids = i + lane < p_end ? c.page_at(s, span.at(i + lane)) : -1;
-        const int page = i < p_end ? __builtin_amdgcn_readlane(ids, k) : -1;
-        return c.page_ok(page) ? page : -1;
-    };
-    auto load = [&](int page) {
-        if (page < 0) return;
-        const size_t at = c.head_at(page, h);
-        const uint4* k = reinterpret_cast<const uint4*>(c.k + at * PAGE * D);
-        const uint4* v = reinterpret_cast<const uint4*>(c.v + at * PAGE * D);
-        scales = *reinterpret_cast<const uint2*>(c.scales + at * 8);
-#pragma unroll
-        for (int n = 0; n < NK; ++n) {
-            const int p = tid + 256 * n;
-            if (PIECES % 256 == 0 || p < PIECES) {
-                kr[n] = k[p];
-                vr[n] = v[p];
-            }
+    auto turn = [&](int n) {   // to the 64 entries that hold the range's page n, a multiple of KW
+        if ((n & 63) == 0) {
+            const int i = p_begin + n + lane;
+            const int page = i < p_end ? c.page_at(s, span.at(i)) : -1;
+            ids = c.page_ok(page) ? page : -1;
         }
     };
-    auto stage = [&](int buf, int tok) {
+    auto load = [&](int n) {
 #pragma unroll
-        for (int n = 0; n < NK; ++n) {
-            const int p = tid + 256 * n;
-            if (PIECES % 256 != 0 && p >= PIECES) continue;
+        for (int z = 0; z < NK; ++z) {
+            const int q = tid + THREADS * z, pk = q / PP, p = q % PP;
+            if (PIECES % THREADS != 0 && q >= PIECES) continue;
+            const int page = KW == 1 ? __builtin_amdgcn_readlane(ids, n & 63) : __shfl(ids, (n + pk) & 63, 64);
+            if (page < 0) continue;
+            const size_t at = c.head_at(page, h);
+            kr[z] = reinterpret_cast<const uint4*>(c.k + at * PAGE * D)[p];
+            vr[z] = reinterpret_cast<const uint4*>(c.v + at * PAGE * D)[p];
+            scales[z] = *reinterpret_cast<const uint2*>(c.scales + at * 8);
+        }
+    };
+    auto stage = [&](int buf, int n) {
+#pragma unroll
+        for (int z = 0; z < NK; ++z) {
+            const int q = tid + THREADS * z, pk = q / PP, p = q % PP;
+            if (PIECES % THREADS != 0 && q >= PIECES) continue;
+            const int tok = span.at(p_begin + n + pk) * PAGE;
             const int t = p / (D / 16), col = p % (D / 16) * 16;
-            const float ks = scale_of((unsigned char)(scales.x >> (8 * (t >> 4))));
-            bf16* kd = &kb[buf][t * KS + col];
-            *reinterpret_cast<bf16x8*>(kd) = operand8(kr[n].x, kr[n].y, ks);
-            *reinterpret_cast<bf16x8*>(kd + 8) = operand8(kr[n].z, kr[n].w, ks);
+            const float ks = scale_of((unsigned char)(scales[z].x >> (8 * (t >> 4))));
+            bf16* kd = &kv[buf][pk * KB + t * KS + col];
+            *reinterpret_cast<bf16x8*>(kd) = operand8(kr[z].x, kr[z].y, ks);
+            *reinterpret_cast<bf16x8*>(kd + 8) = operand8(kr[z].z, kr[z].w, ks);
             const int dim = p >> 2, quarter = p & 3;
             const int live = len - tok - 16 * quarter;   // tokens of the piece within the sequence
-            float vs = scale_of((unsigned char)(scales.y >> (8 * quarter)));
-            uint4 x = vr[n];
+            float vs = scale_of((unsigned char)(scales[z].y >> (8 * quarter)));
+            uint4 x = vr[z];
             if (live < 16) {   // behind the end the page holds anything, NaN codes too
                 unsigned* xw = reinterpret_cast<unsigned*>(&x);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int k4 = min(max(live - 4 * z, 0), 4);
-                    xw[z] &= k4 == 4 ? ~0u : (1u << (8 * k4)) - 1;
+                for (int y = 0; y < 4; ++y) {
+                    const int k4 = min(max(live - 4 * y, 0), 4);
+                    xw[y] &= k4 == 4 ? ~0u : (1u << (8 * k4)) - 1;
                 }
                 if (live <= 0) vs = 1.f;
             }
-            bf16* vd = &vb[buf][dim * VS + quarter * 16];
+            bf16* vd = &kv[buf][KW * KB + pk * VB + dim * VS + quarter * 16];
             *reinterpret_cast<bf16x8*>(vd) = operand8(x.x, x.y, vs);
             *reinterpret_cast<bf16x8*>(vd + 8) = operand8(x.z, x.w, vs);
         }
     };
     const int tau = 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);   // token of row m of a tile
 
-    int page = page_of(p_begin);
-    load(page);
-    if (page >= 0) stage(0, span.at(p_begin) * PAGE);
+    turn(0);
+    load(0);
+    stage(0, 0);
     __syncthreads();
-    for (int i = p_begin; i < p_end; ++i) {
-        const int buf = (i - p_begin) & 1, tok = span.at(i) * PAGE;
-        const int next = page_of(i + 1);
-        load(next);
+    for (int n = 0; n < p_end - p_begin; n += KW) {
+        const int buf = (n / KW) & 1, tok = span.at(p_begin + n + kw) * PAGE;
+        const int page = __builtin_amdgcn_readlane(ids, (n + kw) & 63);
+        const bool more = n + KW < p_end - p_begin;
+        if (more) {
+            turn(n + KW);
+            load(n + KW);
+        }
+        const bf16* kb = &kv[buf][kw * KB];
+        const bf16* vb = &kv[buf][KW * KB + kw * VB];
         // nothing of the page in sight of the wave's rows: its products are skipped
         const bool seen = page >= 0 && tok <= w_max &&
                           (a.window == 0 || tok + PAGE - 1 > w_min - a.window || tok < a.sink);
@@ -565,7 +579,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
             for (int st = 0; st < D / 16; ++st)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&kb[buf][(t * 32 + tau) * KS + 16 * st + 8 * g]);
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&kb[(t * 32 + tau) * KS + 16 * st + 8 * g]);
 #pragma unroll
                     for (int z = 0; z < NP; ++z)
                         sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st][z], sc[t], 0, 0, 0);
@@ -580,19 +594,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
                     for (int e = 0; e < 16; ++e) {
                         const int j = tok + 32 * t + 16 * (e >> 3) + 8 * g + (e & 7);
                         const bool see = (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
-                        sc[t][e] = see ? sc[t][e] * a.scale2 : NEG_INF;
-                        top = fmaxf(top, sc[t][e]);
-                    }
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        sc[t][e] *= a.scale2;
-                        top = fmaxf(top, sc[t][e]);
+                        sc[t][e] = see ? sc[t][e] : NEG_INF;
                     }
             }
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[t][e]);
+            top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.scale2;
             if (__any(top > mx + SLACK)) {
                 top = fmaxf(top, mx);
                 const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
@@ -607,7 +616,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(sc[t][e] - ref);
+                    const float p = __builtin_amdgcn_exp2f(fmaf(sc[t][e], a.scale2, -ref));
                     sum += p;
                     bf16 parts[NP];
                     split_bf16<NP>(p, parts);
@@ -618,18 +627,64 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
             for (int u = 0; u < D / 32; ++u)
 #pragma unroll
                 for (int k4 = 0; k4 < 4; ++k4) {
-                    const bf16x8 vf = *reinterpret_cast<const bf16x8*>(&vb[buf][(32 * u + m) * VS + 16 * k4 + 8 * g]);
+                    const bf16x8 vf = *reinterpret_cast<const bf16x8*>(&vb[(32 * u + m) * VS + 16 * k4 + 8 * g]);
 #pragma unroll
                     for (int z = 0; z < NP; ++z)
                         o[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[k4][z], o[u], 0, 0, 0);
                 }
         }
-        if (next >= 0) stage(buf ^ 1, span.at(i + 1) * PAGE);
+        if (more) stage(buf ^ 1, n + KW);
         __syncthreads();
-        page = next;
     }
-    if (!live_row) return;
     sum += __shfl_xor(sum, 32, 64);
+    if constexpr (KW > 1) {   // join the waves of a row tile, in the pages' place
+        float* ml = reinterpret_cast<float*>(kv);            // [WAVES][32][2]
+        float* acc = ml + WAVES * 64;                        // [WAVES / 2][32][D + 4]
+        static_assert(sizeof(kv) >= 4 * (WAVES * 64 + WAVES / 2 * 32 * (D + 4)), "the join fits the pages' place");
+        if (g == 0) {
+            ml[(w * 32 + m) * 2] = mx;
+            ml[(w * 32 + m) * 2 + 1] = sum;
+        }
+        __syncthreads();
+        const int w0 = w / KW * KW;
+        float top = NEG_INF, total = 0.f;
+#pragma unroll
+        for (int z = 0; z < KW; ++z) top = fmaxf(top, ml[((w0 + z) * 32 + m) * 2]);
+        const float ref = top == NEG_INF ? 0.f : top;
+#pragma unroll
+        for (int z = 0; z < KW; ++z)
+            total += ml[((w0 + z) * 32 + m) * 2 + 1] * __builtin_amdgcn_exp2f(ml[((w0 + z) * 32 + m) * 2] - ref);
+        const float by = __builtin_amdgcn_exp2f(mx - ref);
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) o[u] *= by;
+        mx = top;
+        sum = total;
+#pragma unroll
+        for (int half = KW / 2; half >= 1; half /= 2) {
+            float* at = acc + ((w / KW * (KW / 2) + kw % half) * 32 + m) * (D + 4) + 4 * g;
+            if (kw >= half && kw < 2 * half) {
+#pragma unroll
+                for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        *reinterpret_cast<f32x4*>(at + 32 * u + 8 * z) =
+                            f32x4{o[u][4 * z], o[u][4 * z + 1], o[u][4 * z + 2], o[u][4 * z + 3]};
+            }
+            __syncthreads();
+            if (kw < half) {
+#pragma unroll
+                for (int u = 0; u < D / 32; ++u)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const f32x4 y = *reinterpret_cast<const f32x4*>(at + 32 * u + 8 * z);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[u][4 * z + e] += y[e];
+                    }
+            }
+            __syncthreads();
+        }
+    }
+    if (!live_row || kw != 0) return;
     if (tl.ranges == 1) {
         const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
         typedef T Four __attribute__((ext_vector_type(4)));
@@ -657,6 +712,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void atten
         }
     }
 }
+
+// One launch instead of ranges: head widths and pages up to which single
+// tokens take it.
+constexpr int ONE_DIM = 128, ONE_PAGES = 24;
 
 // Joins the ranges of a row, D / 4 lanes per range so that several are read
 // at a time: a workgroup per row where there are many ranges, else a wave.
@@ -706,49 +765,69 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
     }
 }
 
-constexpr int ONE_DIM = 128, ONE_PAGES = 24;
 // How a call is launched: which kernel, how many tiles of rows, and into how
 // many ranges the sequences are divided.
 struct AttendPlan {
-    bool wide;   // attend_tiles_kernel (128 rows a tile), else attend_rows_kernel (16 wr)
-    int wr, waves, tile_rows, tiles, splits, least;
+    bool wide;       // attend_tiles_kernel, else attend_rows_kernel
+    int wr, kw;      // its WR, or KW
+    int waves, tile_rows, tiles, splits, least;
 };
-static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool f32) {
+static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool divided) {
     AttendPlan p;
-    const long rows = (long)n_tokens * (heads / c->H);
+    const long rows = (long)n_tokens * (heads / c->H), pages = (max_len + PAGE - 1) / PAGE;
     p.wide = rows > 64;
     p.wr = rows > 32 ? 4 : rows > 16 ? 2 : 1;
-    p.tile_rows = p.wide ? TILE_ROWS : 16 * p.wr;
-    p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
-    const long pages = (max_len + PAGE - 1) / PAGE, groups = (long)batch * c->H * p.tiles;
-    // Short sequences (a window's) in one range of eight waves, where the
-    // registers allow eight: one launch instead of two
+    p.kw = 1;
     p.waves = 4;
-    if (!p.wide && p.wr == 1 && c->d <= ONE_DIM && pages <= ONE_PAGES) {
-        p.waves = 8;
-        p.splits = 1;
-        p.least = 1 << 20;
-        return p;
-    }
-    // workgroups in flight: as many as the registers and LDS of a compute unit
-    // take (tiles), or several rounds of them, which even out ragged lengths
-    const int slots = 256 * (c->d <= 64 ? (f32 ? 2 : 3) : c->d <= 128 && !f32 ? 2 : 1);
-    // pages of a range: two a wave while the chip is not full, more as soon as
-    // it is (every range costs a start and a place in the join)
+    p.tile_rows = p.wide ? 128 : 16 * p.wr;
+    p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
+    const long groups = (long)batch * c->H * p.tiles;
+    // Workgroups: as many as the compute units take at a time (tiles), or
+    // several rounds of them, which even out ragged lengths (rows: 48
+    // sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with
+    // 1024 workgroups, 289 us with 8192).  Pages of a range: four (tiles); two
+    // a wave while the chip is not full, more as soon as it is, since every
+    // range costs a start and a place in the join.
     const long eights = groups * ((pages + 7) / 8);
     p.least = p.wide ? 4 : eights <= 1024 ? 8 : eights <= 4096 ? 16 : 32;
-    long s = (p.wide ? slots : 8192) / groups;
     const long most = (pages + p.least - 1) / p.least;
+    long s = (p.wide ? (c->d <= 128 ? 512 : 256) : 8192) / groups;
     if (s > most) s = most;
     if (s > 256) s = 256;
     p.splits = s < 1 ? 1 : (int)s;
+    if (divided) return p;
+    // One launch of eight waves, which share the sequence among them, instead
+    // of ranges and their join (registers and LDS allow it up to width 128).
+    // Rows: up to 24 pages (2 x 6 heads of 64, 500 tokens: 8.7 us against 12.1,
+    // 2064 tokens: the same).  Tiles: counted in page steps, a step of KW pages
+    // at 1.6 of one page's and a join at 8 steps of width 64 and 6 of width
+    // 128 (2 x 1024 queries of 6 heads of 64 over 2064 tokens: 24.7 us against
+    // 30.4; 2 x 512 queries of 8 heads on 2 of 128 over 4000: 78 against 43).
+    if (c->d > ONE_DIM) return p;
+    if (!p.wide) {
+        if (p.wr > 1 || pages > ONE_PAGES) return p;
+        p.waves = 8;
+    } else {
+        const int kw = c->d <= 64 ? 4 : 2, tile = 256 / kw;
+        const long tiles = (rows + tile - 1) / tile, rounds = ((long)batch * c->H * tiles + 255) / 256;
+        const long here = rounds * ((pages + kw - 1) / kw) * 16;
+        const long there = ((pages + p.splits - 1) / p.splits + (p.splits > 1 ? (c->d <= 64 ? 8 : 6) : 0)) * 10 *
+                           ((groups + 511) / 512);
+        if (here > there) return p;
+        p.waves = 8;
+        p.kw = kw;
+        p.tile_rows = tile;
+        p.tiles = (int)tiles;
+    }
+    p.splits = 1;
+    p.least = 1 << 20;
     return p;
 }
 
 size_t attend_workspace(const tm_cache* c, int batch, int n_tokens, int heads) {
     if (heads % c->H != 0 || batch == 0 || n_tokens == 0) return 0;
-    // the most ranges that any max_len and either type lead to
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, (long)c->seq_pages * PAGE, false);
+    // the most ranges that any max_len leads to
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, (long)c->seq_pages * PAGE, true);
     if (p.splits == 1) return 0;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * (heads / c->H);
     return (rows * (c->d + 2) * 4 + 511) / 256 * 256;
@@ -760,7 +839,13 @@ static hipError_t launch_attend(const tm_cache* c, const AttendArgs& a, const At
         return for_head_dim(c->d, [&](auto D) {
             if (p.wide) {
                 const dim3 grid((unsigned)(p.tiles * p.splits * c->H), 1, (unsigned)a.B);
-                launch_k(attend_tiles_kernel<T, D()>, grid, dim3(256), 0, st, a);
+                if constexpr (D() <= 128) {
+                    if (p.kw > 1) {
+                        launch_k(attend_tiles_kernel<T, D(), 8, D() <= 64 ? 4 : 2>, grid, dim3(512), 0, st, a);
+                        return hipGetLastError();
+                    }
+                }
+                launch_k(attend_tiles_kernel<T, D(), 4, 1>, grid, dim3(256), 0, st, a);
                 return hipGetLastError();
             }
             const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c->H, (unsigned)a.B);
@@ -807,14 +892,14 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
     if (batch > 65535 || (!seqs && batch > c->n_seqs) || n_tokens > 1 << 24 || (uintptr_t)seqs % 4 || (uintptr_t)counts % 4 ||
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most, dtype == TM_F32);
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most, false);
     if ((long)p.tiles * p.splits * c->H > 0x7fffffffL) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
     const int G = heads / c->H;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * G;
     float* part = static_cast<float*>(workspace);
     AttendArgs a{cache_view(c, const_cast<void*>(blob)), seqs, counts, q, q_batch, q_token, out, batch, n_tokens, G,
-                 score_scale * 1.44269504088896340736f, window, sink < most ? sink : (int)most, p.splits, p.least, p.tile_rows, part, part + rows * c->d};
+                 fmaxf(fabsf(score_scale) * 1.44269504088896340736f, 1.2e-38f), score_scale < 0 ? -1.f : 1.f, window, sink < most ? sink : (int)most, p.splits, p.least, p.tile_rows, part, part + rows * c->d};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == TM_F32 ? launch_attend<float>(c, a, p, st) : launch_attend<bf16>(c, a, p, st);
     return e == hipSuccess ? TM_OK : TM_ERR_HIP;

@@ -324,6 +324,18 @@ def test_attend(case, max_len):
     expect(p.g, p.m, seqs, q, counts, scale, window, sink, out, before)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, -1e-42])
+@pytest.mark.parametrize("dtype,N", [(BF, 3), (F32, 2), (BF, 40), (F32, 40)])
+def test_attend_scales(dtype, N, scale):
+    """No scale (the mean of what is seen), a negative and a tiny one; masked
+    tokens stay out of it."""
+    p = Pair(1, 64, 10, 2, 4, dtype, seed=12)
+    p.append([0, 1], 150, [150, 70])
+    q, _ = normal((2, N, 3, 64), 6, dtype)
+    out = p.g.attend(ints([0, 1]), q, scale=scale, window=60, sink=4)
+    expect(p.g, p.m, [0, 1], q, None, scale, 60, 4, out, out)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_attend_long_and_divided(dtype):
     """A sequence over many ranges, and the same sequence listed twice."""
