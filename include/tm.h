@@ -259,8 +259,9 @@ tm_status tm_project(const tm_ctx* ctx, const void* x, int model_dim, const void
  * output y is written into the memory (tm_project of y, then tm_store) and
  * gates the final output through the memory's read of it (tm_retrieve of y's
  * queries after the write).  Attention and the persistent tokens' values are
- * the caller's.  These two calls are the wiring the memory's own calls do
- * not cover; both only move and multiply elements.
+ * the caller's (tm_attention.h has an attention over a cache of the window).
+ * These two calls are the wiring the memory's own calls do not cover; both
+ * only move and multiply elements.
  *
  * tm_mac_window: window [batch][n_persist + 2 seg_len][model_dim] (dtype) =
  *   persistent [n_persist][model_dim] (dtype; shared over the batch), then

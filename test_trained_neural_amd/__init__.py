@@ -476,7 +476,7 @@ def mac_segment(mem, state, x, persistent, attention, w_kvq, conv, w_gate, gate_
     marshalling over the C calls).  x [B][S][D] (D = heads * dim; S a
     multiple of the chunk) is the segment's model vectors; ``attention`` is
     the caller's: window [B][P+2S][D] (x's dtype) -> y [B][S][D] for the
-    segment's positions, x's dtype.  The segment's queries (projections of x)
+    segment's positions, x's dtype (``WindowAttention`` is one).  The segment's queries (projections of x)
     read the memory before the segment is written; y is written (its keys,
     values and gates from the same projections) and read back through its
     queries to gate y.  Returns (out [B][S][D] fp32, state).  hist_x, hist_y:
@@ -579,5 +579,5 @@ class NeuralMemory:
 # the attention window's operators (include/tm_attention.h)
 from .attention import (TM_CACHE_BAD_ENTRY, TM_CACHE_BLOCK, TM_CACHE_FULL, TM_CACHE_NO_PAGES,  # noqa: E402,F401
                         TM_CACHE_NONFINITE, TM_CACHE_PAGE, TM_ROPE_BASE, TM_ROPE_HALF, TM_ROPE_INTERLEAVED,
-                        TM_ROPE_LINEAR, TM_ROPE_NONE, TM_ROPE_PARTS, PagedCache, Rotary, tm_rotary,
-                        tm_rotary_frequencies)
+                        TM_ROPE_LINEAR, TM_ROPE_NONE, TM_ROPE_PARTS, PagedCache, Rotary, WindowAttention,
+                        tm_rotary, tm_rotary_frequencies)

@@ -423,3 +423,100 @@ class PagedCache:
         with _Device(self.device, stream) as st:
             self._call("tm_cache_check", st, ctypes.byref(f), ctypes.byref(n))
         return int(f.value), int(n.value)
+
+
+class WindowAttention:
+    """The attention of ``mac_segment``'s window, for whole segments and for
+    the single tokens that follow: grouped-query attention with rotary
+    positions over a paged 8-bit cache.
+
+    w_qkv [(heads + 2 kv_heads) d][D] and w_out [D][heads d] (PyTorch's Linear
+    layout, bf16 or fp32) project the window's vectors and the result; the
+    projections are plain products.  ``persistent`` [P][D] are the window's
+    first rows, the same for every sequence and segment: their keys and
+    values are written once, into a sequence of their own that each segment's
+    sequences fork, so they share its pages.  ``batch`` sequences of up to
+    ``max_tokens`` window tokens behind the persistent ones; ``rotary``
+    rotates queries and keys by their place in the window (None: no
+    positions).
+
+    ``attention(window)`` takes [B][P + 2 S][D] (its first P rows are
+    ``persistent``) and returns the attention output [B][S][D] for the
+    segment's S rows; the window stays in the cache.  ``attention.token(x)``
+    then takes the next tokens' vectors [B][n][D], behind what the cache
+    holds, and returns theirs."""
+
+    def __init__(self, w_qkv, w_out, heads, kv_heads, batch, max_tokens, persistent=None, rotary=None):
+        D, d = w_out.shape[0], w_out.shape[1] // heads
+        T._shape("w_out", w_out, (D, heads * d))
+        T._shape("w_qkv", w_qkv, ((heads + 2 * kv_heads) * d, D))
+        T._same(w_qkv.dtype, ("w_out", w_out), ("persistent", persistent))
+        self.P = 0 if persistent is None else persistent.shape[0]
+        T._shape("persistent", persistent, (self.P, D))
+        if max_tokens < 1 or batch < 1:
+            raise ValueError("batch and max_tokens must be positive")
+        self.w_qkv, self.w_out, self.heads, self.kv_heads, self.head_dim = w_qkv, w_out, heads, kv_heads, d
+        self.batch, self.max_tokens, self.rotary, self.persistent = batch, max_tokens, rotary, persistent
+        dev = w_qkv.device
+        up = lambda n: -(-n // TM_CACHE_PAGE)  # noqa: E731
+        pages = up(self.P + max_tokens)
+        self.cache = PagedCache(kv_heads, d, up(self.P) + batch * (pages - self.P // TM_CACHE_PAGE), batch + 1, pages,
+                                device=dev)
+        self._slots = torch.arange(batch, dtype=torch.int32, device=dev)
+        self._root = torch.full((batch,), batch, dtype=torch.int32, device=dev)
+        self._held = self.P   # tokens of each sequence
+        self.refresh()
+
+    def refresh(self):
+        """Starts over with the weights and persistent rows as they are now:
+        the windows are dropped, the persistent tokens written again."""
+        self.cache.free(None)
+        self._held = self.P
+        if self.P:
+            k, v = self._project(self.persistent[None], 0)[1:]
+            self.cache.append(self._root[:1], k, v)
+            self.cache.fork(self._root, self._slots)
+
+    def _project(self, x, start):
+        """Queries, keys (both rotated) and values of vectors that stand at
+        ``start`` .. of their windows: views of one projection."""
+        B, n, _ = x.shape
+        qkv = torch.nn.functional.linear(x, self.w_qkv).view(B, n, self.heads + 2 * self.kv_heads, self.head_dim)
+        q_k = qkv[:, :, :self.heads + self.kv_heads]
+        if self.rotary is not None:
+            first = torch.full((B,), start, dtype=torch.int32, device=x.device)
+            self.rotary(q_k, first, out=q_k)
+        return qkv[:, :, :self.heads], qkv[:, :, self.heads:self.heads + self.kv_heads], \
+            qkv[:, :, self.heads + self.kv_heads:]
+
+    def _read(self, q):
+        y = self.cache.attend(self._slots, q, max_len=self._held)
+        return torch.nn.functional.linear(y.flatten(2), self.w_out)
+
+    def _room(self, x, n, held):
+        if x.shape[0] != self.batch or x.shape[2] != self.w_qkv.shape[1]:
+            raise ValueError("expected [%d][tokens][%d], got %s" % (self.batch, self.w_qkv.shape[1], tuple(x.shape)))
+        if n < 1 or held + n > self.P + self.max_tokens:
+            raise ValueError("%d tokens behind %d: the window holds %d" % (n, held, self.P + self.max_tokens))
+
+    def __call__(self, window):
+        n = window.shape[1] - self.P
+        self._room(window, n, self.P)
+        if n % 2:
+            raise ValueError("a window holds %d persistent rows and as many recalled as segment rows, got %d rows"
+                             % (self.P, window.shape[1]))
+        self.cache.free(self._slots)
+        if self.P:
+            self.cache.fork(self._root, self._slots)
+        q, k, v = self._project(window[:, self.P:], self.P)
+        self.cache.append(self._slots, k, v)
+        self._held = self.P + n
+        return self._read(q[:, n // 2:])
+
+    def token(self, x):
+        n = x.shape[1]
+        self._room(x, n, self._held)
+        q, k, v = self._project(x, self._held)
+        self.cache.append(self._slots, k, v)
+        self._held += n
+        return self._read(q)
