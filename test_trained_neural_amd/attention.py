@@ -130,30 +130,24 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-class _Device:
-    """The device of a call as the current one, and its stream: ``stream``
-    (then also the one that the call's own buffers are allocated for) or the
-    device's current one."""
+def _elsewhere(index, stream):
+    """Whether a call on device ``index`` has to change the current device or
+    stream first."""
+    return stream is not None or torch._C._cuda_getDevice() != index
 
-    __slots__ = ("guard", "index")
 
-    def __init__(self, device, stream):
-        self.guard, self.index = None, device.index
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("stream is on %s, the call is on %s" % (stream.device, device))
-            self.guard = torch.cuda.stream(stream)
-        elif self.index != torch._C._cuda_getDevice():
-            self.guard = torch.cuda.device(device)
+def _there(device, stream):
+    """The device of a call as the current one, or ``stream`` as the current
+    stream (then also the one that the call's own buffers are allocated
+    for)."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream is on %s, the call is on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 # ---------------------------------------------------------------------------
@@ -181,18 +175,20 @@ def _rotary_geometry(x, y, positions, freq):
     T._shape("positions", positions, (B, N) if per_token else (B,))
     if not positions.is_contiguous() or not freq.is_contiguous() or freq.dim() != 1:
         raise ValueError("positions and freq must be contiguous")
-    return xb, xt, yb, yt, 1 if per_token else 0, (B, N, H, d, 2 * freq.shape[0]), dt
+    return (xb, xt), (yb, yt), 1 if per_token else 0, (B, N, H, d, 2 * freq.shape[0]), dt, x.device.index
 
 
 def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inverse=False, stream=None):
     """x, y [B][T][H][d] (any distances between tokens and entries; y may be
     x); positions int32 [B][T], or [B] (the first token's); freq [rot_dim / 2]
     fp64."""
-    xb, xt, yb, yt, per_token, sizes, dt = _once(
+    d_x, d_y, per_token, sizes, dt, index = _once(
         ("rotary", _look(x), _look(y), _look(positions), _look(freq)), lambda: _rotary_geometry(x, y, positions, freq))
-    with _Device(x.device, stream) as st:
-        rc = _lib().tm_rotary(x.data_ptr(), xb, xt, y.data_ptr(), yb, yt, positions.data_ptr(), per_token,
-                              freq.data_ptr(), result_scale, *sizes, layout, 1 if inverse else 0, dt, st)
+    if _elsewhere(index, stream):
+        with _there(x.device, stream):
+            return tm_rotary(x, y, positions, freq, result_scale, layout, inverse)
+    rc = _lib().tm_rotary(x.data_ptr(), *d_x, y.data_ptr(), *d_y, positions.data_ptr(), per_token, freq.data_ptr(),
+                          result_scale, *sizes, layout, 1 if inverse else 0, dt, _raw_stream(index))
     if rc:
         T._check("tm_rotary", rc)
 
@@ -239,10 +235,10 @@ class Rotary:
     def __call__(self, x, positions, inverse=False, out=None, stream=None):
         if stream is not None:
             _on(x.device, ("x", x))
-            with _Device(x.device, stream):
+            with _there(x.device, stream):
                 return self(x, positions, inverse, out)
         if out is None:
-            out = x.new_empty(x.shape)
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
         tm_rotary(x, out, positions, self.freq, self.result_scale, self.layout, inverse)
         return out
 
@@ -267,7 +263,7 @@ class PagedCache:
         if blob.data_ptr() % 256:
             raise ValueError("blob must be 256-byte aligned")
         self.blob, self.device = blob, blob.device
-        self._h, self._b = self.handle.value, blob.data_ptr()
+        self._h, self._b, self._index = self.handle.value, blob.data_ptr(), blob.device.index
         o, cells = tm_cache_layout(self.handle), n_pages * kv_heads * TM_CACHE_PAGE * head_dim
         ints = 64 + n_seqs + n_pages + n_seqs * seq_pages
         self.meta = blob[:4 * ints].view(torch.int32)
@@ -289,8 +285,8 @@ class PagedCache:
         except Exception:
             pass
 
-    def _call(self, name, st, *args):
-        rc = getattr(_declared, name)(self._h, self._b, *args, st)
+    def _call(self, name, *args):
+        rc = getattr(_declared, name)(self._h, self._b, *args, _raw_stream(self._index))
         if rc:
             T._check(name, rc)
 
@@ -307,12 +303,18 @@ class PagedCache:
         return self.blob.new_empty(need)
 
     def init(self, stream=None):
-        with _Device(self.device, stream) as st:
-            self._call("tm_cache_init", st)
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.init()
+        self._call("tm_cache_init")
 
     def append(self, seqs, k, v, counts=None, stream=None):
         """Writes k, v [B][T][kv_heads][d] behind the sequences ``seqs``
         (int32 [B]; None: 0 ..); counts int32 [B]: tokens of each entry."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.append(seqs, k, v, counts)
+
         def check():
             dt = T._dtype_code(k)
             T._same(k.dtype, ("v", v))
@@ -323,19 +325,22 @@ class PagedCache:
             _list("seqs", seqs, B)
             _list("counts", counts, B)
             _on(self.device, ("k", k), ("v", v), ("seqs", seqs), ("counts", counts))
-            return d_k, d_v, B, N, dt
+            return d_k, d_v, (B, N, dt)
 
-        d_k, d_v, B, N, dt = _once((self._kind, "append", _look(k), _look(v), _look(seqs), _look(counts)), check)
-        pk, pv = _aligned("k", k.data_ptr()), _aligned("v", v.data_ptr())
-        with _Device(self.device, stream) as st:
-            ws = self._workspace(B, N, 0)
-            self._call("tm_cache_append", st, _at(seqs), _at(counts), pk, *d_k, pv, *d_v, B, N, dt, ws.data_ptr())
+        d_k, d_v, sizes = _once((self._kind, "append", _look(k), _look(v), _look(seqs), _look(counts)), check)
+        ws = self._workspace(sizes[0], sizes[1], 0)
+        self._call("tm_cache_append", _at(seqs), _at(counts), _aligned("k", k.data_ptr()), *d_k,
+                   _aligned("v", v.data_ptr()), *d_v, *sizes, ws.data_ptr())
 
     def attend(self, seqs, q, counts=None, scale=None, window=0, sink=0, max_len=0, out=None, stream=None):
         """Attention of q [B][T][heads][d], each sequence's last tokens
         (``counts`` of them), over the cache; scale: 1 / sqrt(d) by default.
         Returns [B][T][heads][d] of q's type.  Rows behind an entry's count
         are left as they were: zeros in a new output."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.attend(seqs, q, counts, scale, window, sink, max_len, out)
+
         def check():
             dt = T._dtype_code(q)
             d_q = _heads_of("q", q)
@@ -349,41 +354,45 @@ class PagedCache:
                 T._shape("out", out, q.shape)
                 if not out.is_contiguous():
                     raise ValueError("out must be contiguous")
-            return d_q, B, N, H, dt
+            return d_q, (B, N, H), dt
 
-        d_q, B, N, H, dt = _once((self._kind, "attend", _look(q), _look(seqs), _look(counts), _look(out)), check)
+        d_q, sizes, dt = _once((self._kind, "attend", _look(q), _look(seqs), _look(counts), _look(out)), check)
         pq = _aligned("q", q.data_ptr())
-        with _Device(self.device, stream) as st:
-            if out is None:
-                out = q.new_empty(q.shape) if counts is None else q.new_zeros(q.shape)
-            ws = self._workspace(B, N, H)
-            self._call("tm_cache_attend", st, _at(seqs), _at(counts), pq, *d_q, out.data_ptr(), B, N, H,
-                       self._scale if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
+        if out is None:
+            out = (torch.empty_like if counts is None else torch.zeros_like)(q, memory_format=torch.contiguous_format)
+        ws = self._workspace(*sizes)
+        self._call("tm_cache_attend", _at(seqs), _at(counts), pq, *d_q, out.data_ptr(), *sizes,
+                   self._scale if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
         return out
 
     def read(self, seqs, start, n_tokens, dtype=torch.float32, k=None, v=None, stream=None):
         """(k, v) [B][n_tokens][kv_heads][d]: the values that the tokens
         start .. of each sequence are held as; rows behind a sequence's end
         are left as they were (zeros in new outputs)."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.read(seqs, start, n_tokens, dtype, k, v)
         B = self.n_seqs if seqs is None else seqs.shape[0]
         shape = (B, n_tokens, self.kv_heads, self.head_dim)
         _list("seqs", seqs, B)
-        with _Device(self.device, stream) as st:
-            k = torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
-            v = torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
-            dt = T._dtype_code(k)
-            T._same(k.dtype, ("v", v))
-            T._shape("k", k, shape)
-            T._shape("v", v, shape)
-            if not k.is_contiguous() or not v.is_contiguous():
-                raise ValueError("k and v must be contiguous")
-            _on(self.device, ("k", k), ("v", v), ("seqs", seqs))
-            self._call("tm_cache_read", st, _at(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
+        k = torch.zeros(shape, dtype=dtype, device=self.device) if k is None else k
+        v = torch.zeros(shape, dtype=dtype, device=self.device) if v is None else v
+        dt = T._dtype_code(k)
+        T._same(k.dtype, ("v", v))
+        T._shape("k", k, shape)
+        T._shape("v", v, shape)
+        if not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("k and v must be contiguous")
+        _on(self.device, ("k", k), ("v", v), ("seqs", seqs))
+        self._call("tm_cache_read", _at(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
         return k, v
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] (empty) becomes a copy of src[i] that shares its
         pages (int32 [n] each)."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.fork(src, dst)
         n = src.shape[0]
 
         def check():
@@ -393,12 +402,14 @@ class PagedCache:
             return True
 
         _once((self._kind, "fork", _look(src), _look(dst)), check)
-        with _Device(self.device, stream) as st:
-            self._call("tm_cache_fork", st, src.data_ptr(), dst.data_ptr(), n)
+        self._call("tm_cache_fork", src.data_ptr(), dst.data_ptr(), n)
 
     def free(self, seqs, keep=None, stream=None):
         """Drops all tokens of the sequences, or those behind the first
         keep[i] (int32 [n] each; seqs None: 0 .. n_seqs - 1)."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.free(seqs, keep)
         n = self.n_seqs if seqs is None else seqs.shape[0]
 
         def check():
@@ -408,20 +419,23 @@ class PagedCache:
             return True
 
         _once((self._kind, "free", n, _look(seqs), _look(keep)), check)
-        with _Device(self.device, stream) as st:
-            self._call("tm_cache_free", st, _at(seqs), _at(keep), n)
+        self._call("tm_cache_free", _at(seqs), _at(keep), n)
 
     def compact(self, stream=None):
         """Moves the pages in use to the lowest numbers."""
-        with _Device(self.device, stream) as st:
-            ws = self._workspace(0, 0, 0)
-            self._call("tm_cache_compact", st, ws.data_ptr())
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.compact()
+        ws = self._workspace(0, 0, 0)
+        self._call("tm_cache_compact", ws.data_ptr())
 
     def check(self, stream=None):
         """(sticky flags, pages in use); waits for the stream."""
+        if _elsewhere(self._index, stream):
+            with _there(self.device, stream):
+                return self.check()
         f, n = _i(0), _i(0)
-        with _Device(self.device, stream) as st:
-            self._call("tm_cache_check", st, ctypes.byref(f), ctypes.byref(n))
+        self._call("tm_cache_check", ctypes.byref(f), ctypes.byref(n))
         return int(f.value), int(n.value)
 
 
