@@ -153,38 +153,47 @@ __device__ __forceinline__ float group_sum(float x) {
     return x + __shfl_xor(x, 32, 64);
 }
 
-// Few rows of one kv head against its sequence (single tokens, drafts): WR
-// tiles of 16 rows per workgroup (row r = i G + g: query token i, head g of
-// the group).  Wave w takes row tile w % WR and every (WAVES / WR)-th page of
-// the workgroup's range; the waves of a tile are joined in LDS at the end.  With
+// Few rows of one kv head against its sequence (single tokens, drafts): RT
+// tiles of 16 rows per wave (row r = i G + g: query token i, head g of the
+// group), which share the codes' conversion; WR such groups per workgroup.
+// Wave w takes row group w % WR and every (WAVES / WR)-th page of the
+// workgroup's range; the waves of a group are joined in LDS at the end.  With
 // one range the workgroup writes the output, otherwise its accumulators,
 // maxima and sums for combine_kernel.  Bound by reading the pages: a wave's
 // next keys and present values are in flight while it computes.
-template <class T, int D, int WR, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
+template <class T, int D, int WR, int RT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
     constexpr int NP = sizeof(T) == 4 ? 3 : 1;
-    constexpr int WP = WAVES / WR;   // waves that share a row tile
+    constexpr int WP = WAVES / WR;   // waves that share a row group
     const CacheView& c = a.c;
     const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
     const int wr = w % WR, wp = w / WR;
     const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, h = blockIdx.y, b = blockIdx.z;
-    const int s = uniform(a.seqs ? a.seqs[b] : b), row0 = (tile * WR + wr) * 16;
+    const int s = uniform(a.seqs ? a.seqs[b] : b), row0 = (tile * WR + wr) * 16 * RT;
     const Tile tl = tile_of(a, b, s, tile);
     const int rows = tl.rows, len = tl.len, pos_min = tl.pos_min, pos_max = tl.pos_max;
-    if (tile * WR * 16 >= rows || split >= tl.ranges) return;
+    if (tile * WR * RT * 16 >= rows || split >= tl.ranges) return;
     const PageSpan span = tl.span;
     const int p_begin = min(split * tl.per, span.n), p_end = min(p_begin + tl.per, span.n);
-    const bool full = row0 + 16 <= rows;
+    const bool full = row0 + 16 * RT <= rows;
 
-    // this lane's row: its queries as matrix operands, its position
-    // (three parts of them would take too many registers: in LDS, per row tile)
-    constexpr bool Q_LDS = NP > 1;
-    __shared__ bf16x8 ql[Q_LDS ? WR : 1][Q_LDS ? D / 32 * NP : 1][64];
-    bf16x8 qf[Q_LDS ? 1 : D / 32];
-    const int HG = c.H * a.G, r = row0 + m, hg = h * a.G + r % a.G;
-    const int pos = r < rows ? tl.first + r / a.G : -1;
-    {
-        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)hg * D;
+    // this lane's rows: their queries as matrix operands, their positions
+    // (too many for the registers in three parts or with wide heads: in LDS)
+    constexpr bool Q_LDS = NP > 1 || RT * D > 256;
+    constexpr int QL = Q_LDS ? WR * RT * (D / 32) * NP * 64 * 16 : 0;                   // their bytes
+    constexpr int ACC = WP > 1 ? WAVES / 2 * RT * 16 * (D + 4) * 4 : 0;                 // the join's, in their place
+    __shared__ __align__(16) unsigned char lds[QL > ACC ? QL : ACC > 16 ? ACC : 16];
+    bf16x8* ql = reinterpret_cast<bf16x8*>(lds);
+    bf16x8 qf[RT][Q_LDS ? 1 : D / 32];
+    const int HG = c.H * a.G;
+    int pos[RT];
+    auto row_of = [&](int rt) { return row0 + 16 * rt + m; };
+    auto head_of = [&](int rt) { return h * a.G + row_of(rt) % a.G; };
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = row_of(rt);
+        pos[rt] = r < rows ? tl.first + r / a.G : -1;
+        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)head_of(rt) * D;
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
             bf16x8 f[NP];
@@ -203,19 +212,24 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
             if constexpr (Q_LDS) {
                 if (wp == 0) {
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) ql[wr][st * NP + p][lane] = f[p];
+                    for (int p = 0; p < NP; ++p) ql[((wr * RT + rt) * (D / 32) * NP + st * NP + p) * 64 + lane] = f[p];
                 }
             } else {
-                qf[st] = f[0];
+                qf[rt][st] = f[0];
             }
         }
-        if constexpr (Q_LDS) __syncthreads();
     }
+    if constexpr (Q_LDS) __syncthreads();
 
-    f32x4 o[D / 16];
-    float mx = NEG_INF, sum = 0.f;
+    f32x4 o[RT][D / 16];
+    float mx[RT], sum[RT];
 #pragma unroll
-    for (int u = 0; u < D / 16; ++u) o[u] = f32x4{0, 0, 0, 0};
+    for (int rt = 0; rt < RT; ++rt) {
+        mx[rt] = NEG_INF;
+        sum[rt] = 0.f;
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) o[rt][u] = f32x4{0, 0, 0, 0};
+    }
 
     // Table entries of this wave's next 64 pages, one a lane, read ahead of the
     // codes: a load behind them would be waited for together with them.
@@ -247,10 +261,14 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
     // one page's step; `then` starts loads as soon as the keys are used up
     auto step = [&](Codes& x, int i, int here, auto&& then) {
         // scores, transposed: lane's row m, tokens 16 g + 4 t + e
-        f32x4 sc[4];
+        f32x4 sc[RT][4];
         const float ks = scale_of(x.ks);
+        int ql_lane = lane;   // hidden from the optimizer, which would lift the queries' reads into registers
+        if constexpr (Q_LDS) asm volatile("" : "+v"(ql_lane));
 #pragma unroll
-        for (int t = 0; t < 4; ++t) sc[t] = f32x4{0, 0, 0, 0};
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) sc[rt][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
             bf16x8 kf[4];
@@ -260,56 +278,62 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
                 kf[t] = st & 1 ? operand8(y.z, y.w, ks) : operand8(y.x, y.y, ks);
             }
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                bf16x8 f;
-                if constexpr (Q_LDS) f = ql[wr][st * NP + p][lane];
-                else f = qf[st];
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) mma(sc[t], kf[t], f);
-            }
+                for (int p = 0; p < NP; ++p) {
+                    bf16x8 f;
+                    if constexpr (Q_LDS) f = ql[((wr * RT + rt) * (D / 32) * NP + st * NP + p) * 64 + ql_lane];
+                    else f = qf[rt][st];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) mma(sc[rt][t], kf[t], f);
+                }
         }
         then();
         const int tok = span.at(i) * PAGE;
         // a page that every row sees whole needs no mask
         const bool whole = full && here >= 0 && tok + PAGE - 1 <= pos_min &&
                            (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
-        float top = NEG_INF;
-        if (!whole) {
+        bf16x8 pf[RT][2][NP];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = tok + 16 * g + 4 * t + e;
+                        const bool see = (here >= 0) & (j <= pos[rt]) &
+                                         ((a.window == 0) | (j > pos[rt] - a.window) | (j < a.sink));
+                        sc[rt][t][e] = see ? sc[rt][t][e] : NEG_INF;
+                    }
+            }
+            float top = NEG_INF;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[rt][t][e]);
+            top = group_max(top) * a.scale2;
+            if (__any(top > mx[rt] + SLACK)) {
+                top = fmaxf(top, mx[rt]);
+                const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - top);
+                sum[rt] *= by;
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) o[rt][u] *= by;
+                mx[rt] = top;
+            }
+            const float ref = mx[rt] == NEG_INF ? 0.f : mx[rt];   // nothing seen yet: every weight 2^-inf = 0
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int j = tok + 16 * g + 4 * t + e;
-                    const bool see = (here >= 0) & (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
-                    sc[t][e] = see ? sc[t][e] : NEG_INF;
+                    const float p = __builtin_amdgcn_exp2f(fmaf(sc[rt][t][e], a.scale2, -ref));
+                    sum[rt] += p;
+                    bf16 parts[NP];
+                    split_bf16<NP>(p, parts);
+#pragma unroll
+                    for (int z = 0; z < NP; ++z) pf[rt][t >> 1][z][(t & 1) * 4 + e] = parts[z];
                 }
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][e]);
-        top = group_max(top) * a.scale2;
-        if (__any(top > mx + SLACK)) {
-            top = fmaxf(top, mx);
-            const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
-            sum *= by;
-#pragma unroll
-            for (int u = 0; u < D / 16; ++u) o[u] *= by;
-            mx = top;
-        }
-        const float ref = mx == NEG_INF ? 0.f : mx;   // nothing seen yet: every weight 2^-inf = 0
-        bf16x8 pf[2][NP];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(sc[t][e], a.scale2, -ref));
-                sum += p;
-                bf16 parts[NP];
-                split_bf16<NP>(p, parts);
-#pragma unroll
-                for (int z = 0; z < NP; ++z) pf[t >> 1][z][(t & 1) * 4 + e] = parts[z];
-            }
         float vs = scale_of(x.vs);
         // behind the sequence's end the page holds anything, NaN codes too
         if (tok + PAGE > len) {
@@ -343,7 +367,9 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
 #pragma unroll
                 for (int z = 0; z < NP; ++z)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) mma(o[u + y], vf[y][k2], pf[k2][z]);
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) mma(o[rt][u + y], vf[y][k2], pf[rt][k2][z]);
         }
     };
     const int pages = i0 < p_end ? (p_end - i0 + WP - 1) / WP : 0;
@@ -366,62 +392,81 @@ __global__ __launch_bounds__(64 * WAVES, D * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2
             });
         }
     }
-    sum = group_sum(sum);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) sum[rt] = group_sum(sum[rt]);
 
-    // join the waves of a row tile: common maximum, then sums in a tree
-    __shared__ float ml[WAVES][16][2];
-    __shared__ float acc[WP > 1 ? WAVES / 2 : 1][16][D + 4];
+    // join the waves of a row group: common maximum, then sums in a tree
+    __shared__ float ml[WAVES][RT * 16][2];
     if constexpr (WP > 1) {
+        float(*acc)[RT * 16][D + 4] = reinterpret_cast<float(*)[RT * 16][D + 4]>(lds);
         if (g == 0) {
-            ml[w][m][0] = mx;
-            ml[w][m][1] = sum;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                ml[w][rt * 16 + m][0] = mx[rt];
+                ml[w][rt * 16 + m][1] = sum[rt];
+            }
         }
         __syncthreads();
-        float top = NEG_INF, total = 0.f;
 #pragma unroll
-        for (int z = 0; z < WP; ++z) top = fmaxf(top, ml[z * WR + wr][m][0]);
-        const float ref = top == NEG_INF ? 0.f : top;
+        for (int rt = 0; rt < RT; ++rt) {
+            const int at = rt * 16 + m;
+            float top = NEG_INF, total = 0.f;
 #pragma unroll
-        for (int z = 0; z < WP; ++z) total += ml[z * WR + wr][m][1] * __builtin_amdgcn_exp2f(ml[z * WR + wr][m][0] - ref);
-        const float by = __builtin_amdgcn_exp2f(mx - ref);
+            for (int z = 0; z < WP; ++z) top = fmaxf(top, ml[z * WR + wr][at][0]);
+            const float ref = top == NEG_INF ? 0.f : top;
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) o[u] *= by;
-        mx = top;
-        sum = total;
+            for (int z = 0; z < WP; ++z)
+                total += ml[z * WR + wr][at][1] * __builtin_amdgcn_exp2f(ml[z * WR + wr][at][0] - ref);
+            const float by = __builtin_amdgcn_exp2f(mx[rt] - ref);
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) o[rt][u] *= by;
+            mx[rt] = top;
+            sum[rt] = total;
+        }
 #pragma unroll
         for (int half = WP / 2; half >= 1; half /= 2) {
             if (wp >= half && wp < 2 * half) {
 #pragma unroll
-                for (int u = 0; u < D / 16; ++u)
-                    *reinterpret_cast<f32x4*>(&acc[w - half * WR][m][16 * u + 4 * g]) = o[u];
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u)
+                        *reinterpret_cast<f32x4*>(&acc[w - half * WR][rt * 16 + m][16 * u + 4 * g]) = o[rt][u];
             }
             __syncthreads();
             if (wp < half) {
 #pragma unroll
-                for (int u = 0; u < D / 16; ++u) o[u] += *reinterpret_cast<const f32x4*>(&acc[w][m][16 * u + 4 * g]);
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u)
+                        o[rt][u] += *reinterpret_cast<const f32x4*>(&acc[w][rt * 16 + m][16 * u + 4 * g]);
             }
             __syncthreads();
         }
     }
-    if (wp != 0 || r >= rows) return;
-    if (tl.ranges == 1) {
-        typedef T Four __attribute__((ext_vector_type(4)));
-        const float by = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + hg) * D;
+    if (wp != 0) return;
+    typedef T Four __attribute__((ext_vector_type(4)));
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            Four y;
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = row_of(rt);
+        if (r >= rows) continue;
+        if (tl.ranges == 1) {
+            const float by = sum[rt] > 0.f ? 1.f / sum[rt] : (sum[rt] == 0.f ? 0.f : sum[rt]);
+            T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * HG + head_of(rt)) * D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (T)(o[u][e] * by);
-            *reinterpret_cast<Four*>(out + 16 * u + 4 * g) = y;
-        }
-    } else {
-        const size_t at = (((size_t)b * c.H + h) * a.splits + split) * ((size_t)a.T * a.G) + r;
+            for (int u = 0; u < D / 16; ++u) {
+                Four y;
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) *reinterpret_cast<f32x4*>(a.part + at * D + 16 * u + 4 * g) = o[u];
-        if (g == 0) {
-            a.ml[2 * at] = mx;
-            a.ml[2 * at + 1] = sum;
+                for (int e = 0; e < 4; ++e) y[e] = (T)(o[rt][u][e] * by);
+                *reinterpret_cast<Four*>(out + 16 * u + 4 * g) = y;
+            }
+        } else {
+            const size_t at = (((size_t)b * c.H + h) * a.splits + split) * ((size_t)a.T * a.G) + r;
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) *reinterpret_cast<f32x4*>(a.part + at * D + 16 * u + 4 * g) = o[rt][u];
+            if (g == 0) {
+                a.ml[2 * at] = mx[rt];
+                a.ml[2 * at + 1] = sum[rt];
+            }
         }
     }
 }
@@ -717,26 +762,29 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
 // tokens take it.
 constexpr int ONE_DIM = 128, ONE_PAGES = 24;
 
-// Joins the ranges of a row, D / 4 lanes per range so that several are read
-// at a time: a workgroup per row where there are many ranges, else a wave.
-template <class T, int D, int ROWS>
+// Joins the ranges of a row, a few lanes per range so that several are read
+// at a time: a wave per row (ONE), or where there are many ranges a workgroup
+// per row and slice of its dims (2 x 32 rows of 256 dims in 256 ranges,
+// 17 MB: 9 us against 16 with a workgroup a row).
+template <class T, int D, bool ONE>
 __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
-    constexpr int LP = D / 4, GW = 64 / LP, GROUPS = 4 / ROWS * GW;   // lanes of a range, ranges at a time
+    constexpr int SL = ONE ? D : D % 64 ? 32 : 64;                        // dims of a slice
+    constexpr int LP = SL / 4, GW = 64 / LP, GROUPS = ONE ? GW : 4 * GW;   // lanes of a range, ranges at a time
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = blockIdx.y, b = blockIdx.z;
-    const int r = blockIdx.x * ROWS + (ROWS > 1 ? w : 0);
+    const int r = ONE ? blockIdx.x * 4 + w : blockIdx.x / (D / SL), d0 = ONE ? 0 : blockIdx.x % (D / SL) * SL;
     const Tile tl = tile_of(a, b, uniform(a.seqs ? a.seqs[b] : b), r / a.tile_rows);
     const bool out_of = r >= tl.rows || tl.ranges == 1;
-    if (ROWS == 1 && out_of) return;
+    if (!ONE && out_of) return;
     const int ranges = out_of ? 0 : tl.ranges;
     const size_t rows = (size_t)a.T * a.G, at0 = ((size_t)b * a.c.H + h) * a.splits * rows + r;
-    __shared__ __align__(16) float acc[4 * GW][D + 4];
+    __shared__ __align__(16) float acc[4 * GW][SL + 4];
     __shared__ float sums[4 * GW];
     float top = NEG_INF;
     for (int s = lane; s < ranges; s += 64) top = fmaxf(top, a.ml[2 * (at0 + s * rows)]);
 #pragma unroll
     for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
     const float ref = top == NEG_INF ? 0.f : top;
-    const int grp = (ROWS > 1 ? 0 : w * GW) + lane / LP, col = lane % LP * 4;
+    const int grp = (ONE ? 0 : w * GW) + lane / LP, col = lane % LP * 4;
     if (lane < GW * LP) {
         f32x4 o = {0, 0, 0, 0};
         float total = 0.f;
@@ -745,16 +793,16 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
             const size_t at = at0 + s * rows;
             const float by = __builtin_amdgcn_exp2f(a.ml[2 * at] - ref);
             total += a.ml[2 * at + 1] * by;
-            o += *reinterpret_cast<const f32x4*>(a.part + at * D + col) * by;
+            o += *reinterpret_cast<const f32x4*>(a.part + at * D + d0 + col) * by;
         }
         *reinterpret_cast<f32x4*>(&acc[w * GW + lane / LP][col]) = o;
         if (col == 0) sums[w * GW + lane / LP] = total;
     }
     __syncthreads();
     if (out_of) return;
-    T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * a.c.H * a.G + h * a.G + r % a.G) * D;
-    const int z0 = ROWS > 1 ? w * GW : 0, step = ROWS > 1 ? 64 : 256;
-    for (int dim = ROWS > 1 ? lane : threadIdx.x; dim < D; dim += step) {
+    T* out = reinterpret_cast<T*>(a.out) + (((long)b * a.T + r / a.G) * a.c.H * a.G + h * a.G + r % a.G) * D + d0;
+    const int z0 = ONE ? w * GW : 0;
+    for (int dim = ONE ? lane : threadIdx.x; dim < SL; dim += ONE ? 64 : 256) {
         float y = 0.f, total = 0.f;
 #pragma unroll
         for (int z = 0; z < GROUPS; ++z) {
@@ -769,17 +817,16 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
 // many ranges the sequences are divided.
 struct AttendPlan {
     bool wide;       // attend_tiles_kernel, else attend_rows_kernel
-    int wr, kw;      // its WR, or KW
+    int kw;          // its KW
     int waves, tile_rows, tiles, splits, least;
 };
 static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool divided) {
     AttendPlan p;
     const long rows = (long)n_tokens * (heads / c->H), pages = (max_len + PAGE - 1) / PAGE;
     p.wide = rows > 64;
-    p.wr = rows > 32 ? 4 : rows > 16 ? 2 : 1;
     p.kw = 1;
     p.waves = 4;
-    p.tile_rows = p.wide ? 128 : 16 * p.wr;
+    p.tile_rows = p.wide ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
     p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     const long groups = (long)batch * c->H * p.tiles;
     // Workgroups: as many as the compute units take at a time (tiles), or
@@ -799,13 +846,14 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     // One launch of eight waves, which share the sequence among them, instead
     // of ranges and their join (registers and LDS allow it up to width 128).
     // Rows: up to 24 pages (2 x 6 heads of 64, 500 tokens: 8.7 us against 12.1,
-    // 2064 tokens: the same).  Tiles: counted in page steps, a step of KW pages
+    // 2064 tokens: the same), 40 where the heads and entries fill the chip
+    // (22 x 6 heads of 64, 2064 tokens: 12.7 us against 15.7).  Tiles: counted in page steps, a step of KW pages
     // at 1.6 of one page's and a join at 8 steps of width 64 and 6 of width
     // 128 (2 x 1024 queries of 6 heads of 64 over 2064 tokens: 24.7 us against
     // 30.4; 2 x 512 queries of 8 heads on 2 of 128 over 4000: 78 against 43).
     if (c->d > ONE_DIM) return p;
     if (!p.wide) {
-        if (p.wr > 1 || pages > ONE_PAGES) return p;
+        if (rows > 16 || pages > (groups >= 64 && groups <= 256 ? 40 : ONE_PAGES)) return p;
         p.waves = 8;
     } else {
         const int kw = c->d <= 64 ? 4 : 2, tile = 256 / kw;
@@ -851,13 +899,18 @@ static hipError_t launch_attend(const tm_cache* c, const AttendArgs& a, const At
             const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c->H, (unsigned)a.B);
             if constexpr (D() <= ONE_DIM) {
                 if (p.waves == 8) {
-                    launch_k(attend_rows_kernel<T, D(), 1, 8>, grid, dim3(512), 0, st, a);
+                    launch_k(attend_rows_kernel<T, D(), 1, 1, 8>, grid, dim3(512), 0, st, a);
                     return hipGetLastError();
                 }
             }
-            if (p.wr == 1) launch_k(attend_rows_kernel<T, D(), 1, 4>, grid, dim3(256), 0, st, a);
-            else if (p.wr == 2) launch_k(attend_rows_kernel<T, D(), 2, 4>, grid, dim3(256), 0, st, a);
-            else launch_k(attend_rows_kernel<T, D(), 4, 4>, grid, dim3(256), 0, st, a);
+            // more rows: tiles of other waves, which read the same pages from L2, or
+            // at width 256, where a wave is alone on its SIMD anyway, two tiles a
+            // wave (8 x 60000 tokens, 24 rows on 8 heads, bf16: width 128 250 us
+            // against 260, width 256 496 against 443)
+            constexpr int RT = D() < 256 ? 1 : 2;
+            if (p.tile_rows == 16) launch_k(attend_rows_kernel<T, D(), 1, 1, 4>, grid, dim3(256), 0, st, a);
+            else if (p.tile_rows == 32) launch_k(attend_rows_kernel<T, D(), 2 / RT, RT, 4>, grid, dim3(256), 0, st, a);
+            else launch_k(attend_rows_kernel<T, D(), 4 / RT, RT, 4>, grid, dim3(256), 0, st, a);
             return hipGetLastError();
         });
     });
@@ -866,9 +919,10 @@ static hipError_t launch_attend(const tm_cache* c, const AttendArgs& a, const At
         return for_head_dim(c->d, [&](auto D) {
             const int rows = a.T * a.G;
             if (p.splits > 16)
-                launch_k(combine_kernel<T, D(), 1>, dim3((unsigned)rows, (unsigned)c->H, (unsigned)a.B), dim3(256), 0, st, a);
+                launch_k(combine_kernel<T, D(), false>, dim3((unsigned)(rows * (D() / (D() % 64 ? 32 : 64))), (unsigned)c->H, (unsigned)a.B),
+                         dim3(256), 0, st, a);
             else
-                launch_k(combine_kernel<T, D(), 4>, dim3((unsigned)((rows + 3) / 4), (unsigned)c->H, (unsigned)a.B), dim3(256),
+                launch_k(combine_kernel<T, D(), true>, dim3((unsigned)((rows + 3) / 4), (unsigned)c->H, (unsigned)a.B), dim3(256),
                          0, st, a);
             return hipGetLastError();
         });
