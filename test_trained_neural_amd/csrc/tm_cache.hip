@@ -263,25 +263,22 @@ __device__ __forceinline__ float wave_max(float x) {
     return x;
 }
 
-// One workgroup writes the tokens of one page and head, each of its four
-// waves one block of 16.  Keys: a lane takes 8 consecutive elements of a
+// A wave writes what a call has for block w of page `page` (the entry's
+// slot-th) and head h: the block's new tokens, and, where the page is a copy,
+// what the shared page holds.  Keys: a lane takes 8 consecutive elements of a
 // token.  Values, whose tokens are innermost: a lane takes two neighbouring
 // dims of all 16 tokens (4 or 8 bytes a lane and token, so a token's row is
 // read whole) and stores the block's 16 codes of a dim at once; the page's
-// 64-byte row of a dim is made of the four waves' pieces.  All tokens are
-// read up front, once, and stay as they are in registers through the wave's
-// reduction to the block's largest magnitude.
+// 64-byte row of a dim is made of four waves' pieces.  All tokens are read up
+// front, once, and stay as they are in registers through the wave's reduction
+// to the block's largest magnitude.
 template <class T, int D>
-__global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
+__device__ __forceinline__ void write_block(const AppendArgs& a, const AppendPlan& p, int b, int h, int slot, int page,
+                                            int w, bool copied) {
     const CacheView& c = a.c;
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const AppendPlan p = a.plan[b];
-    if (p.n == 0) return;
-    const int slot = p.old / PAGE + blockIdx.x;
+    const int lane = threadIdx.x & 63;
     const int b0 = slot * PAGE + w * BLOCK, end = p.old + p.n;   // the block's first token
-    if (slot * PAGE >= end) return;
     const int lo = max(p.old, b0), hi = min(end, b0 + BLOCK);    // the new tokens in it
-    const bool copied = blockIdx.x == 0 && p.copy_from >= 0;
     if (lo >= hi && !copied) return;
     const T* kx = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * D;
     const T* vx = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * D;
@@ -306,8 +303,6 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
                 vr[it][t] = *reinterpret_cast<const Two*>(vx + (long)(b0 + t - p.old) * a.vt + dim);
         }
     }
-    const int page = blockIdx.x == 0 ? p.page : c.page_at(a.seqs ? a.seqs[b] : b, slot);
-    if (!c.page_ok(page)) return;
     const int from = copied ? p.copy_from : page;   // where the block's present codes are
     const bool begun = lo > b0 && lo < hi;          // it holds earlier tokens, and gets new ones
     const size_t at = c.head_at(page, h), at0 = c.head_at(from, h);
@@ -418,6 +413,78 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
             }
         }
         if (lane == 0) c.scales[at * 8 + 4 + w] = scale;
+    }
+    if (__any(bad) && lane == 0) atomicOr(&c.status[0], TM_CACHE_NONFINITE);
+}
+
+// One workgroup per page and head, a wave per block.
+template <class T, int D>
+__global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
+    const int b = blockIdx.z, w = threadIdx.x >> 6;
+    const AppendPlan p = a.plan[b];
+    const int slot = p.old / PAGE + blockIdx.x;
+    if (p.n == 0 || slot * PAGE >= p.old + p.n) return;
+    const int page = blockIdx.x == 0 ? p.page : a.c.page_at(a.seqs ? a.seqs[b] : b, slot);
+    if (a.c.page_ok(page))
+        write_block<T, D>(a, p, b, blockIdx.y, slot, page, w, blockIdx.x == 0 && p.copy_from >= 0);
+}
+
+// Calls of one token an entry (a decode step): a workgroup per head, of which
+// one wave writes the token.  Where the block's scales stay, that is a byte a
+// dim in each of the two; a scale that grows goes the way above, and so does
+// a page that is a copy, all four waves.
+template <class T, int D>
+__global__ __launch_bounds__(256) void append_token_kernel(AppendArgs a) {
+    const CacheView& c = a.c;
+    const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int IT = (D + 63) / 64;
+    T kr[IT], vr[IT];
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int dim = it * 64 + lane;
+        kr[it] = vr[it] = (T)0.f;
+        if (dim < D) {
+            kr[it] = reinterpret_cast<const T*>(a.k)[b * a.kb + (long)h * D + dim];
+            vr[it] = reinterpret_cast<const T*>(a.v)[b * a.vb + (long)h * D + dim];
+        }
+    }
+    const AppendPlan p = a.plan[b];
+    if (p.n == 0 || !c.page_ok(p.page)) return;
+    if (p.copy_from >= 0) {
+        write_block<T, D>(a, p, b, h, p.old / PAGE, p.page, wave, true);
+        return;
+    }
+    if (wave != 0) return;
+    const int tok = p.old % PAGE, w = tok / BLOCK;
+    const size_t at = c.head_at(p.page, h);
+    bool bad = false;
+    float topk = 0.f, topv = 0.f;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        topk = fmaxf(topk, fabsf(finite_or_zero((float)kr[it], bad)));
+        topv = fmaxf(topv, fabsf(finite_or_zero((float)vr[it], bad)));
+    }
+    int ek = block_exponent(wave_max(topk)), ev = block_exponent(wave_max(topv));
+    if (tok % BLOCK) {   // the block holds earlier tokens: its scales stay, or grow
+        const int had_k = (int)c.scales[at * 8 + w] - 127, had_v = (int)c.scales[at * 8 + 4 + w] - 127;
+        if (ek > had_k || ev > had_v) {
+            write_block<T, D>(a, p, b, h, p.old / PAGE, p.page, w, false);
+            return;
+        }
+        ek = had_k;
+        ev = had_v;
+    } else if (lane == 0) {
+        c.scales[at * 8 + w] = (unsigned char)(ek + 127);
+        c.scales[at * 8 + 4 + w] = (unsigned char)(ev + 127);
+    }
+    const float bk = pow2(-ek), bv = pow2(-ev);
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int dim = it * 64 + lane;
+        if (dim >= D) continue;
+        const unsigned o = codes4(finite_or_zero((float)kr[it], bad) * bk, finite_or_zero((float)vr[it], bad) * bv, 0.f, 0.f);
+        c.k[(at * PAGE + tok) * D + dim] = (unsigned char)o;
+        c.v[(at * D + dim) * PAGE + tok] = (unsigned char)(o >> 8);
     }
     if (__any(bad) && lane == 0) atomicOr(&c.status[0], TM_CACHE_NONFINITE);
 }
@@ -766,8 +833,14 @@ tm_status tm_cache_append(const tm_cache* c, void* blob, const int* seqs, const 
     if (e != hipSuccess) return TM_ERR_HIP;
     const long tokens = n_tokens < most ? n_tokens : most;
     const dim3 grid((unsigned)((tokens + PAGE - 2) / PAGE + 1), (unsigned)c->H, (unsigned)batch);
+    const dim3 each((unsigned)c->H, (unsigned)batch);
     return status_of(timed_attn(st, [&] {
         return for_head_dim(c->d, [&](auto D) {
+            if (n_tokens == 1) {
+                if (dtype == TM_F32) launch_k(append_token_kernel<float, D()>, each, dim3(256), 0, st, a);
+                else launch_k(append_token_kernel<bf16, D()>, each, dim3(256), 0, st, a);
+                return hipGetLastError();
+            }
             if (dtype == TM_F32) launch_k(append_write_kernel<float, D()>, grid, dim3(256), 0, st, a);
             else launch_k(append_write_kernel<bf16, D()>, grid, dim3(256), 0, st, a);
             return hipGetLastError();
