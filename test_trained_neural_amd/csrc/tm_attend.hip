@@ -820,7 +820,21 @@ struct AttendPlan {
     int kw;          // its KW
     int waves, tile_rows, tiles, splits, least;
 };
-static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool divided) {
+// Ranges, at most: as many workgroups as the compute units take at a time
+// (tiles), or several rounds of them, which even out ragged lengths (rows: 48
+// sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with 1024
+// workgroups, 289 us with 8192), and at least TILE_PAGES or ROW_PAGES pages a
+// range.  Grows with `pages`, so the workspace is that of the longest sequence
+// whatever max_len a call names.
+constexpr int TILE_PAGES = 4, ROW_PAGES = 8;
+static int most_ranges(const tm_cache* c, bool wide, long groups, long pages) {
+    long s = (wide ? (c->d <= 128 ? 512 : 256) : 8192) / groups;
+    const long most = wide ? (pages + TILE_PAGES - 1) / TILE_PAGES : (pages + ROW_PAGES - 1) / ROW_PAGES;
+    if (s > most) s = most;
+    if (s > 256) s = 256;
+    return s < 1 ? 1 : (int)s;
+}
+static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len) {
     AttendPlan p;
     const long rows = (long)n_tokens * (heads / c->H), pages = (max_len + PAGE - 1) / PAGE;
     p.wide = rows > 64;
@@ -829,20 +843,13 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     p.tile_rows = p.wide ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
     p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     const long groups = (long)batch * c->H * p.tiles;
-    // Workgroups: as many as the compute units take at a time (tiles), or
-    // several rounds of them, which even out ragged lengths (rows: 48
-    // sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with
-    // 1024 workgroups, 289 us with 8192).  Pages of a range: four (tiles); two
-    // a wave while the chip is not full, more as soon as it is, since every
-    // range costs a start and a place in the join.
+    // Rows: two pages a wave while the chip is not full, more as soon as it is,
+    // since every range costs a start and a place in the join.
     const long eights = groups * ((pages + 7) / 8);
-    p.least = p.wide ? 4 : eights <= 1024 ? 8 : eights <= 4096 ? 16 : 32;
-    const long most = (pages + p.least - 1) / p.least;
-    long s = (p.wide ? (c->d <= 128 ? 512 : 256) : 8192) / groups;
-    if (s > most) s = most;
-    if (s > 256) s = 256;
-    p.splits = s < 1 ? 1 : (int)s;
-    if (divided) return p;
+    p.least = p.wide ? TILE_PAGES : eights <= 1024 ? ROW_PAGES : eights <= 4096 ? 2 * ROW_PAGES : 4 * ROW_PAGES;
+    p.splits = most_ranges(c, p.wide, groups, pages);
+    const long fit = (pages + p.least - 1) / p.least;
+    if (p.splits > fit) p.splits = fit < 1 ? 1 : (int)fit;
     // One launch of eight waves, which share the sequence among them, instead
     // of ranges and their join (registers and LDS allow it up to width 128).
     // Rows: up to 24 pages (2 x 6 heads of 64, 500 tokens: 8.7 us against 12.1,
@@ -875,10 +882,10 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
 size_t attend_workspace(const tm_cache* c, int batch, int n_tokens, int heads) {
     if (heads % c->H != 0 || batch == 0 || n_tokens == 0) return 0;
     // the most ranges that any max_len leads to
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, (long)c->seq_pages * PAGE, true);
-    if (p.splits == 1) return 0;
-    const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * (heads / c->H);
-    return (rows * (c->d + 2) * 4 + 511) / 256 * 256;
+    const long rows = (long)n_tokens * (heads / c->H), tile = rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    const int splits = most_ranges(c, rows > 64, (long)batch * c->H * ((rows + tile - 1) / tile), c->seq_pages);
+    if (splits == 1) return 0;
+    return ((size_t)batch * c->H * splits * rows * (c->d + 2) * 4 + 511) / 256 * 256;
 }
 
 template <class T>
@@ -946,14 +953,14 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
     if (batch > 65535 || (!seqs && batch > c->n_seqs) || n_tokens > 1 << 24 || (uintptr_t)seqs % 4 || (uintptr_t)counts % 4 ||
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most, false);
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most);
     if ((long)p.tiles * p.splits * c->H > 0x7fffffffL) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
     const int G = heads / c->H;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * G;
     float* part = static_cast<float*>(workspace);
     AttendArgs a{cache_view(c, const_cast<void*>(blob)), seqs, counts, q, q_batch, q_token, out, batch, n_tokens, G,
-                 fmaxf(fabsf(score_scale) * 1.44269504088896340736f, 1.2e-38f), score_scale < 0 ? -1.f : 1.f, window, sink < most ? sink : (int)most, p.splits, p.least, p.tile_rows, part, part + rows * c->d};
+                 fmaxf(fabsf(score_scale) * 1.44269504088896340736f, 1.2e-38f), score_scale < 0 ? -1.f : 1.f, window < most ? window : (int)most, sink < most ? sink : (int)most, p.splits, p.least, p.tile_rows, part, part + rows * c->d};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == TM_F32 ? launch_attend<float>(c, a, p, st) : launch_attend<bf16>(c, a, p, st);
     return e == hipSuccess ? TM_OK : TM_ERR_HIP;

@@ -350,6 +350,65 @@ def test_attend_long_and_divided(dtype):
         expect(p.g, p.m, [1, 1], q, None, 0.125, 3000, 200, out, out)
 
 
+@pytest.mark.parametrize("N", [1, 5, 14, 33])
+def test_attend_stays_in_its_workspace(N):
+    """Whatever max_len a call names, it writes its partial results within
+    the workspace that tm_cache_workspace_bytes gives (here inside a larger
+    buffer), and the result holds."""
+    A = T.attention
+    c = T.PagedCache(4, 32, 700, 5, 600)
+    x = normal((1, 1500, 8, 32), 3)[0]
+    c.append(ints([4]), x[:, :, :4], x[:, :, 4:])
+    for s in range(4):
+        c.fork(ints([4]), ints([s]))
+    q = normal((4, N, 8, 32), 4)[0]
+    need = A.tm_cache_workspace_bytes(c.handle, 4, N, 8)
+    want = c.attend(None, q)
+    room = torch.full((need + (64 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    for pages in (1, 7, 24, 25, 64, 128, 256, 511, 512, 513, 600):
+        out = torch.empty_like(q)
+        rc = A._lib().tm_cache_attend(c.handle, c.blob.data_ptr(), None, None, q.data_ptr(), q.stride(0), q.stride(1),
+                                      out.data_ptr(), 4, N, 8, 1 / math.sqrt(32), 0, 0, 64 * pages, T.TM_BF16,
+                                      room.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == T.TM_OK
+        assert bool((room[need:] == 0x5a).all()), pages
+        # each of the two is off by a weight's and the result's rounding: the weighted mean of |v| is at most the largest
+        assert float((out.float() - want.float()).abs().max()) <= 2 * 2.0 ** -8 * float(x.abs().max() + want.abs().max()) * 1.01
+
+
+def test_attend_window_beyond_any_sequence():
+    """A window wider than any sequence is none, also for rows that stand
+    before the sequence's start."""
+    p = Pair(1, 64, 10, 2, 4, BF, seed=13)
+    p.append([0, 1], 150, [150, 5])
+    for N in (3, 40, 100):
+        q = normal((2, N, 2, 64), N)[0]
+        out = p.g.attend(ints([0, 1]), q, window=(1 << 31) - 1, sink=(1 << 31) - 1)
+        expect(p.g, p.m, [0, 1], q, None, 0.125, 0, 0, out, out)
+
+
+def test_pools_past_32_bit_offsets():
+    """Pages whose keys and values lie beyond 4 GiB of the pool's start: the
+    same calls as on a small pool give the same codes and results."""
+    H, d, far = 8, 256, 36000
+    small, big = T.PagedCache(H, d, 12, 3, 4), T.PagedCache(H, d, far + 12, 3, 4)
+    assert big.k.numel() > 1 << 32
+    big.refs[:far] = 1                                              # all but the last pages are taken
+    x, q = normal((2, 130, 2 * H, d), 1)[0], normal((2, 3, 2 * H, d), 2)[0]
+    outs = []
+    for c in (small, big):
+        c.append(ints([0, 2]), x[:, :, :H], x[:, :, H:])
+        c.fork(ints([2]), ints([1]))
+        c.append(ints([1]), x[:1, :1, :H], x[:1, :1, H:])           # a copy of the shared last page
+        outs.append([c.attend(None, torch.cat([q, q[:1]])), c.attend(ints([1]), x[:1, :, :H])] + list(c.read(None, 0, 131)))
+        c.free(ints([0]))
+    big.compact()                                                   # the last pages move down by one sequence's
+    outs.append([outs[1][0]] + [big.attend(ints([1]), x[:1, :, :H])] + list(big.read(None, 0, 131)))
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[1]))
+    assert torch.equal(outs[2][1], outs[1][1]) and torch.equal(outs[2][2][1:], outs[1][2][1:])
+    assert int(big.table[1, 0]) >= far and big.check() == (0, far + 4)
+
+
 def test_attend_sharp_scores_and_masked_rows():
     """Scores of hundreds (one token takes all the weight), a sequence out of
     range, a non-finite query row beside finite ones."""
