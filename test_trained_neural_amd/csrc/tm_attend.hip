@@ -143,10 +143,21 @@ template <int D> __device__ __forceinline__ int key_dim(int step, int g) {
     return step / 2 < D / 64 ? 64 * (step / 2) + 16 * g + 8 * (step & 1) : D / 64 * 64 + 8 * g;
 }
 
-// max over the four lane groups (lanes 16 apart)
+// Over the lanes 32 apart, and 16 and 32 apart: row swaps of the vector
+// units, no trip through LDS.  Each of the two results holds one side (taken
+// out before it is reinterpreted: a bit cast of a vector's element in place
+// reads the first).
+__device__ __forceinline__ float pair_max(float x) {
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned lo = r[0], hi = r[1];
+    return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
 __device__ __forceinline__ float group_max(float x) {
-    x = fmaxf(x, __shfl_xor(x, 16, 64));
-    return fmaxf(x, __shfl_xor(x, 32, 64));
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const unsigned lo = r[0], hi = r[1];
+    return pair_max(fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)));
 }
 __device__ __forceinline__ float group_sum(float x) {
     x += __shfl_xor(x, 16, 64);
@@ -646,7 +657,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[t][e]);
-            top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.scale2;
+            top = pair_max(top) * a.scale2;
             if (__any(top > mx + SLACK)) {
                 top = fmaxf(top, mx);
                 const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
