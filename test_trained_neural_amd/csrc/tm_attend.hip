@@ -91,6 +91,19 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, int b, int s, int t
     return t;
 }
 
+// What a row at `pos` sees: the tokens lo .. lo + n - 1 (one unsigned
+// comparison a token) and those below `sink`; nothing before the sequence's
+// start.
+struct Sight {
+    int lo, sink;
+    unsigned n;
+    __device__ bool sees(int j) const { return ((unsigned)(j - lo) < n) | (j < sink); }
+};
+__device__ __forceinline__ Sight sight_of(const AttendArgs& a, int pos) {
+    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    return Sight{lo, a.window > 0 ? min(a.sink, pos + 1) : 0, pos < 0 ? 0u : (unsigned)(pos - lo + 1)};
+}
+
 // Three bf16 values whose sum is x to 24 bits (NP parts of it).
 template <int NP> __device__ __forceinline__ void split_bf16(float x, bf16 (&out)[NP]) {
 #pragma unroll
@@ -186,7 +199,6 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
     if (tile * WR * RT * 16 >= rows || split >= tl.ranges) return;
     const PageSpan span = tl.span;
     const int p_begin = min(split * tl.per, span.n), p_end = min(p_begin + tl.per, span.n);
-    const bool full = row0 + 16 * RT <= rows;
 
     // this lane's rows: their queries as matrix operands, their positions
     // (too many for the registers in three parts or with wide heads: in LDS)
@@ -197,13 +209,13 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
     bf16x8* ql = reinterpret_cast<bf16x8*>(lds);
     bf16x8 qf[RT][Q_LDS ? 1 : D / 32];
     const int HG = c.H * a.G;
-    int pos[RT];
+    Sight sight[RT];
     auto row_of = [&](int rt) { return row0 + 16 * rt + m; };
     auto head_of = [&](int rt) { return h * a.G + row_of(rt) % a.G; };
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = row_of(rt);
-        pos[rt] = r < rows ? tl.first + r / a.G : -1;
+        sight[rt] = sight_of(a, tl.first + r / a.G);   // (rows behind the last see as if there: dropped)
         const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + (long)(r / a.G) * a.qt + (long)head_of(rt) * D;
 #pragma unroll
         for (int st = 0; st < D / 32; ++st) {
@@ -302,7 +314,7 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
         then();
         const int tok = span.at(i) * PAGE;
         // a page that every row sees whole needs no mask
-        const bool whole = full && here >= 0 && tok + PAGE - 1 <= pos_min &&
+        const bool whole = here >= 0 && tok + PAGE - 1 <= pos_min &&
                            (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
         bf16x8 pf[RT][2][NP];
 #pragma unroll
@@ -313,8 +325,7 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int j = tok + 16 * g + 4 * t + e;
-                        const bool see = (here >= 0) & (j <= pos[rt]) &
-                                         ((a.window == 0) | (j > pos[rt] - a.window) | (j < a.sink));
+                        const bool see = (here >= 0) & sight[rt].sees(j);
                         sc[rt][t][e] = see ? sc[rt][t][e] : NEG_INF;
                     }
             }
@@ -523,9 +534,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
     // this wave's rows, and what all of them and any of them see
     const int wr0 = row0 + 32 * (w / KW), r = wr0 + m, HG = c.H * a.G;
     const bool live_row = r < rows;
-    const int pos = live_row ? first + r / a.G : -1;
+    const Sight sight = sight_of(a, first + r / a.G);   // (rows behind the last see as if there: dropped)
     const int w_min = first + wr0 / a.G, w_max = wr0 < rows ? first + (min(rows, wr0 + 32) - 1) / a.G : -1;
-    const bool full = wr0 + 32 <= rows;
 
     bf16x8 qf[D / 16][NP];
     {
@@ -640,7 +650,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
                     for (int z = 0; z < NP; ++z)
                         sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[st][z], sc[t], 0, 0, 0);
                 }
-            const bool whole = full && tok + PAGE - 1 <= w_min &&
+            const bool whole = tok + PAGE - 1 <= w_min &&
                                (a.window == 0 || tok > w_max - a.window || tok + PAGE <= a.sink);
             float top = NEG_INF;
             if (!whole) {
@@ -649,8 +659,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int j = tok + 32 * t + 16 * (e >> 3) + 8 * g + (e & 7);
-                        const bool see = (j <= pos) & ((a.window == 0) | (j > pos - a.window) | (j < a.sink));
-                        sc[t][e] = see ? sc[t][e] : NEG_INF;
+                        sc[t][e] = sight.sees(j) ? sc[t][e] : NEG_INF;
                     }
             }
 #pragma unroll
