@@ -32,7 +32,8 @@
  *           [n_pages][kv_heads][64][head_dim]
  *   values  e4m3 [n_pages][kv_heads][head_dim][64] (tokens innermost)
  * A copy of meta is a snapshot of the sequences' bookkeeping.  status[0]
- * holds sticky flags (below); status[1] is the calls' own.
+ * holds sticky flags (below); status[1] and status[2] are the calls' own (0 in a
+ * new cache).
  * Quantisation: a block's exponent is the least e in [-110, 119] with
  * max |x| <= 448 2^e over its tokens, a code is x 2^-e rounded to nearest
  * even.  A block that is appended to keeps the larger of its exponent and

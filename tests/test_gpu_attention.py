@@ -208,6 +208,35 @@ def test_random_calls_against_model():
     say("flags", p.m.flags, "used", p.m.used())
 
 
+@pytest.mark.parametrize("H,d,dtype,n_seqs,n_pages", [(1, 32, BF, 300, 420), (3, 64, F32, 40, 60), (2, 256, BF, 9, 14)])
+def test_single_tokens_against_model(H, d, dtype, n_seqs, n_pages):
+    """Calls of one token an entry: new pages, copies of shared ones, scales
+    that grow, entries left out, until the pool is used up."""
+    p = Pair(H, d, n_pages, n_seqs, 3, dtype, seed=d)
+    rng = np.random.default_rng(d)
+    p.append(list(range(n_seqs)), 62, rng.integers(0, 63, n_seqs).tolist())
+    p.fork([0, 1, 0], [n_seqs - 1, n_seqs - 2, n_seqs - 3])        # (not empty: left out)
+    p.free([2, 3, 4])
+    p.fork([5, 5, 6], [2, 3, 4])
+    p.check()
+    for i in range(12):
+        seqs = rng.permutation(n_seqs + 2)[:rng.integers(1, n_seqs + 1)] - 1   # -1 and n_seqs are out of range
+        seqs[rng.integers(len(seqs))] = seqs[0]                     # and one is listed twice
+        p.append(seqs.tolist(), 1, rng.integers(-1, 3, len(seqs)).tolist() if i % 3 == 2 else None)
+        if i % 4 == 3:
+            p.check()
+    for i in range(100 if n_seqs < 100 else 30):                    # everyone, over page ends, out of pages
+        p.append(list(range(n_seqs)), 1)
+        if i % 25 == 24:
+            p.check()
+    p.check()
+    assert p.m.flags & O.NO_PAGES
+    p.free([0])
+    p.append([1, 2, 3], 1)
+    p.check()
+    say("flags", p.m.flags, "used", p.m.used(), "longest", max(p.m.lengths))
+
+
 def test_entries_left_out():
     p = Pair(1, 64, 4, 6, 3, BF, seed=5)
     p.append([0, 0, 9, -1, 1], 10)                       # the second 0, 9 and -1 are left out
