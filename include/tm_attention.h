@@ -16,7 +16,8 @@
  * batch entries and between tokens are given in elements (so that queries,
  * keys and values may be views of one projection's output).  Token arrays
  * are 16-byte aligned and their distances are multiples of 8 elements
- * (tm_rotary takes any).
+ * (tm_rotary takes any).  A call whose launch would have 2^32 threads or
+ * more along an axis is refused (TM_ERR_INVALID).
  *
  * The cache.  A cache holds n_seqs sequences of up to seq_pages * 64 tokens
  * in n_pages pages of 64 tokens, in one caller-owned blob of

@@ -458,7 +458,9 @@ class WindowAttention:
     ``persistent``) and returns the attention output [B][S][D] for the
     segment's S rows; the window stays in the cache.  ``attention.token(x)``
     then takes the next tokens' vectors [B][n][D], behind what the cache
-    holds, and returns theirs."""
+    holds, and returns theirs.  Nothing is recorded for gradients.  The tokens
+    held are counted on the host, so these calls are not for capture into a
+    graph (the cache's own are)."""
 
     def __init__(self, w_qkv, w_out, heads, kv_heads, batch, max_tokens, persistent=None, rotary=None):
         D, d = w_out.shape[0], w_out.shape[1] // heads
@@ -481,6 +483,7 @@ class WindowAttention:
         self._held = self.P   # tokens of each sequence
         self.refresh()
 
+    @torch.no_grad()
     def refresh(self):
         """Starts over with the weights and persistent rows as they are now:
         the windows are dropped, the persistent tokens written again."""
@@ -508,11 +511,14 @@ class WindowAttention:
         return torch.nn.functional.linear(y.flatten(2), self.w_out)
 
     def _room(self, x, n, held):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("WindowAttention counts its tokens on the host: it cannot be captured into a graph")
         if x.shape[0] != self.batch or x.shape[2] != self.w_qkv.shape[1]:
             raise ValueError("expected [%d][tokens][%d], got %s" % (self.batch, self.w_qkv.shape[1], tuple(x.shape)))
         if n < 1 or held + n > self.P + self.max_tokens:
             raise ValueError("%d tokens behind %d: the window holds %d" % (n, held, self.P + self.max_tokens))
 
+    @torch.no_grad()
     def __call__(self, window):
         n = window.shape[1] - self.P
         self._room(window, n, self.P)
@@ -527,6 +533,7 @@ class WindowAttention:
         self._held = self.P + n
         return self._read(q[:, n // 2:])
 
+    @torch.no_grad()
     def token(self, x):
         n = x.shape[1]
         self._room(x, n, self._held)

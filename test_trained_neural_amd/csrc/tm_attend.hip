@@ -335,9 +335,10 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[rt][t][e]);
             top = group_max(top) * a.scale2;
-            if (__any(top > mx[rt] + SLACK)) {
-                top = fmaxf(top, mx[rt]);
-                const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - top);
+            const bool grown = top > mx[rt] + SLACK;
+            if (__any(grown)) {   // a row's steps follow from the row alone: the others' factor is 1
+                top = grown ? top : mx[rt];
+                const float by = grown ? __builtin_amdgcn_exp2f(mx[rt] - top) : 1.f;
                 sum[rt] *= by;
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u) o[rt][u] *= by;
@@ -667,9 +668,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[t][e]);
             top = pair_max(top) * a.scale2;
-            if (__any(top > mx + SLACK)) {
-                top = fmaxf(top, mx);
-                const float by = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
+            const bool grown = top > mx + SLACK;
+            if (__any(grown)) {   // a row's steps follow from the row alone: the others' factor is 1
+                top = grown ? top : mx;
+                const float by = grown ? __builtin_amdgcn_exp2f(mx - top) : 1.f;
                 sum *= by;
 #pragma unroll
                 for (int u = 0; u < D / 32; ++u) o[u] *= by;
@@ -974,7 +976,8 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
     const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most);
-    if ((long)p.tiles * p.splits * c->H > 0x7fffffffL) return TM_ERR_INVALID;
+    // a launch has fewer than 2^32 threads along an axis
+    if ((long)p.tiles * p.splits * c->H * 64 * p.waves >= 1L << 32) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;
     const int G = heads / c->H;
     const size_t rows = (size_t)batch * c->H * p.splits * n_tokens * G;

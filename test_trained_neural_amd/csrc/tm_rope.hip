@@ -119,7 +119,7 @@ static hipError_t launch_v(RopeArgs a, bool half, hipStream_t st) {
     a.units = (half || V == 1 ? a.r / 2 / V : a.r / V) + (a.d - a.r) / V;
     const long threads = (long)a.B * a.T * a.units;
     const long blocks = (threads + 255) / 256;
-    if (blocks > 0x7fffffffL) return hipErrorInvalidValue;
+    if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
     // What does not fit the 256 MB of the last-level cache goes past the
     // caches, with more workgroups (2 x 16384 tokens of 40 heads of 128 in
     // bf16, 671 MB: 131 us against 138; 4 x 8192 of 10 heads of 64, 84 MB:
@@ -237,7 +237,7 @@ tm_status tm_rotary(const void* x, long x_batch, long x_token, void* y, long y_b
     const hipError_t e = timed_attn(st, [&] {
         return dtype == TM_F32 ? launch_t<float>(a, half, st) : launch_t<bf16>(a, half, st);
     });
-    return e == hipSuccess ? TM_OK : TM_ERR_HIP;
+    return e == hipSuccess ? TM_OK : e == hipErrorInvalidValue ? TM_ERR_INVALID : TM_ERR_HIP;
 }
 
 }  // extern "C"

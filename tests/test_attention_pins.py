@@ -220,6 +220,17 @@ def test_calls_refuse_before_launch():
     A.tm_cache_destroy(h)
 
 
+def test_calls_beyond_a_launch():
+    # as above, nothing is launched: more than 2^32 threads along an axis
+    L, P, bf = A._lib(), 1 << 20, T.TM_BF16
+    n = 1 << 28
+    assert L.tm_rotary(P, 0, 33, P, 0, 33, P, 1, P, 1.0, 1, n, 1, 33, 32, 0, 0, bf, None) == T.TM_ERR_INVALID
+    h = A.tm_cache_create(1024, 32, 8, 4, 4)
+    assert L.tm_cache_attend(h, P, None, None, P, 0, 1024 * 32, P, 1, 1 << 24, 1024, 1.0, 0, 0, 0, bf, P,
+                             None) == T.TM_ERR_INVALID
+    A.tm_cache_destroy(h)
+
+
 def test_binding_checks():
     bf, f32 = torch.bfloat16, torch.float32
     x = torch.zeros((1, 2, 3, 8))

@@ -458,6 +458,23 @@ def test_attend_sharp_scores_and_masked_rows():
     expect(p.g, p.m, [0, 2, 7, -1], q0, None, 1.0, 0, 0, w, w)
 
 
+@pytest.mark.parametrize("dtype,N", [(BF, 2), (F32, 3), (BF, 11), (BF, 50), (F32, 50)])
+def test_attend_rows_do_not_depend_on_each_other(dtype, N):
+    """A row's bits are the same whatever the rows beside it are (small
+    queries among large ones, whose maxima grow at other pages)."""
+    p = Pair(1, 64, 20, 2, 12, dtype, seed=14)
+    p.append([0, 1], 700, [700, 333])
+    q, _ = normal((2, N, 4, 64), 15, dtype)
+    small, big = q * 1.5, q * 12
+    mixed, others = small.clone(), small.clone()
+    mixed[:, ::2, 1::2] = big[:, ::2, 1::2]
+    others[:, ::2, 1::2] = 0
+    a, b = (p.g.attend(ints([0, 1]), x) for x in (mixed, others))
+    a[:, ::2, 1::2] = 0
+    b[:, ::2, 1::2] = 0
+    assert torch.equal(a, b)
+
+
 def test_streams_and_graphs():
     """Append, attend and free in a captured graph, replayed between eager
     calls; two graphs of one cache's reads on two streams."""

@@ -117,6 +117,20 @@ def test_segments_and_tokens(dtype, heads, kv, d, P, S):
     assert torch.equal(at(window), ref.segment(window))
 
 
+def test_window_records_no_gradients_and_refuses_capture(monkeypatch):
+    w, w_out, pers = weights(4, 2, 32, 48, 5, BF, 1)
+    at = T.WindowAttention(w.requires_grad_(), w_out.requires_grad_(), 4, 2, 2, 20, pers, T.Rotary(32))
+    x = torch.cat([pers[None].expand(2, 5, 48), torch.ones((2, 8, 48), dtype=BF, device="cuda")], dim=1)
+    y = at(x)
+    assert not y.requires_grad and not at.token(x[:, :1]).requires_grad
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    for call in (lambda: at(x), lambda: at.token(x[:, :1])):
+        with pytest.raises(RuntimeError, match="captured"):
+            call()
+    monkeypatch.undo()
+    assert torch.equal(at(x), y)                                    # the refusals changed nothing
+
+
 def test_as_attention_of_mac_segment():
     """Two segments through mac_segment with WindowAttention equal those with
     a function that makes its calls one by one on a cache of its own."""
