@@ -3,7 +3,7 @@
 //
 // Everything that decides which page a token goes to runs on the device, in
 // one workgroup per call (append, compact), one per entry (fork, free) or all
-// of them alike (an append of single tokens), so no call waits for the host
+// of them alike (an append of a few tokens), so no call waits for the host
 // and every call can be captured into a graph.
 // Pages are found by a scan of the reference counts from a lower bound on the
 // first free one, in ascending order: which page an entry gets follows from
@@ -444,23 +444,16 @@ __global__ __launch_bounds__(256) void append_write_kernel(AppendArgs a) {
         write_block<T, D>(a, p, b, blockIdx.y, slot, page, w, blockIdx.x == 0 && p.copy_from >= 0);
 }
 
-// One token of an entry into head h, by a wave (SOLO) or the first wave of a
-// workgroup.  Where the block's scales stay, that is a byte a dim in keys and
-// values each; a scale that grows goes the way above, and so does a page that
-// is a copy, by the wave or all four.  kr, vr: the token's elements, dims lane,
-// lane + 64, ...
-template <class T, int D, bool SOLO>
+// One token of an entry into head h of a page of its own, by a wave.  Where
+// the block's scales stay, that is a byte a dim in keys and values each; a
+// scale that grows goes the way above.  kr, vr: the token's elements, dims
+// lane, lane + 64, ...
+template <class T, int D>
 __device__ __forceinline__ void write_token(const AppendArgs& a, const AppendPlan& p, int b, int h,
                                             const T (&kr)[(D + 63) / 64], const T (&vr)[(D + 63) / 64]) {
     const CacheView& c = a.c;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     constexpr int IT = (D + 63) / 64;
-    if (p.copy_from >= 0) {
-        for (int x = SOLO ? 0 : wave; x < (SOLO ? PAGE / BLOCK : wave + 1); ++x)
-            write_block<T, D>(a, p, b, h, p.old / PAGE, p.page, x, true);
-        return;
-    }
-    if (!SOLO && wave != 0) return;
     const int tok = p.old % PAGE, w = tok / BLOCK;
     const size_t at = c.head_at(p.page, h);
     bool bad = false;
@@ -515,34 +508,41 @@ __global__ __launch_bounds__(256) void append_token_kernel(AppendArgs a) {
     T kr[(D + 63) / 64], vr[(D + 63) / 64];
     load_token<T, D>(a, b, h, kr, vr);
     const AppendPlan p = a.plan[b];
-    if (p.n > 0 && a.c.page_ok(p.page)) write_token<T, D, false>(a, p, b, h, kr, vr);
+    if (p.n == 0 || !a.c.page_ok(p.page)) return;
+    const int wave = threadIdx.x >> 6;
+    if (p.copy_from >= 0) write_block<T, D>(a, p, b, h, p.old / PAGE, p.page, wave, true);   // a block a wave
+    else if (wave == 0) write_token<T, D>(a, p, b, h, kr, vr);
 }
 
-// The same with the plan, in one launch (a decode step), a wave per head and
-// four heads a workgroup: every workgroup works out the entries' needs (at
-// most one page each) and its own entry's page for itself, from bookkeeping
-// that no workgroup changes; the last of them to be done, by a count in
-// status[2] that it sets back, makes the plan's changes.  64 entries of 8
-// heads: 8 us against 5 and 4 in two launches, a call 3 us shorter.
-constexpr int STEP_ENTRIES = 256;
-template <class T, int D>
+// Calls of a few tokens an entry with the plan, in one launch (a decode step,
+// drafts): every workgroup works out the entries' needs (at most two pages
+// each) and its own entry's pages for itself, from bookkeeping that no
+// workgroup changes; the last of them to be done, by a count in status[2] that
+// it sets back, makes the plan's changes.  A wave writes a head's token (ONE:
+// one token an entry at most), two its even and odd blocks.  64 entries of 8
+// heads, one token: 8 us against 5.5 and 4 in two launches, a call 3 us
+// shorter (with two waves a head as well 10 us: twice the workgroups).
+constexpr int STEP_ENTRIES = 256, STEP_TOKENS = 16;
+template <class T, int D, bool ONE>
 __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a) {
+    static_assert(STEP_TOKENS <= PAGE, "two pages an entry");
     const CacheView& c = a.c;
-    const int b = blockIdx.y, h = blockIdx.x * 4 + (threadIdx.x >> 6), i = threadIdx.x;
-    __shared__ int seqs[STEP_ENTRIES], slots[STEP_ENTRIES], by_rank[STEP_ENTRIES], wave_sums[STEP_ENTRIES / 64];
+    const int b = blockIdx.y, i = threadIdx.x, w = threadIdx.x >> 6;
+    constexpr int WAVES = ONE ? 1 : 2;   // of a head
+    const int h = blockIdx.x * (4 / WAVES) + w / WAVES;
+    __shared__ int seqs[STEP_ENTRIES], page_of[2 * STEP_ENTRIES], wave_sums[STEP_ENTRIES / 64];
     __shared__ unsigned listed[MAX_SEQS / 32];   // bit s: sequence s is in the list
-    __shared__ int flags, hint, page_found, last, doubles;
+    __shared__ int flags, hint, last, doubles, own_rank, own_need;
     __shared__ AppendPlan own;
-    __shared__ int own_rank;
     const int from = min(max(c.status[1], 0), c.n_pages);
     auto is_free = [&](int p) { return p < c.n_pages && c.refs[p] <= 0; };
-    bool free0 = is_free(from + i);
+    const bool free0 = is_free(from + i);
     T kr[(D + 63) / 64], vr[(D + 63) / 64];
-    if (h < c.H) load_token<T, D>(a, b, h, kr, vr);
+    if constexpr (ONE)
+        if (h < c.H) load_token<T, D>(a, b, h, kr, vr);
     if (i == 0) {
         flags = doubles = 0;
         hint = 0x7fffffff;
-        page_found = -1;
     }
     static_assert(MAX_SEQS / 32 == STEP_ENTRIES, "a word a thread");
     listed[i] = 0;
@@ -555,7 +555,7 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
         __syncthreads();
     }
     AppendPlan p{0, 0, -1, -1};
-    int flag = i < a.B && s < 0 ? TM_CACHE_BAD_ENTRY : 0;
+    int flag = i < a.B && s < 0 ? TM_CACHE_BAD_ENTRY : 0, need = 0;
     if (s >= 0) {
         bool twice = false;
         if (doubles)
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
         if (twice) flag = TM_CACHE_BAD_ENTRY;
         else {
             p.old = c.length(s);
-            p.n = a.counts ? min(max(a.counts[i], 0), 1) : 1;
+            p.n = a.counts ? min(max(a.counts[i], 0), a.T) : a.T;
             if (p.n > c.seq_pages * PAGE - p.old) {
                 flag = TM_CACHE_FULL;
                 p.n = 0;
@@ -577,38 +577,56 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
                     p.copy_from = p.page;
                 }
             }
+            if (p.n > 0) need = (p.old + p.n + PAGE - 1) / PAGE - (p.old + PAGE - 1) / PAGE + (p.copy_from >= 0);
         }
     }
-    const int need = p.n > 0 && (p.old % PAGE == 0 || p.copy_from >= 0);
-    slots[i] = p.old / PAGE;
     int want;
     const int rank = block_scan<STEP_ENTRIES>(need, wave_sums, want) - need;
-    if (need) by_rank[rank] = i;
     if (i == b) {
         own = p;
-        own_rank = need ? rank : -1;
+        own_rank = rank;
+        own_need = need;
     }
     __syncthreads();
-    // the free pages in order, 256 at a time; f(rank, page) for each
-    auto scan_free = [&](int upto, auto&& f) {
+    // page_of: the first `upto` free pages in order, 256 at a time; how many there are
+    auto scan_free = [&](int upto) {
         int found = 0;
         for (int p0 = from; p0 < c.n_pages && found < upto; p0 += STEP_ENTRIES) {
             const bool is = p0 == from ? free0 : is_free(p0 + i);
             int total;
             const int r = found + block_scan<STEP_ENTRIES>(is, wave_sums, total) - 1;
-            if (is && r < upto) f(r, p0 + i);
+            if (is && r < upto) page_of[r] = p0 + i;
             found += total;
         }
+        __syncthreads();
         return min(found, upto);
     };
-    if (own_rank >= 0) {
-        scan_free(own_rank + 1, [&](int r, int page) {
-            if (r == own_rank) page_found = page;
-        });
-        __syncthreads();
+    const int upto = own_need > 0 ? own_rank + own_need : 0;
+    if (upto == 0 || scan_free(upto) == upto) {
+        const int at = upto - own_need;   // rank of the entry's first new page
+        const bool begins = own.copy_from >= 0 || own.old % PAGE == 0;   // its tokens' first page is new
+        const AppendPlan mine{own.old, own.n, own.copy_from, begins && upto ? page_of[at] : own.page};
+        if (h < c.H && mine.n > 0) {
+            const bool copied = mine.copy_from >= 0;
+            const int first = mine.old / PAGE, after = begins ? at + 1 : at;
+            if constexpr (ONE) {
+                if (!copied) write_token<T, D>(a, mine, b, h, kr, vr);
+                else
+                    for (int x = 0; x < PAGE / BLOCK; ++x) write_block<T, D>(a, mine, b, h, first, mine.page, x, true);
+            } else {
+                int x = mine.old / BLOCK, x1 = (mine.old + mine.n - 1) / BLOCK;
+                if (copied) {   // all of the page
+                    x = first * (PAGE / BLOCK);
+                    x1 = max(x1, x + PAGE / BLOCK - 1);
+                }
+                for (x += w % WAVES; x <= x1; x += WAVES) {
+                    const int slot = x / (PAGE / BLOCK);
+                    write_block<T, D>(a, mine, b, h, slot, slot == first ? mine.page : page_of[after], x % (PAGE / BLOCK),
+                                      copied && slot == first);
+                }
+            }
+        }
     }
-    const AppendPlan mine{own.old, own.n, own.copy_from, own_rank >= 0 ? page_found : own.page};
-    if (h < c.H && mine.n > 0 && c.page_ok(mine.page)) write_token<T, D, true>(a, mine, b, h, kr, vr);
 
     // What this workgroup needs of the bookkeeping is in its registers (the
     // barrier is behind their use), and it has written none of it: the count
@@ -618,19 +636,20 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
     if (i == 0) last = atomicAdd(&c.status[2], 1) == (int)(gridDim.x * gridDim.y) - 1;
     __syncthreads();
     if (!last) return;
-    const int have = want > 0 ? scan_free(want, [&](int r, int page) {
-        const int e = by_rank[r];
-        c.table[(size_t)seqs[e] * c.seq_pages + slots[e]] = page;
-        c.refs[page] = 1;
-        if (r == want - 1) hint = page + 1;
-    }) : 0;
-    __syncthreads();
-    if (i == 0 && have < want) hint = c.n_pages;   // every free page was taken
+    const int have = want > 0 ? scan_free(want) : 0;
+    if (i == 0 && want > 0) hint = have < want ? c.n_pages : page_of[want - 1] + 1;
     __syncthreads();
     if (p.n > 0) {
-        if (need && rank >= have) flag = TM_CACHE_NO_PAGES;
-        else {
-            c.lengths[s] = p.old + 1;
+        const int slot = p.copy_from >= 0 ? p.old / PAGE : (p.old + PAGE - 1) / PAGE;   // of the first new page
+        if (rank + need > have && need > 0) {
+            flag = TM_CACHE_NO_PAGES;
+            if (rank < have) atomicMin(&hint, page_of[rank]);   // not taken
+        } else {
+            for (int r = 0; r < need; ++r) {
+                c.table[(size_t)s * c.seq_pages + slot + r] = page_of[rank + r];
+                c.refs[page_of[rank + r]] = 1;
+            }
+            c.lengths[s] = p.old + p.n;
             if (p.copy_from >= 0 && atomicSub(&c.refs[p.copy_from], 1) == 1) atomicMin(&hint, p.copy_from);
         }
     }
@@ -984,15 +1003,24 @@ tm_status tm_cache_append(const tm_cache* c, void* blob, const int* seqs, const 
                  static_cast<AppendPlan*>(workspace)};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const dim3 each((unsigned)c->H, (unsigned)batch);
-    // One launch while its workgroups are few: the count that ends it is a place
-    // that each of them goes to, and a wave copies a shared page's head by itself
-    // (128 entries of 8 heads that all copy: 23 us against 11 and the plan).
-    const dim3 four((unsigned)((c->H + 3) / 4), (unsigned)batch);
-    if (n_tokens == 1 && batch <= STEP_ENTRIES && (long)batch * four.x <= 128) {
+    // One launch while its workgroups are few, since the count that ends it is a
+    // place that each of them goes to, and one or two waves copy a shared page's
+    // head where the write has four.  8 heads of 128, passes with the calls that
+    // free or fork beside: 2 tokens, 64 entries 17.5 us against 19.8, 128 that
+    // all copy 30 against 34; one token, 64 entries 17.4 against 20, 128 that
+    // all copy 30.5 against 27.3.
+    const int heads = n_tokens == 1 ? 4 : 2;
+    const dim3 step((unsigned)((c->H + heads - 1) / heads), (unsigned)batch);
+    if (n_tokens <= STEP_TOKENS && batch <= STEP_ENTRIES && (long)batch * step.x <= (n_tokens == 1 ? 128 : 512)) {
         return status_of(timed_attn(st, [&] {
             return for_head_dim(c->d, [&](auto D) {
-                if (dtype == TM_F32) launch_k(append_step_kernel<float, D()>, four, dim3(STEP_ENTRIES), 0, st, a);
-                else launch_k(append_step_kernel<bf16, D()>, four, dim3(STEP_ENTRIES), 0, st, a);
+                if (dtype == TM_F32) {
+                    if (n_tokens == 1) launch_k(append_step_kernel<float, D(), true>, step, dim3(STEP_ENTRIES), 0, st, a);
+                    else launch_k(append_step_kernel<float, D(), false>, step, dim3(STEP_ENTRIES), 0, st, a);
+                } else {
+                    if (n_tokens == 1) launch_k(append_step_kernel<bf16, D(), true>, step, dim3(STEP_ENTRIES), 0, st, a);
+                    else launch_k(append_step_kernel<bf16, D(), false>, step, dim3(STEP_ENTRIES), 0, st, a);
+                }
                 return hipGetLastError();
             });
         }));
