@@ -80,7 +80,9 @@ typedef enum {
     TM_ROPE_PARTS = 3     /* by wavelength: pairs that turn at least beta_fast times within original_len
                              positions keep their frequency, those that turn at most beta_slow times are
                              divided by factor, and between them the share goes linearly with the pair's
-                             index; *result_scale = 0.1 ln(factor) + 1 for factor > 1 */
+                             index, from the last whole index that turns beta_fast times to the first
+                             that turns beta_slow times (wherever those lie: no pair need turn so much or
+                             so little); *result_scale = 0.1 ln(factor) + 1 for factor > 1 */
 } tm_rope_scaling;
 
 /* Host only: freq [rot_dim / 2] = base^(-2 i / rot_dim), scaled as `scaling`

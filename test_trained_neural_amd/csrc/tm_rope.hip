@@ -186,10 +186,13 @@ tm_status tm_rotary_frequencies(int rot_dim, double base, tm_rope_scaling scalin
     *result_scale = 1.0;
     double lo = 0.0, hi = 0.0;
     if (scaling == TM_ROPE_PARTS) {
-        // pair index at which a pair turns `beta` times within original_len
+        // pair index at which a pair turns `beta` times within original_len;
+        // the ramp's ends may lie before the first pair and behind the last
+        // (drawn in to them, it would divide a last pair that still turns
+        // several times by the whole factor)
         auto at = [&](double beta) { return r * log(original_len / (beta * 2.0 * pi)) / (2.0 * log(base)); };
-        lo = fmax(floor(at(beta_fast)), 0.0);
-        hi = fmin(ceil(at(beta_slow)), n - 1.0);
+        lo = floor(at(beta_fast));
+        hi = ceil(at(beta_slow));   // above lo: beta_fast > beta_slow
         if (factor > 1.0) *result_scale = 0.1 * log(factor) + 1.0;
     }
     for (int i = 0; i < n; ++i) {
@@ -197,7 +200,7 @@ tm_status tm_rotary_frequencies(int rot_dim, double base, tm_rope_scaling scalin
         if (scaling == TM_ROPE_LINEAR) {
             freq[i] = f / factor;
         } else if (scaling == TM_ROPE_PARTS) {
-            const double share = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+            const double share = fmin(fmax((i - lo) / (hi - lo), 0.0), 1.0);
             freq[i] = f * (1.0 - share) + f / factor * share;
         } else {
             freq[i] = f;

@@ -129,6 +129,29 @@ def test_frequencies():
     assert np.all(np.diff(np.array(f) / plain) <= 1e-15)
 
 
+@pytest.mark.parametrize("rot_dim,base,length,factor,fast,slow", [
+    (4, 10000.0, 4096, 16.0, 32.0, 1.0), (6, 10000.0, 4096, 16.0, 32.0, 1.0), (64, 10000.0, 131072, 8.0, 32.0, 1.0),
+    (128, 10000.0, 131072, 4.0, 32.0, 1.0), (128, 500000.0, 8192, 8.0, 4.0, 1.0), (64, 10000.0, 4096, 16.0, 32.0, 1.0),
+    (16, 10000.0, 100, 4.0, 32.0, 1.0), (16, 10000.0, 4, 4.0, 32.0, 1.0), (2, 10000.0, 64, 2.0, 32.0, 1.0),
+    (32, 10000.0, 1e12, 2.0, 32.0, 1.0)])
+def test_frequencies_by_parts(rot_dim, base, length, factor, fast, slow):
+    """Pairs that turn enough keep their frequency, those that turn too little
+    are divided, also where no pair turns so much or so little, and between
+    them the share is linear."""
+    n = rot_dim // 2
+    f, _ = T.tm_rotary_frequencies(rot_dim, base, T.TM_ROPE_PARTS, factor, length, fast, slow)
+    plain = base ** (-np.arange(n) / n)
+    turns = length * plain / (2 * math.pi)
+    ratio = np.array(f) / plain
+    share = (1 - ratio) / (1 - 1 / factor)
+    assert np.allclose(ratio[turns >= fast * (1 + 1e-9)], 1, rtol=1e-14)
+    assert np.allclose(ratio[turns <= slow * (1 - 1e-9)], 1 / factor, rtol=1e-14)
+    # a pair's index goes with the logarithm of its turns
+    at = lambda turn: n * math.log(length / (2 * math.pi) / turn) / math.log(base)  # noqa: E731
+    lo, hi = math.floor(at(fast)), math.ceil(at(slow))
+    assert np.allclose(share, np.clip((np.arange(n) - lo) / (hi - lo), 0, 1), atol=1e-12)
+
+
 @pytest.mark.parametrize("args", [dict(rot_dim=0), dict(rot_dim=7), dict(rot_dim=1026), dict(rot_dim=8, base=1.0),
                                   dict(rot_dim=8, base=math.inf), dict(rot_dim=8, base=math.nan),
                                   dict(rot_dim=8, scaling=7), dict(rot_dim=8, scaling=1, factor=0.0),
