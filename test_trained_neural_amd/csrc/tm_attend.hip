@@ -360,9 +360,10 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
                 }
         }
         float vs = scale_of(x.vs);
-        // behind the sequence's end the page holds anything, NaN codes too
-        if (tok + PAGE > len) {
-            const int live = len - tok - 16 * g;   // tokens of this lane's block
+        // behind the sequence's end the page holds anything, NaN codes too, and
+        // so does the page that was loaded for an entry out of range
+        if (tok + PAGE > len || here < 0) {
+            const int live = here < 0 ? 0 : len - tok - 16 * g;   // tokens of this lane's block
             if (live <= 0) vs = 1.f;
             unsigned keep[4];
 #pragma unroll

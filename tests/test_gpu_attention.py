@@ -346,6 +346,39 @@ def test_snapshot_and_bad_tables():
     assert p.g.lengths.tolist() == [0, 0, 0]
 
 
+def unwritten_first_page(pair):
+    """Takes page 0 out of the pool as it lies there (NaN codes, NaN scales)."""
+    pair.g.refs[0], pair.m.refs[0] = 1, 1
+
+
+@pytest.mark.parametrize("H,d,dtype,N,L", [(2, 64, BF, 1, 300), (1, 64, F32, 3, 300), (1, 32, BF, 17, 300), (1, 128, BF, 40, 300),
+                                           (1, 256, BF, 20, 300), (1, 160, F32, 1, 300), (1, 64, BF, 2, 5000),
+                                           (1, 96, F32, 1, 5000), (1, 64, BF, 70, 300), (2, 128, F32, 100, 300),
+                                           (1, 192, BF, 90, 2000), (1, 64, BF, 130, 5000)])
+def test_attend_bad_tables(H, d, dtype, N, L):
+    """Pages whose table entries are out of range are not visible, whatever
+    lies in the others: few and many rows, one range and several."""
+    p = Pair(H, d, 90, 3, 80, dtype, seed=d + N)
+    unwritten_first_page(p)
+    p.append([2, 1], L, [L, 150], x=p.tokens(2, L, scale=1.0))
+    bad, scale = {0: 99, 2: -3, (L - 1) // 64: 1 << 30}, 1 / math.sqrt(d)
+    for page, entry in bad.items():
+        p.g.table[2, page] = entry
+    q, qn = normal((2, N, 2 * H, d), 3, dtype, 0.5)
+    out = p.g.attend(ints([2, 1]), q, max_len=L)
+    k, v = p.m.held(2)
+    see = np.ones(L, bool)
+    for page in bad:
+        see[page * 64:page * 64 + 64] = False
+    u, half = 2.0 ** -24, torch.finfo(dtype).eps / 2
+    for i in range(N):
+        at = see & (np.arange(L) <= L - N + i)
+        want, spread, size = O.attend(k[at], v[at], qn[0, i:i + 1], scale)
+        tol = spread * (2 * (d + 8) * u * size + 8 * u + L * u + (2.0 ** -8 if dtype == BF else 2.0 ** -23)) + half * np.abs(want)
+        assert np.all(np.abs(out[0, i].float().cpu().numpy() - want[0]) <= tol[0]), i
+    expect(p.g, p.m, [1], q[1:], None, scale, 0, 0, out[1:], out[1:])
+
+
 # ---- attention ----
 
 def expect(cache, model, seqs, q, counts, scale, window, sink, got, before):
