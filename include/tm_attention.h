@@ -170,7 +170,8 @@ tm_status tm_cache_append(const tm_cache* cache, void* blob, const int* seqs, co
  * heads: a multiple of kv_heads, at most 64 * kv_heads.  out: contiguous
  * [batch][n_tokens][heads][head_dim] of dtype.  Products of bf16 calls are
  * of bf16 operands with fp32 accumulation (the cache's values are exact in
- * bf16; the softmax weights are rounded to it), those of fp32 calls keep 24
+ * bf16; the softmax weights keep 16 bits where n_tokens * heads / kv_heads is
+ * at most 64, and are rounded to bf16 above), those of fp32 calls keep 24
  * bits of q and of the weights; statistics are fp32.
  * max_len: at least the longest listed sequence's length lets the call
  * choose its launch (0: seq_pages * 64); results are right whatever it is.

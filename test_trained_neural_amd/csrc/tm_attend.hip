@@ -13,7 +13,9 @@
 // in bf16: a code times its power-of-two scale is exact in bf16, and the
 // hardware conversion applies the scale.  In fp32 calls the other operand
 // (the queries, then the weights) is split into three bf16 parts whose sum
-// holds 24 bits, each with a product of its own.
+// holds 24 bits, each with a product of its own.  In bf16 calls the queries
+// are bf16 already; the weights are split into two parts (16 bits) for few
+// rows and rounded to one for many (the kernels say why).
 //
 // The scores are computed transposed (S^T = K Q^T, then O^T = V^T P^T), so
 // that a lane's scores of one row are, without any exchange, the operand of
@@ -184,12 +186,18 @@ __device__ __forceinline__ float group_sum(float x) {
 // workgroup's range; the waves of a group are joined in LDS at the end.  With
 // one range the workgroup writes the output, otherwise its accumulators,
 // maxima and sums for combine_kernel.  Bound by reading the pages: a wave's
-// next keys and present values are in flight while it computes.  48 sequences
+// next keys and present values are in flight while it computes.  That leaves
+// room for the weights' second part in bf16 calls: with it results differ from
+// 64 bits by their own rounding (0.0017 of their size; with one part 0.0023).
+// 48 sequences as below: 285 us with either; 16 of 2000 to 20000 tokens, 4 key
+// heads, single tokens of 16 heads and 4 tokens of 64: width 64 22.8 to 23.8
+// and 46 to 50 us, 128 40.6 to 40.8 and 115 to 114, 256 96 to 97 and 178 to
+// 190; width 32, bound by the vector units, 16.7 to 18.4 and 38 to 47.  48 sequences
 // of 2000 to 30000 tokens, 32 heads on 8 of 128, bf16: 288 us, 5.4 TB/s; 4
 // fp32 tokens of one of 10^6, 16 heads on 2 of 256: 224 us, 4.6 TB/s.
 template <class T, int D, int WR, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
-    constexpr int NP = sizeof(T) == 4 ? 3 : 1;
+    constexpr int NP = sizeof(T) == 4 ? 3 : 1, NW = sizeof(T) == 4 ? 3 : 2;   // parts of a query, of a weight
     constexpr int WP = WAVES / WR;   // waves that share a row group
     const CacheView& c = a.c;
     const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), m = lane & 15, g = lane >> 4;
@@ -318,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
         // a page that every row sees whole needs no mask
         const bool whole = here >= 0 && tok + PAGE - 1 <= pos_min &&
                            (a.window == 0 || tok > pos_max - a.window || tok + PAGE <= a.sink);
-        bf16x8 pf[RT][2][NP];
+        bf16x8 pf[RT][2][NW];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             if (!whole) {
@@ -353,10 +361,10 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
                 for (int e = 0; e < 4; ++e) {
                     const float p = __builtin_amdgcn_exp2f(fmaf(sc[rt][t][e], a.scale2, -ref));
                     sum[rt] += p;
-                    bf16 parts[NP];
-                    split_bf16<NP>(p, parts);
+                    bf16 parts[NW];
+                    split_bf16<NW>(p, parts);
 #pragma unroll
-                    for (int z = 0; z < NP; ++z) pf[rt][t >> 1][z][(t & 1) * 4 + e] = parts[z];
+                    for (int z = 0; z < NW; ++z) pf[rt][t >> 1][z][(t & 1) * 4 + e] = parts[z];
                 }
         }
         float vs = scale_of(x.vs);
@@ -391,7 +399,7 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-                for (int z = 0; z < NP; ++z)
+                for (int z = 0; z < NW; ++z)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -507,10 +515,17 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
 // queries over 7000 tokens in a window of 4096, 32 heads on 8 of 128, bf16:
 // 238 us, 870 TFLOP/s; 2 x 1024 over 2064, 6 heads of 64: 24 us, 208 TFLOP/s.
 // (The next page's scores computed beside the present one's weights: 252 and
-// 27 us, since two waves a SIMD overlap already.)  The transposed scores' layout (lane group h of 2 holds
-// rows 8 a + 4 h + b) is again made the second product's operand by the order
-// in which rows of K are fed: row 8 a + 4 h + b of a 32-token tile is token
-// 16 (a / 2) + 8 h + 4 (a % 2) + b, so a lane ends up with runs of 8 tokens.
+// 27 us, since two waves a SIMD overlap already.)  bf16 calls round a weight
+// to bf16 once, and results differ from 64 bits by 0.0023 of their size
+// instead of 0.0017: a second part, as single tokens take it, is half as many
+// matrix instructions again where those bound the kernel (331 us against 244
+// and 27.7 against 24.4), and the sum of the rounded weights in place of the
+// exact ones' gains next to nothing (0.00226; 253 us).  The same call in fp32
+// keeps 24 bits.
+// The transposed scores' layout (lane group h of 2 holds rows 8 a + 4 h + b) is
+// again made the second product's operand by the order in which rows of K are
+// fed: row 8 a + 4 h + b of a 32-token tile is token 16 (a / 2) + 8 h + 4 (a % 2) + b,
+// so a lane ends up with runs of 8 tokens.
 //
 // KW waves share a row tile and take a page each of the KW that a step holds;
 // they are joined in LDS at the end.  Large calls take KW = 1 (128 rows of

@@ -461,6 +461,23 @@ def test_attend_long_and_divided(dtype):
         expect(p.g, p.m, [1, 1], q, None, 0.125, 3000, 200, out, out)
 
 
+@pytest.mark.parametrize("d,heads,N,L", [(64, 6, 1, 1000), (128, 8, 1, 4000), (96, 4, 3, 300), (32, 2, 20, 700), (256, 4, 12, 900),
+                                         (192, 3, 16, 500), (64, 64, 1, 3000)])
+def test_attend_weights_of_few_rows(d, heads, N, L):
+    """bf16 calls of up to 64 rows a key head keep 16 bits of the softmax
+    weights (two parts, each off by 2^-8 at most): r = 2^-16 in the bound."""
+    p = Pair(1, d, 70, 1, 70, BF, seed=d)
+    p.append([0], L, x=p.tokens(1, L, scale=1.0))
+    q, qn = normal((1, N, heads, d), 21, BF)
+    scale, u = 1 / math.sqrt(d), 2.0 ** -24
+    for max_len in (0, L):
+        got = p.g.attend(ints([0]), q, max_len=max_len).float().cpu().numpy()[0]
+        want, spread, size = O.attend(*p.m.held(0), qn[0], scale)
+        tol = spread * (2 * (d + 8) * u * size + 8 * u + L * u + 2.0 ** -16) + 2.0 ** -8 * np.abs(want)
+        off = np.abs(got - want)
+        assert np.all(off <= tol), float((off - tol).max())
+
+
 @pytest.mark.parametrize("N", [1, 5, 14, 33])
 def test_attend_stays_in_its_workspace(N):
     """Whatever max_len a call names, it writes its partial results within
