@@ -487,12 +487,13 @@ class WindowAttention:
     def refresh(self):
         """Starts over with the weights and persistent rows as they are now:
         the windows are dropped, the persistent tokens written again."""
-        self.cache.free(None)
-        self._held = self.P
         if self.P:
             k, v = self._project(self.persistent[None], 0)[1:]
+        self.cache.free(None)
+        if self.P:
             self.cache.append(self._root[:1], k, v)
             self.cache.fork(self._root, self._slots)
+        self._held = self.P
 
     def _project(self, x, start):
         """Queries, keys (both rotated) and values of vectors that stand at
@@ -513,7 +514,9 @@ class WindowAttention:
     def _room(self, x, n, held):
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("WindowAttention counts its tokens on the host: it cannot be captured into a graph")
-        if x.shape[0] != self.batch or x.shape[2] != self.w_qkv.shape[1]:
+        T._same(self.w_qkv.dtype, ("the window", x))
+        _on(self.cache.device, ("the window", x))
+        if x.dim() != 3 or x.shape[0] != self.batch or x.shape[2] != self.w_qkv.shape[1]:
             raise ValueError("expected [%d][tokens][%d], got %s" % (self.batch, self.w_qkv.shape[1], tuple(x.shape)))
         if n < 1 or held + n > self.P + self.max_tokens:
             raise ValueError("%d tokens behind %d: the window holds %d" % (n, held, self.P + self.max_tokens))
@@ -525,10 +528,11 @@ class WindowAttention:
         if n % 2:
             raise ValueError("a window holds %d persistent rows and as many recalled as segment rows, got %d rows"
                              % (self.P, window.shape[1]))
+        q, k, v = self._project(window[:, self.P:], self.P)   # before anything is dropped, should it fail
         self.cache.free(self._slots)
         if self.P:
             self.cache.fork(self._root, self._slots)
-        q, k, v = self._project(window[:, self.P:], self.P)
+        self._held = self.P
         self.cache.append(self._slots, k, v)
         self._held = self.P + n
         return self._read(q[:, n // 2:])

@@ -131,6 +131,47 @@ def test_window_records_no_gradients_and_refuses_capture(monkeypatch):
     assert torch.equal(at(x), y)                                    # the refusals changed nothing
 
 
+@pytest.mark.parametrize("P", [0, 5])
+def test_window_after_a_call_that_failed(P, monkeypatch):
+    """A window or tokens of another type, device or rank are refused with the
+    sequences as they were; where a later step fails, what is counted is what
+    the cache holds."""
+    w, w_out, pers = weights(4, 2, 32, 48, P, BF, 2)
+    at, ref = (T.WindowAttention(w, w_out, 4, 2, 2, 24, pers, T.Rotary(32)) for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = lambda n: torch.randn((2, n, 48), generator=g, device="cuda").to(BF)  # noqa: E731
+    window = rows(P + 8)
+    if P:
+        window[:, :P] = pers
+    x, nxt = rows(1), rows(2)
+    assert torch.equal(at(window), ref(window))
+    for bad, error in ((window.float(), TypeError), (window.cpu(), ValueError), (window[0], (ValueError, IndexError))):
+        for call in (at, at.token):
+            with pytest.raises(error):
+                call(bad)
+        assert at.cache.lengths.tolist() == ref.cache.lengths.tolist()
+    assert torch.equal(at.token(x), ref.token(x))
+    append = at.cache.append
+
+    def fails(*args):
+        raise T.TMError("append", T.TM_ERR_HIP)
+
+    monkeypatch.setattr(at.cache, "append", fails)
+    with pytest.raises(T.TMError):
+        at.token(x)
+    monkeypatch.setattr(at.cache, "append", append)
+    assert torch.equal(at.token(nxt), ref.token(nxt))               # the failed token counts nowhere
+    monkeypatch.setattr(at.cache, "append", fails)
+    with pytest.raises(T.TMError):
+        at(window)
+    monkeypatch.setattr(at.cache, "append", append)
+    ref.cache.free(ints([0, 1]), ints([P, P]))                      # the persistent rows alone are held
+    ref._held = P
+    assert at.cache.lengths.tolist() == ref.cache.lengths.tolist()
+    assert torch.equal(at.token(x), ref.token(x))
+    assert torch.equal(at(window), ref(window))
+
+
 def test_as_attention_of_mac_segment():
     """Two segments through mac_segment with WindowAttention equal those with
     a function that makes its calls one by one on a cache of its own."""
