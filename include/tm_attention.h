@@ -33,8 +33,10 @@
  *           [n_pages][kv_heads][64][head_dim]
  *   values  e4m3 [n_pages][kv_heads][head_dim][64] (tokens innermost)
  * A copy of meta is a snapshot of the sequences' bookkeeping.  status[0]
- * holds sticky flags (below); status[1] and status[2] are the calls' own (0 in a
- * new cache).
+ * holds sticky flags (below); status[1] and status[2] are the calls' own: 0 in a
+ * new cache, and status[2] is 0 between calls, in a blob or a snapshot that is
+ * given back too (an append that finds it otherwise sets TM_CACHE_BAD_ENTRY,
+ * and the bookkeeping and codes mean nothing until tm_cache_init).
  * Quantisation: a block's exponent is the least e in [-110, 119] with
  * max |x| <= 448 2^e over its tokens, a code is x 2^-e rounded to nearest
  * even.  A block that is appended to keeps the larger of its exponent and
@@ -122,7 +124,8 @@ tm_status tm_rotary(const void* x, long x_batch, long x_token, void* y, long y_b
 #define TM_CACHE_NO_PAGES 2    /* an append was left out: not enough free pages */
 #define TM_CACHE_FULL 4        /* an append was left out: longer than seq_pages * 64 tokens */
 #define TM_CACHE_BAD_ENTRY 8   /* an entry was left out: a sequence out of range or listed before in the
-                                  call, a fork into a sequence that is not empty, a table entry out of range */
+                                  call, a fork into a sequence that is not empty, a table entry out of range;
+                                  or an append found status[2] other than 0 */
 
 typedef struct tm_cache tm_cache;
 

@@ -245,8 +245,9 @@ class Rotary:
 
 class PagedCache:
     """A paged cache in 8 bits: the handle and its blob (``blob``: a uint8
-    tensor of ``tm_cache_bytes`` bytes that already holds a cache; by default
-    a new, empty one).  The views ``meta``, ``lengths``, ``refs``, ``table``,
+    tensor of ``tm_cache_bytes`` bytes that already holds a cache, whose count
+    of an append in progress is cleared in the order of the current stream; by
+    default a new, empty one).  The views ``meta``, ``lengths``, ``refs``, ``table``,
     ``scales``, ``k``, ``v`` and ``status`` show its regions."""
 
     def __init__(self, kv_heads, head_dim, n_pages, n_seqs, seq_pages, device="cuda", blob=None):
@@ -277,6 +278,8 @@ class PagedCache:
         self._scale = 1.0 / math.sqrt(head_dim)
         if fresh:
             self.init()
+        else:
+            self.status[2:3].zero_()
 
     def __del__(self):
         try:

@@ -633,7 +633,11 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
     // orders nothing else, so it needs no fence (with one, a write-back
     // of the L2 each, a launch of 512 workgroups took 22 us instead of 13).
     __syncthreads();
-    if (i == 0) last = atomicAdd(&c.status[2], 1) == (int)(gridDim.x * gridDim.y) - 1;
+    if (i == 0) {
+        const unsigned n = gridDim.x * gridDim.y, before = (unsigned)atomicAdd(&c.status[2], 1);
+        last = before == n - 1;
+        if (before >= n) atomicOr(&c.status[0], TM_CACHE_BAD_ENTRY);   // the count did not begin at 0
+    }
     __syncthreads();
     if (!last) return;
     const int have = want > 0 ? scan_free(want) : 0;

@@ -379,6 +379,27 @@ def test_attend_bad_tables(H, d, dtype, N, L):
     expect(p.g, p.m, [1], q[1:], None, scale, 0, 0, out[1:], out[1:])
 
 
+@pytest.mark.parametrize("N", [1, 5])
+@pytest.mark.parametrize("left", [7, 100000, -3])
+def test_append_count_left_behind(N, left):
+    """A blob whose append count is not 0 (a copy taken in the middle of a
+    call): cleared where a handle adopts it, otherwise an append says so."""
+    p = Pair(1, 64, 6, 2, 3, BF, seed=N)
+    p.append([0], 30)
+    p.g.status[2] = left
+    old = p.g
+    p.g = T.PagedCache(1, 64, 6, 2, 3, blob=old.blob)
+    p.append([0], N)
+    p.check()
+    old.status[2] = left
+    x = p.tokens(1, N)
+    old.append(ints([0]), x[:, :, :1], x[:, :, 1:])                  # one workgroup: it is not the last by this count
+    assert old.lengths.tolist() == [30 + N, 0] and old.check()[0] == O.BAD_ENTRY
+    old.status.zero_()
+    p.append([0, 1], N)
+    p.check()
+
+
 # ---- attention ----
 
 def expect(cache, model, seqs, q, counts, scale, window, sink, got, before):
