@@ -520,8 +520,8 @@ __global__ __launch_bounds__(256) void append_token_kernel(AppendArgs a) {
 // workgroup changes; the last of them to be done, by a count in status[2] that
 // it sets back, makes the plan's changes.  A wave writes a head's token (ONE:
 // one token an entry at most), two its even and odd blocks.  64 entries of 8
-// heads, one token: 8 us against 5.5 and 4 in two launches, a call 3 us
-// shorter (with two waves a head as well 10 us: twice the workgroups).
+// heads, one token: 8 us against 5.5 and 4 in two launches, a call from the
+// host 2 to 3 us shorter (with two waves a head as well 10 us: twice the workgroups).
 constexpr int STEP_ENTRIES = 256, STEP_TOKENS = 16;
 template <class T, int D, bool ONE>
 __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a) {
@@ -535,8 +535,16 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
     __shared__ int flags, hint, last, doubles, own_rank, own_need;
     __shared__ AppendPlan own;
     const int from = min(max(c.status[1], 0), c.n_pages);
-    auto is_free = [&](int p) { return p < c.n_pages && c.refs[p] <= 0; };
-    const bool free0 = is_free(from + i);
+    constexpr int STEP = STEP_ENTRIES * 4;
+    auto free_of = [&](int p) {   // bit e: page p + e is free
+        int r[4], f = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = p + e < c.n_pages ? c.refs[p + e] : 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f |= (r[e] <= 0) << e;
+        return f;
+    };
+    const int free4 = free_of(from + i * 4);
     T kr[(D + 63) / 64], vr[(D + 63) / 64];
     if constexpr (ONE)
         if (h < c.H) load_token<T, D>(a, b, h, kr, vr);
@@ -588,14 +596,26 @@ __global__ __launch_bounds__(STEP_ENTRIES) void append_step_kernel(AppendArgs a)
         own_need = need;
     }
     __syncthreads();
-    // page_of: the first `upto` free pages in order, 256 at a time; how many there are
+    // page_of: the first free pages in order, `upto` of them at least, where
+    // there are so many; how many there are, `upto` at most.  A thread reads
+    // four references, and the last workgroup's second call goes on where its
+    // first stopped: behind one low hole and 30000 used pages an append takes
+    // 38 us, as the plan of its own launch does (a reference a thread and the
+    // whole scan twice: 145).
+    int found = 0, next = from;
     auto scan_free = [&](int upto) {
-        int found = 0;
-        for (int p0 = from; p0 < c.n_pages && found < upto; p0 += STEP_ENTRIES) {
-            const bool is = p0 == from ? free0 : is_free(p0 + i);
+        while (found < upto && next < c.n_pages) {
+            const int p = next + i * 4, now4 = next == from ? free4 : free_of(p);
+            next += STEP;
             int total;
-            const int r = found + block_scan<STEP_ENTRIES>(is, wave_sums, total) - 1;
-            if (is && r < upto) page_of[r] = p0 + i;
+            const int n4 = __popc(now4);
+            int r = found + block_scan<STEP_ENTRIES>(n4, wave_sums, total) - n4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!(now4 >> e & 1)) continue;
+                if (r < 2 * STEP_ENTRIES) page_of[r] = p + e;
+                ++r;
+            }
             found += total;
         }
         __syncthreads();
@@ -1007,15 +1027,23 @@ tm_status tm_cache_append(const tm_cache* c, void* blob, const int* seqs, const 
                  static_cast<AppendPlan*>(workspace)};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const dim3 each((unsigned)c->H, (unsigned)batch);
-    // One launch while its workgroups are few, since the count that ends it is a
-    // place that each of them goes to, and one or two waves copy a shared page's
-    // head where the write has four.  8 heads of 128, passes with the calls that
-    // free or fork beside: 2 tokens, 64 entries 17.5 us against 19.8, 128 that
-    // all copy 30 against 34; one token, 64 entries 17.4 against 20, 128 that
-    // all copy 30.5 against 27.3.
+    // One launch while its workgroups are few: it saves the host a launch, and
+    // takes the GPU longer than the two, the more the more workgroups go to the
+    // count that ends it; a shared page's head is copied by one or two waves
+    // where the write has four.  8 heads of 128, a call from the host (with a
+    // small copy beside it) / on the GPU alone (in a graph), us, one launch against two; tokens into begun
+    // blocks, then into copies of shared pages:
+    //   one token, 16 entries   14.5/5.9 against 16.9/5.0    20.2/18.1 against 17.1/11.1
+    //              64           14.6/7.5 against 16.8/5.9    21.7/19.5 against 17.0/13.4
+    //              128          14.6/9.6 against 16.8/7.2    25.0/22.9 against 19.6/17.6
+    //   4 tokens,  16           14.6/8.9 against 16.9/8.1    16.1/14.2 against 17.0/12.0
+    //              64           14.6/11.5 against 16.9/9.6   19.2/17.1 against 19.8/17.8
+    //              128          17.8/15.7 against 16.8/12.0  25.5/23.3 against 27.8/25.7
+    // So: 4 tokens up to 64 entries of these; one token, whose copies lose by
+    // it, too, though other single tokens would gain up to 256 entries.
     const int heads = n_tokens == 1 ? 4 : 2;
     const dim3 step((unsigned)((c->H + heads - 1) / heads), (unsigned)batch);
-    if (n_tokens <= STEP_TOKENS && batch <= STEP_ENTRIES && (long)batch * step.x <= (n_tokens == 1 ? 128 : 512)) {
+    if (n_tokens <= STEP_TOKENS && batch <= STEP_ENTRIES && (long)batch * step.x <= (n_tokens == 1 ? 128 : 256)) {
         return status_of(timed_attn(st, [&] {
             return for_head_dim(c->d, [&](auto D) {
                 if (dtype == TM_F32) {

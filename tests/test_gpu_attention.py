@@ -268,6 +268,29 @@ def test_few_tokens_against_model(H, d, dtype, n_seqs, n_pages):
     p.check()
 
 
+@pytest.mark.parametrize("N", [1, 9, 40])
+def test_append_into_a_scattered_pool(N):
+    """Free pages far apart and in bunches of more than a call wants: each
+    entry gets the lowest ones, whatever lies between, until there are none."""
+    p = Pair(1, 32, 3300, 40, 6, BF, seed=N)
+    rng = np.random.default_rng(N)
+    holes = {0, 3, 255, 256, 1023, 1024, 1500, 2047, 2048, 2600, 3290, 3299}
+    holes |= set(range(2700, 3240, 7)) | {3 + int(x) for x in rng.integers(0, 900, 12)}
+    for page in range(3300):
+        if page not in holes:
+            p.m.refs[page] = 1
+    p.g.refs.copy_(ints(p.m.refs))
+    seqs = list(range(30))
+    p.append(seqs, 63 if N < 40 else 30, [60 + i % 4 if N < 40 else 30 for i in range(30)])
+    p.fork([0, 1, 2], [30, 31, 32])
+    for i in range(14):
+        p.append([int(x) for x in rng.permutation(33)], N)
+        if i % 3 == 2:
+            p.free([int(x) for x in rng.permutation(33)[:2]])        # low pages go free again: the bound follows
+        p.check()
+    assert p.m.flags & ~(O.NO_PAGES | O.FULL) == 0
+
+
 def test_few_tokens_take_the_last_pages():
     """An entry that needs two pages (a copy and the next) and finds one takes
     none; the page goes to the next call."""
