@@ -126,6 +126,15 @@ def _list(name, t, n):
             raise ValueError("%s must be contiguous and hold %d values, got %s" % (name, n, tuple(t.shape)))
 
 
+_INT_MAX = (1 << 31) - 1
+
+
+def _int(v):
+    """A number as the C calls take it: one beyond 32 bits (which would lose
+    its upper ones) as the largest, or as -1, which they refuse or treat as it."""
+    return v if -1 <= v <= _INT_MAX else max(-1, min(v, _INT_MAX))
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -156,7 +165,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def tm_rotary_frequencies(rot_dim, base=10000.0, scaling=TM_ROPE_NONE, factor=1.0, original_len=0.0, beta_fast=32.0,
                           beta_slow=1.0):
     """(list of rot_dim / 2 frequencies, factor of the result)."""
-    f, s = (_d * max(1, rot_dim // 2))(), _d(1.0)
+    rot_dim = _int(rot_dim)
+    f, s = (_d * max(1, min(rot_dim, 1024) // 2))(), _d(1.0)
     T._check("tm_rotary_frequencies", _lib().tm_rotary_frequencies(rot_dim, base, scaling, factor, original_len,
                                                                   beta_fast, beta_slow, f, ctypes.byref(s)))
     return list(f), s.value
@@ -195,7 +205,7 @@ def tm_rotary(x, y, positions, freq, result_scale=1.0, layout=TM_ROPE_HALF, inve
 
 def tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages):
     h = _vp()
-    T._check("tm_cache_create", _lib().tm_cache_create(kv_heads, head_dim, n_pages, n_seqs, seq_pages,
+    T._check("tm_cache_create", _lib().tm_cache_create(*map(_int, (kv_heads, head_dim, n_pages, n_seqs, seq_pages)),
                                                        ctypes.byref(h)))
     return h
 
@@ -216,7 +226,7 @@ def tm_cache_layout(cache):
 
 
 def tm_cache_workspace_bytes(cache, batch, n_tokens, heads=0):
-    return _lib().tm_cache_workspace_bytes(cache, batch, n_tokens, heads)
+    return _lib().tm_cache_workspace_bytes(cache, _int(batch), _int(n_tokens), _int(heads))
 
 
 # ---------------------------------------------------------------------------
@@ -365,7 +375,7 @@ class PagedCache:
             out = (torch.empty_like if counts is None else torch.zeros_like)(q, memory_format=torch.contiguous_format)
         ws = self._workspace(*sizes)
         self._call("tm_cache_attend", _at(seqs), _at(counts), pq, *d_q, out.data_ptr(), *sizes,
-                   self._scale if scale is None else scale, window, sink, max_len, dt, ws.data_ptr())
+                   self._scale if scale is None else scale, _int(window), _int(sink), _int(max_len), dt, ws.data_ptr())
         return out
 
     def read(self, seqs, start, n_tokens, dtype=torch.float32, k=None, v=None, stream=None):
@@ -387,7 +397,7 @@ class PagedCache:
         if not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("k and v must be contiguous")
         _on(self.device, ("k", k), ("v", v), ("seqs", seqs))
-        self._call("tm_cache_read", _at(seqs), start, k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
+        self._call("tm_cache_read", _at(seqs), _int(start), k.data_ptr(), v.data_ptr(), B, n_tokens, dt)
         return k, v
 
     def fork(self, src, dst, stream=None):

@@ -254,6 +254,23 @@ def test_calls_beyond_a_launch():
     A.tm_cache_destroy(h)
 
 
+def test_numbers_beyond_32_bits():
+    """They are refused or count as the largest, never as what is left of them."""
+    assert [A._int(v) for v in (0, -1, 7, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, -5, -(1 << 32))] == [
+        0, -1, 7, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, -1, -1]
+    big = 1 << 32
+    for args in ((big + 1, 32, 2, 1, 2), (1, big + 32, 2, 1, 2), (1, 32, big + 2, 1, 2), (1, 32, 2, big + 1, 2),
+                 (1, 32, 2, 1, big + 2)):
+        with pytest.raises(T.TMError):
+            A.tm_cache_create(*args)
+    for rot_dim in (big + 8, -big + 8, -7):
+        with pytest.raises(T.TMError):
+            T.tm_rotary_frequencies(rot_dim)
+    h = A.tm_cache_create(1, 32, 2, 4, 2)
+    assert A.tm_cache_workspace_bytes(h, 1, big + 1, 1) >= A.tm_cache_workspace_bytes(h, 1, 1 << 30, 1)
+    A.tm_cache_destroy(h)
+
+
 def test_binding_checks():
     bf, f32 = torch.bfloat16, torch.float32
     x = torch.zeros((1, 2, 3, 8))

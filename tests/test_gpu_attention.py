@@ -559,6 +559,23 @@ def test_attend_window_beyond_any_sequence():
         expect(p.g, p.m, [0, 1], q, None, 0.125, 0, 0, out, out)
 
 
+def test_numbers_past_32_bits():
+    """Windows, sinks, lengths and starts past 32 bits are what they say."""
+    p = Pair(1, 64, 10, 2, 4, BF, seed=16)
+    p.append([0, 1], 150, [150, 70])
+    q, big = normal((2, 3, 2, 64), 3)[0], 1 << 32
+    want = p.g.attend(None, q)
+    for kw in (dict(window=big + 5), dict(window=20, sink=big + 1), dict(max_len=big + 64), dict(window=big, sink=big)):
+        assert torch.equal(p.g.attend(None, q, **kw), want)
+    k, v = p.g.read(None, big + 3, 10)
+    assert not k.any() and not v.any()
+    for kw in (dict(window=-big), dict(sink=-big + 2), dict(max_len=-big)):
+        with pytest.raises(T.TMError):
+            p.g.attend(None, q, **kw)
+    with pytest.raises(T.TMError):
+        p.g.read(None, -big, 10)
+
+
 def test_pools_past_32_bit_offsets():
     """Pages whose keys and values lie beyond 4 GiB of the pool's start: the
     same calls as on a small pool give the same codes and results."""
