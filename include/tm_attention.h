@@ -90,7 +90,8 @@ typedef enum {
 /* Host only: freq [rot_dim / 2] = base^(-2 i / rot_dim), scaled as `scaling`
  * says (factor > 0; original_len, beta_fast > beta_slow > 0 for
  * TM_ROPE_PARTS), and the factor the rotated elements take (1 unless
- * TM_ROPE_PARTS).  rot_dim: even, 2 .. 1024; base > 1. */
+ * TM_ROPE_PARTS).  rot_dim: even, 2 .. 1024; base > 1; a scaled base or a
+ * frequency that would overflow is refused. */
 tm_status tm_rotary_frequencies(int rot_dim, double base, tm_rope_scaling scaling, double factor,
                                 double original_len, double beta_fast, double beta_slow, double* freq,
                                 double* result_scale);

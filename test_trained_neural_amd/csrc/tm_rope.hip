@@ -182,7 +182,10 @@ tm_status tm_rotary_frequencies(int rot_dim, double base, tm_rope_scaling scalin
         return TM_ERR_INVALID;
     const int n = rot_dim / 2;
     const double r = rot_dim, pi = 3.14159265358979323846;
-    if (scaling == TM_ROPE_BASE) base *= pow(factor, r / (r - 2.0));
+    if (scaling == TM_ROPE_BASE) {
+        base *= pow(factor, r / (r - 2.0));
+        if (!(base > 0.0) || !isfinite(base)) return TM_ERR_INVALID;
+    }
     *result_scale = 1.0;
     double lo = 0.0, hi = 0.0;
     if (scaling == TM_ROPE_PARTS) {
@@ -205,6 +208,7 @@ tm_status tm_rotary_frequencies(int rot_dim, double base, tm_rope_scaling scalin
         } else {
             freq[i] = f;
         }
+        if (!isfinite(freq[i])) return TM_ERR_INVALID;
     }
     return TM_OK;
 }

@@ -163,6 +163,15 @@ def test_frequencies_refusals(args):
     assert e.value.code == T.TM_ERR_INVALID
 
 
+@pytest.mark.parametrize("args", [dict(rot_dim=8, scaling=1, factor=1e-310), dict(rot_dim=4, scaling=2, factor=1e200),
+                                  dict(rot_dim=4, scaling=2, factor=1e-200),
+                                  dict(rot_dim=8, scaling=3, factor=1e-310, original_len=4)])
+def test_frequencies_that_overflow(args):
+    with pytest.raises(T.TMError) as e:
+        T.tm_rotary_frequencies(**args)
+    assert e.value.code == T.TM_ERR_INVALID
+
+
 def test_create_refusals_and_sizes():
     for args in [(0, 64, 4, 1, 1), (1025, 64, 4, 1, 1), (2, 48, 4, 1, 1), (2, 288, 4, 1, 1), (2, 0, 4, 1, 1),
                  (2, 64, 0, 1, 1), (2, 64, (1 << 24) + 1, 1, 1), (2, 64, 4, 0, 1), (2, 64, 4, 8193, 1), (2, 64, 4, 1, 0),
