@@ -479,6 +479,39 @@ def test_attend(case, max_len):
     expect(p.g, p.m, seqs, q, counts, scale, window, sink, out, before)
 
 
+SHAPES = {  # how a call is launched: entries, kv heads, heads of each, query tokens, lengths (entries take them in turn), pages
+    "few rows, waves share the sequence": (2, 2, 3, 4, [300, 70], 5),
+    "few rows, ranges": (2, 2, 3, 4, [1500, 700], 30),
+    "few rows, many ranges": (2, 1, 2, 1, [9300, 1000], 150),
+    "two row groups": (2, 1, 5, 5, [1500, 70], 30),
+    "four row groups": (2, 1, 12, 5, [1500, 70], 30),
+    "four row groups, many ranges": (1, 1, 60, 1, [9000], 150),
+    "many rows, waves share the sequence": (2, 1, 2, 70, [200, 130], 4),
+    "many rows, ranges": (2, 1, 2, 70, [2600, 900], 41),
+    "many rows, many ranges": (1, 1, 5, 33, [5000], 80),
+    "many rows, many tiles": (8, 64, 1, 70, [150, 71, 20], 3)}
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", range(32, 257, 32))
+@pytest.mark.parametrize("shape", SHAPES)
+def test_attend_every_width(shape, d, dtype):
+    """Each way that a call is launched, at every head width and type: ragged
+    counts, without a mask and with a window and a sink."""
+    B, H, G, N, lengths, pages = SHAPES[shape]
+    lengths = [lengths[b % len(lengths)] for b in range(B)]
+    seqs = list(range(B))[::-1]
+    p = Pair(H, d, sum(-(-n // 64) for n in lengths) + 2, B, pages, dtype, seed=d + N)
+    p.append(seqs, max(lengths), lengths, x=p.tokens(B, max(lengths), scale=1.0))
+    q, _ = normal((B, N, H * G, d), 5, dtype, 0.5)
+    counts = [N - 2 * b % N for b in range(B)] if N > 1 else None
+    for window, sink in ((0, 0), (100, 70)):
+        out = torch.full((B, N, H * G, d), 3.0, dtype=dtype, device="cuda")
+        before = out.clone()
+        p.g.attend(ints(seqs), q, None if counts is None else ints(counts), window=window, sink=sink, out=out)
+        expect(p.g, p.m, seqs, q, counts, 1 / math.sqrt(d), window, sink, out, before)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, -1e-42])
 @pytest.mark.parametrize("dtype,N", [(BF, 3), (F32, 2), (BF, 40), (F32, 40)])
 def test_attend_scales(dtype, N, scale):
