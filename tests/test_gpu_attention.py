@@ -87,6 +87,25 @@ def test_rotary_in_place_and_strided_output():
     assert rot(x[:, :0], pos[:, :0].contiguous()).shape == (2, 0, 4, 64)
 
 
+@pytest.mark.parametrize("layout", [T.TM_ROPE_HALF, T.TM_ROPE_INTERLEAVED])
+@pytest.mark.parametrize("dtype,d,r", [(BF, 128, 128), (F32, 96, 64)])
+def test_rotary_of_large_tensors(dtype, d, r, layout):
+    """What is too large for the caches takes another way to memory: the same
+    bits as in parts, in place too."""
+    x = torch.randn((2, 9000, 40, d), device="cuda", dtype=dtype)
+    assert x.numel() * x.element_size() * 2 > 256 << 20
+    pos = torch.arange(18000, dtype=torch.int32, device="cuda").view(2, 9000) * 7
+    rot = T.Rotary(r, layout=layout)
+    y = rot(x, pos)
+    for b in range(2):
+        for t in range(0, 9000, 3000):
+            part = x[b:b + 1, t:t + 3000]
+            assert part.numel() * part.element_size() * 2 < 256 << 20
+            assert torch.equal(y[b:b + 1, t:t + 3000], rot(part, pos[b:b + 1, t:t + 3000].contiguous()))
+    rot(x, pos, out=x)
+    assert torch.equal(x, y)
+
+
 # ---- the cache against its model ----
 
 class Pair:
@@ -266,6 +285,26 @@ def test_few_tokens_against_model(H, d, dtype, n_seqs, n_pages):
     p.free([0])
     p.append([1, 2, 3], 9)
     p.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", range(32, 257, 32))
+def test_append_and_read_every_width(d, dtype):
+    """Each way that an append is launched (single tokens of few and of many
+    entries, a few tokens, many), into copies too, at every head width and
+    type; what is held reads back exactly in both types."""
+    p = Pair(1, d, 330, 140, 3, dtype, seed=d + 3)
+    p.append(list(range(130)), 20, [1 + i % 20 for i in range(130)])
+    p.fork([3, 4, 15, 20], [130, 131, 132, 133])
+    p.append(list(range(4, 134)), 1)
+    p.append([5, 3, 20], 1)
+    p.fork([7, 7], [134, 135])
+    p.append([134, 7, 8], 9)
+    p.append([135, 9, 10], 50)
+    p.check()
+    k, v = p.g.read(None, 5, 40)
+    for x, y in zip((k, v), p.g.read(None, 5, 40, dtype=BF)):
+        assert torch.equal(x.to(BF), y) and torch.equal(x, y.float())
 
 
 @pytest.mark.parametrize("N", [1, 9, 40])
