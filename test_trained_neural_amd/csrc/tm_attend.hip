@@ -803,9 +803,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && D <= 128 ? 2 : 1) voi
     }
 }
 
-// One launch instead of ranges: head widths and pages up to which single
-// tokens take it.
-constexpr int ONE_DIM = 128, ONE_PAGES = 24;
+// One launch instead of ranges: head widths up to which calls take it, and
+// pages up to which single tokens do (ONE_PAGES_MID: 65 to 256 workgroups).
+constexpr int ONE_DIM = 128, ONE_PAGES = 24, ONE_PAGES_MID = 40;
 
 // Joins the ranges of a row, a few lanes per range so that several are read
 // at a time: a wave per row (ONE), or where there are many ranges a workgroup
@@ -897,15 +897,23 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     if (p.splits > fit) p.splits = fit < 1 ? 1 : (int)fit;
     // One launch of eight waves, which share the sequence among them, instead
     // of ranges and their join (registers and LDS allow it up to width 128).
-    // Rows: up to 24 pages (2 x 6 heads of 64, 500 tokens: 8.7 us against 12.1,
-    // 2064 tokens: the same), 40 where the heads and entries fill the chip
-    // (22 x 6 heads of 64, 2064 tokens: 12.7 us against 15.7).  Tiles: counted in page steps, a step of KW pages
+    // Rows: where there would be ranges (more than 8 pages) but few of them.
+    // Eight waves against four with ranges, us on the GPU, single tokens in bf16:
+    //   heads x entries  width   200       1000       1500       2064       4000 tokens
+    //   12               64      5.6/5.5   7.7/9.4    8.8/9.4    10.2/9.5   15.0/9.6
+    //                    128     7.6/7.4   12.6/11.9  15.4/12.1  18.1/12.3  28/12
+    //   128              64      5.8/5.5   7.9/9.8    9.7/11.7   12.0/14.1  17.5/18.6
+    //                    128     7.8/7.3   13.9/13.6  17.1/18.9  19.8/24.2  31/31
+    //   384              64      7.2/6.5   13.5/16.8  17.6/20.4  22.2/25.6  37/38
+    //                    128     14/10     28/27      35/33      43/43      90/83
+    // (fp32 the same to 10%).  Tiles: counted in page steps, a step of KW pages
     // at 1.6 of one page's and a join at 8 steps of width 64 and 6 of width
     // 128 (2 x 1024 queries of 6 heads of 64 over 2064 tokens: 24.7 us against
     // 30.4; 2 x 512 queries of 8 heads on 2 of 128 over 4000: 78 against 43).
     if (c->d > ONE_DIM) return p;
     if (!p.wide) {
-        if (rows > 16 || pages > (groups >= 64 && groups <= 256 ? 40 : ONE_PAGES)) return p;
+        const int most = groups > 64 && groups <= 256 ? ONE_PAGES_MID : c->d < ONE_DIM ? ONE_PAGES : 0;
+        if (rows > 16 || pages <= ROW_PAGES || pages > most) return p;
         p.waves = 8;
     } else {
         const int kw = c->d <= 64 ? 4 : 2, tile = 256 / kw;

@@ -520,6 +520,7 @@ def test_attend(case, max_len):
 
 SHAPES = {  # how a call is launched: entries, kv heads, heads of each, query tokens, lengths (entries take them in turn), pages
     "few rows, waves share the sequence": (2, 2, 3, 4, [300, 70], 5),
+    "few rows of many heads, waves share the sequence": (2, 40, 3, 4, [700, 70], 11),
     "few rows, ranges": (2, 2, 3, 4, [1500, 700], 30),
     "few rows, many ranges": (2, 1, 2, 1, [9300, 1000], 150),
     "two row groups": (2, 1, 5, 5, [1500, 70], 30),
