@@ -865,8 +865,8 @@ struct AttendPlan {
     int kw;          // its KW
     int waves, tile_rows, tiles, splits, least;
 };
-// Ranges, at most: as many workgroups as the compute units take at a time
-// (tiles), or several rounds of them, which even out ragged lengths (rows: 48
+// Ranges, at most: as many workgroups as the compute units take at a time in
+// bf16 (tiles; in fp32 a unit takes one from width 96 on, so two rounds), or several rounds of them, which even out ragged lengths (rows: 48
 // sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with 1024
 // workgroups, 289 us with 8192), and at least TILE_PAGES or ROW_PAGES pages a
 // range.  Grows with `pages`, so the workspace is that of the longest sequence
@@ -879,7 +879,7 @@ static int most_ranges(const tm_cache* c, bool wide, long groups, long pages) {
     if (s > 256) s = 256;
     return s < 1 ? 1 : (int)s;
 }
-static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len) {
+static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int heads, long max_len, bool f32) {
     AttendPlan p;
     const long rows = (long)n_tokens * (heads / c->H), pages = (max_len + PAGE - 1) / PAGE;
     p.wide = rows > 64;
@@ -906,10 +906,21 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     //                    128     7.8/7.3   13.9/13.6  17.1/18.9  19.8/24.2  31/31
     //   384              64      7.2/6.5   13.5/16.8  17.6/20.4  22.2/25.6  37/38
     //                    128     14/10     28/27      35/33      43/43      90/83
-    // (fp32 the same to 10%).  Tiles: counted in page steps, a step of KW pages
-    // at 1.6 of one page's and a join at 8 steps of width 64 and 6 of width
-    // 128 (2 x 1024 queries of 6 heads of 64 over 2064 tokens: 24.7 us against
-    // 30.4; 2 x 512 queries of 8 heads on 2 of 128 over 4000: 78 against 43).
+    // (fp32 the same to 10%).
+    // Tiles: by the time that 256 workgroups take for a page, that as many of
+    // eight waves take for KW pages, and of the ranges' join (its launch and the
+    // partial results' way out and in), fitted to 480 calls measured in both
+    // forms; the choice is 2% slower than the better one on average, 1.5 times
+    // at most.  us on the GPU, eight waves against four:
+    //   heads x entries  queries, of   width 64: bf16, fp32   width 128: bf16, fp32
+    //   6 x 2            512, 1040     16/19      24/24      29/26      54/35
+    //   6 x 2            1024, 2064    24/31      37/42      48/38      96/70
+    //   6 x 2            2048, 2048    27/42      40/60      45/51      93/83
+    //   8 x 2 (2 key)    512, 4096     36/32      60/47      77/43      163/85
+    //   8 x 2 (2 key)    2048, 2048    29/50      44/75      45/61      93/100
+    //   8 x 8            128, 128      8.7/8.8    11/12      11/11      18/17
+    //   8 x 8            128, 4096     36/30      58/46      78/41      170/86
+    //   32 x 8 (8 key)   1024, 2064    277/150    433/345    299/249    660/757
     if (c->d > ONE_DIM) return p;
     if (!p.wide) {
         const int most = groups > 64 && groups <= 256 ? ONE_PAGES_MID : c->d < ONE_DIM ? ONE_PAGES : 0;
@@ -918,9 +929,12 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     } else {
         const int kw = c->d <= 64 ? 4 : 2, tile = 256 / kw;
         const long tiles = (rows + tile - 1) / tile, rounds = ((long)batch * c->H * tiles + 255) / 256;
-        const long here = rounds * ((pages + kw - 1) / kw) * 16;
-        const long there = ((pages + p.splits - 1) / p.splits + (p.splits > 1 ? (c->d <= 64 ? 8 : 6) : 0)) * 10 *
-                           ((groups + 511) / 512);
+        const double page = (0.3 + c->d * 0.0043) * (f32 ? 2.6 : 1.0);   // us
+        const double step = page * (c->d <= 64 ? (f32 ? 2.2 : 3.0) : (f32 ? 1.6 : 2.3));
+        const double part = (double)groups * p.tile_rows * p.splits * (c->d + 2) * 8;   // bytes, written and read
+        const double here = (double)(rounds * ((pages + kw - 1) / kw)) * step;
+        const double there = (double)((groups * p.splits + 255) / 256 * ((pages + p.splits - 1) / p.splits)) * page +
+                             (p.splits > 1 ? 3.3 + part * 0.35e-6 : 0.0);
         if (here > there) return p;
         p.waves = 8;
         p.kw = kw;
@@ -1006,7 +1020,8 @@ extern "C" tm_status tm_cache_attend(const tm_cache* c, const void* blob, const 
     if (batch > 65535 || (!seqs && batch > c->n_seqs) || n_tokens > 1 << 24 || (uintptr_t)seqs % 4 || (uintptr_t)counts % 4 ||
         !ptr_ok(q, 16) || !ptr_ok(out, 16) || !strides_ok(q_batch, q_token))
         return TM_ERR_INVALID;
-    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most);
+    const AttendPlan p = attend_plan(c, batch, n_tokens, heads, max_len > 0 && max_len < most ? max_len : most,
+                                     dtype == TM_F32);
     // a launch has fewer than 2^32 threads along an axis
     if ((long)p.tiles * p.splits * c->H * 64 * p.waves >= 1L << 32) return TM_ERR_INVALID;
     if (p.splits > 1 && !ptr_ok(workspace, 256)) return TM_ERR_INVALID;

@@ -527,6 +527,7 @@ SHAPES = {  # how a call is launched: entries, kv heads, heads of each, query to
     "four row groups": (2, 1, 12, 5, [1500, 70], 30),
     "four row groups, many ranges": (1, 1, 60, 1, [9000], 150),
     "many rows, waves share the sequence": (2, 1, 2, 70, [200, 130], 4),
+    "many rows of many heads, waves share the sequence": (4, 64, 1, 70, [500, 460], 8),
     "many rows, ranges": (2, 1, 2, 70, [2600, 900], 41),
     "many rows, many ranges": (1, 1, 5, 33, [5000], 80),
     "many rows, many tiles": (8, 64, 1, 70, [150, 71, 20], 3)}
