@@ -42,8 +42,8 @@
  * even.  A block that is appended to keeps the larger of its exponent and
  * the new tokens'; where it grows, the codes it held are rounded to the new
  * scale (exactly, but for those that become subnormal: scales are powers of
- * two).  A non-finite element of k or v is held as zero and sets
- * TM_CACHE_NONFINITE.
+ * two).  An element beyond 448 * 2^119 (2.98e38) is held as that.  A
+ * non-finite element of k or v is held as zero and sets TM_CACHE_NONFINITE.
  * Pages.  Sequences may share pages (tm_cache_fork); a call never writes to
  * a page that others hold too: tm_cache_append first gives the sequence a
  * copy of a shared last page.  Pages are handed out the lowest free one
@@ -172,7 +172,8 @@ tm_status tm_cache_append(const tm_cache* cache, void* blob, const int* seqs, co
  * one out of range) gives zeros; rows i >= counts[b] of out are left as they
  * were.  A page whose table entry is out of range counts as not visible.
  * heads: a multiple of kv_heads, at most 64 * kv_heads.  out: contiguous
- * [batch][n_tokens][heads][head_dim] of dtype.  Products of bf16 calls are
+ * [batch][n_tokens][heads][head_dim] of dtype; it may be q, if q is contiguous,
+ * and must not overlap it otherwise.  Products of bf16 calls are
  * of bf16 operands with fp32 accumulation (the cache's values are exact in
  * bf16; the softmax weights keep 16 bits where n_tokens * heads / kv_heads is
  * at most 64, and are rounded to bf16 above), those of fp32 calls keep 24
@@ -196,8 +197,8 @@ tm_status tm_cache_read(const tm_cache* cache, const void* blob, const int* seqs
 
 /* dst[i] becomes a copy of sequence src[i] that shares its pages.  dst[i]
  * must be empty and listed once; sources are read as they were before the
- * call, and a destination must not be another entry's source.  An entry
- * against these rules is left out (TM_CACHE_BAD_ENTRY).  n at most n_seqs. */
+ * call.  An entry whose dst is not empty or listed before, or whose src is
+ * listed as a dst, is left out (TM_CACHE_BAD_ENTRY).  n at most n_seqs. */
 tm_status tm_cache_fork(const tm_cache* cache, void* blob, const int* src, const int* dst, int n, void* stream);
 
 /* Drops the tokens from keep[i] (device int32; null: 0) on of sequence

@@ -6,7 +6,8 @@ is argument marshalling only: the functions carry the C names and check
 types, shapes and devices before a pointer is passed on.  ``Rotary`` and
 ``PagedCache`` keep a frequency table and a cache's blob and allocate
 outputs; ``WindowAttention`` puts them together as the attention of
-``mac_segment``.
+``mac_segment``, with torch's plain products for its two projections.
+Nothing here records gradients (``Rotary``'s is a call of its own).
 
 Calls run on the current stream of the tensors' device (or on ``stream``).
 """
@@ -348,8 +349,9 @@ class PagedCache:
     def attend(self, seqs, q, counts=None, scale=None, window=0, sink=0, max_len=0, out=None, stream=None):
         """Attention of q [B][T][heads][d], each sequence's last tokens
         (``counts`` of them), over the cache; scale: 1 / sqrt(d) by default.
-        Returns [B][T][heads][d] of q's type.  Rows behind an entry's count
-        are left as they were: zeros in a new output."""
+        Returns [B][T][heads][d] of q's type (``out`` may be a contiguous q).
+        Rows behind an entry's count are left as they were: zeros in a new
+        output."""
         if _elsewhere(self._index, stream):
             with _there(self.device, stream):
                 return self.attend(seqs, q, counts, scale, window, sink, max_len, out)

@@ -633,6 +633,34 @@ def test_attend_window_beyond_any_sequence():
         expect(p.g, p.m, [0, 1], q, None, 0.125, 0, 0, out, out)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,heads,L,max_len", [(1, 8, 200, 200), (4, 8, 700, 700), (4, 8, 2000, 0), (14, 8, 700, 0), (40, 8, 300, 300),
+                                               (50, 8, 2000, 0)])
+def test_attend_into_its_queries(dtype, N, heads, L, max_len):
+    """The output may take the queries' place, however the call is launched."""
+    p = Pair(2, 64, 70, 2, 32, dtype, seed=N)
+    p.append([0, 1], L, [L, 150], x=p.tokens(2, L, scale=1.0))
+    q = normal((2, N, heads, 64), 3, dtype)[0]
+    counts = ints([N, max(1, N // 2)])
+    want = p.g.attend(None, q, counts, max_len=max_len, out=q.clone())
+    assert torch.equal(p.g.attend(None, q, counts, max_len=max_len, out=q), want)
+
+
+def test_values_beyond_the_largest_scale():
+    """Finite elements beyond 448 * 2^119 are held as that, in the order of a
+    block's other elements, and set no flag."""
+    c = T.PagedCache(1, 32, 4, 2, 2)
+    top = 448.0 * 2.0 ** 119
+    x = torch.full((1, 20, 1, 32), 1.0, device="cuda")
+    x[0, 3, 0, 4], x[0, 3, 0, 5], x[0, 3, 0, 6] = 3.4e38, -3.3e38, top
+    c.append(ints([0]), x, x)
+    c.append(ints([1]), x[:, 3:4].contiguous(), x[:, 3:4].contiguous())
+    for s, t in ((0, 3), (1, 0)):
+        for y in c.read(ints([s]), t, 1):
+            assert y[0, 0, 0, 4:7].tolist() == [top, -top, top] and not y[0, 0, 0, 7:].any()
+    assert c.check()[0] == 0
+
+
 def test_numbers_past_32_bits():
     """Windows, sinks, lengths and starts past 32 bits are what they say."""
     p = Pair(1, 64, 10, 2, 4, BF, seed=16)
