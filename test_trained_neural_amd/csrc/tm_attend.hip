@@ -194,7 +194,7 @@ __device__ __forceinline__ float group_sum(float x) {
 // and 46 to 50 us, 128 40.6 to 40.8 and 115 to 114, 256 96 to 97 and 178 to
 // 190; width 32, bound by the vector units, 16.7 to 18.4 and 38 to 47.  48 sequences
 // of 2000 to 30000 tokens, 32 heads on 8 of 128, bf16: 288 us, 5.4 TB/s; 4
-// fp32 tokens of one of 10^6, 16 heads on 2 of 256: 224 us, 4.6 TB/s.
+// fp32 tokens of one of 10^6, 16 heads on 2 of 256: 232 us, 4.4 TB/s.
 template <class T, int D, int WR, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
     constexpr int NP = sizeof(T) == 4 ? 3 : 1, NW = sizeof(T) == 4 ? 3 : 2;   // parts of a query, of a weight
@@ -513,15 +513,20 @@ __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 19
 // D + 8 and 64 + 8 elements keep the 16-byte operand reads off each other's
 // banks.  Bound by the matrix and vector units in turn: 2 x 2048 ragged
 // queries over 7000 tokens in a window of 4096, 32 heads on 8 of 128, bf16:
-// 238 us, 870 TFLOP/s; 2 x 1024 over 2064, 6 heads of 64: 24 us, 208 TFLOP/s.
+// 240 to 250 us, 830 to 860 TFLOP/s; 2 x 1024 over 2064, 6 heads of 64: 24 us,
+// 208 TFLOP/s; the prompt at widths 64, 160, 192, 224, 256: 140, 478, 538, 684,
+// 670 us (above 128 a wave is alone on its SIMD).  In fp32, with three products
+// for each: the prompt at 64, 128, 256 345, 562, 1480 us, the segment 35 us; the
+// queries' three parts do not all fit the registers at widths 224 and 256 and for
+// eight waves of width 128 (232, 336 and 108 bytes a lane go to memory).
 // (The next page's scores computed beside the present one's weights: 252 and
 // 27 us, since two waves a SIMD overlap already.)  bf16 calls round a weight
 // to bf16 once, and results differ from 64 bits by 0.0023 of their size
 // instead of 0.0017: a second part, as single tokens take it, is half as many
-// matrix instructions again where those bound the kernel (331 us against 244
-// and 27.7 against 24.4), and the sum of the rounded weights in place of the
-// exact ones' gains next to nothing (0.00226; 253 us).  The same call in fp32
-// keeps 24 bits.
+// matrix instructions again where those bound the kernel (323 us against 250
+// and 28.6 against 24.5, at best), and the sum of the rounded weights in place
+// of the exact ones' gains next to nothing (0.00226; 3% slower).  The same call
+// in fp32 keeps 24 bits.
 // The transposed scores' layout (lane group h of 2 holds rows 8 a + 4 h + b) is
 // again made the second product's operand by the order in which rows of K are
 // fed: row 8 a + 4 h + b of a 32-token tile is token 16 (a / 2) + 8 h + 4 (a % 2) + b,
