@@ -505,10 +505,10 @@ class WindowAttention:
         if self.P:
             k, v = self._project(self.persistent[None], 0)[1:]
         self.cache.free(None)
+        self._held = self.P
         if self.P:
             self.cache.append(self._root[:1], k, v)
             self.cache.fork(self._root, self._slots)
-        self._held = self.P
 
     def _project(self, x, start):
         """Queries, keys (both rotated) and values of vectors that stand at

@@ -189,11 +189,12 @@ __device__ __forceinline__ float group_sum(float x) {
 // next keys and present values are in flight while it computes.  That leaves
 // room for the weights' second part in bf16 calls: with it results differ from
 // 64 bits by their own rounding (0.0017 of their size; with one part 0.0023).
-// 48 sequences as below: 285 us with either; 16 of 2000 to 20000 tokens, 4 key
-// heads, single tokens of 16 heads and 4 tokens of 64: width 64 22.8 to 23.8
-// and 46 to 50 us, 128 40.6 to 40.8 and 115 to 114, 256 96 to 97 and 178 to
-// 190; width 32, bound by the vector units, 16.7 to 18.4 and 38 to 47.  48 sequences
-// of 2000 to 30000 tokens, 32 heads on 8 of 128, bf16: 288 us, 5.4 TB/s; 4
+// One part against two: 48 sequences as below 285 us each; 16 of 2000 to 20000
+// tokens with 4 key heads, single tokens of 16 heads, then 4 tokens of 64: width
+// 64 22.8 against 23.8 and 46 against 50 us, 128 40.6 against 40.8 and 114 each,
+// 256 96 against 97 and 178 against 190; width 32, bound by the vector units,
+// 16.7 against 18.4 and 38 against 47.
+// 48 sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, bf16: 288 us, 5.4 TB/s; 4
 // fp32 tokens of one of 10^6, 16 heads on 2 of 256: 232 us, 4.4 TB/s.
 template <class T, int D, int WR, int RT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D * RT * (sizeof(T) == 4 ? 3 : 1) <= 192 ? 2 : 1) void attend_rows_kernel(AttendArgs a) {
@@ -871,10 +872,10 @@ struct AttendPlan {
     int waves, tile_rows, tiles, splits, least;
 };
 // Ranges, at most: as many workgroups as the compute units take at a time in
-// bf16 (tiles; in fp32 a unit takes one from width 96 on, so two rounds), or several rounds of them, which even out ragged lengths (rows: 48
-// sequences of 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with 1024
-// workgroups, 289 us with 8192), and at least TILE_PAGES or ROW_PAGES pages a
-// range.  Grows with `pages`, so the workspace is that of the longest sequence
+// bf16 (tiles; in fp32 a unit takes one from width 96 on, so two rounds), or
+// several rounds of them, which even out ragged lengths (rows: 48 sequences of
+// 2000 to 30000 tokens, 32 heads on 8 of 128, 336 us with 1024 workgroups, 289
+// us with 8192), and at least TILE_PAGES or ROW_PAGES pages a range.  Grows with `pages`, so the workspace is that of the longest sequence
 // whatever max_len a call names.
 constexpr int TILE_PAGES = 4, ROW_PAGES = 8;
 static int most_ranges(const tm_cache* c, bool wide, long groups, long pages) {
@@ -904,14 +905,16 @@ static AttendPlan attend_plan(const tm_cache* c, int batch, int n_tokens, int he
     // of ranges and their join (registers and LDS allow it up to width 128).
     // Rows: where there would be ranges (more than 8 pages) but few of them.
     // Eight waves against four with ranges, us on the GPU, single tokens in bf16:
-    //   heads x entries  width   200       1000       1500       2064       4000 tokens
+    //   key heads x
+    //   entries          width   200       1000       1500       2064       4000 tokens
     //   12               64      5.6/5.5   7.7/9.4    8.8/9.4    10.2/9.5   15.0/9.6
     //                    128     7.6/7.4   12.6/11.9  15.4/12.1  18.1/12.3  28/12
     //   128              64      5.8/5.5   7.9/9.8    9.7/11.7   12.0/14.1  17.5/18.6
     //                    128     7.8/7.3   13.9/13.6  17.1/18.9  19.8/24.2  31/31
     //   384              64      7.2/6.5   13.5/16.8  17.6/20.4  22.2/25.6  37/38
     //                    128     14/10     28/27      35/33      43/43      90/83
-    // (fp32 the same to 10%).
+    // fp32 is 10 to 40% longer and turns at the same sizes, but for 12 and 64
+    // key heads of width 64 and 96, from 1500 tokens on (11.1 against 10.4).
     // Tiles: by the time that 256 workgroups take for a page, that as many of
     // eight waves take for KW pages, and of the ranges' join (its launch and the
     // partial results' way out and in), fitted to 480 calls measured in both
