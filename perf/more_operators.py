@@ -126,7 +126,7 @@ def prepare(case, seed):
         if own:
             rotary = T.Rotary(case["rot"], layout=T.TM_ROPE_HALF if case["layout"] == "half" else T.TM_ROPE_INTERLEAVED) \
                 if case["rot"] else None
-            s["norm"] = T.HeadNorm(s["w_q"], s["w_k"], eps=EPS, rotary=rotary)
+            s["norm"] = T.HeadNorm(case["heads"], case["kv_heads"], s["w_q"], s["w_k"], eps=EPS, rotary=rotary)
         return s
     if case["op"] == "linear":
         B, N, H, K, dk, dv = (case[n] for n in ("batch", "tokens", "heads", "kv_heads", "key", "value"))
