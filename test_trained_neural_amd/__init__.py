@@ -581,3 +581,9 @@ from .attention import (TM_CACHE_BAD_ENTRY, TM_CACHE_BLOCK, TM_CACHE_FULL, TM_CA
                         TM_CACHE_NONFINITE, TM_CACHE_PAGE, TM_ROPE_BASE, TM_ROPE_HALF, TM_ROPE_INTERLEAVED,
                         TM_ROPE_LINEAR, TM_ROPE_NONE, TM_ROPE_PARTS, PagedCache, Rotary, WindowAttention,
                         tm_rotary, tm_rotary_frequencies)
+
+# a layer's operators beside the memory (include/tm_layer.h)
+from .layer import (HeadNorm, Int8Linear, LinearAttention, tm_head_norm, tm_head_norm_backward,  # noqa: E402,F401
+                    tm_head_norm_workspace_bytes, tm_int8_linear, tm_int8_matmul, tm_int8_quantize,
+                    tm_int8_workspace_bytes, tm_linear_attention, tm_linear_attention_backward,
+                    tm_linear_workspace_bytes)

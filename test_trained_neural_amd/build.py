@@ -16,9 +16,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("tm_kernels.hip", "tm_r3.hip", "tm_retrieve.hip", "tm_project.hip",
                                            "tm_mac.hip", "tm_bwd.hip", "tm_rope.hip", "tm_cache.hip",
-                                           "tm_attend.hip", "tm_api.hip")]
+                                           "tm_attend.hip", "tm_norm.hip", "tm_linear.hip", "tm_int8.hip", "tm_api.hip")]
 HEADERS = [os.path.join(CSRC, "tm_internal.h"), os.path.join(CSRC, "tm_device.h"), os.path.join(CSRC, "tm_cache.h"),
-           os.path.join(ROOT, "include", "tm.h"), os.path.join(ROOT, "include", "tm_attention.h")]
+           os.path.join(ROOT, "include", "tm.h"), os.path.join(ROOT, "include", "tm_attention.h"),
+           os.path.join(ROOT, "include", "tm_layer.h")]
 LIB = os.path.join(HERE, "libtm.so")
 OBJDIR = os.path.join(ROOT, "_build")
 

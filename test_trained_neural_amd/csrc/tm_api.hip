@@ -291,7 +291,8 @@ enum {
     K_BSTATE = 8,   // tm_backward: the launches that stream the state (recompute's write, adjoint update)
     K_BREST = 9,    // tm_backward: its other products, element-wise steps and coefficients
     K_ATTN = 10,    // the attention window's kernels (tm_attention.h)
-    K_CLASSES = 11
+    K_LAYER = 11,   // the layer's kernels (tm_layer.h)
+    K_CLASSES = 12
 };
 struct Timed {
     hipEvent_t a, b;
@@ -352,6 +353,10 @@ hipError_t timed(int kind, hipStream_t st, F&& launch) {
 
 hipError_t tmk::timed_attn_call(hipStream_t st, hipError_t (*call)(void*), void* arg) {
     return timed(K_ATTN, st, [&] { return call(arg); });
+}
+
+hipError_t tmk::timed_layer_call(hipStream_t st, hipError_t (*call)(void*), void* arg) {
+    return timed(K_LAYER, st, [&] { return call(arg); });
 }
 
 namespace {

@@ -528,6 +528,13 @@ template <class F> inline hipError_t timed_attn(hipStream_t st, F launch) {
     return timed_attn_call(st, [](void* f) { return (*static_cast<F*>(f))(); }, &launch);
 }
 
+// The same for the layer's kernels (tm_norm.hip, tm_linear.hip, tm_int8.hip),
+// one launch a call.
+hipError_t timed_layer_call(hipStream_t st, hipError_t (*call)(void*), void* arg);
+template <class F> inline hipError_t timed_layer(hipStream_t st, F launch) {
+    return timed_layer_call(st, [](void* f) { return (*static_cast<F*>(f))(); }, &launch);
+}
+
 // ---- launchers (tm_project.hip) ----
 hipError_t launch_project(const ProjArgs& p, int f32, hipStream_t st);
 

@@ -1,0 +1,1043 @@
+// Linear attention with a decay (include/tm_layer.h): the memory of one
+// matrix,  S_t = e^{g_t} S_{t-1} + k_t v_t^T,  y_t = scale S_t^T q_t,  and
+// its gradients.
+//
+// Over a chunk of C tokens, with G the running sum of g in it (fp64) and S_0
+// the state before it:
+//   y_i = scale (sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j + e^{G_i} S_0^T q_i)
+//   S_C = e^{G_C} S_0 + sum_j e^{G_C - G_j} k_j v_j^T
+// No factor ever exceeds what the formula has (differences are taken before
+// the exponential), and none is divided by, so a decay of -inf is a value
+// like another: it is held as -1000, whose exponential is zero in any type.
+//
+// The gradients are three more runs of the same form.  With R_t the gradient
+// of S_t (R goes over the tokens backwards) and y' = scale dy:
+//   dq_i = sum_{j <= i} e^{G_i - G_j} (y'_i . v_j) k_j + e^{G_i} S_0 y'_i
+//   dk_j = sum_{i >= j} e^{G_i - G_j} (v_j . y'_i) q_i + e^{G_C - G_j} R_C v_j
+//   dv_j = sum_{i >= j} e^{G_i - G_j} (k_j . q_i) y'_i + e^{G_C - G_j} R_C^T k_j
+//   R_0  = e^{G_C} R_C + sum_i e^{G_i} q_i y'_i^T
+// so one kernel serves all: (query, key, value, state) is (q, k, v, S),
+// (dy, v, k, S^T), (v, dy, q, R^T) or (k, q, dy, R).  The gradient of g_t is
+// all that flows over the border before t, from tokens j < t to tokens i >= t:
+//   dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} fq_i + sum_{j < t} fk_j + through,
+// the sums over the chunk, X_ij = e^{G_i - G_j} (q_i . k_j) (y'_i . v_j),
+// fq_i = q_i . (the state's part of dq_i) what tokens before the chunk give
+// to i, fk_j = k_j . (the state's part of dk_j) what j gives to tokens behind
+// the chunk, and `through` what passes the chunk: <R_C, S_C> - sum fk at its
+// end, <R_0, S_0> - sum fq at its start.  Taken as a running difference of
+// what enters and leaves (q_i . dq_i - k_i . dk_i, the shorter formula), a
+// decay's sum over n tokens would lose n^1.5 roundings.
+#include <math.h>
+
+#include "../../include/tm_layer.h"
+#include "tm_device.h"
+
+namespace tmk {
+
+constexpr double LOG2E = 1.4426950408889634074;
+constexpr int LIN_REC = 16;        // calls of up to as many tokens go token by token
+constexpr int LIN_BACK_SEG = 256;  // tokens of a segment in the backward
+
+// What a chunk run does (see the table of roles above).
+enum { LIN_OUT, LIN_STATE, LIN_STATE_BACK, LIN_DQ, LIN_DK, LIN_DV };
+
+struct LinArgs {
+    const void *q, *k, *v, *z;           // z: rows that the far part is multiplied with (LIN_DQ: q, LIN_DK: k)
+    long qb, qt, kb, kt, vb, vt, zb, zt; // elements between batch entries and between tokens
+    int dk, dv;                          // width of queries and keys, width of values
+    const float* ld;                     // log_decay
+    const int* counts;
+    const float* s_in;                   // [batch * key heads][s_seg][...]; null: zeros
+    float* s_out;                        // null: not wanted
+    long s_in_bh, s_in_seg, s_out_bh, s_out_seg;   // elements between heads' and between segments' states
+    long sa, sc;                         // elements between the rows and between the columns of a state
+    void* out;
+    float* dot;                          // [slabs][batch * key heads][T]
+    double* gsum;                        // [batch * key heads][nseg]: log2 of what a segment keeps
+    float pair_scale, far_scale, state_scale;
+    int per_token, B, T, Hk, G, nseg, L, slabs;
+};
+
+__device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
+    return a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
+}
+// log2 of what a token keeps: -inf as -1000 (NaN stays NaN)
+__device__ __forceinline__ double lin_gate(float g) {
+    return (double)(g < -1000.f ? -1000.f : g) * LOG2E;
+}
+
+template <class T> __device__ __forceinline__ bool lin_finite(T x) { return __builtin_isfinite((float)x); }
+
+// Rows t0 .. t0 + C - 1 (zeros from n on) and columns c0 .. c0 + D - 1 (zeros
+// from `cols` on) of a token array, 16 bytes at a time: row-major into `rows`
+// [C][RP], transposed into `cols_t` [D][CP].  bad: the first row with a
+// non-finite element, which is taken as zero.
+template <class T, int D, int C, int RP, int CP, bool ROWS, bool COLS, bool CHECK>
+__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int n, int c0, int cols, T* rows, T* cols_t,
+                                          int* bad) {
+    constexpr int VE = 16 / sizeof(T), UNITS = D / VE;
+    struct __align__(16) Vec { T e[VE]; };
+    for (int i = threadIdx.x; i < C * UNITS; i += 256) {
+        const int r = i / UNITS, u = i % UNITS, c = c0 + u * VE;
+        Vec v;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v.e[e] = (T)0.f;
+        if (t0 + r < n && c < cols) v = *reinterpret_cast<const Vec*>(x + (long)(t0 + r) * step + c);
+        if constexpr (CHECK) {
+            bool fine = true;
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (!lin_finite(v.e[e])) {
+                    fine = false;
+                    v.e[e] = (T)0.f;
+                }
+            if (!fine) atomicMin(bad, r);
+        }
+        if constexpr (ROWS) *reinterpret_cast<Vec*>(rows + r * RP + u * VE) = v;
+        if constexpr (COLS) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) cols_t[(u * VE + e) * CP + r] = v.e[e];
+        }
+    }
+}
+
+// 8 values in the order in which two stacked accumulator tiles hold 32 rows:
+// lane group g has 4 g .. and 16 + 4 g ..
+__device__ __forceinline__ bf16x8 lin_split8(const bf16* p, int g) {
+    typedef bf16 V4 __attribute__((ext_vector_type(4)));
+    const V4 a = *reinterpret_cast<const V4*>(p + 4 * g), b = *reinterpret_cast<const V4*>(p + 16 + 4 * g);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x8 lin_split8(const float* p, int g) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + 4 * g), b = *reinterpret_cast<const f32x4*>(p + 16 + 4 * g);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// fp32 values as operands: one for fp32, N of 8 bits each for bf16.
+template <class T, int N> struct Parts {
+    typename Frag<T>::T p[N];
+    __device__ __forceinline__ void set(f32x8 x) {
+        if constexpr (sizeof(T) == 4) {
+            p[0] = x;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                p[i] = to_bf16(x);
+                x -= to_f32(p[i]);
+            }
+        }
+    }
+};
+template <class T> constexpr int lin_parts(int n) { return sizeof(T) == 4 ? 1 : n; }
+
+template <class T, int DK, int C> struct LinLds {
+    static constexpr int PAD = 16 / sizeof(T);
+    static constexpr int RP = DK + PAD, CP = C + PAD;
+    static constexpr size_t q = 0, k = q + sizeof(T) * C * RP, kt = k + sizeof(T) * C * RP,
+                            vt = kt + sizeof(T) * DK * CP, p = vt + sizeof(T) * 64 * CP, g = p + sizeof(T) * C * CP,
+                            head = g + 8 * 64, tail = head + 4 * 64, dot = tail + 4 * 64, bad = dot + 4 * 4 * 64,
+                            bytes = bad + 16;
+};
+
+// One workgroup of 4 waves takes one key head of one entry, one segment of its
+// tokens, and 64 columns of the values (16 a wave), whose slice of the state
+// its waves hold in accumulators.
+template <class T, int DK, int C, int KIND>
+__global__ __launch_bounds__(256) void lin_kernel(LinArgs a) {
+    constexpr bool STATE = KIND == LIN_STATE || KIND == LIN_STATE_BACK;
+    constexpr bool REV = KIND == LIN_STATE_BACK || KIND == LIN_DK || KIND == LIN_DV;
+    constexpr bool SUM = REV;   // the group's heads are summed (else each has an output of its own)
+    constexpr bool DOT = KIND == LIN_DQ || KIND == LIN_DK;
+    constexpr int NT = C / 16, NS = DK / 32, NM = DK / 16, KS = C / 32;
+    // the state as an operand keeps 16 bits, 24 where its products enter the gradients of the decays
+    constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP = lin_parts<T>(3);
+    typedef typename Frag<T>::T F;
+    typedef LinLds<T, DK, C> S_;
+    constexpr int RP = S_::RP, CP = S_::CP;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    T* qs = reinterpret_cast<T*>(lds + S_::q);
+    T* ks = reinterpret_cast<T*>(lds + S_::k);
+    T* kT = reinterpret_cast<T*>(lds + S_::kt);
+    T* vT = reinterpret_cast<T*>(lds + S_::vt);
+    T* ps = reinterpret_cast<T*>(lds + S_::p);
+    double* gs = reinterpret_cast<double*>(lds + S_::g);
+    float* head = reinterpret_cast<float*>(lds + S_::head);
+    float* tail = reinterpret_cast<float*>(lds + S_::tail);
+    float* dots = reinterpret_cast<float*>(lds + S_::dot);
+    int* bad = reinterpret_cast<int*>(lds + S_::bad);
+
+    const int slab = blockIdx.x % a.slabs, rest = blockIdx.x / a.slabs;
+    const int seg = rest % a.nseg, bh = rest / a.nseg, b = bh / a.Hk, h = bh % a.Hk;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
+    const int col0 = slab * 64, wcol = col0 + 16 * wave;   // the wave's first column
+    const int n = lin_tokens(a, b), first = seg * a.L, last = (int)min((long)n, (long)first + a.L);
+    const int chunks = last > first ? (last - first + C - 1) / C : 0;
+
+    const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb;
+    const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb;
+    const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb;
+    const T* z = reinterpret_cast<const T*>(a.z) + b * a.zb;
+
+    f32x4 S[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!STATE && a.s_in) {
+        const float* s = a.s_in + bh * a.s_in_bh + seg * a.s_in_seg;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * m + 4 * lg + r, c = wcol + l16;
+                if (i < a.dk && c < a.dv) S[m][r] = s[i * a.sa + c * a.sc];
+            }
+    }
+    double kept = 0.0;
+
+    for (int ci = 0; ci < chunks; ++ci) {
+        const int t0 = first + (REV ? chunks - 1 - ci : ci) * C;
+        const int rows = min(C, last - t0);   // tokens of the chunk
+        __syncthreads();
+        if (wave == 0) {
+            double g = 0.0;
+            if (lane < rows)
+                g = lin_gate(a.ld[a.per_token ? ((long)b * a.T + t0 + lane) * a.Hk + h : h]);
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double o = __shfl_up(g, m, 64);
+                if (lane >= m) g += o;
+            }
+            const double end = __shfl(g, 63, 64);
+            gs[lane] = g;
+            const float before = __builtin_amdgcn_exp2f((float)g), after = __builtin_amdgcn_exp2f((float)(end - g));
+            head[lane] = (REV ? after : before) * a.far_scale;
+            tail[lane] = (REV ? before : after) * a.state_scale;
+            if (lane == 0) *bad = C;
+        }
+        if constexpr (KIND == LIN_OUT) __syncthreads();   // bad is set
+        f32x4 O[NT];
+        float far_dot[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) far_dot[i] = 0.f;
+        for (int g = 0; g < a.G; ++g) {
+            if (g > 0) __syncthreads();
+            const int many = h * a.G + g;
+            if constexpr (!STATE)
+                if (!SUM || g == 0)
+                    lin_stage<T, DK, C, RP, CP, true, false, false>(q + (long)(SUM ? h : many) * a.dk, a.qt, t0, last, 0,
+                                                                   a.dk, qs, nullptr, nullptr);
+            if (SUM || g == 0) {
+                const int kh = SUM ? many : h;
+                lin_stage<T, DK, C, RP, CP, !STATE, true, false>(k + (long)kh * a.dk, a.kt, t0, last, 0, a.dk, ks, kT,
+                                                               nullptr);
+                lin_stage<T, 64, C, RP, CP, false, true, KIND == LIN_OUT>(v + (long)kh * a.dv, a.vt, t0, last, col0,
+                                                                        a.dv, nullptr, vT, bad);
+            }
+            __syncthreads();
+            if constexpr (!STATE) {
+                // the pairs' weights: 16 queries a wave against their keys
+                if (wave < NT) {
+                    const int i = 16 * wave + l16;
+                    const double gi = gs[i];
+#pragma unroll
+                    for (int kt = 0; kt < NT; ++kt) {
+                        f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f};
+                        if (REV ? kt >= wave : kt <= wave) {
+#pragma unroll
+                            for (int s = 0; s < NS; ++s)
+                                mma(w, lin_split8(ks + (16 * kt + l16) * RP + 32 * s, lg),
+                                    lin_split8(qs + i * RP + 32 * s, lg));
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int j = 16 * kt + 4 * lg + r;
+                                const double x = REV ? gs[j] - gi : gi - gs[j];
+                                w[r] = (REV ? j >= i : j <= i)
+                                           ? w[r] * (__builtin_amdgcn_exp2f((float)x) * a.pair_scale) : 0.f;
+                            }
+                        }
+                        struct __align__(4 * sizeof(T)) V4 { T e[4]; } o;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o.e[r] = (T)w[r];
+                        *reinterpret_cast<V4*>(ps + i * CP + 16 * kt + 4 * lg) = o;
+                    }
+                }
+                __syncthreads();
+                // the far part, out of the state before the chunk
+                if (!SUM || g == 0) {
+                    f32x4 far[NT];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) far[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        Parts<T, SP> sp;
+                        sp.set(__builtin_shufflevector(S[2 * s], S[2 * s + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const F qf = lin_split8(qs + (16 * i + l16) * RP + 32 * s, lg);
+#pragma unroll
+                            for (int p = SP - 1; p >= 0; --p) mma(far[i], sp.p[p], qf);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const float by = head[16 * i + l16];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) O[i][r] = far[i][r] * by;
+                        if constexpr (DOT) {
+                            const int t = t0 + 16 * i + l16, c = wcol + 4 * lg;
+                            if (t < last && c < a.dv) {
+                                const T* zr = z + (long)t * a.zt + (long)(SUM ? h : many) * a.dv + c;
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) far_dot[i] += O[i][r] * (float)zr[r];
+                            }
+                        }
+                    }
+                }
+                // the chunk's own
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const F vf = ld8(vT + (16 * wave + l16) * CP + 32 * s + 8 * lg);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma(O[i], vf, ld8(ps + (16 * i + l16) * CP + 32 * s + 8 * lg));
+                }
+                if (!SUM || g == a.G - 1) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const int t = t0 + 16 * i + l16, c = wcol + 4 * lg;
+                        if (t < last && c < a.dv) {
+                            struct __align__(4 * sizeof(T)) V4 { T e[4]; } o;
+                            // a non-finite value is zero in vT: its products with the weights of earlier
+                            // tokens, which are zero, would not be
+                            const bool lost = KIND == LIN_OUT && 16 * i + l16 >= *bad;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o.e[r] = (T)(lost ? __builtin_nanf("") : O[i][r]);
+                            const int heads = SUM ? a.Hk : a.Hk * a.G;
+                            *reinterpret_cast<V4*>(reinterpret_cast<T*>(a.out) +
+                                                   (((long)b * a.T + t) * heads + (SUM ? h : many)) * a.dv + c) = o;
+                        }
+                    }
+                }
+            }
+            // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
+            if (SUM || g == a.G - 1) {
+                if (!SUM || g == 0) {
+                    const float keep = __builtin_amdgcn_exp2f((float)gs[63]);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[m] *= keep;
+                    kept += gs[63];
+                }
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const F vf = ld8(vT + (16 * wave + l16) * CP + 32 * s + 8 * lg);
+                    f32x8 x = to_f32v(vf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= tail[32 * s + 8 * lg + e];
+                    Parts<T, VP> vp;
+                    vp.set(x);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) {
+                        const F kf = ld8(kT + (16 * m + l16) * CP + 32 * s + 8 * lg);
+#pragma unroll
+                        for (int p = VP - 1; p >= 0; --p) mma(S[m], kf, vp.p[p]);
+                    }
+                }
+                if (KIND == LIN_OUT && *bad < C) {
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) S[m] += __builtin_nanf("");
+                }
+            }
+        }
+        if constexpr (DOT) {   // over the workgroup's columns
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float d = far_dot[i];
+                d += __shfl_xor(d, 16, 64);
+                d += __shfl_xor(d, 32, 64);
+                if (lg == 0) dots[wave * 64 + 16 * i + l16] = d;
+            }
+            __syncthreads();
+            const int i = threadIdx.x;
+            if (i < rows)
+                a.dot[((long)slab * a.B * a.Hk + bh) * a.T + t0 + i] =
+                    (dots[i] + dots[64 + i]) + (dots[128 + i] + dots[192 + i]);
+        }
+    }
+    if (a.s_out) {
+        float* s = a.s_out + bh * a.s_out_bh + seg * a.s_out_seg;
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * m + 4 * lg + r, c = wcol + l16;
+                if (i < a.dk && c < a.dv) s[i * a.sa + c * a.sc] = S[m][r];
+            }
+    }
+    if (STATE && a.gsum && slab == 0 && threadIdx.x == 0) a.gsum[(long)bh * a.nseg + seg] = kept;
+}
+
+// Single tokens and short drafts, token by token: 32 columns of a head's
+// state a workgroup, in its registers (4 columns and DK / 32 rows a thread).
+// Bound by reading and writing the state once.
+template <class T, int DK>
+__global__ __launch_bounds__(256) void lin_token_kernel(LinArgs a) {
+    constexpr int R = DK / 32;
+    extern __shared__ float red[];   // [2][G][4 waves][32]
+    const int slab = blockIdx.x % a.slabs, bh = blockIdx.x / a.slabs, b = bh / a.Hk, h = bh % a.Hk;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, wave = threadIdx.x >> 6, c = slab * 32 + 4 * cg;
+    const bool on = c < a.dv;
+    const int n = lin_tokens(a, b);
+    f32x4 S[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int row = rg + 32 * i;
+        if (a.s_in && on && row < a.dk)
+            S[i] = *reinterpret_cast<const f32x4*>(a.s_in + bh * a.s_in_bh + (long)row * a.dv + c);
+    }
+    for (int t = 0; t < n; ++t) {
+        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + t * a.qt + (long)h * a.G * a.dk;
+        const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + t * a.kt + (long)h * a.dk;
+        const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + t * a.vt + (long)h * a.dv;
+        const float keep = expf(a.ld[a.per_token ? ((long)b * a.T + t) * a.Hk + h : h]);
+        f32x4 vv = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (on) {
+            struct __align__(4 * sizeof(T)) V4 { T e[4]; };
+            const V4 x = *reinterpret_cast<const V4*>(v + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vv[e] = (float)x.e[e];
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = rg + 32 * i;
+            const float kr = row < a.dk ? (float)k[row] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] = fmaf(keep, S[i][e], kr * vv[e]);
+        }
+        float* buf = red + (t & 1) * a.G * 128;
+        for (int g = 0; g < a.G; ++g) {
+            f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = rg + 32 * i;
+                if (row < a.dk) {
+                    const float qr = (float)q[(long)g * a.dk + row];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fmaf(qr, S[i][e], y[e]);
+                }
+            }
+#pragma unroll
+            for (int m = 8; m < 64; m <<= 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], m, 64);
+            if ((threadIdx.x & 63) < 8) *reinterpret_cast<f32x4*>(buf + (g * 4 + wave) * 32 + 4 * cg) = y;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.G * 32; i += 256) {
+            const int g = i >> 5, col = i & 31;
+            const float* p = buf + g * 128 + col;
+            const float y = ((p[0] + p[32]) + (p[64] + p[96])) * a.far_scale;
+            if (slab * 32 + col < a.dv)
+                reinterpret_cast<T*>(a.out)[(((long)b * a.T + t) * a.Hk * a.G + (long)h * a.G + g) * a.dv + slab * 32 + col] = (T)y;
+        }
+    }
+    if (a.s_out && on)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = rg + 32 * i;
+            if (row < a.dk) *reinterpret_cast<f32x4*>(a.s_out + bh * a.s_out_bh + (long)row * a.dv + c) = S[i];
+        }
+}
+
+// The states at the segments' borders from what each segment adds by itself:
+// slot s becomes the state before segment s (BACK: the gradient of the state
+// behind it), and what comes out at the far end goes to `end` (null: not
+// wanted) and, with slots = nseg + 1, to the last slot.
+struct LinScan {
+    float* part;         // [batch * key heads][slots][cells]
+    const float* begin;  // [batch * key heads][cells]; null: zeros
+    float* end;
+    const double* gsum;
+    int nseg, slots, cells, back;
+};
+__global__ __launch_bounds__(256) void lin_scan_kernel(LinScan s) {
+    const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (i >= s.cells) return;
+    const long bh = blockIdx.x;
+    f32x4 run = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (s.begin) run = *reinterpret_cast<const f32x4*>(s.begin + bh * s.cells + i);
+    for (int n = 0; n < s.nseg; ++n) {
+        const int seg = s.back ? s.nseg - 1 - n : n;
+        float* p = s.part + (bh * s.slots + seg) * s.cells + i;
+        const f32x4 own = *reinterpret_cast<const f32x4*>(p);
+        *reinterpret_cast<f32x4*>(p) = run;
+        const float keep = __builtin_amdgcn_exp2f((float)s.gsum[bh * s.nseg + seg]);
+        run = keep * run + own;
+    }
+    if (s.slots > s.nseg) *reinterpret_cast<f32x4*>(s.part + (bh * s.slots + s.nseg) * s.cells + i) = run;
+    if (s.end) *reinterpret_cast<f32x4*>(s.end + bh * s.cells + i) = run;
+}
+
+// <R, S> at the end of every segment.
+__global__ __launch_bounds__(256) void lin_flow_kernel(const float* S, const float* R, double* flow, int nseg,
+                                                       int slots, int cells) {
+    __shared__ double red[4];
+    const long bh = blockIdx.x / nseg;
+    const int seg = blockIdx.x % nseg;
+    const float* s = S + (bh * slots + seg + 1) * cells;
+    const float* r = R + (bh * slots + seg) * cells;
+    double d = 0.0;
+    for (int i = threadIdx.x * 4; i < cells; i += 1024) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(s + i), y = *reinterpret_cast<const f32x4*>(r + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d = fma((double)x[e], (double)y[e], d);
+    }
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) d += __shfl_xor(d, m, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) flow[bh * nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// dg of a chunk's tokens but for what passes the chunk, and the sums of fq
+// and fk that this follows from.
+struct LinPairs {
+    const void *q, *k, *v, *dy;
+    long qb, qt, kb, kt, vb, vt, gb, gt;
+    const float* ld;
+    const int* counts;
+    const float *dotq, *dotk;   // fq, fk: [slabs][batch * key heads][T]
+    float* h;                   // [batch * key heads][T]
+    float* sums;                // [batch * key heads][chunks][2]
+    float scale;
+    int per_token, B, T, Hk, G, dk, dv, chunks, slabs;
+};
+template <class T, int D, int C>
+__global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
+    constexpr int PAD = 16 / sizeof(T), RP = D + PAD, NT = C / 16, NS = D / 32, XP = C + 1;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    T* qs = reinterpret_cast<T*>(lds);
+    T* ks = qs + C * RP;
+    T* vs = ks + C * RP;
+    T* ys = vs + C * RP;
+    double* gs = reinterpret_cast<double*>(ys + C * RP);
+    float* cross = reinterpret_cast<float*>(gs + 64);   // [64]
+    float* X = reinterpret_cast<float*>(lds);           // [C][XP], in the operands' place once they are read
+    static_assert(4 * C * XP <= 4 * (int)sizeof(T) * C * RP, "X fits in the operands' place");
+    const int chunk = blockIdx.x % a.chunks, bh = blockIdx.x / a.chunks, b = bh / a.Hk, h = bh % a.Hk;
+    const int n = a.counts ? min(max(a.counts[b], 0), a.T) : a.T, t0 = chunk * C;
+    if (t0 >= n) return;
+    const int rows = min(C, n - t0);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
+    if (wave == 0) {
+        double g = 0.0;
+        if (lane < rows) g = lin_gate(a.ld[a.per_token ? ((long)b * a.T + t0 + lane) * a.Hk + h : h]);
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const double o = __shfl_up(g, m, 64);
+            if (lane >= m) g += o;
+        }
+        gs[lane] = g;
+    }
+    const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb;
+    const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * a.dk;
+    const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * a.dv;
+    const T* y = reinterpret_cast<const T*>(a.dy) + b * a.gb;
+    lin_stage<T, D, C, RP, C, true, false, false>(k, a.kt, t0, n, 0, a.dk, ks, nullptr, nullptr);
+    lin_stage<T, D, C, RP, C, true, false, false>(v, a.vt, t0, n, 0, a.dv, vs, nullptr, nullptr);
+    float x[NT][4];
+#pragma unroll
+    for (int kt = 0; kt < NT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[kt][r] = 0.f;
+    const int i = 16 * wave + l16;
+    for (int g = 0; g < a.G; ++g) {
+        if (g > 0) __syncthreads();
+        lin_stage<T, D, C, RP, C, true, false, false>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, n, 0, a.dk, qs, nullptr, nullptr);
+        lin_stage<T, D, C, RP, C, true, false, false>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, n, 0, a.dv, ys, nullptr, nullptr);
+        __syncthreads();
+        if (wave < NT) {
+            const double gi = gs[i];
+#pragma unroll
+            for (int kt = 0; kt < NT; ++kt) {
+                if (kt > wave) continue;
+                f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, p = s;
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    mma(s, ld8(ks + (16 * kt + l16) * RP + 32 * u + 8 * lg), ld8(qs + i * RP + 32 * u + 8 * lg));
+                    mma(p, ld8(vs + (16 * kt + l16) * RP + 32 * u + 8 * lg), ld8(ys + i * RP + 32 * u + 8 * lg));
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * kt + 4 * lg + r;
+                    x[kt][r] += j < i ? s[r] * p[r] * (__builtin_amdgcn_exp2f((float)(gi - gs[j])) * a.scale) : 0.f;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (wave < NT)
+#pragma unroll
+        for (int kt = 0; kt < NT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) X[i * XP + 16 * kt + 4 * lg + r] = x[kt][r];
+    __syncthreads();
+    // sums over j < t of every row, then of those over i >= t: four threads a row, then four a column
+    const int at = threadIdx.x >> 2, quarter = threadIdx.x & 3, E = C / 4;
+    if (at < C) {
+        float* row = X + at * XP + quarter * E;
+        float run = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float v0 = row[e];
+            row[e] = run;
+            run += v0;
+        }
+        float before = 0.f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const float o = __shfl(run, (lane & ~3) + p, 64);
+            if (p < quarter) before += o;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) row[e] += before;
+    }
+    __syncthreads();
+    if (at < C) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (quarter * E + e >= at) s += X[(quarter * E + e) * XP + at];
+        s += __shfl_xor(s, 1, 64);
+        s += __shfl_xor(s, 2, 64);
+        if (quarter == 0) cross[at] = s;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        float fq = 0.f, fk = 0.f;
+        const long to = (long)bh * a.T + t0 + lane, step = (long)a.B * a.Hk * a.T;
+        if (lane < rows)
+            for (int z = 0; z < a.slabs; ++z) {
+                fq += a.dotq[z * step + to];
+                fk += a.dotk[z * step + to];
+            }
+        float from = fq, upto = fk;   // sums from this token on, and up to it
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const float o = __shfl_down(from, m, 64), p = __shfl_up(upto, m, 64);
+            if (lane + m < 64) from += o;
+            if (lane >= m) upto += p;
+        }
+        const float earlier = __shfl_up(upto, 1, 64);
+        if (lane < rows) a.h[to] = cross[lane] + (from + (lane ? earlier : 0.f));
+        const float all_k = __shfl(upto, 63, 64);
+        if (lane == 0) {
+            float* s = a.sums + ((long)bh * a.chunks + chunk) * 2;
+            s[0] = from;
+            s[1] = all_k;
+        }
+    }
+}
+
+// dg of a segment's tokens (per token), or their sum (into part): from the
+// segment's last chunk to its first, with what passes each.
+__global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const float* sums, const double* flow,
+                                                       const int* counts, float* dg, double* part, int per_token, int T,
+                                                       int Hk, int nseg, int L, int C) {
+    const int seg = blockIdx.x % nseg, bh = blockIdx.x / nseg, b = bh / Hk, kh = bh % Hk, lane = threadIdx.x;
+    const int n = counts ? min(max(counts[b], 0), T) : T, chunks = (T + C - 1) / C;
+    const int first = seg * L, last = (int)min((long)n, (long)first + L);
+    double border = flow[(long)bh * nseg + seg], sum = 0.0;
+    for (int c = (last - first + C - 1) / C - 1; c >= 0; --c) {
+        const int t = first + c * C + lane;
+        const float* s = sums + ((long)bh * chunks + first / C + c) * 2;
+        const double through = border - (double)s[1];
+        border = through + (double)s[0];
+        if (lane < C && t < last) {
+            const double g = through + (double)h[(long)bh * T + t];
+            if (per_token) dg[((long)b * T + t) * Hk + kh] = (float)g;
+            sum += g;
+        }
+    }
+    if (!per_token) {
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
+        if (lane == 0) part[(long)bh * nseg + seg] = sum;
+    }
+}
+__global__ __launch_bounds__(64) void lin_gate_sum_kernel(const double* part, float* dg, int B, int Hk, int nseg) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (long i = lane; i < (long)B * nseg; i += 64) s += part[(i / nseg * Hk + h) * nseg + i % nseg];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+    if (lane == 0) dg[h] = (float)s;
+}
+
+// to = from (null: zeros), n a multiple of 4
+__global__ __launch_bounds__(256) void lin_copy_kernel(const float* from, float* to, long n) {
+    for (long i = ((long)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (long)gridDim.x * 1024) {
+        f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (from) x = *reinterpret_cast<const f32x4*>(from + i);
+        *reinterpret_cast<f32x4*>(to + i) = x;
+    }
+}
+__global__ void lin_zero_kernel(float* p, int n) {
+    for (int i = threadIdx.x; i < n; i += 256) p[i] = 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// launches
+
+static int lin_width(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+template <class T, int DK, int C, int KIND>
+static hipError_t lin_run(LinArgs a, hipStream_t st) {
+    a.slabs = (a.dv + 63) / 64;
+    const long blocks = (long)a.B * a.Hk * a.nseg * a.slabs;
+    if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
+    constexpr size_t bytes = LinLds<T, DK, C>::bytes;
+    static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+    if (bytes > 64 * 1024) {   // above the default dynamic LDS limit
+        const hipError_t e = hipFuncSetAttribute((const void*)lin_kernel<T, DK, C, KIND>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != hipSuccess) return e;
+    }
+    return timed_layer(st, [&] {
+        launch_k((lin_kernel<T, DK, C, KIND>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
+        return hipGetLastError();
+    });
+}
+// Tokens of a chunk: 64, or 32 where 64 rows of 256 fp32 values would not fit
+// the LDS.  All runs of a call have the same.
+static int lin_chunk(int dk, int dv, size_t es) { return es == 4 && (dk > 128 || dv > 128) ? 32 : 64; }
+
+// wide: the other width of the call's heads, which decides the chunk with it
+template <class T, int KIND> static hipError_t lin_launch(const LinArgs& a, int wide, hipStream_t st) {
+    const int w = lin_width(a.dk);
+    if constexpr (sizeof(T) == 4) {
+        if (w == 256) return lin_run<T, 256, 32, KIND>(a, st);
+        if (lin_width(wide) == 256)
+            return w == 128 ? lin_run<T, 128, 32, KIND>(a, st) : lin_run<T, 64, 32, KIND>(a, st);
+    } else {
+        if (w == 256) return lin_run<T, 256, 64, KIND>(a, st);
+    }
+    return w == 128 ? lin_run<T, 128, 64, KIND>(a, st) : lin_run<T, 64, 64, KIND>(a, st);
+}
+
+template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hipStream_t st) {
+    a.chunks = (a.T + C - 1) / C;
+    const long blocks = (long)a.B * a.Hk * a.chunks;
+    if (blocks >= 1L << 24) return hipErrorInvalidValue;
+    constexpr size_t bytes = 4 * sizeof(T) * C * (D + 16 / sizeof(T)) + 8 * 64 + 4 * 64;
+    static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+    if (bytes > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)lin_pairs_kernel<T, D, C>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != hipSuccess) return e;
+    }
+    return timed_layer(st, [&] {
+        launch_k((lin_pairs_kernel<T, D, C>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
+        return hipGetLastError();
+    });
+}
+template <class T> static hipError_t lin_pairs(const LinPairs& a, hipStream_t st) {
+    const int w = lin_width(a.dk > a.dv ? a.dk : a.dv);
+    if constexpr (sizeof(T) == 4) {
+        if (w == 256) return lin_pairs_run<T, 256, 32>(a, st);
+    } else {
+        if (w == 256) return lin_pairs_run<T, 256, 64>(a, st);
+    }
+    return w == 128 ? lin_pairs_run<T, 128, 64>(a, st) : lin_pairs_run<T, 64, 64>(a, st);
+}
+
+template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
+    a.slabs = (a.dv + 31) / 32;
+    const long blocks = (long)a.B * a.Hk * a.slabs;
+    if (blocks >= 1L << 24) return hipErrorInvalidValue;
+    const size_t bytes = (size_t)a.G * 1024;
+    const dim3 grid((unsigned)blocks);
+    return timed_layer(st, [&] {
+        const int w = lin_width(a.dk);
+        if (w == 64) launch_k((lin_token_kernel<T, 64>), grid, dim3(256), bytes, st, a);
+        else if (w == 128) launch_k((lin_token_kernel<T, 128>), grid, dim3(256), bytes, st, a);
+        else launch_k((lin_token_kernel<T, 256>), grid, dim3(256), bytes, st, a);
+        return hipGetLastError();
+    });
+}
+
+// How a call is divided, and where its workspace holds what.
+struct LinPlan {
+    int nseg, L;
+    size_t states, grads, gsum, flow, dotq, dotk, h, sums, part, bytes;
+};
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
+    LinPlan p{};
+    const size_t bh = (size_t)B * Hk, cells = (size_t)dk * dv;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += up256(n);
+        return o;
+    };
+    if (back) {
+        p.L = LIN_BACK_SEG;
+        p.nseg = (T + p.L - 1) / p.L;
+        p.states = take(bh * (p.nseg + 1) * cells * 4);
+        p.grads = take(bh * (p.nseg + 1) * cells * 4);
+        p.gsum = take(bh * p.nseg * 8);
+        p.flow = take(bh * p.nseg * 8);
+        p.dotq = take(bh * T * 4 * ((dk + 63) / 64));
+        p.dotk = take(bh * T * 4 * ((dk + 63) / 64));
+        p.h = take(bh * T * 4);
+        p.sums = take(bh * ((T + 31) / 32) * 8);   // chunks of 32 tokens, or 64
+        p.part = take(bh * p.nseg * 8);
+    } else {
+        // the sequence is divided where its heads alone do not fill the chip
+        const long wgs = (long)bh * ((dv + 63) / 64);
+        long seg = wgs >= 256 || T <= 256 ? 1 : (1024 + wgs - 1) / wgs;
+        seg = seg < (T + 255) / 256 ? seg : (T + 255) / 256;
+        p.L = (int)(((T + seg - 1) / seg + 63) / 64 * 64);
+        if (T > 0 && p.L == 0) p.L = 64;
+        p.nseg = p.L ? (T + p.L - 1) / p.L : 0;
+        if (p.nseg > 1) {
+            p.states = take(bh * p.nseg * cells * 4);
+            p.gsum = take(bh * p.nseg * 8);
+        }
+    }
+    p.bytes = at < 256 ? 256 : at;
+    return p;
+}
+
+static hipError_t lin_scan(const LinScan& s, long bh, hipStream_t st) {
+    return timed_layer(st, [&] {
+        launch_k(lin_scan_kernel, dim3((unsigned)bh, (s.cells + 1023) / 1024), dim3(256), 0, st, s);
+        return hipGetLastError();
+    });
+}
+
+static hipError_t lin_copy(const float* from, float* to, long n, hipStream_t st) {
+    const long blocks = (n + 1023) / 1024;
+    return timed_layer(st, [&] {
+        launch_k(lin_copy_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, from, to, n);
+        return hipGetLastError();
+    });
+}
+
+#define LIN_TRY(x) do { const hipError_t e_ = (x); if (e_ != hipSuccess) return e_; } while (0)
+
+template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, char* ws, hipStream_t st) {
+    const long cells = (long)a.dk * a.dv;
+    a.s_in_bh = a.s_out_bh = cells;
+    a.sa = a.dv;
+    a.sc = 1;
+    if (a.T <= LIN_REC) {
+        a.s_out = state_out;
+        return lin_tokens_run<T>(a, st);
+    }
+    const LinPlan p = lin_plan(a.B, a.T, a.Hk, a.dk, a.dv, false);
+    a.nseg = p.nseg;
+    a.L = p.L;
+    if (p.nseg == 1) {
+        a.s_out = state_out;
+        return lin_launch<T, LIN_OUT>(a, a.dk, st);
+    }
+    float* parts = reinterpret_cast<float*>(ws + p.states);
+    double* gsum = reinterpret_cast<double*>(ws + p.gsum);
+    LinArgs b = a;
+    b.G = 1;
+    b.s_out = parts;
+    b.s_out_bh = p.nseg * cells;
+    b.s_out_seg = cells;
+    b.gsum = gsum;
+    LIN_TRY((lin_launch<T, LIN_STATE>(b, a.dk, st)));
+    LIN_TRY(lin_scan(LinScan{parts, a.s_in, state_out, gsum, p.nseg, p.nseg, (int)cells, 0}, (long)a.B * a.Hk, st));
+    a.s_in = parts;
+    a.s_in_bh = p.nseg * cells;
+    a.s_in_seg = cells;
+    return lin_launch<T, LIN_OUT>(a, a.dk, st);
+}
+
+struct LinBack {
+    const void* dy;
+    long gb, gt;
+    const float* dstate_out;
+    void *dq, *dk, *dv;
+    float *dld, *dstate_in;
+};
+
+template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, char* ws, hipStream_t st) {
+    const int dk = a.dk, dv = a.dv;
+    const long cells = (long)dk * dv, bh = (long)a.B * a.Hk;
+    const LinPlan p = lin_plan(a.B, a.T, a.Hk, dk, dv, true);
+    const int slots = p.nseg + 1, wide = dk > dv ? dk : dv;
+    a.nseg = p.nseg;
+    a.L = p.L;
+    float* S = reinterpret_cast<float*>(ws + p.states);
+    float* R = reinterpret_cast<float*>(ws + p.grads);
+    double* gsum = reinterpret_cast<double*>(ws + p.gsum);
+    double* flow = reinterpret_cast<double*>(ws + p.flow);
+    float* dotq = reinterpret_cast<float*>(ws + p.dotq);
+    float* dotk = reinterpret_cast<float*>(ws + p.dotk);
+    const float scale = a.far_scale;
+    // what each segment adds to the state and to its gradient, then the borders
+    LinArgs s = a;
+    s.G = 1;
+    s.s_out = S;
+    s.s_out_bh = slots * cells;
+    s.s_out_seg = cells;
+    s.sa = dv;
+    s.sc = 1;
+    s.gsum = gsum;
+    LIN_TRY((lin_launch<T, LIN_STATE>(s, wide, st)));
+    LinArgs r = s;
+    r.G = a.G;
+    r.k = a.q; r.kb = a.qb; r.kt = a.qt;
+    r.v = g.dy; r.vb = g.gb; r.vt = g.gt;
+    r.s_out = R;
+    r.state_scale = scale;
+    r.gsum = nullptr;
+    LIN_TRY((lin_launch<T, LIN_STATE_BACK>(r, wide, st)));
+    LIN_TRY(lin_scan(LinScan{S, a.s_in, nullptr, gsum, p.nseg, slots, (int)cells, 0}, bh, st));
+    LIN_TRY(lin_scan(LinScan{R, g.dstate_out, g.dstate_in, gsum, p.nseg, slots, (int)cells, 1}, bh, st));
+    // the three gradients of token arrays
+    LinArgs x = a;
+    x.s_in_bh = slots * cells;
+    x.s_in_seg = cells;
+    x.s_out = nullptr;
+    x.gsum = nullptr;
+    LinArgs y = x;
+    y.q = g.dy; y.qb = g.gb; y.qt = g.gt; y.k = a.v; y.kb = a.vb; y.kt = a.vt; y.v = a.k; y.vb = a.kb; y.vt = a.kt;
+    y.z = a.q; y.zb = a.qb; y.zt = a.qt;
+    y.dk = dv; y.dv = dk; y.s_in = S; y.sa = 1; y.sc = dv; y.out = g.dq; y.dot = dotq;
+    LIN_TRY((lin_launch<T, LIN_DQ>(y, wide, st)));
+    y = x;
+    y.q = a.v; y.qb = a.vb; y.qt = a.vt; y.k = g.dy; y.kb = g.gb; y.kt = g.gt; y.v = a.q; y.vb = a.qb; y.vt = a.qt;
+    y.z = a.k; y.zb = a.kb; y.zt = a.kt;
+    y.dk = dv; y.dv = dk; y.s_in = R; y.sa = 1; y.sc = dv; y.out = g.dk; y.dot = dotk;
+    y.far_scale = 1.f; y.state_scale = scale;
+    LIN_TRY((lin_launch<T, LIN_DK>(y, wide, st)));
+    y = x;
+    y.q = a.k; y.qb = a.kb; y.qt = a.kt; y.k = a.q; y.kb = a.qb; y.kt = a.qt; y.v = g.dy; y.vb = g.gb; y.vt = g.gt;
+    y.s_in = R; y.sa = dv; y.sc = 1; y.out = g.dv;
+    y.far_scale = 1.f; y.state_scale = scale;
+    LIN_TRY((lin_launch<T, LIN_DV>(y, wide, st)));
+    if (!g.dld) return hipSuccess;
+    // the decays
+    LIN_TRY(timed_layer(st, [&] {
+        launch_k(lin_flow_kernel, dim3((unsigned)(bh * p.nseg)), dim3(256), 0, st, S, R, flow, p.nseg, slots, (int)cells);
+        return hipGetLastError();
+    }));
+    float* h = reinterpret_cast<float*>(ws + p.h);
+    double* part = reinterpret_cast<double*>(ws + p.part);
+    float* sums = reinterpret_cast<float*>(ws + p.sums);
+    LinPairs w{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
+               scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + 63) / 64};
+    LIN_TRY(lin_pairs<T>(w, st));
+    LIN_TRY(timed_layer(st, [&] {
+        launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.counts, g.dld,
+                 part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk(dk, dv, sizeof(T)));
+        return hipGetLastError();
+    }));
+    if (a.per_token) return hipSuccess;
+    return timed_layer(st, [&] {
+        launch_k(lin_gate_sum_kernel, dim3(a.Hk), dim3(64), 0, st, part, g.dld, a.B, a.Hk, p.nseg);
+        return hipGetLastError();
+    });
+}
+
+static bool lin_sizes_ok(int B, int T, int H, int Hk, int dk, int dv) {
+    return B >= 0 && T >= 0 && T <= 1 << 30 && H > 0 && Hk > 0 && H % Hk == 0 && H / Hk <= 64 && Hk <= 65535 && dk >= 8 && dk <= 256 &&
+           dk % 8 == 0 && dv >= 8 && dv <= 256 && dv % 8 == 0 && (long)B * Hk < 1L << 24 &&
+           (B == 0 || T <= (1L << 40) / ((long)B * H * 256));
+}
+static bool lin_tokens_ok(const void* p, long batch, long token, int B, int T) {
+    const long lim = 1L << 40;
+    return p && (uintptr_t)p % 16 == 0 && batch >= 0 && token >= 0 && batch <= lim && token <= lim && batch % 8 == 0 &&
+           token % 8 == 0 && (double)B * (double)batch < 4e18 && (double)T * (double)token < 4e18;
+}
+static tm_status lin_status(hipError_t e) {
+    return e == hipSuccess ? TM_OK : e == hipErrorInvalidValue ? TM_ERR_INVALID : TM_ERR_HIP;
+}
+
+}  // namespace tmk
+
+using namespace tmk;
+
+extern "C" {
+
+size_t tm_linear_workspace_bytes(int batch, int n_tokens, int heads, int kv_heads, int key_dim, int value_dim,
+                                 int backward) {
+    if (!lin_sizes_ok(batch, n_tokens, heads, kv_heads, key_dim, value_dim)) return 0;
+    return lin_plan(batch, n_tokens, kv_heads, key_dim, value_dim, backward != 0).bytes;
+}
+
+tm_status tm_linear_attention(const void* q, long q_batch, long q_token, const void* k, long k_batch, long k_token,
+                              const void* v, long v_batch, long v_token, const float* log_decay, int per_token,
+                              const int* counts, const float* state_in, float* state_out, void* out, double scale,
+                              int batch, int n_tokens, int heads, int kv_heads, int key_dim, int value_dim,
+                              tm_dtype dtype, void* workspace, void* stream) {
+    if (dtype != TM_F32 && dtype != TM_BF16) return TM_ERR_DTYPE;
+    if (!lin_sizes_ok(batch, n_tokens, heads, kv_heads, key_dim, value_dim) || !isfinite((float)scale) ||
+        (uintptr_t)state_in % 16 || (uintptr_t)state_out % 16)
+        return TM_ERR_INVALID;
+    if (batch == 0) return TM_OK;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (n_tokens == 0) {
+        if (!state_out || state_out == state_in) return TM_OK;
+        return lin_status(lin_copy(state_in, state_out, (long)batch * kv_heads * key_dim * value_dim, st));
+    }
+    if (!lin_tokens_ok(q, q_batch, q_token, batch, n_tokens) || !lin_tokens_ok(k, k_batch, k_token, batch, n_tokens) ||
+        !lin_tokens_ok(v, v_batch, v_token, batch, n_tokens) || !out || (uintptr_t)out % 16 || !log_decay ||
+        (uintptr_t)log_decay % 4 || (uintptr_t)counts % 4 || !workspace || (uintptr_t)workspace % 256)
+        return TM_ERR_INVALID;
+    LinArgs a{};
+    a.q = q; a.qb = q_batch; a.qt = q_token; a.k = k; a.kb = k_batch; a.kt = k_token; a.v = v; a.vb = v_batch; a.vt = v_token;
+    a.ld = log_decay; a.per_token = per_token != 0; a.counts = counts; a.s_in = state_in; a.out = out;
+    a.pair_scale = a.far_scale = (float)scale; a.state_scale = 1.f;
+    a.B = batch; a.T = n_tokens; a.Hk = kv_heads; a.G = heads / kv_heads; a.dk = key_dim; a.dv = value_dim;
+    char* ws = static_cast<char*>(workspace);
+    return lin_status(dtype == TM_F32 ? lin_forward<float>(a, state_out, ws, st) : lin_forward<bf16>(a, state_out, ws, st));
+}
+
+tm_status tm_linear_attention_backward(const void* q, long q_batch, long q_token, const void* k, long k_batch,
+                                       long k_token, const void* v, long v_batch, long v_token,
+                                       const float* log_decay, int per_token, const int* counts,
+                                       const float* state_in, const void* dout, long dout_batch, long dout_token,
+                                       const float* dstate_out, void* dq, void* dk, void* dv, float* dlog_decay,
+                                       float* dstate_in, double scale, int batch, int n_tokens, int heads,
+                                       int kv_heads, int key_dim, int value_dim, tm_dtype dtype, void* workspace,
+                                       void* stream) {
+    if (dtype != TM_F32 && dtype != TM_BF16) return TM_ERR_DTYPE;
+    if (!lin_sizes_ok(batch, n_tokens, heads, kv_heads, key_dim, value_dim) || !isfinite((float)scale) ||
+        (uintptr_t)state_in % 16 || (uintptr_t)dstate_out % 16 || (uintptr_t)dstate_in % 16 || (uintptr_t)dlog_decay % 4)
+        return TM_ERR_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (batch == 0 || n_tokens == 0) {
+        if (dlog_decay && !per_token) {
+            const hipError_t e = timed_layer(st, [&] {
+                launch_k(lin_zero_kernel, dim3(1), dim3(256), 0, st, dlog_decay, kv_heads);
+                return hipGetLastError();
+            });
+            if (e != hipSuccess) return lin_status(e);
+        }
+        if (batch == 0 || !dstate_in || dstate_in == dstate_out) return TM_OK;
+        return lin_status(lin_copy(dstate_out, dstate_in, (long)batch * kv_heads * key_dim * value_dim, st));
+    }
+    if (!lin_tokens_ok(q, q_batch, q_token, batch, n_tokens) || !lin_tokens_ok(k, k_batch, k_token, batch, n_tokens) ||
+        !lin_tokens_ok(v, v_batch, v_token, batch, n_tokens) ||
+        !lin_tokens_ok(dout, dout_batch, dout_token, batch, n_tokens) || !dq || (uintptr_t)dq % 16 || !dk ||
+        (uintptr_t)dk % 16 || !dv || (uintptr_t)dv % 16 || !log_decay || (uintptr_t)log_decay % 4 ||
+        (uintptr_t)counts % 4 || !workspace || (uintptr_t)workspace % 256)
+        return TM_ERR_INVALID;
+    LinArgs a{};
+    a.q = q; a.qb = q_batch; a.qt = q_token; a.k = k; a.kb = k_batch; a.kt = k_token; a.v = v; a.vb = v_batch; a.vt = v_token;
+    a.ld = log_decay; a.per_token = per_token != 0; a.counts = counts; a.s_in = state_in;
+    a.pair_scale = a.far_scale = (float)scale; a.state_scale = 1.f;
+    a.B = batch; a.T = n_tokens; a.Hk = kv_heads; a.G = heads / kv_heads; a.dk = key_dim; a.dv = value_dim;
+    const LinBack g{dout, dout_batch, dout_token, dstate_out, dq, dk, dv, dlog_decay, dstate_in};
+    char* ws = static_cast<char*>(workspace);
+    return lin_status(dtype == TM_F32 ? lin_backward<float>(a, g, ws, st) : lin_backward<bf16>(a, g, ws, st));
+}
+
+}  // extern "C"
