@@ -792,14 +792,13 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         p.h = take(bh * T * 4);
         p.sums = take(bh * ((T + 31) / 32) * 8);   // chunks of 32 tokens, or 64
         p.part = take(bh * p.nseg * 8);
-    } else {
+    } else if (T > 0 && B > 0) {
         // the sequence is divided where its heads alone do not fill the chip
         const long wgs = (long)bh * ((dv + 63) / 64);
         long seg = wgs >= 256 || T <= 256 ? 1 : (1024 + wgs - 1) / wgs;
         seg = seg < (T + 255) / 256 ? seg : (T + 255) / 256;
         p.L = (int)(((T + seg - 1) / seg + 63) / 64 * 64);
-        if (T > 0 && p.L == 0) p.L = 64;
-        p.nseg = p.L ? (T + p.L - 1) / p.L : 0;
+        p.nseg = (T + p.L - 1) / p.L;
         if (p.nseg > 1) {
             p.states = take(bh * p.nseg * cells * 4);
             p.gsum = take(bh * p.nseg * 8);

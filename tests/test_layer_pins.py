@@ -164,6 +164,8 @@ def test_linear_empty_calls_and_sizes():
     a = list(LIN)
     a[17], a[13] = 0, None
     assert L._lib().tm_linear_attention(*a) == T.TM_OK
+    for b, n in ((0, 0), (0, 5), (3, 0), (1, 1)):
+        assert T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64) == 256 and T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64, True) >= 256
     assert T.tm_linear_workspace_bytes(2, 4, 2, 2, 64, 60) == 0 and T.tm_linear_workspace_bytes(2, 4, 3, 2, 64, 64) == 0
     assert 0 < T.tm_linear_workspace_bytes(2, 4096, 2, 2, 64, 64) < T.tm_linear_workspace_bytes(2, 4096, 2, 2, 64, 64, True)
 
