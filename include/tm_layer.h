@@ -124,7 +124,9 @@ tm_status tm_linear_attention_backward(const void* q, long q_batch, long q_token
 
 /* Rows of x [rows][cols] (x_row elements apart, aligned to their type) as
  * 8-bit integers with a scale each: with m = max |x| over a row,
- *   codes = 127 x / m rounded to nearest even, scales = m / 127
+ *   codes = (127 x) / m rounded to nearest even, scales = m / 127,
+ * product and quotients in fp32 (exact for bf16: a code is off by one only
+ * where an fp32 quotient stands within its rounding of a half)
  * (a row of zeros: codes and scale 0; one with a non-finite element: codes 0,
  * scale NaN).  codes: int8 [rows][code_row], 16-byte aligned, code_row a
  * multiple of 16 and at least cols; the columns behind cols become 0.
@@ -132,11 +134,12 @@ tm_status tm_linear_attention_backward(const void* q, long q_batch, long q_token
 tm_status tm_int8_quantize(const void* x, long x_row, signed char* codes, long code_row, float* scales, long rows,
                            int cols, tm_dtype dtype, void* stream);
 
-/* y[m][n] = (sum_k a[m][k] w[n][k]) a_scales[m] w_scales[n] rounded once to
+/* y[m][n] = (sum_k a[m][k] w[n][k]) a_scales[m] w_scales[n], rounded once to
  * dtype: a [rows][code_row], w [outs][code_row] int8 (16-byte aligned,
  * code_row a multiple of 16 and at least cols; what stands behind cols must
  * be 0 in both), y rows y_row elements apart, aligned to its type.  The sum
- * is exact (32-bit integers); it takes a_scales, then w_scales, in fp32. */
+ * is exact (32-bit integers); it takes a_scales, then w_scales, in 64
+ * bits. */
 tm_status tm_int8_matmul(const signed char* a, const float* a_scales, const signed char* w, const float* w_scales,
                          long code_row, void* y, long y_row, long rows, int outs, int cols, tm_dtype dtype,
                          void* stream);

@@ -77,10 +77,13 @@ def linear_backward(q, k, v, g, scale, state, dy, dstate, counts=None):
 
 
 def int8_rows(x):
-    """(codes, scales) of rows of fp32 values, as the header defines them."""
+    """(codes, scales) of rows of fp32 values, as the header defines them:
+    (127 x) / m in fp32 (for bf16 values the same in 64 bits)."""
+    x = x.astype(np.float32)
     m = np.abs(x).max(axis=1)
     fine = np.isfinite(m)
     with np.errstate(all="ignore"):
-        q = np.where((fine & (m > 0))[:, None], 127.0 * x.astype(np.float64) / m.astype(np.float64)[:, None], 0.0)
-    scales = np.where(fine, m.astype(np.float32) / np.float32(127), np.float32(np.nan)).astype(np.float32)
+        down = np.where(m > 1e36, np.float32(2.0 ** -10), np.float32(1))[:, None]   # 127 x would overflow
+        q = np.where((fine & (m > 0))[:, None], np.float32(127) * (x * down) / (m[:, None] * down), np.float32(0))
+    scales = np.where(fine, m / np.float32(127), np.float32(np.nan)).astype(np.float32)
     return np.rint(np.where(fine[:, None], q, 0.0)).astype(np.int64), scales

@@ -11,8 +11,9 @@ namespace tmk {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// codes = rint(127 x / m): the product first, which is exact for bf16, so a
-// quotient halfway between two codes is one in fp32 too; a row whose 127 m
+// codes = rint((127 x) / m) in fp32.  The product comes first: it is exact for
+// bf16, so that a quotient halfway between two codes is one in fp32 too, and
+// (127 x and m have 15 and 8 bits) no other is; a row whose 127 m
 // would overflow is divided by 2^10 beforehand (exactly).
 template <class T>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* x, long x_row, signed char* codes, long code_row,
@@ -98,14 +99,14 @@ template <class T> __global__ __launch_bounds__(256) void int8_matmul_kernel(Int
     for (int i = 0; i < 4; ++i) {
         const long m = m0 + wm + 16 * i + l16;
         if (m >= g.M) continue;
-        const float s = g.as[m];
+        const double s = g.as[m];   // 64 bits: neither product overflows where the result does not
         T* y = reinterpret_cast<T*>(g.y) + m * g.y_row;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = n0 + wn + 16 * j + 4 * lg;
             struct __align__(4 * sizeof(T)) V4 { T e[4]; } o;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o.e[r] = (T)((float)acc[i][j][r] * s * (n + r < g.N ? g.wsc[n + r] : 0.f));
+            for (int r = 0; r < 4; ++r) o.e[r] = (T)((double)acc[i][j][r] * s * (double)(n + r < g.N ? g.wsc[n + r] : 0.f));
             if (g.vec && n + 3 < g.N) {
                 *reinterpret_cast<V4*>(y + n) = o;
             } else {

@@ -82,6 +82,9 @@ def test_linear_gradients_are_differences():
 
 def test_int8_by_hand():
     codes, scales = O.int8_rows(np.array([[127.0, 2.5, -3.5, 0.4], [0, 0, 0, 0], [1, np.inf, 0, 0]], dtype=np.float32))
+    x = torch.from_numpy(rand(50, 300, seed=8)).to(torch.bfloat16).double().numpy()
+    m = np.abs(x).max(axis=1, keepdims=True)
+    assert np.array_equal(O.int8_rows(x)[0], np.rint(127 * x / m))   # bf16: what 64 bits give
     assert codes.tolist() == [[127, 2, -4, 0], [0] * 4, [0] * 4] and scales[:2].tolist() == [1.0, 0.0] and np.isnan(scales[2])
 
 
