@@ -14,12 +14,12 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // codes = rint((127 x) / m) in fp32.  The product comes first: it is exact for
 // bf16, so that a quotient halfway between two codes is one in fp32 too, and
 // (127 x and m have 15 and 8 bits) no other is; a row whose 127 m would
-// overflow is divided by 2^10 beforehand (exactly).  Products with 1 / m give
-// the quotients to 3.1e-5 (two roundings at up to 127, and the quotient's
-// own), so only those within 1e-4 of a half are divided.
+// overflow is divided by 2^10 beforehand (exactly).  Products with 127 / m
+// give the quotients to 2.3e-5 (127 times two roundings and the quotient's
+// own), so only where one is within 1e-4 of a half are four of them divided.
 struct Int8Scale {
-    float scale, down, top, inv;   // the row's scale; its factors
-    bool any;                      // false: all codes are 0
+    float scale, down, top, by;   // the row's scale; its factors
+    bool any;                     // false: all codes are 0
 };
 __device__ __forceinline__ Int8Scale int8_scale(float m) {   // m: infinity where an element is not finite
     Int8Scale s;
@@ -27,7 +27,7 @@ __device__ __forceinline__ Int8Scale int8_scale(float m) {   // m: infinity wher
     s.any = m > 0.f && !lost;
     s.down = m > 1e36f ? 0x1p-10f : 1.f;
     s.top = m * s.down;
-    s.inv = 1.f / s.top;
+    s.by = 127.f / m;   // infinite for the smallest m: all are divided then
     s.scale = lost ? __builtin_nanf("") : m / 127.f;
     return s;
 }
@@ -36,18 +36,26 @@ __device__ __forceinline__ float int8_size(float m, float x) {
     const float v = fabsf(x);
     return v <= 3.402823466e38f ? fmaxf(m, v) : __builtin_inff();
 }
-// 4 values as the bytes of a word
+// 4 values as the bytes of a word.  Added to 1.5 * 2^23 a quotient is rounded
+// to a whole number, to even at a half, which stands in the low bits.
 __device__ __forceinline__ unsigned int8_pack(const float* x, const Int8Scale& s) {
-    unsigned w = 0;
+    constexpr float ONES = 12582912.f;
+    float v[4], far = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float p = 127.f * (x[e] * s.down);
-        float q = p * s.inv, v = rintf(q);
-        // 1 / m overflows for the smallest m: then every quotient is divided
-        if (!(fabsf(fabsf(q - v) - 0.5f) > 1e-4f)) v = rintf(p / s.top);
-        w |= ((unsigned)(int)v & 255u) << (8 * e);
+        const float q = x[e] * s.by;
+        v[e] = q + ONES;
+        const float off = fabsf(q - (v[e] - ONES));
+        far = off < 0.4999f ? far : 1.f;   // also where q is not finite
     }
-    return s.any ? w : 0u;
+    if (far != 0.f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = 127.f * (x[e] * s.down) / s.top + ONES;
+    const unsigned a = __builtin_bit_cast(unsigned, v[0]), b = __builtin_bit_cast(unsigned, v[1]),
+                   c = __builtin_bit_cast(unsigned, v[2]), d = __builtin_bit_cast(unsigned, v[3]);
+    // the low bytes: of a and b, then of c and d, then both pairs
+    const unsigned ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+    return s.any ? (ab | cd << 16) : 0u;
 }
 
 // One row a workgroup.  VEC: rows allow loads of 16 bytes; up to 32 elements a
@@ -276,13 +284,21 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
         const int row = threadIdx.x / lanes, at = threadIdx.x % lanes;
         const bool on = row < M;
         const T* x = reinterpret_cast<const T*>(g.x) + (on ? row : 0) * g.x_row;
-        constexpr int VE = 16 / sizeof(T);
+        constexpr int VE = 16 / sizeof(T), KEEP = 64 / VE;
         struct __align__(16) Vec { T e[VE]; };
         const int units = g.xvec ? g.cols / VE : 0;
         float m = 0.f;
+        Vec kept[KEEP];
         if (on) {
-#pragma unroll 4
-            for (int u = at; u < units; u += lanes) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (at + i * lanes < units) kept[i] = *reinterpret_cast<const Vec*>(x + (long)(at + i * lanes) * VE);
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (at + i * lanes < units)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) m = int8_size(m, (float)kept[i].e[e]);
+            for (int u = at + KEEP * lanes; u < units; u += lanes) {
                 const Vec v = *reinterpret_cast<const Vec*>(x + (long)u * VE);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) m = int8_size(m, (float)v.e[e]);
@@ -301,15 +317,22 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
         if (on) {
             if (at == 0) sc[row] = s.scale;
             signed char* c = lds + row * stride;
-#pragma unroll 2
-            for (int u = at; u < units; u += lanes) {
-                const Vec v = *reinterpret_cast<const Vec*>(x + (long)u * VE);
+            auto put = [&](int u, const Vec& v) {
                 float f[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) f[e] = (float)v.e[e];
+                if constexpr (VE == 8) {
+                    const uint2 w = {int8_pack(f, s), int8_pack(f + 4, s)};
+                    *reinterpret_cast<uint2*>(c + u * 8) = w;
+                } else {
+                    *reinterpret_cast<unsigned*>(c + u * 4) = int8_pack(f, s);
+                }
+            };
 #pragma unroll
-                for (int e = 0; e < VE; e += 4) *reinterpret_cast<unsigned*>(c + u * VE + e) = int8_pack(f + e, s);
-            }
+            for (int i = 0; i < KEEP; ++i)
+                if (at + i * lanes < units) put(at + i * lanes, kept[i]);
+            for (int u = at + KEEP * lanes; u < units; u += lanes)
+                put(u, *reinterpret_cast<const Vec*>(x + (long)u * VE));
             for (int i = units * VE + 4 * at; i < blocks * 64; i += 4 * lanes) {
                 float f[4];
 #pragma unroll
