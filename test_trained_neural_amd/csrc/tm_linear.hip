@@ -68,39 +68,6 @@ __device__ __forceinline__ double lin_gate(float g) {
 
 template <class T> __device__ __forceinline__ bool lin_finite(T x) { return __builtin_isfinite((float)x); }
 
-// Rows t0 .. t0 + C - 1 (zeros from n on) and columns c0 .. c0 + D - 1 (zeros
-// from `cols` on) of a token array, 16 bytes at a time: row-major into `rows`
-// [C][RP], transposed into `cols_t` [D][CP].  bad: the first row with a
-// non-finite element, which is taken as zero.
-template <class T, int D, int C, int RP, int CP, bool ROWS, bool COLS, bool CHECK>
-__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int n, int c0, int cols, T* rows, T* cols_t,
-                                          int* bad) {
-    constexpr int VE = 16 / sizeof(T), UNITS = D / VE;
-    struct __align__(16) Vec { T e[VE]; };
-    for (int i = threadIdx.x; i < C * UNITS; i += 256) {
-        const int r = i / UNITS, u = i % UNITS, c = c0 + u * VE;
-        Vec v;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v.e[e] = (T)0.f;
-        if (t0 + r < n && c < cols) v = *reinterpret_cast<const Vec*>(x + (long)(t0 + r) * step + c);
-        if constexpr (CHECK) {
-            bool fine = true;
-#pragma unroll
-            for (int e = 0; e < VE; ++e)
-                if (!lin_finite(v.e[e])) {
-                    fine = false;
-                    v.e[e] = (T)0.f;
-                }
-            if (!fine) atomicMin(bad, r);
-        }
-        if constexpr (ROWS) *reinterpret_cast<Vec*>(rows + r * RP + u * VE) = v;
-        if constexpr (COLS) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) cols_t[(u * VE + e) * CP + r] = v.e[e];
-        }
-    }
-}
-
 // 8 values in the order in which two stacked accumulator tiles hold 32 rows:
 // lane group g has 4 g .. and 16 + 4 g ..
 __device__ __forceinline__ bf16x8 lin_split8(const bf16* p, int g) {
@@ -130,248 +97,375 @@ template <class T, int N> struct Parts {
 };
 template <class T> constexpr int lin_parts(int n) { return sizeof(T) == 4 ? 1 : n; }
 
-template <class T, int DK, int C> struct LinLds {
-    static constexpr int PAD = 16 / sizeof(T);
-    static constexpr int RP = DK + PAD, CP = C + PAD;
-    static constexpr size_t q = 0, k = q + sizeof(T) * C * RP, kt = k + sizeof(T) * C * RP,
-                            vt = kt + sizeof(T) * DK * CP, p = vt + sizeof(T) * 64 * CP, g = p + sizeof(T) * C * CP,
-                            head = g + 8 * 64, tail = head + 4 * 64, dot = tail + 4 * 64, bad = dot + 4 * 4 * 64,
-                            bytes = bad + 16;
+// Tokens of a chunk: 64, for fp32 32 (with its four times slower matrix
+// instructions the pairs of a chunk cost more than the state it saves).
+template <class T> constexpr int lin_chunk() { return sizeof(T) == 4 ? 32 : 64; }
+
+// Row lengths in LDS: operands read along a row are 8 (fp32: 4) elements
+// longer than theirs, those read across rows 16, so that 16 rows, or 4 rows
+// of 16 columns, stand at different banks.
+template <class T, int DK, int CW> struct LinLds {
+    static constexpr int C = lin_chunk<T>(), PAD = 16 / sizeof(T), TPAD = sizeof(T) == 4 ? 4 : 16;
+    static constexpr int QP = DK + PAD, KP = DK + TPAD, VP = 64 * CW + TPAD, PP = C + PAD;
+    static constexpr int GATES = 512;   // tokens whose decays are summed at a time
+    static constexpr size_t q = 0, k = q + sizeof(T) * C * QP, v = k + sizeof(T) * C * KP, p = v + sizeof(T) * C * VP,
+                            g = p + sizeof(T) * C * PP, head = g + 8 * GATES, tail = head + 4 * GATES,
+                            dot = tail + 4 * GATES, bad = dot + 4 * 4 * 64, bytes = bad + 16;
 };
 
+// A tile [C][D] of a token array on its way from memory to LDS, 16 bytes at a
+// time.  Rows behind the last and columns behind the array's are read as ones
+// that are there and taken as zeros when they are put down.
+template <class T, int D, int C> struct LinTile {
+    static constexpr int VE = 16 / sizeof(T), UNITS = D / VE, N = (C * UNITS + 255) / 256;
+    typedef T Vec __attribute__((ext_vector_type(VE)));
+    Vec v[N];
+    __device__ __forceinline__ void load(const T* x, long step, int t0, int last, int c0, int cols) {
+        const int u = threadIdx.x % UNITS, c = c0 + u * VE < cols ? c0 + u * VE : 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = threadIdx.x / UNITS + i * (256 / UNITS);
+            v[i] = *reinterpret_cast<const Vec*>(x + (long)min(t0 + r, last - 1) * step + c);
+        }
+    }
+    // bad: the first row with a non-finite element, which is taken as zero
+    template <bool CHECK>
+    __device__ __forceinline__ void store(T* to, int row, int t0, int last, int c0, int cols, int* bad) {
+        const int u = threadIdx.x % UNITS;
+        const bool there = c0 + u * VE < cols;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = threadIdx.x / UNITS + i * (256 / UNITS);
+            Vec x = keep_if(v[i], there && t0 + r < last);
+            if constexpr (CHECK) {
+                bool fine = true;
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (!lin_finite((T)x[e])) {
+                        fine = false;
+                        x[e] = (T)0.f;
+                    }
+                if (!fine) atomicMin(bad, r);
+            }
+            if (C * UNITS % 256 == 0 || r < C) *reinterpret_cast<Vec*>(to + r * row + u * VE) = x;
+        }
+    }
+};
+
+// 8 rows from r0 of column c + (lane % 16), for lane group g rows 8 g ..
+__device__ __forceinline__ bf16x8 lin_column8(const bf16* m, int row, int c) {
+    typedef short S4 __attribute__((ext_vector_type(4)));
+    typedef short S8 __attribute__((ext_vector_type(8)));
+    const int l = threadIdx.x & 63, i = l & 15;
+    // the transposing read: a lane names 4 columns of a row, and gets 4 rows of its column
+    const bf16* p = m + (8 * (l >> 4) + (i >> 2)) * row + c + 4 * (i & 3);
+    const S4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(p));
+    const S4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(p + 4 * row));
+    return __builtin_bit_cast(bf16x8, (S8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ f32x8 lin_column8(const float* m, int row, int c) {
+    const int l = threadIdx.x & 63;
+    const float* p = m + 8 * (l >> 4) * row + c + (l & 15);
+    f32x8 x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = p[e * row];
+    return x;
+}
+
 // One workgroup of 4 waves takes one key head of one entry, one segment of its
-// tokens, and 64 columns of the values (16 a wave), whose slice of the state
-// its waves hold in accumulators.
-template <class T, int DK, int C, int KIND>
-__global__ __launch_bounds__(256) void lin_kernel(LinArgs a) {
+// tokens, and 64 CW columns of the values (16 CW a wave), whose slice of the
+// state its waves hold in accumulators.  The next chunk's rows are read while
+// a chunk is computed.
+template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin_body(const LinArgs& a, int block) {
     constexpr bool STATE = KIND == LIN_STATE || KIND == LIN_STATE_BACK;
     constexpr bool REV = KIND == LIN_STATE_BACK || KIND == LIN_DK || KIND == LIN_DV;
     constexpr bool SUM = REV;   // the group's heads are summed (else each has an output of its own)
     constexpr bool DOT = KIND == LIN_DQ || KIND == LIN_DK;
-    constexpr int NT = C / 16, NS = DK / 32, NM = DK / 16, KS = C / 32;
+    constexpr int C = lin_chunk<T>(), NT = C / 16, NS = DK / 32, NM = DK / 16, KS = C / 32;
     // the state as an operand keeps 16 bits, 24 where its products enter the gradients of the decays
-    constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP = lin_parts<T>(3);
+    constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP3 = lin_parts<T>(3);
     typedef typename Frag<T>::T F;
-    typedef LinLds<T, DK, C> S_;
-    constexpr int RP = S_::RP, CP = S_::CP;
+    typedef LinLds<T, DK, CW> S_;
+    constexpr int QP = S_::QP, KP = S_::KP, VP = S_::VP, PP = S_::PP, BATCH = S_::GATES / C;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     T* qs = reinterpret_cast<T*>(lds + S_::q);
     T* ks = reinterpret_cast<T*>(lds + S_::k);
-    T* kT = reinterpret_cast<T*>(lds + S_::kt);
-    T* vT = reinterpret_cast<T*>(lds + S_::vt);
+    T* vs = reinterpret_cast<T*>(lds + S_::v);
     T* ps = reinterpret_cast<T*>(lds + S_::p);
     double* gs = reinterpret_cast<double*>(lds + S_::g);
     float* head = reinterpret_cast<float*>(lds + S_::head);
     float* tail = reinterpret_cast<float*>(lds + S_::tail);
     float* dots = reinterpret_cast<float*>(lds + S_::dot);
-    int* bad = reinterpret_cast<int*>(lds + S_::bad);
+    int* bads = reinterpret_cast<int*>(lds + S_::bad);
 
-    const int slab = blockIdx.x % a.slabs, rest = blockIdx.x / a.slabs;
+    const int slab = block % a.slabs, rest = block / a.slabs;
     const int seg = rest % a.nseg, bh = rest / a.nseg, b = bh / a.Hk, h = bh % a.Hk;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
-    const int col0 = slab * 64, wcol = col0 + 16 * wave;   // the wave's first column
+    const int col0 = slab * 64 * CW, wcol = 16 * CW * wave;   // the workgroup's first column, the wave's in it
     const int n = lin_tokens(a, b), first = seg * a.L, last = (int)min((long)n, (long)first + a.L);
-    const int chunks = last > first ? (last - first + C - 1) / C : 0;
+    const int chunks = last > first ? (last - first + C - 1) / C : 0, steps = chunks * a.G;
 
     const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb;
     const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb;
     const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb;
     const T* z = reinterpret_cast<const T*>(a.z) + b * a.zb;
 
-    f32x4 S[NM];
+    f32x4 S[NM][CW];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int w = 0; w < CW; ++w) S[m][w] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (!STATE && a.s_in) {
         const float* s = a.s_in + bh * a.s_in_bh + seg * a.s_in_seg;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * lg + r, c = wcol + l16;
-                if (i < a.dk && c < a.dv) S[m][r] = s[i * a.sa + c * a.sc];
-            }
+            for (int w = 0; w < CW; ++w)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * m + 4 * lg + r, c = col0 + wcol + 16 * w + l16;
+                    if (i < a.dk && c < a.dv) S[m][w][r] = s[i * a.sa + c * a.sc];
+                }
     }
     double kept = 0.0;
 
-    for (int ci = 0; ci < chunks; ++ci) {
-        const int t0 = first + (REV ? chunks - 1 - ci : ci) * C;
-        const int rows = min(C, last - t0);   // tokens of the chunk
+    LinTile<T, DK, C> qv, kv;
+    LinTile<T, 64 * CW, C> vv;
+    auto start = [&](int ci) { return first + (REV ? chunks - 1 - ci : ci) * C; };
+    auto fetch = [&](int ci, int g) {
+        const int t0 = start(ci), many = h * a.G + g;
+        if constexpr (!STATE)
+            if (!SUM || g == 0) qv.load(q + (long)(SUM ? h : many) * a.dk, a.qt, t0, last, 0, a.dk);
+        if (SUM || g == 0) {
+            const int kh = SUM ? many : h;
+            kv.load(k + (long)kh * a.dk, a.kt, t0, last, 0, a.dk);
+            vv.load(v + (long)kh * a.dv, a.vt, t0, last, col0, a.dv);
+        }
+    };
+    f32x4 O[NT][CW];
+    float far_dot[NT];
+    auto put_dots = [&](int t0) {   // over the workgroup's columns
+        const int i = threadIdx.x;
+        if (i < min(C, last - t0))
+            a.dot[((long)slab * a.B * a.Hk + bh) * a.T + t0 + i] = (dots[i] + dots[64 + i]) + (dots[128 + i] + dots[192 + i]);
+    };
+    if (steps) fetch(0, 0);
+    if (KIND == LIN_OUT && threadIdx.x < 2) bads[threadIdx.x] = C;
+    int ci = 0, g = 0;
+#pragma unroll 1
+    for (int st = 0; st < steps; ++st) {
+        const int t0 = start(ci), many = h * a.G + g, gate0 = ci % BATCH * C;
+        int* bad = bads + (ci & 1);
+        __syncthreads();   // the step before is done with what stands in LDS
+        if constexpr (!STATE)
+            if (!SUM || g == 0) qv.template store<false>(qs, QP, t0, last, 0, a.dk, nullptr);
+        if (SUM || g == 0) {
+            kv.template store<false>(ks, KP, t0, last, 0, a.dk, nullptr);
+            vv.template store<KIND == LIN_OUT>(vs, VP, t0, last, col0, a.dv, bad);
+        }
+        if constexpr (DOT)
+            if (g == 0 && ci > 0) put_dots(start(ci - 1));
+        const int next_g = g + 1 < a.G ? g + 1 : 0, next_ci = next_g ? ci : ci + 1;
+        if (st + 1 < steps) fetch(next_ci, next_g);
+        if (g == 0 && gate0 == 0) {   // the decays of the next 512 tokens, C lanes a chunk
+#pragma unroll
+            for (int it = 0; it < S_::GATES / 256; ++it) {
+                const int slot = it * 256 + threadIdx.x, c = ci + slot / C, i = slot % C;
+                double x = 0.0;
+                if (c < chunks && start(c) + i < last)
+                    x = lin_gate(a.ld[a.per_token ? ((long)b * a.T + start(c) + i) * a.Hk + h : h]);
+#pragma unroll
+                for (int m = 1; m < C; m <<= 1) {
+                    const double o = __shfl_up(x, m, C);
+                    if (i >= m) x += o;
+                }
+                const double end = __shfl(x, C - 1, C);
+                gs[slot] = x;
+                const float before = __builtin_amdgcn_exp2f((float)x), after = __builtin_amdgcn_exp2f((float)(end - x));
+                head[slot] = (REV ? after : before) * a.far_scale;
+                tail[slot] = (REV ? before : after) * a.state_scale;
+            }
+        }
         __syncthreads();
-        if (wave == 0) {
-            double g = 0.0;
-            if (lane < rows)
-                g = lin_gate(a.ld[a.per_token ? ((long)b * a.T + t0 + lane) * a.Hk + h : h]);
+        if constexpr (!STATE) {
+            if (KIND == LIN_OUT && g == 0 && threadIdx.x == 0) bads[(ci + 1) & 1] = C;
+            // the pairs' weights: tiles of 16 queries by 16 keys, those that a step of 32 keys reads
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const double o = __shfl_up(g, m, 64);
-                if (lane >= m) g += o;
-            }
-            const double end = __shfl(g, 63, 64);
-            gs[lane] = g;
-            const float before = __builtin_amdgcn_exp2f((float)g), after = __builtin_amdgcn_exp2f((float)(end - g));
-            head[lane] = (REV ? after : before) * a.far_scale;
-            tail[lane] = (REV ? before : after) * a.state_scale;
-            if (lane == 0) *bad = C;
-        }
-        if constexpr (KIND == LIN_OUT) __syncthreads();   // bad is set
-        f32x4 O[NT];
-        float far_dot[NT];
+            for (int pi = 0; pi < (NT == 4 ? 3 : 1); ++pi) {
+                const int p = wave + 4 * pi;
+                int qt = p < 4 ? p >> 1 : 2 + ((p - 4) >> 2), kt = p < 4 ? p & 1 : (p - 4) & 3;
+                if (REV) {
+                    qt = NT - 1 - qt;
+                    kt = NT - 1 - kt;
+                }
+                const int i = 16 * qt + l16;
+                f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (REV ? kt >= qt : kt <= qt) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) far_dot[i] = 0.f;
-        for (int g = 0; g < a.G; ++g) {
-            if (g > 0) __syncthreads();
-            const int many = h * a.G + g;
-            if constexpr (!STATE)
-                if (!SUM || g == 0)
-                    lin_stage<T, DK, C, RP, CP, true, false, false>(q + (long)(SUM ? h : many) * a.dk, a.qt, t0, last, 0,
-                                                                   a.dk, qs, nullptr, nullptr);
-            if (SUM || g == 0) {
-                const int kh = SUM ? many : h;
-                lin_stage<T, DK, C, RP, CP, !STATE, true, false>(k + (long)kh * a.dk, a.kt, t0, last, 0, a.dk, ks, kT,
-                                                               nullptr);
-                lin_stage<T, 64, C, RP, CP, false, true, KIND == LIN_OUT>(v + (long)kh * a.dv, a.vt, t0, last, col0,
-                                                                        a.dv, nullptr, vT, bad);
-            }
-            __syncthreads();
-            if constexpr (!STATE) {
-                // the pairs' weights: 16 queries a wave against their keys
-                if (wave < NT) {
-                    const int i = 16 * wave + l16;
-                    const double gi = gs[i];
+                    for (int s = 0; s < NS; ++s)
+                        if (32 * s < a.dk)
+                            mma(w, lin_split8(ks + (16 * kt + l16) * KP + 32 * s, lg), lin_split8(qs + i * QP + 32 * s, lg));
+                    const double gi = gs[gate0 + i];
 #pragma unroll
-                    for (int kt = 0; kt < NT; ++kt) {
-                        f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f};
-                        if (REV ? kt >= wave : kt <= wave) {
-#pragma unroll
-                            for (int s = 0; s < NS; ++s)
-                                mma(w, lin_split8(ks + (16 * kt + l16) * RP + 32 * s, lg),
-                                    lin_split8(qs + i * RP + 32 * s, lg));
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int j = 16 * kt + 4 * lg + r;
-                                const double x = REV ? gs[j] - gi : gi - gs[j];
-                                w[r] = (REV ? j >= i : j <= i)
-                                           ? w[r] * (__builtin_amdgcn_exp2f((float)x) * a.pair_scale) : 0.f;
-                            }
-                        }
-                        struct __align__(4 * sizeof(T)) V4 { T e[4]; } o;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o.e[r] = (T)w[r];
-                        *reinterpret_cast<V4*>(ps + i * CP + 16 * kt + 4 * lg) = o;
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = 16 * kt + 4 * lg + r;
+                        const double gj = gs[gate0 + j], x = REV ? gj - gi : gi - gj;
+                        w[r] = (REV ? j >= i : j <= i) ? w[r] * (__builtin_amdgcn_exp2f((float)x) * a.pair_scale) : 0.f;
                     }
                 }
-                __syncthreads();
-                // the far part, out of the state before the chunk
-                if (!SUM || g == 0) {
-                    f32x4 far[NT];
+                typedef T V4 __attribute__((ext_vector_type(4)));
+                V4 o;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) far[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < 4; ++r) o[r] = (T)w[r];
+                *reinterpret_cast<V4*>(ps + i * PP + 16 * kt + 4 * lg) = o;
+            }
+            // the far part, out of the state before the chunk
+            if (!SUM || g == 0) {
+                f32x4 far[NT][CW];
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        Parts<T, SP> sp;
-                        sp.set(__builtin_shufflevector(S[2 * s], S[2 * s + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            const F qf = lin_split8(qs + (16 * i + l16) * RP + 32 * s, lg);
+                    for (int w = 0; w < CW; ++w) far[i][w] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int p = SP - 1; p >= 0; --p) mma(far[i], sp.p[p], qf);
-                        }
-                    }
+                for (int s = 0; s < NS; ++s) {
+                    if (32 * s >= a.dk) continue;
+                    Parts<T, SP> sp[CW];
+#pragma unroll
+                    for (int w = 0; w < CW; ++w)
+                        sp[w].set(__builtin_shufflevector(S[2 * s][w], S[2 * s + 1][w], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        const float by = head[16 * i + l16];
+                        const F qf = lin_split8(qs + (16 * i + l16) * QP + 32 * s, lg);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) O[i][r] = far[i][r] * by;
+                        for (int w = 0; w < CW; ++w)
+#pragma unroll
+                            for (int p = SP - 1; p >= 0; --p) mma(far[i][w], sp[w].p[p], qf);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float by = head[gate0 + 16 * i + l16];
+                    if (DOT && g == 0) far_dot[i] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) {
+                        O[i][w] = far[i][w] * by;
                         if constexpr (DOT) {
-                            const int t = t0 + 16 * i + l16, c = wcol + 4 * lg;
+                            const int t = t0 + 16 * i + l16, c = col0 + wcol + 16 * w + 4 * lg;
                             if (t < last && c < a.dv) {
-                                const T* zr = z + (long)t * a.zt + (long)(SUM ? h : many) * a.dv + c;
+                                typedef T V4 __attribute__((ext_vector_type(4)));
+                                const V4 zr = *reinterpret_cast<const V4*>(z + (long)t * a.zt + (long)(SUM ? h : many) * a.dv + c);
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) far_dot[i] += O[i][r] * (float)zr[r];
+                                for (int r = 0; r < 4; ++r) far_dot[i] += O[i][w][r] * (float)zr[r];
                             }
                         }
                     }
                 }
-                // the chunk's own
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const F vf = ld8(vT + (16 * wave + l16) * CP + 32 * s + 8 * lg);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) mma(O[i], vf, ld8(ps + (16 * i + l16) * CP + 32 * s + 8 * lg));
-                }
-                if (!SUM || g == a.G - 1) {
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const int t = t0 + 16 * i + l16, c = wcol + 4 * lg;
-                        if (t < last && c < a.dv) {
-                            struct __align__(4 * sizeof(T)) V4 { T e[4]; } o;
-                            // a non-finite value is zero in vT: its products with the weights of earlier
-                            // tokens, which are zero, would not be
-                            const bool lost = KIND == LIN_OUT && 16 * i + l16 >= *bad;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o.e[r] = (T)(lost ? __builtin_nanf("") : O[i][r]);
-                            const int heads = SUM ? a.Hk : a.Hk * a.G;
-                            *reinterpret_cast<V4*>(reinterpret_cast<T*>(a.out) +
-                                                   (((long)b * a.T + t) * heads + (SUM ? h : many)) * a.dv + c) = o;
-                        }
-                    }
-                }
-            }
-            // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
-            if (SUM || g == a.G - 1) {
-                if (!SUM || g == 0) {
-                    const float keep = __builtin_amdgcn_exp2f((float)gs[63]);
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) S[m] *= keep;
-                    kept += gs[63];
-                }
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const F vf = ld8(vT + (16 * wave + l16) * CP + 32 * s + 8 * lg);
-                    f32x8 x = to_f32v(vf);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= tail[32 * s + 8 * lg + e];
-                    Parts<T, VP> vp;
-                    vp.set(x);
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) {
-                        const F kf = ld8(kT + (16 * m + l16) * CP + 32 * s + 8 * lg);
-#pragma unroll
-                        for (int p = VP - 1; p >= 0; --p) mma(S[m], kf, vp.p[p]);
-                    }
-                }
-                if (KIND == LIN_OUT && *bad < C) {
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) S[m] += __builtin_nanf("");
-                }
-            }
-        }
-        if constexpr (DOT) {   // over the workgroup's columns
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                float d = far_dot[i];
-                d += __shfl_xor(d, 16, 64);
-                d += __shfl_xor(d, 32, 64);
-                if (lg == 0) dots[wave * 64 + 16 * i + l16] = d;
             }
             __syncthreads();
-            const int i = threadIdx.x;
-            if (i < rows)
-                a.dot[((long)slab * a.B * a.Hk + bh) * a.T + t0 + i] =
-                    (dots[i] + dots[64 + i]) + (dots[128 + i] + dots[192 + i]);
+            // the chunk's own
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                F vf[CW];
+#pragma unroll
+                for (int w = 0; w < CW; ++w) vf[w] = lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (REV ? s < i / 2 : s > i / 2) continue;
+                    const F pf = ld8(ps + (16 * i + l16) * PP + 32 * s + 8 * lg);
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) mma(O[i][w], vf[w], pf);
+                }
+            }
+            if (!SUM || g == a.G - 1) {
+                const int heads = SUM ? a.Hk : a.Hk * a.G, oh = SUM ? h : many;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int t = t0 + 16 * i + l16;
+                    // a non-finite value is zero in vs: its products with the weights of earlier tokens, which are
+                    // zero, would not be
+                    const bool lost = KIND == LIN_OUT && 16 * i + l16 >= *bad;
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) {
+                        const int c = col0 + wcol + 16 * w + 4 * lg;
+                        if (t < last && c < a.dv) {
+                            typedef T V4 __attribute__((ext_vector_type(4)));
+                            V4 o;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[r] = (T)(lost ? __builtin_nanf("") : O[i][w][r]);
+                            *reinterpret_cast<V4*>(reinterpret_cast<T*>(a.out) +
+                                                   (((long)b * a.T + t) * heads + oh) * a.dv + c) = o;
+                        }
+                    }
+                    if constexpr (DOT)
+                        if (g == a.G - 1) {
+                            float d = far_dot[i];
+                            d += __shfl_xor(d, 16, 64);
+                            d += __shfl_xor(d, 32, 64);
+                            if (lg == 0) dots[wave * 64 + 16 * i + l16] = d;
+                        }
+                }
+            }
         }
+        // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
+        if (SUM || g == a.G - 1) {
+            if (!SUM || g == 0) {
+                const double end = gs[gate0 + C - 1];
+                const float keep = __builtin_amdgcn_exp2f((float)end);
+                kept += end;
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) S[m][w] *= keep;
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Parts<T, VP3> vp[CW];
+                const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
+#pragma unroll
+                for (int w = 0; w < CW; ++w)
+                    vp[w].set(to_f32v(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    if (16 * m >= a.dk) continue;
+                    const F kf = lin_column8(ks + 32 * s * KP, KP, 16 * m);
+#pragma unroll
+                    for (int w = 0; w < CW; ++w)
+#pragma unroll
+                        for (int p = VP3 - 1; p >= 0; --p) mma(S[m][w], kf, vp[w].p[p]);
+                }
+            }
+            if (KIND == LIN_OUT && *bad < C) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) S[m][w] += __builtin_nanf("");
+            }
+        }
+        g = next_g;
+        ci = next_ci;
     }
+    if constexpr (DOT)
+        if (chunks) {
+            __syncthreads();
+            put_dots(start(chunks - 1));
+        }
     if (a.s_out) {
         float* s = a.s_out + bh * a.s_out_bh + seg * a.s_out_seg;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * m + 4 * lg + r, c = wcol + l16;
-                if (i < a.dk && c < a.dv) s[i * a.sa + c * a.sc] = S[m][r];
-            }
+            for (int w = 0; w < CW; ++w)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * m + 4 * lg + r, c = col0 + wcol + 16 * w + l16;
+                    if (i < a.dk && c < a.dv) s[i * a.sa + c * a.sc] = S[m][w][r];
+                }
     }
     if (STATE && a.gsum && slab == 0 && threadIdx.x == 0) a.gsum[(long)bh * a.nseg + seg] = kept;
+}
+
+template <class T, int DK, int CW, int KIND> __global__ __launch_bounds__(256, 2) void lin_kernel(LinArgs a) {
+    lin_body<T, DK, CW, KIND>(a, blockIdx.x);
 }
 
 // Single tokens and short drafts, token by token: 32 columns of a head's
@@ -497,6 +591,15 @@ __global__ __launch_bounds__(256) void lin_flow_kernel(const float* S, const flo
     if (threadIdx.x == 0) flow[bh * nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// Rows t0 .. t0 + C - 1 (zeros from n on) of a token array into LDS, 16 bytes
+// at a time, with zeros behind its columns.
+template <class T, int D, int C, int RP>
+__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int n, int cols, T* rows) {
+    LinTile<T, D, C> t;
+    t.load(x, step, t0, n, 0, cols);
+    t.template store<false>(rows, RP, t0, n, 0, cols, nullptr);
+}
+
 // dg of a chunk's tokens but for what passes the chunk, and the sums of fq
 // and fk that this follows from.
 struct LinPairs {
@@ -541,8 +644,8 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
     const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * a.dk;
     const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * a.dv;
     const T* y = reinterpret_cast<const T*>(a.dy) + b * a.gb;
-    lin_stage<T, D, C, RP, C, true, false, false>(k, a.kt, t0, n, 0, a.dk, ks, nullptr, nullptr);
-    lin_stage<T, D, C, RP, C, true, false, false>(v, a.vt, t0, n, 0, a.dv, vs, nullptr, nullptr);
+    lin_stage<T, D, C, RP>(k, a.kt, t0, n, a.dk, ks);
+    lin_stage<T, D, C, RP>(v, a.vt, t0, n, a.dv, vs);
     float x[NT][4];
 #pragma unroll
     for (int kt = 0; kt < NT; ++kt)
@@ -551,8 +654,8 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
     const int i = 16 * wave + l16;
     for (int g = 0; g < a.G; ++g) {
         if (g > 0) __syncthreads();
-        lin_stage<T, D, C, RP, C, true, false, false>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, n, 0, a.dk, qs, nullptr, nullptr);
-        lin_stage<T, D, C, RP, C, true, false, false>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, n, 0, a.dv, ys, nullptr, nullptr);
+        lin_stage<T, D, C, RP>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, n, a.dk, qs);
+        lin_stage<T, D, C, RP>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, n, a.dv, ys);
         __syncthreads();
         if (wave < NT) {
             const double gi = gs[i];
@@ -689,38 +792,32 @@ __global__ void lin_zero_kernel(float* p, int n) {
 
 static int lin_width(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <class T, int DK, int C, int KIND>
+template <class T, int DK, int CW, int KIND>
 static hipError_t lin_run(LinArgs a, hipStream_t st) {
-    a.slabs = (a.dv + 63) / 64;
+    a.slabs = (a.dv + 64 * CW - 1) / (64 * CW);
     const long blocks = (long)a.B * a.Hk * a.nseg * a.slabs;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
-    constexpr size_t bytes = LinLds<T, DK, C>::bytes;
+    constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
     static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
     if (bytes > 64 * 1024) {   // above the default dynamic LDS limit
-        const hipError_t e = hipFuncSetAttribute((const void*)lin_kernel<T, DK, C, KIND>,
+        const hipError_t e = hipFuncSetAttribute((const void*)lin_kernel<T, DK, CW, KIND>,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != hipSuccess) return e;
     }
     return timed_layer(st, [&] {
-        launch_k((lin_kernel<T, DK, C, KIND>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
+        launch_k((lin_kernel<T, DK, CW, KIND>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
         return hipGetLastError();
     });
 }
-// Tokens of a chunk: 64, or 32 where 64 rows of 256 fp32 values would not fit
-// the LDS.  All runs of a call have the same.
-static int lin_chunk(int dk, int dv, size_t es) { return es == 4 && (dk > 128 || dv > 128) ? 32 : 64; }
-
-// wide: the other width of the call's heads, which decides the chunk with it
-template <class T, int KIND> static hipError_t lin_launch(const LinArgs& a, int wide, hipStream_t st) {
+// 128 columns a workgroup where its registers hold them (the queries' and
+// keys' rows are then read once), 64 for narrow values or wide keys.
+static int lin_columns(int dk, int dv) { return dv > 64 && dk <= 128 ? 128 : 64; }
+template <class T, int KIND> static hipError_t lin_launch(const LinArgs& a, hipStream_t st) {
     const int w = lin_width(a.dk);
-    if constexpr (sizeof(T) == 4) {
-        if (w == 256) return lin_run<T, 256, 32, KIND>(a, st);
-        if (lin_width(wide) == 256)
-            return w == 128 ? lin_run<T, 128, 32, KIND>(a, st) : lin_run<T, 64, 32, KIND>(a, st);
-    } else {
-        if (w == 256) return lin_run<T, 256, 64, KIND>(a, st);
-    }
-    return w == 128 ? lin_run<T, 128, 64, KIND>(a, st) : lin_run<T, 64, 64, KIND>(a, st);
+    if (w == 256) return lin_run<T, 256, 1, KIND>(a, st);
+    if (lin_columns(a.dk, a.dv) == 128)
+        return w == 128 ? lin_run<T, 128, 2, KIND>(a, st) : lin_run<T, 64, 2, KIND>(a, st);
+    return w == 128 ? lin_run<T, 128, 1, KIND>(a, st) : lin_run<T, 64, 1, KIND>(a, st);
 }
 
 template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hipStream_t st) {
@@ -741,12 +838,8 @@ template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hip
 }
 template <class T> static hipError_t lin_pairs(const LinPairs& a, hipStream_t st) {
     const int w = lin_width(a.dk > a.dv ? a.dk : a.dv);
-    if constexpr (sizeof(T) == 4) {
-        if (w == 256) return lin_pairs_run<T, 256, 32>(a, st);
-    } else {
-        if (w == 256) return lin_pairs_run<T, 256, 64>(a, st);
-    }
-    return w == 128 ? lin_pairs_run<T, 128, 64>(a, st) : lin_pairs_run<T, 64, 64>(a, st);
+    constexpr int C = lin_chunk<T>();
+    return w == 256 ? lin_pairs_run<T, 256, C>(a, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, st) : lin_pairs_run<T, 64, C>(a, st);
 }
 
 template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
@@ -794,8 +887,8 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         p.part = take(bh * p.nseg * 8);
     } else if (T > 0 && B > 0) {
         // the sequence is divided where its heads alone do not fill the chip
-        const long wgs = (long)bh * ((dv + 63) / 64);
-        long seg = wgs >= 256 || T <= 256 ? 1 : (1024 + wgs - 1) / wgs;
+        const long cols = lin_columns(dk, dv), wgs = (long)bh * ((dv + cols - 1) / cols);
+        long seg = wgs >= 256 || T <= 256 ? 1 : (512 + wgs - 1) / wgs;
         seg = seg < (T + 255) / 256 ? seg : (T + 255) / 256;
         p.L = (int)(((T + seg - 1) / seg + 63) / 64 * 64);
         p.nseg = (T + p.L - 1) / p.L;
@@ -839,7 +932,7 @@ template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, ch
     a.L = p.L;
     if (p.nseg == 1) {
         a.s_out = state_out;
-        return lin_launch<T, LIN_OUT>(a, a.dk, st);
+        return lin_launch<T, LIN_OUT>(a, st);
     }
     float* parts = reinterpret_cast<float*>(ws + p.states);
     double* gsum = reinterpret_cast<double*>(ws + p.gsum);
@@ -849,12 +942,12 @@ template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, ch
     b.s_out_bh = p.nseg * cells;
     b.s_out_seg = cells;
     b.gsum = gsum;
-    LIN_TRY((lin_launch<T, LIN_STATE>(b, a.dk, st)));
+    LIN_TRY((lin_launch<T, LIN_STATE>(b, st)));
     LIN_TRY(lin_scan(LinScan{parts, a.s_in, state_out, gsum, p.nseg, p.nseg, (int)cells, 0}, (long)a.B * a.Hk, st));
     a.s_in = parts;
     a.s_in_bh = p.nseg * cells;
     a.s_in_seg = cells;
-    return lin_launch<T, LIN_OUT>(a, a.dk, st);
+    return lin_launch<T, LIN_OUT>(a, st);
 }
 
 struct LinBack {
@@ -869,7 +962,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     const int dk = a.dk, dv = a.dv;
     const long cells = (long)dk * dv, bh = (long)a.B * a.Hk;
     const LinPlan p = lin_plan(a.B, a.T, a.Hk, dk, dv, true);
-    const int slots = p.nseg + 1, wide = dk > dv ? dk : dv;
+    const int slots = p.nseg + 1;
     a.nseg = p.nseg;
     a.L = p.L;
     float* S = reinterpret_cast<float*>(ws + p.states);
@@ -888,7 +981,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     s.sa = dv;
     s.sc = 1;
     s.gsum = gsum;
-    LIN_TRY((lin_launch<T, LIN_STATE>(s, wide, st)));
+    LIN_TRY((lin_launch<T, LIN_STATE>(s, st)));
     LinArgs r = s;
     r.G = a.G;
     r.k = a.q; r.kb = a.qb; r.kt = a.qt;
@@ -896,7 +989,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     r.s_out = R;
     r.state_scale = scale;
     r.gsum = nullptr;
-    LIN_TRY((lin_launch<T, LIN_STATE_BACK>(r, wide, st)));
+    LIN_TRY((lin_launch<T, LIN_STATE_BACK>(r, st)));
     LIN_TRY(lin_scan(LinScan{S, a.s_in, nullptr, gsum, p.nseg, slots, (int)cells, 0}, bh, st));
     LIN_TRY(lin_scan(LinScan{R, g.dstate_out, g.dstate_in, gsum, p.nseg, slots, (int)cells, 1}, bh, st));
     // the three gradients of token arrays
@@ -909,18 +1002,18 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     y.q = g.dy; y.qb = g.gb; y.qt = g.gt; y.k = a.v; y.kb = a.vb; y.kt = a.vt; y.v = a.k; y.vb = a.kb; y.vt = a.kt;
     y.z = a.q; y.zb = a.qb; y.zt = a.qt;
     y.dk = dv; y.dv = dk; y.s_in = S; y.sa = 1; y.sc = dv; y.out = g.dq; y.dot = dotq;
-    LIN_TRY((lin_launch<T, LIN_DQ>(y, wide, st)));
+    LIN_TRY((lin_launch<T, LIN_DQ>(y, st)));
     y = x;
     y.q = a.v; y.qb = a.vb; y.qt = a.vt; y.k = g.dy; y.kb = g.gb; y.kt = g.gt; y.v = a.q; y.vb = a.qb; y.vt = a.qt;
     y.z = a.k; y.zb = a.kb; y.zt = a.kt;
     y.dk = dv; y.dv = dk; y.s_in = R; y.sa = 1; y.sc = dv; y.out = g.dk; y.dot = dotk;
     y.far_scale = 1.f; y.state_scale = scale;
-    LIN_TRY((lin_launch<T, LIN_DK>(y, wide, st)));
+    LIN_TRY((lin_launch<T, LIN_DK>(y, st)));
     y = x;
     y.q = a.k; y.qb = a.kb; y.qt = a.kt; y.k = a.q; y.kb = a.qb; y.kt = a.qt; y.v = g.dy; y.vb = g.gb; y.vt = g.gt;
     y.s_in = R; y.sa = dv; y.sc = 1; y.out = g.dv;
     y.far_scale = 1.f; y.state_scale = scale;
-    LIN_TRY((lin_launch<T, LIN_DV>(y, wide, st)));
+    LIN_TRY((lin_launch<T, LIN_DV>(y, st)));
     if (!g.dld) return hipSuccess;
     // the decays
     LIN_TRY(timed_layer(st, [&] {
@@ -931,11 +1024,11 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     double* part = reinterpret_cast<double*>(ws + p.part);
     float* sums = reinterpret_cast<float*>(ws + p.sums);
     LinPairs w{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
-               scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + 63) / 64};
+               scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_columns(dv, dk) - 1) / lin_columns(dv, dk)};
     LIN_TRY(lin_pairs<T>(w, st));
     LIN_TRY(timed_layer(st, [&] {
         launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.counts, g.dld,
-                 part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk(dk, dv, sizeof(T)));
+                 part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk<T>());
         return hipGetLastError();
     }));
     if (a.per_token) return hipSuccess;
