@@ -337,9 +337,17 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                     for (int i = 0; i < NT; ++i) {
                         const F qf = lin_split8(qs + (16 * i + l16) * QP + 32 * s, lg);
 #pragma unroll
-                        for (int w = 0; w < CW; ++w)
+                        for (int p = SP - 1; p >= 0; --p)
 #pragma unroll
-                            for (int p = SP - 1; p >= 0; --p) mma(far[i][w], sp[w].p[p], qf);
+                            for (int w = 0; w < CW; ++w) {
+                                if constexpr (sizeof(T) == 4) {   // sums of 32, then of those
+                                    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+                                    mma(sum, sp[w].p[p], qf);
+                                    far[i][w] += sum;
+                                } else {
+                                    mma(far[i][w], sp[w].p[p], qf);
+                                }
+                            }
                     }
                 }
 #pragma unroll
@@ -408,31 +416,39 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
         }
         // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
         if (SUM || g == a.G - 1) {
+            // a chunk's sum is formed by itself: the state takes one rounding a chunk, not one a product
+            float keep = 1.f;
             if (!SUM || g == 0) {
                 const double end = gs[gate0 + C - 1];
-                const float keep = __builtin_amdgcn_exp2f((float)end);
+                keep = __builtin_amdgcn_exp2f((float)end);
                 kept += end;
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int w = 0; w < CW; ++w) S[m][w] *= keep;
             }
+            Parts<T, VP3> vp[KS][CW];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                Parts<T, VP3> vp[CW];
                 const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
 #pragma unroll
                 for (int w = 0; w < CW; ++w)
-                    vp[w].set(to_f32v(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
+                    vp[s][w].set(to_f32v(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
+            }
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    if (16 * m >= a.dk) continue;
+            for (int m = 0; m < NM; ++m) {
+                if (16 * m >= a.dk) continue;
+                f32x4 sum[CW];
+#pragma unroll
+                for (int w = 0; w < CW; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
                     const F kf = lin_column8(ks + 32 * s * KP, KP, 16 * m);
 #pragma unroll
-                    for (int w = 0; w < CW; ++w)
+                    for (int p = VP3 - 1; p >= 0; --p)
 #pragma unroll
-                        for (int p = VP3 - 1; p >= 0; --p) mma(S[m][w], kf, vp[w].p[p]);
+                        for (int w = 0; w < CW; ++w) mma(sum[w], kf, vp[s][w].p[p]);
                 }
+#pragma unroll
+                for (int w = 0; w < CW; ++w)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[m][w][r] = fmaf(keep, S[m][w][r], sum[w][r]);
             }
             if (KIND == LIN_OUT && *bad < C) {
 #pragma unroll
@@ -466,6 +482,23 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
 
 template <class T, int DK, int CW, int KIND> __global__ __launch_bounds__(256, 2) void lin_kernel(LinArgs a) {
     lin_body<T, DK, CW, KIND>(a, blockIdx.x);
+}
+// The backward's runs that do not need each other, in one launch each: what
+// the segments add to the state and to its gradient, then the three gradients.
+struct LinMany {
+    LinArgs a[3];
+    int blocks[3];
+};
+template <class T, int DK, int CW> __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinMany m) {
+    const int i = blockIdx.x;
+    if (i < m.blocks[0]) lin_body<T, DK, CW, LIN_STATE_BACK>(m.a[0], i);
+    else lin_body<T, DK, CW, LIN_STATE>(m.a[1], i - m.blocks[0]);
+}
+template <class T, int DK, int CW> __global__ __launch_bounds__(256, 2) void lin_gradients_kernel(LinMany m) {
+    const int i = blockIdx.x;
+    if (i < m.blocks[0]) lin_body<T, DK, CW, LIN_DK>(m.a[0], i);
+    else if (i < m.blocks[0] + m.blocks[1]) lin_body<T, DK, CW, LIN_DQ>(m.a[1], i - m.blocks[0]);
+    else lin_body<T, DK, CW, LIN_DV>(m.a[2], i - m.blocks[0] - m.blocks[1]);
 }
 
 // Single tokens and short drafts, token by token: 32 columns of a head's
@@ -550,24 +583,41 @@ struct LinScan {
     const float* begin;  // [batch * key heads][cells]; null: zeros
     float* end;
     const double* gsum;
-    int nseg, slots, cells, back;
+    int nseg, slots, cells;
 };
-__global__ __launch_bounds__(256) void lin_scan_kernel(LinScan s) {
+template <bool BACK> __device__ __forceinline__ void lin_scan(const LinScan& s) {
+    constexpr int AHEAD = 8;   // segments read at a time
     const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (i >= s.cells) return;
     const long bh = blockIdx.x;
     f32x4 run = f32x4{0.f, 0.f, 0.f, 0.f};
     if (s.begin) run = *reinterpret_cast<const f32x4*>(s.begin + bh * s.cells + i);
-    for (int n = 0; n < s.nseg; ++n) {
-        const int seg = s.back ? s.nseg - 1 - n : n;
-        float* p = s.part + (bh * s.slots + seg) * s.cells + i;
-        const f32x4 own = *reinterpret_cast<const f32x4*>(p);
-        *reinterpret_cast<f32x4*>(p) = run;
-        const float keep = __builtin_amdgcn_exp2f((float)s.gsum[bh * s.nseg + seg]);
-        run = keep * run + own;
+    for (int n0 = 0; n0 < s.nseg; n0 += AHEAD) {
+        f32x4 own[AHEAD];
+        float keep[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const int n = min(n0 + e, s.nseg - 1), seg = BACK ? s.nseg - 1 - n : n;
+            own[e] = *reinterpret_cast<const f32x4*>(s.part + (bh * s.slots + seg) * s.cells + i);
+            keep[e] = __builtin_amdgcn_exp2f((float)s.gsum[bh * s.nseg + seg]);
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const int n = n0 + e, seg = BACK ? s.nseg - 1 - n : n;
+            if (n < s.nseg) {
+                *reinterpret_cast<f32x4*>(s.part + (bh * s.slots + seg) * s.cells + i) = run;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) run[c] = fmaf(keep[e], run[c], own[e][c]);
+            }
+        }
     }
     if (s.slots > s.nseg) *reinterpret_cast<f32x4*>(s.part + (bh * s.slots + s.nseg) * s.cells + i) = run;
     if (s.end) *reinterpret_cast<f32x4*>(s.end + bh * s.cells + i) = run;
+}
+// forward: the states (blockIdx.z 0), and their gradients (1)
+__global__ __launch_bounds__(256) void lin_scan_kernel(LinScan states, LinScan grads) {
+    if (blockIdx.z == 0) lin_scan<false>(states);
+    else lin_scan<true>(grads);
 }
 
 // <R, S> at the end of every segment.
@@ -820,6 +870,37 @@ template <class T, int KIND> static hipError_t lin_launch(const LinArgs& a, hipS
     return w == 128 ? lin_run<T, 128, 1, KIND>(a, st) : lin_run<T, 64, 1, KIND>(a, st);
 }
 
+// a launch of several runs: the wider of keys and values decides for all
+template <class T, int DK, int CW, bool STATES> static hipError_t lin_many_run(LinMany m, hipStream_t st) {
+    long blocks = 0;
+    for (int i = 0; i < (STATES ? 2 : 3); ++i) {
+        m.a[i].slabs = (m.a[i].dv + 64 * CW - 1) / (64 * CW);
+        m.blocks[i] = m.a[i].B * m.a[i].Hk * m.a[i].nseg * m.a[i].slabs;
+        blocks += (long)m.a[i].B * m.a[i].Hk * m.a[i].nseg * m.a[i].slabs;
+    }
+    if (blocks >= 1L << 24) return hipErrorInvalidValue;
+    constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
+    auto go = [&](auto kernel) {
+        if (bytes > 64 * 1024) {
+            const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            if (e != hipSuccess) return e;
+        }
+        return timed_layer(st, [&] {
+            launch_k(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, m);
+            return hipGetLastError();
+        });
+    };
+    if constexpr (STATES) return go(lin_states_kernel<T, DK, CW>);
+    else return go(lin_gradients_kernel<T, DK, CW>);
+}
+template <class T, bool STATES> static hipError_t lin_many(const LinMany& m, int wide, hipStream_t st) {
+    const int w = lin_width(wide);
+    return w == 256   ? lin_many_run<T, 256, 1, STATES>(m, st)
+           : w == 128 ? lin_many_run<T, 128, 2, STATES>(m, st)
+                      : lin_many_run<T, 64, 1, STATES>(m, st);
+}
+static int lin_many_columns(int wide) { return lin_width(wide) == 128 ? 128 : 64; }
+
 template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hipStream_t st) {
     a.chunks = (a.T + C - 1) / C;
     const long blocks = (long)a.B * a.Hk * a.chunks;
@@ -874,7 +955,9 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         return o;
     };
     if (back) {
+        // shorter segments where they would not fill the chip
         p.L = LIN_BACK_SEG;
+        while (p.L > 64 && (long)bh * ((T + p.L - 1) / p.L) < 256) p.L /= 2;
         p.nseg = (T + p.L - 1) / p.L;
         p.states = take(bh * (p.nseg + 1) * cells * 4);
         p.grads = take(bh * (p.nseg + 1) * cells * 4);
@@ -901,9 +984,10 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
     return p;
 }
 
-static hipError_t lin_scan(const LinScan& s, long bh, hipStream_t st) {
+static hipError_t lin_scan_run(const LinScan& s, const LinScan* grads, long bh, hipStream_t st) {
     return timed_layer(st, [&] {
-        launch_k(lin_scan_kernel, dim3((unsigned)bh, (s.cells + 1023) / 1024), dim3(256), 0, st, s);
+        launch_k(lin_scan_kernel, dim3((unsigned)bh, (s.cells + 1023) / 1024, grads ? 2 : 1), dim3(256), 0, st, s,
+                 grads ? *grads : LinScan{});
         return hipGetLastError();
     });
 }
@@ -943,7 +1027,7 @@ template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, ch
     b.s_out_seg = cells;
     b.gsum = gsum;
     LIN_TRY((lin_launch<T, LIN_STATE>(b, st)));
-    LIN_TRY(lin_scan(LinScan{parts, a.s_in, state_out, gsum, p.nseg, p.nseg, (int)cells, 0}, (long)a.B * a.Hk, st));
+    LIN_TRY(lin_scan_run(LinScan{parts, a.s_in, state_out, gsum, p.nseg, p.nseg, (int)cells}, nullptr, (long)a.B * a.Hk, st));
     a.s_in = parts;
     a.s_in_bh = p.nseg * cells;
     a.s_in_seg = cells;
@@ -962,7 +1046,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     const int dk = a.dk, dv = a.dv;
     const long cells = (long)dk * dv, bh = (long)a.B * a.Hk;
     const LinPlan p = lin_plan(a.B, a.T, a.Hk, dk, dv, true);
-    const int slots = p.nseg + 1;
+    const int slots = p.nseg + 1, wide = dk > dv ? dk : dv;
     a.nseg = p.nseg;
     a.L = p.L;
     float* S = reinterpret_cast<float*>(ws + p.states);
@@ -981,7 +1065,6 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     s.sa = dv;
     s.sc = 1;
     s.gsum = gsum;
-    LIN_TRY((lin_launch<T, LIN_STATE>(s, st)));
     LinArgs r = s;
     r.G = a.G;
     r.k = a.q; r.kb = a.qb; r.kt = a.qt;
@@ -989,9 +1072,9 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     r.s_out = R;
     r.state_scale = scale;
     r.gsum = nullptr;
-    LIN_TRY((lin_launch<T, LIN_STATE_BACK>(r, st)));
-    LIN_TRY(lin_scan(LinScan{S, a.s_in, nullptr, gsum, p.nseg, slots, (int)cells, 0}, bh, st));
-    LIN_TRY(lin_scan(LinScan{R, g.dstate_out, g.dstate_in, gsum, p.nseg, slots, (int)cells, 1}, bh, st));
+    LIN_TRY((lin_many<T, true>(LinMany{{r, s}, {}}, wide, st)));
+    const LinScan back{R, g.dstate_out, g.dstate_in, gsum, p.nseg, slots, (int)cells};
+    LIN_TRY(lin_scan_run(LinScan{S, a.s_in, nullptr, gsum, p.nseg, slots, (int)cells}, &back, bh, st));
     // the three gradients of token arrays
     LinArgs x = a;
     x.s_in_bh = slots * cells;
@@ -1002,18 +1085,15 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     y.q = g.dy; y.qb = g.gb; y.qt = g.gt; y.k = a.v; y.kb = a.vb; y.kt = a.vt; y.v = a.k; y.vb = a.kb; y.vt = a.kt;
     y.z = a.q; y.zb = a.qb; y.zt = a.qt;
     y.dk = dv; y.dv = dk; y.s_in = S; y.sa = 1; y.sc = dv; y.out = g.dq; y.dot = dotq;
-    LIN_TRY((lin_launch<T, LIN_DQ>(y, st)));
-    y = x;
-    y.q = a.v; y.qb = a.vb; y.qt = a.vt; y.k = g.dy; y.kb = g.gb; y.kt = g.gt; y.v = a.q; y.vb = a.qb; y.vt = a.qt;
-    y.z = a.k; y.zb = a.kb; y.zt = a.kt;
-    y.dk = dv; y.dv = dk; y.s_in = R; y.sa = 1; y.sc = dv; y.out = g.dk; y.dot = dotk;
-    y.far_scale = 1.f; y.state_scale = scale;
-    LIN_TRY((lin_launch<T, LIN_DK>(y, st)));
-    y = x;
-    y.q = a.k; y.qb = a.kb; y.qt = a.kt; y.k = a.q; y.kb = a.qb; y.kt = a.qt; y.v = g.dy; y.vb = g.gb; y.vt = g.gt;
-    y.s_in = R; y.sa = dv; y.sc = 1; y.out = g.dv;
-    y.far_scale = 1.f; y.state_scale = scale;
-    LIN_TRY((lin_launch<T, LIN_DV>(y, st)));
+    LinArgs w = x;
+    w.q = a.v; w.qb = a.vb; w.qt = a.vt; w.k = g.dy; w.kb = g.gb; w.kt = g.gt; w.v = a.q; w.vb = a.qb; w.vt = a.qt;
+    w.z = a.k; w.zb = a.kb; w.zt = a.kt;
+    w.dk = dv; w.dv = dk; w.s_in = R; w.sa = 1; w.sc = dv; w.out = g.dk; w.dot = dotk;
+    w.far_scale = 1.f; w.state_scale = scale;
+    x.q = a.k; x.qb = a.kb; x.qt = a.kt; x.k = a.q; x.kb = a.qb; x.kt = a.qt; x.v = g.dy; x.vb = g.gb; x.vt = g.gt;
+    x.s_in = R; x.sa = dv; x.sc = 1; x.out = g.dv;
+    x.far_scale = 1.f; x.state_scale = scale;
+    LIN_TRY((lin_many<T, false>(LinMany{{w, y, x}, {}}, wide, st)));
     if (!g.dld) return hipSuccess;
     // the decays
     LIN_TRY(timed_layer(st, [&] {
@@ -1023,9 +1103,9 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     float* h = reinterpret_cast<float*>(ws + p.h);
     double* part = reinterpret_cast<double*>(ws + p.part);
     float* sums = reinterpret_cast<float*>(ws + p.sums);
-    LinPairs w{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
-               scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_columns(dv, dk) - 1) / lin_columns(dv, dk)};
-    LIN_TRY(lin_pairs<T>(w, st));
+    LinPairs pairs{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
+               scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_many_columns(wide) - 1) / lin_many_columns(wide)};
+    LIN_TRY(lin_pairs<T>(pairs, st));
     LIN_TRY(timed_layer(st, [&] {
         launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.counts, g.dld,
                  part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk<T>());
