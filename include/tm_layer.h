@@ -80,7 +80,8 @@ tm_status tm_head_norm_backward(const void* x, long x_batch, long x_token, const
  * aligned; state_in null: zeros; state_out null: not wanted; state_out may be
  * state_in.  An entry without tokens keeps its state.
  * key_dim, value_dim: multiples of 8, 8 .. 256; heads a multiple of kv_heads;
- * token arrays 16-byte aligned, distances multiples of 8 elements.
+ * token arrays 16-byte aligned, distances multiples of 8 elements, those of
+ * tokens below 2^23.
  * Products of bf16 calls are of bf16 operands with fp32 accumulation (the
  * pairs' weights within a chunk of tokens are rounded to bf16, the state is
  * read with 16 bits; what is added to it keeps 24), those of fp32 calls are

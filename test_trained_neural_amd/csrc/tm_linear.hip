@@ -66,8 +66,6 @@ __device__ __forceinline__ double lin_gate(float g) {
     return (double)(g < -1000.f ? -1000.f : g) * LOG2E;
 }
 
-template <class T> __device__ __forceinline__ bool lin_finite(T x) { return __builtin_isfinite((float)x); }
-
 // 8 values in the order in which two stacked accumulator tiles hold 32 rows:
 // lane group g has 4 g .. and 16 + 4 g ..
 __device__ __forceinline__ bf16x8 lin_split8(const bf16* p, int g) {
@@ -80,6 +78,19 @@ __device__ __forceinline__ f32x8 lin_split8(const float* p, int g) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+__device__ __forceinline__ f32x8 lin_f32(f32x8 x) { return x; }
+__device__ __forceinline__ f32x8 lin_f32(bf16x8 x) {   // a bf16's bits are an fp32's upper ones
+    typedef unsigned U4 __attribute__((ext_vector_type(4)));
+    const U4 u = __builtin_bit_cast(U4, x);
+    f32x8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = __builtin_bit_cast(float, u[i] << 16);
+        r[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xffff0000u);
+    }
+    return r;
+}
+
 // fp32 values as operands: one for fp32, N of 8 bits each for bf16.
 template <class T, int N> struct Parts {
     typename Frag<T>::T p[N];
@@ -89,8 +100,8 @@ template <class T, int N> struct Parts {
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                p[i] = to_bf16(x);
-                x -= to_f32(p[i]);
+                p[i] = __builtin_convertvector(x, bf16x8);
+                if (i + 1 < N) x -= lin_f32(p[i]);
             }
         }
     }
@@ -113,41 +124,67 @@ template <class T, int DK, int CW> struct LinLds {
                             dot = tail + 4 * GATES, bad = dot + 4 * 4 * 64, bytes = bad + 16;
 };
 
+// Whether 16 bytes hold a non-finite value: an exponent of ones.
+__device__ __forceinline__ bool lin_lost(f32x4 x) {
+    const f32x4 zero = x * 0.f;   // NaN where x is not finite
+    return !((zero[0] + zero[1]) + (zero[2] + zero[3]) == 0.f);
+}
+__device__ __forceinline__ bool lin_lost(bf16x8 x) {
+    typedef unsigned short H8 __attribute__((ext_vector_type(8)));
+    const H8 h = __builtin_bit_cast(H8, x) & (unsigned short)0x7fff;
+    typedef unsigned short H4 __attribute__((ext_vector_type(4)));
+    typedef unsigned short H2 __attribute__((ext_vector_type(2)));
+    const H4 a = __builtin_elementwise_max(__builtin_shufflevector(h, h, 0, 1, 2, 3), __builtin_shufflevector(h, h, 4, 5, 6, 7));
+    const H2 b = __builtin_elementwise_max(__builtin_shufflevector(a, a, 0, 1), __builtin_shufflevector(a, a, 2, 3));
+    return b[0] >= 0x7f80 || b[1] >= 0x7f80;
+}
+
 // A tile [C][D] of a token array on its way from memory to LDS, 16 bytes at a
 // time.  Rows behind the last and columns behind the array's are read as ones
-// that are there and taken as zeros when they are put down.
+// that are there and taken as zeros when they are put down.  x: the tile's
+// first row; step: elements between rows (64 rows are less than 2^31 bytes
+// apart: an offset is 32 bits beside an address of the whole workgroup).
 template <class T, int D, int C> struct LinTile {
-    static constexpr int VE = 16 / sizeof(T), UNITS = D / VE, N = (C * UNITS + 255) / 256;
+    static constexpr int VE = 16 / sizeof(T), UNITS = D / VE, PER = 256 / UNITS, N = (C * UNITS + 255) / 256;
     typedef T Vec __attribute__((ext_vector_type(VE)));
     Vec v[N];
-    __device__ __forceinline__ void load(const T* x, long step, int t0, int last, int c0, int cols) {
-        const int u = threadIdx.x % UNITS, c = c0 + u * VE < cols ? c0 + u * VE : 0;
+    __device__ __forceinline__ void load(const T* x, unsigned step, int rows, int c0, int cols) {
+        const unsigned u = threadIdx.x % UNITS, c = c0 + u * VE < (unsigned)cols ? c0 + u * VE : 0u, r0 = threadIdx.x / UNITS;
+        const char* at = reinterpret_cast<const char*>(x);
+        if (rows == C) {
+            const unsigned off = (r0 * step + c) * (unsigned)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = threadIdx.x / UNITS + i * (256 / UNITS);
-            v[i] = *reinterpret_cast<const Vec*>(x + (long)min(t0 + r, last - 1) * step + c);
+            for (int i = 0; i < N; ++i) {
+                // a tile of fewer rows than threads: the last are read again
+                const unsigned o = C * UNITS % 256 == 0 || r0 < (unsigned)C ? off : c * (unsigned)sizeof(T);
+                v[i] = *reinterpret_cast<const Vec*>(at + (unsigned long)(i * PER) * step * sizeof(T) + o);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = *reinterpret_cast<const Vec*>(at + (min(r0 + i * PER, rows - 1u) * step + c) * (unsigned)sizeof(T));
         }
     }
     // bad: the first row with a non-finite element, which is taken as zero
     template <bool CHECK>
-    __device__ __forceinline__ void store(T* to, int row, int t0, int last, int c0, int cols, int* bad) {
-        const int u = threadIdx.x % UNITS;
-        const bool there = c0 + u * VE < cols;
+    __device__ __forceinline__ void store(T* to, int row, int rows, int c0, int cols, int* bad) {
+        const int u = threadIdx.x % UNITS, r0 = threadIdx.x / UNITS;
+        if (rows < C || c0 + D > cols) {
+            const bool there = c0 + u * VE < cols;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = keep_if(v[i], there && r0 + i * PER < rows);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = threadIdx.x / UNITS + i * (256 / UNITS);
-            Vec x = keep_if(v[i], there && t0 + r < last);
-            if constexpr (CHECK) {
-                bool fine = true;
+            const int r = r0 + i * PER;
+            if constexpr (CHECK)
+                if (lin_lost(v[i])) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (!lin_finite((T)x[e])) {
-                        fine = false;
-                        x[e] = (T)0.f;
-                    }
-                if (!fine) atomicMin(bad, r);
-            }
-            if (C * UNITS % 256 == 0 || r < C) *reinterpret_cast<Vec*>(to + r * row + u * VE) = x;
+                    for (int e = 0; e < VE; ++e)
+                        if (!__builtin_isfinite((float)v[i][e])) v[i][e] = (T)0.f;
+                    atomicMin(bad, r);
+                }
+            if (C * UNITS % 256 == 0 || r < C) *reinterpret_cast<Vec*>(to + r * row + u * VE) = v[i];
         }
     }
 };
@@ -233,13 +270,13 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     LinTile<T, 64 * CW, C> vv;
     auto start = [&](int ci) { return first + (REV ? chunks - 1 - ci : ci) * C; };
     auto fetch = [&](int ci, int g) {
-        const int t0 = start(ci), many = h * a.G + g;
+        const int t0 = start(ci), many = h * a.G + g, rows = min(C, last - t0);
         if constexpr (!STATE)
-            if (!SUM || g == 0) qv.load(q + (long)(SUM ? h : many) * a.dk, a.qt, t0, last, 0, a.dk);
+            if (!SUM || g == 0) qv.load(q + t0 * a.qt + (long)(SUM ? h : many) * a.dk, (unsigned)a.qt, rows, 0, a.dk);
         if (SUM || g == 0) {
             const int kh = SUM ? many : h;
-            kv.load(k + (long)kh * a.dk, a.kt, t0, last, 0, a.dk);
-            vv.load(v + (long)kh * a.dv, a.vt, t0, last, col0, a.dv);
+            kv.load(k + t0 * a.kt + (long)kh * a.dk, (unsigned)a.kt, rows, 0, a.dk);
+            vv.load(v + t0 * a.vt + (long)kh * a.dv, (unsigned)a.vt, rows, col0, a.dv);
         }
     };
     f32x4 O[NT][CW];
@@ -254,14 +291,14 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     int ci = 0, g = 0;
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
-        const int t0 = start(ci), many = h * a.G + g, gate0 = ci % BATCH * C;
+        const int t0 = start(ci), many = h * a.G + g, gate0 = ci % BATCH * C, rows = min(C, last - t0);
         int* bad = bads + (ci & 1);
         __syncthreads();   // the step before is done with what stands in LDS
         if constexpr (!STATE)
-            if (!SUM || g == 0) qv.template store<false>(qs, QP, t0, last, 0, a.dk, nullptr);
+            if (!SUM || g == 0) qv.template store<false>(qs, QP, rows, 0, a.dk, nullptr);
         if (SUM || g == 0) {
-            kv.template store<false>(ks, KP, t0, last, 0, a.dk, nullptr);
-            vv.template store<KIND == LIN_OUT>(vs, VP, t0, last, col0, a.dv, bad);
+            kv.template store<false>(ks, KP, rows, 0, a.dk, nullptr);
+            vv.template store<KIND == LIN_OUT>(vs, VP, rows, col0, a.dv, bad);
         }
         if constexpr (DOT)
             if (g == 0 && ci > 0) put_dots(start(ci - 1));
@@ -429,7 +466,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                 const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
 #pragma unroll
                 for (int w = 0; w < CW; ++w)
-                    vp[s][w].set(to_f32v(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
+                    vp[s][w].set(lin_f32(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
             }
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -641,13 +678,13 @@ __global__ __launch_bounds__(256) void lin_flow_kernel(const float* S, const flo
     if (threadIdx.x == 0) flow[bh * nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// Rows t0 .. t0 + C - 1 (zeros from n on) of a token array into LDS, 16 bytes
-// at a time, with zeros behind its columns.
+// Rows t0 .. of a token array into LDS, zeros behind the last and behind its
+// columns.
 template <class T, int D, int C, int RP>
-__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int n, int cols, T* rows) {
+__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int rows, int cols, T* to) {
     LinTile<T, D, C> t;
-    t.load(x, step, t0, n, 0, cols);
-    t.template store<false>(rows, RP, t0, n, 0, cols, nullptr);
+    t.load(x + t0 * step, (unsigned)step, rows, 0, cols);
+    t.template store<false>(to, RP, rows, 0, cols, nullptr);
 }
 
 // dg of a chunk's tokens but for what passes the chunk, and the sums of fq
@@ -694,8 +731,8 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
     const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * a.dk;
     const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * a.dv;
     const T* y = reinterpret_cast<const T*>(a.dy) + b * a.gb;
-    lin_stage<T, D, C, RP>(k, a.kt, t0, n, a.dk, ks);
-    lin_stage<T, D, C, RP>(v, a.vt, t0, n, a.dv, vs);
+    lin_stage<T, D, C, RP>(k, a.kt, t0, rows, a.dk, ks);
+    lin_stage<T, D, C, RP>(v, a.vt, t0, rows, a.dv, vs);
     float x[NT][4];
 #pragma unroll
     for (int kt = 0; kt < NT; ++kt)
@@ -704,8 +741,8 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
     const int i = 16 * wave + l16;
     for (int g = 0; g < a.G; ++g) {
         if (g > 0) __syncthreads();
-        lin_stage<T, D, C, RP>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, n, a.dk, qs);
-        lin_stage<T, D, C, RP>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, n, a.dv, ys);
+        lin_stage<T, D, C, RP>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, rows, a.dk, qs);
+        lin_stage<T, D, C, RP>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, rows, a.dv, ys);
         __syncthreads();
         if (wave < NT) {
             const double gi = gs[i];
@@ -1124,8 +1161,8 @@ static bool lin_sizes_ok(int B, int T, int H, int Hk, int dk, int dv) {
            (B == 0 || T <= (1L << 40) / ((long)B * H * 256));
 }
 static bool lin_tokens_ok(const void* p, long batch, long token, int B, int T) {
-    const long lim = 1L << 40;
-    return p && (uintptr_t)p % 16 == 0 && batch >= 0 && token >= 0 && batch <= lim && token <= lim && batch % 8 == 0 &&
+    const long lim = 1L << 40;   // 64 rows within 2^31 bytes
+    return p && (uintptr_t)p % 16 == 0 && batch >= 0 && token >= 0 && batch <= lim && token < 1L << 23 && batch % 8 == 0 &&
            token % 8 == 0 && (double)B * (double)batch < 4e18 && (double)T * (double)token < 4e18;
 }
 static tm_status lin_status(hipError_t e) {
