@@ -50,7 +50,6 @@ struct LinArgs {
     const float* s_in;                   // [batch * key heads][s_seg][...]; null: zeros
     float* s_out;                        // null: not wanted
     long s_in_bh, s_in_seg, s_out_bh, s_out_seg;   // elements between heads' and between segments' states
-    long sa, sc;                         // elements between the rows and between the columns of a state
     void* out;
     float* dot;                          // [slabs][batch * key heads][T]
     double* gsum;                        // [batch * key heads][nseg]: log2 of what a segment keeps
@@ -174,18 +173,28 @@ template <class T, int D, int C> struct LinTile {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = keep_if(v[i], there && r0 + i * PER < rows);
         }
+        if constexpr (CHECK) {
+            bool any = false;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = r0 + i * PER;
-            if constexpr (CHECK)
-                if (lin_lost(v[i])) {
+            for (int i = 0; i < N; ++i) any |= lin_lost(v[i]);
+            if (any)
+#pragma unroll 1
+                for (int i = 0; i < N; ++i) {
+                    bool here = false;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        if (!__builtin_isfinite((float)v[i][e])) v[i][e] = (T)0.f;
-                    atomicMin(bad, r);
+                    for (int j = 0; j < N; ++j)
+                        if (j == i && lin_lost(v[j])) {
+                            here = true;
+#pragma unroll
+                            for (int e = 0; e < VE; ++e)
+                                if (!__builtin_isfinite((float)v[j][e])) v[j][e] = (T)0.f;
+                        }
+                    if (here) atomicMin(bad, r0 + i * PER);
                 }
-            if (C * UNITS % 256 == 0 || r < C) *reinterpret_cast<Vec*>(to + r * row + u * VE) = v[i];
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (C * UNITS % 256 == 0 || r0 + i * PER < C) *reinterpret_cast<Vec*>(to + (r0 + i * PER) * row + u * VE) = v[i];
     }
 };
 
@@ -220,7 +229,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     constexpr bool DOT = KIND == LIN_DQ || KIND == LIN_DK;
     constexpr int C = lin_chunk<T>(), NT = C / 16, NS = DK / 32, NM = DK / 16, KS = C / 32;
     // the state as an operand keeps 16 bits, 24 where its products enter the gradients of the decays
-    constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP3 = lin_parts<T>(3);
+    constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP3 = lin_parts<T>(3);   // what is added to the state: 24
     typedef typename Frag<T>::T F;
     typedef LinLds<T, DK, CW> S_;
     constexpr int QP = S_::QP, KP = S_::KP, VP = S_::VP, PP = S_::PP, BATCH = S_::GATES / C;
@@ -252,17 +261,29 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int w = 0; w < CW; ++w) S[m][w] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // a row of the state is a row of the array, or (where queries and keys are the values) a column
+    constexpr bool TURNED = KIND == LIN_DQ || KIND == LIN_DK;
+    auto cell = [&](int i, int c) { return TURNED ? c * a.dk + i : i * a.dv + c; };
     if (!STATE && a.s_in) {
         const float* s = a.s_in + bh * a.s_in_bh + seg * a.s_in_seg;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int w = 0; w < CW; ++w)
+            for (int w = 0; w < CW; ++w) {
+                const int i = 16 * m + 4 * lg, c = col0 + wcol + 16 * w + l16;   // dk: a multiple of 8
+                const bool there = i < a.dk && c < a.dv;
+                if constexpr (TURNED) {
+                    S[m][w] = *reinterpret_cast<const f32x4*>(s + (there ? cell(i, c) : 0));
+                } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * m + 4 * lg + r, c = col0 + wcol + 16 * w + l16;
-                    if (i < a.dk && c < a.dv) S[m][w][r] = s[i * a.sa + c * a.sc];
+                    for (int r = 0; r < 4; ++r) S[m][w][r] = s[there ? cell(i + r, c) : 0];
                 }
+            }
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int w = 0; w < CW; ++w)
+                S[m][w] = keep_if(S[m][w], 16 * m + 4 * lg < a.dk && col0 + wcol + 16 * w + l16 < a.dv);
     }
     double kept = 0.0;
 
@@ -286,6 +307,8 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
         if (i < min(C, last - t0))
             a.dot[((long)slab * a.B * a.Hk + bh) * a.T + t0 + i] = (dots[i] + dots[64 + i]) + (dots[128 + i] + dots[192 + i]);
     };
+    // the state is there: seen as still under way, its first use in every chunk would wait for the rows read ahead
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
     if (steps) fetch(0, 0);
     if (KIND == LIN_OUT && threadIdx.x < 2) bads[threadIdx.x] = C;
     int ci = 0, g = 0;
@@ -335,21 +358,18 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                     qt = NT - 1 - qt;
                     kt = NT - 1 - kt;
                 }
-                const int i = 16 * qt + l16;
-                f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (REV ? kt >= qt : kt <= qt) {
+                const int i = 16 * qt + l16, j0 = 16 * kt + 4 * lg;
+                f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f}, by;
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        if (32 * s < a.dk)
-                            mma(w, lin_split8(ks + (16 * kt + l16) * KP + 32 * s, lg), lin_split8(qs + i * QP + 32 * s, lg));
-                    const double gi = gs[gate0 + i];
+                for (int s = 0; s < NS; ++s)
+                    mma(w, lin_split8(ks + (16 * kt + l16) * KP + 32 * s, lg), lin_split8(qs + i * QP + 32 * s, lg));
+                const double gi = gs[gate0 + i];
+                const double* gj = gs + gate0 + j0;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = 16 * kt + 4 * lg + r;
-                        const double gj = gs[gate0 + j], x = REV ? gj - gi : gi - gj;
-                        w[r] = (REV ? j >= i : j <= i) ? w[r] * (__builtin_amdgcn_exp2f((float)x) * a.pair_scale) : 0.f;
-                    }
-                }
+                for (int r = 0; r < 4; ++r)   // pairs of the other order: their weight is not used
+                    by[r] = __builtin_amdgcn_exp2f((float)(REV ? gj[r] - gi : gi - gj[r])) * a.pair_scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r] = (REV ? j0 + r >= i : j0 + r <= i) ? w[r] * by[r] : 0.f;
                 typedef T V4 __attribute__((ext_vector_type(4)));
                 V4 o;
 #pragma unroll
@@ -358,14 +378,12 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             }
             // the far part, out of the state before the chunk
             if (!SUM || g == 0) {
-                f32x4 far[NT][CW];
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int w = 0; w < CW; ++w) far[i][w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int w = 0; w < CW; ++w) O[i][w] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    if (32 * s >= a.dk) continue;
                     Parts<T, SP> sp[CW];
 #pragma unroll
                     for (int w = 0; w < CW; ++w)
@@ -380,9 +398,9 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                                 if constexpr (sizeof(T) == 4) {   // sums of 32, then of those
                                     f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
                                     mma(sum, sp[w].p[p], qf);
-                                    far[i][w] += sum;
+                                    O[i][w] += sum;
                                 } else {
-                                    mma(far[i][w], sp[w].p[p], qf);
+                                    mma(O[i][w], sp[w].p[p], qf);
                                 }
                             }
                     }
@@ -393,7 +411,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                     if (DOT && g == 0) far_dot[i] = 0.f;
 #pragma unroll
                     for (int w = 0; w < CW; ++w) {
-                        O[i][w] = far[i][w] * by;
+                        O[i][w] *= by;
                         if constexpr (DOT) {
                             const int t = t0 + 16 * i + l16, c = col0 + wcol + 16 * w + 4 * lg;
                             if (t < last && c < a.dv) {
@@ -423,69 +441,86 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             }
             if (!SUM || g == a.G - 1) {
                 const int heads = SUM ? a.Hk : a.Hk * a.G, oh = SUM ? h : many;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int t = t0 + 16 * i + l16;
+                const unsigned step = (unsigned)(heads * a.dv);
+                char* to = reinterpret_cast<char*>(reinterpret_cast<T*>(a.out) + ((long)b * a.T + t0) * step + (long)oh * a.dv + col0);
+                const unsigned off = (l16 * step + wcol + 4 * lg) * (unsigned)sizeof(T);
+                typedef T V4 __attribute__((ext_vector_type(4)));
+                auto put = [&](bool all) {
                     // a non-finite value is zero in vs: its products with the weights of earlier tokens, which are
                     // zero, would not be
-                    const bool lost = KIND == LIN_OUT && 16 * i + l16 >= *bad;
+                    const int from = KIND == LIN_OUT && !all ? *bad : C;
 #pragma unroll
-                    for (int w = 0; w < CW; ++w) {
-                        const int c = col0 + wcol + 16 * w + 4 * lg;
-                        if (t < last && c < a.dv) {
-                            typedef T V4 __attribute__((ext_vector_type(4)));
-                            V4 o;
+                    for (int i = 0; i < NT; ++i) {
+                        const bool lost = KIND == LIN_OUT && !all && 16 * i + l16 >= from;
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) o[r] = (T)(lost ? __builtin_nanf("") : O[i][w][r]);
-                            *reinterpret_cast<V4*>(reinterpret_cast<T*>(a.out) +
-                                                   (((long)b * a.T + t) * heads + oh) * a.dv + c) = o;
-                        }
+                        for (int w = 0; w < CW; ++w)
+                            if (all || (16 * i + l16 < rows && col0 + wcol + 16 * w + 4 * lg < a.dv)) {
+                                V4 o;
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) o[r] = (T)(lost ? __builtin_nanf("") : O[i][w][r]);
+                                *reinterpret_cast<V4*>(to + (unsigned long)(16 * i) * step * sizeof(T) + 16 * w * sizeof(T) + off) = o;
+                            }
                     }
-                    if constexpr (DOT)
-                        if (g == a.G - 1) {
+                };
+                if (rows == C && col0 + 64 * CW <= a.dv && (KIND != LIN_OUT || *bad == C)) put(true);
+                else put(false);
+                if constexpr (DOT)
+                    if (g == a.G - 1)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
                             float d = far_dot[i];
                             d += __shfl_xor(d, 16, 64);
                             d += __shfl_xor(d, 32, 64);
                             if (lg == 0) dots[wave * 64 + 16 * i + l16] = d;
                         }
-                }
             }
         }
         // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
         if (SUM || g == a.G - 1) {
-            // a chunk's sum is formed by itself: the state takes one rounding a chunk, not one a product
             float keep = 1.f;
             if (!SUM || g == 0) {
                 const double end = gs[gate0 + C - 1];
                 keep = __builtin_amdgcn_exp2f((float)end);
                 kept += end;
             }
-            Parts<T, VP3> vp[KS][CW];
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
+                for (int m = 0; m < NM; ++m)
 #pragma unroll
-                for (int w = 0; w < CW; ++w)
-                    vp[s][w].set(lin_f32(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
-            }
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                if (16 * m >= a.dk) continue;
-                f32x4 sum[CW];
-#pragma unroll
-                for (int w = 0; w < CW; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int w = 0; w < CW; ++w) S[m][w] *= keep;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    const F kf = lin_column8(ks + 32 * s * KP, KP, 16 * m);
+                    Parts<T, VP3> vp[CW];
+                    const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
 #pragma unroll
-                    for (int p = VP3 - 1; p >= 0; --p)
+                    for (int w = 0; w < CW; ++w)
+                        vp[w].set(lin_f32(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
 #pragma unroll
-                        for (int w = 0; w < CW; ++w) mma(sum[w], kf, vp[s][w].p[p]);
+                    for (int m = 0; m < NM; ++m) {
+                        const F kf = lin_column8(ks + 32 * s * KP, KP, 16 * m);
+#pragma unroll
+                        for (int p = VP3 - 1; p >= 0; --p)
+#pragma unroll
+                            for (int w = 0; w < CW; ++w) mma(S[m][w], kf, vp[w].p[p]);
+                    }
                 }
+            } else {   // a chunk's sum is formed by itself: the state takes one rounding a chunk, not one a product of 4 tokens
+                static_assert(sizeof(T) == 2 || KS == 1, "a chunk of 32 tokens");
+                const f32x8 by = ld8(tail + gate0 + 8 * lg);
+                F vf[CW];
 #pragma unroll
-                for (int w = 0; w < CW; ++w)
+                for (int w = 0; w < CW; ++w) vf[w] = lin_column8(vs, VP, wcol + 16 * w) * by;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) S[m][w][r] = fmaf(keep, S[m][w][r], sum[w][r]);
+                for (int m = 0; m < NM; ++m) {
+                    const F kf = lin_column8(ks, KP, 16 * m);
+#pragma unroll
+                    for (int w = 0; w < CW; ++w) {
+                        f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+                        mma(sum, kf, vf[w]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) S[m][w][r] = fmaf(keep, S[m][w][r], sum[r]);
+                    }
+                }
             }
             if (KIND == LIN_OUT && *bad < C) {
 #pragma unroll
@@ -502,17 +537,18 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             __syncthreads();
             put_dots(start(chunks - 1));
         }
-    if (a.s_out) {
+    if (!TURNED && a.s_out) {
         float* s = a.s_out + bh * a.s_out_bh + seg * a.s_out_seg;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int w = 0; w < CW; ++w) {
+            const int c = col0 + wcol + 16 * w + l16;
+            if (c < a.dv)
 #pragma unroll
-            for (int w = 0; w < CW; ++w)
+                for (int m = 0; m < NM; ++m)
+                    if (16 * m + 4 * lg < a.dk)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * m + 4 * lg + r, c = col0 + wcol + 16 * w + l16;
-                    if (i < a.dk && c < a.dv) s[i * a.sa + c * a.sc] = S[m][w][r];
-                }
+                        for (int r = 0; r < 4; ++r) s[cell(16 * m + 4 * lg + r, c)] = S[m][w][r];
+        }
     }
     if (STATE && a.gsum && slab == 0 && threadIdx.x == 0) a.gsum[(long)bh * a.nseg + seg] = kept;
 }
@@ -877,7 +913,7 @@ __global__ void lin_zero_kernel(float* p, int n) {
 // ---------------------------------------------------------------------------
 // launches
 
-static int lin_width(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+static int lin_width(int d) { return (d + 63) / 64 * 64; }
 
 template <class T, int DK, int CW, int KIND>
 static hipError_t lin_run(LinArgs a, hipStream_t st) {
@@ -902,6 +938,7 @@ static int lin_columns(int dk, int dv) { return dv > 64 && dk <= 128 ? 128 : 64;
 template <class T, int KIND> static hipError_t lin_launch(const LinArgs& a, hipStream_t st) {
     const int w = lin_width(a.dk);
     if (w == 256) return lin_run<T, 256, 1, KIND>(a, st);
+    if (w == 192) return lin_run<T, 192, 1, KIND>(a, st);
     if (lin_columns(a.dk, a.dv) == 128)
         return w == 128 ? lin_run<T, 128, 2, KIND>(a, st) : lin_run<T, 64, 2, KIND>(a, st);
     return w == 128 ? lin_run<T, 128, 1, KIND>(a, st) : lin_run<T, 64, 1, KIND>(a, st);
@@ -933,6 +970,7 @@ template <class T, int DK, int CW, bool STATES> static hipError_t lin_many_run(L
 template <class T, bool STATES> static hipError_t lin_many(const LinMany& m, int wide, hipStream_t st) {
     const int w = lin_width(wide);
     return w == 256   ? lin_many_run<T, 256, 1, STATES>(m, st)
+           : w == 192 ? lin_many_run<T, 192, 1, STATES>(m, st)
            : w == 128 ? lin_many_run<T, 128, 2, STATES>(m, st)
                       : lin_many_run<T, 64, 1, STATES>(m, st);
 }
@@ -957,7 +995,7 @@ template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hip
 template <class T> static hipError_t lin_pairs(const LinPairs& a, hipStream_t st) {
     const int w = lin_width(a.dk > a.dv ? a.dk : a.dv);
     constexpr int C = lin_chunk<T>();
-    return w == 256 ? lin_pairs_run<T, 256, C>(a, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, st) : lin_pairs_run<T, 64, C>(a, st);
+    return w >= 192 ? lin_pairs_run<T, 256, C>(a, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, st) : lin_pairs_run<T, 64, C>(a, st);
 }
 
 template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
@@ -967,9 +1005,8 @@ template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
     const size_t bytes = (size_t)a.G * 1024;
     const dim3 grid((unsigned)blocks);
     return timed_layer(st, [&] {
-        const int w = lin_width(a.dk);
-        if (w == 64) launch_k((lin_token_kernel<T, 64>), grid, dim3(256), bytes, st, a);
-        else if (w == 128) launch_k((lin_token_kernel<T, 128>), grid, dim3(256), bytes, st, a);
+        if (a.dk <= 64) launch_k((lin_token_kernel<T, 64>), grid, dim3(256), bytes, st, a);
+        else if (a.dk <= 128) launch_k((lin_token_kernel<T, 128>), grid, dim3(256), bytes, st, a);
         else launch_k((lin_token_kernel<T, 256>), grid, dim3(256), bytes, st, a);
         return hipGetLastError();
     });
@@ -1042,8 +1079,6 @@ static hipError_t lin_copy(const float* from, float* to, long n, hipStream_t st)
 template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, char* ws, hipStream_t st) {
     const long cells = (long)a.dk * a.dv;
     a.s_in_bh = a.s_out_bh = cells;
-    a.sa = a.dv;
-    a.sc = 1;
     if (a.T <= LIN_REC) {
         a.s_out = state_out;
         return lin_tokens_run<T>(a, st);
@@ -1099,8 +1134,6 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     s.s_out = S;
     s.s_out_bh = slots * cells;
     s.s_out_seg = cells;
-    s.sa = dv;
-    s.sc = 1;
     s.gsum = gsum;
     LinArgs r = s;
     r.G = a.G;
@@ -1121,14 +1154,14 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     LinArgs y = x;
     y.q = g.dy; y.qb = g.gb; y.qt = g.gt; y.k = a.v; y.kb = a.vb; y.kt = a.vt; y.v = a.k; y.vb = a.kb; y.vt = a.kt;
     y.z = a.q; y.zb = a.qb; y.zt = a.qt;
-    y.dk = dv; y.dv = dk; y.s_in = S; y.sa = 1; y.sc = dv; y.out = g.dq; y.dot = dotq;
+    y.dk = dv; y.dv = dk; y.s_in = S; y.out = g.dq; y.dot = dotq;
     LinArgs w = x;
     w.q = a.v; w.qb = a.vb; w.qt = a.vt; w.k = g.dy; w.kb = g.gb; w.kt = g.gt; w.v = a.q; w.vb = a.qb; w.vt = a.qt;
     w.z = a.k; w.zb = a.kb; w.zt = a.kt;
-    w.dk = dv; w.dv = dk; w.s_in = R; w.sa = 1; w.sc = dv; w.out = g.dk; w.dot = dotk;
+    w.dk = dv; w.dv = dk; w.s_in = R; w.out = g.dk; w.dot = dotk;
     w.far_scale = 1.f; w.state_scale = scale;
     x.q = a.k; x.qb = a.kb; x.qt = a.kt; x.k = a.q; x.kb = a.qb; x.kt = a.qt; x.v = g.dy; x.vb = g.gb; x.vt = g.gt;
-    x.s_in = R; x.sa = dv; x.sc = 1; x.out = g.dv;
+    x.s_in = R; x.out = g.dv;
     x.far_scale = 1.f; x.state_scale = scale;
     LIN_TRY((lin_many<T, false>(LinMany{{w, y, x}, {}}, wide, st)));
     if (!g.dld) return hipSuccess;
