@@ -65,15 +65,30 @@ __device__ __forceinline__ double lin_gate(float g) {
     return (double)(g < -1000.f ? -1000.f : g) * LOG2E;
 }
 
-// 8 values in the order in which two stacked accumulator tiles hold 32 rows:
-// lane group g has 4 g .. and 16 + 4 g ..
-__device__ __forceinline__ bf16x8 lin_split8(const bf16* p, int g) {
+// Rows in LDS, D elements long without gaps: the piece of 4 elements at column
+// 4 u of row r stands at piece u ^ g(r), so that the reads of a wave are spread
+// over the 32 banks: 16 rows at one column (8 bytes a lane for bf16, 16 lanes a
+// cycle), 4 rows of 16 columns (transposing reads), for fp32 8 rows of 16
+// bytes and 2 rows of 16 columns.  Padded rows had served one kind of read or
+// the other (2300 of a chunk's 26000 cycles were conflicts).
+template <class T> __device__ __forceinline__ int lin_turn(int r) {
+    return sizeof(T) == 2 ? (r & 3) * 4 + (r >> 2 & 3) : (r & 7) ^ (r >> 1 & 4);
+}
+
+// 8 values of row `row` from column c on (a multiple of 32), in the order in
+// which two stacked accumulator tiles hold 32 rows: lane group g has 4 g ..
+// and 16 + 4 g ..
+template <int D> __device__ __forceinline__ bf16x8 lin_split8(const bf16* m, int row, int c, int g) {
     typedef bf16 V4 __attribute__((ext_vector_type(4)));
-    const V4 a = *reinterpret_cast<const V4*>(p + 4 * g), b = *reinterpret_cast<const V4*>(p + 16 + 4 * g);
+    const bf16* p = m + row * D;
+    const int t = lin_turn<bf16>(row), u = c / 4 + g;
+    const V4 a = *reinterpret_cast<const V4*>(p + 4 * (u ^ t)), b = *reinterpret_cast<const V4*>(p + 4 * (u ^ t ^ 4));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-__device__ __forceinline__ f32x8 lin_split8(const float* p, int g) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p + 4 * g), b = *reinterpret_cast<const f32x4*>(p + 16 + 4 * g);
+template <int D> __device__ __forceinline__ f32x8 lin_split8(const float* m, int row, int c, int g) {
+    const float* p = m + row * D;
+    const int t = lin_turn<float>(row), u = c / 4 + g;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + 4 * (u ^ t)), b = *reinterpret_cast<const f32x4*>(p + 4 * (u ^ t ^ 4));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -111,14 +126,10 @@ template <class T> constexpr int lin_parts(int n) { return sizeof(T) == 4 ? 1 : 
 // instructions the pairs of a chunk cost more than the state it saves).
 template <class T> constexpr int lin_chunk() { return sizeof(T) == 4 ? 32 : 64; }
 
-// Row lengths in LDS: operands read along a row are 8 (fp32: 4) elements
-// longer than theirs, those read across rows 16, so that 16 rows, or 4 rows
-// of 16 columns, stand at different banks.
 template <class T, int DK, int CW> struct LinLds {
-    static constexpr int C = lin_chunk<T>(), PAD = 16 / sizeof(T), TPAD = sizeof(T) == 4 ? 4 : 16;
-    static constexpr int QP = DK + PAD, KP = DK + TPAD, VP = 64 * CW + TPAD, PP = C + PAD;
+    static constexpr int C = lin_chunk<T>(), VD = 64 * CW, PP = C + 16 / sizeof(T);
     static constexpr int GATES = 512;   // tokens whose decays are summed at a time
-    static constexpr size_t q = 0, k = q + sizeof(T) * C * QP, v = k + sizeof(T) * C * KP, p = v + sizeof(T) * C * VP,
+    static constexpr size_t q = 0, k = q + sizeof(T) * C * DK, v = k + sizeof(T) * C * DK, p = v + sizeof(T) * C * VD,
                             g = p + sizeof(T) * C * PP, head = g + 8 * GATES, tail = head + 4 * GATES,
                             dot = tail + 4 * GATES, bad = dot + 4 * 4 * 64, bytes = bad + 16;
 };
@@ -164,8 +175,9 @@ template <class T, int D, int C> struct LinTile {
                 v[i] = *reinterpret_cast<const Vec*>(at + (min(r0 + i * PER, rows - 1u) * step + c) * (unsigned)sizeof(T));
         }
     }
-    // bad: the first row with a non-finite element, which is taken as zero
-    template <bool CHECK>
+    // TURN: pieces permuted (lin_turn).  bad: the first row with a non-finite
+    // element, which is taken as zero
+    template <bool CHECK, bool TURN>
     __device__ __forceinline__ void store(T* to, int row, int rows, int c0, int cols, int* bad) {
         const int u = threadIdx.x % UNITS, r0 = threadIdx.x / UNITS;
         if (rows < C || c0 + D > cols) {
@@ -194,28 +206,53 @@ template <class T, int D, int C> struct LinTile {
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (C * UNITS % 256 == 0 || r0 + i * PER < C) *reinterpret_cast<Vec*>(to + (r0 + i * PER) * row + u * VE) = v[i];
+            if (C * UNITS % 256 == 0 || r0 + i * PER < C) {
+                const int r = r0 + i * PER;
+                if constexpr (!TURN) {
+                    *reinterpret_cast<Vec*>(to + r * row + u * VE) = v[i];
+                } else if constexpr (VE == 4) {
+                    *reinterpret_cast<Vec*>(to + r * row + 4 * (u ^ lin_turn<T>(r))) = v[i];
+                } else {
+                    typedef T V4 __attribute__((ext_vector_type(4)));
+                    *reinterpret_cast<V4*>(to + r * row + 4 * (2 * u ^ lin_turn<T>(r))) = __builtin_shufflevector(v[i], v[i], 0, 1, 2, 3);
+                    *reinterpret_cast<V4*>(to + r * row + 4 * ((2 * u + 1) ^ lin_turn<T>(r))) = __builtin_shufflevector(v[i], v[i], 4, 5, 6, 7);
+                }
+            }
     }
 };
 
-// 8 rows from r0 of column c + (lane % 16), for lane group g rows 8 g ..
-__device__ __forceinline__ bf16x8 lin_column8(const bf16* m, int row, int c) {
+// 8 rows from r0 on (a multiple of 32; lane group g has rows r0 + 8 g ..) of
+// column c + (lane % 16), c a multiple of 16.  l: the lane.
+template <int D> __device__ __forceinline__ bf16x8 lin_column8(const bf16* m, int r0, int c, int l) {
     typedef short S4 __attribute__((ext_vector_type(4)));
     typedef short S8 __attribute__((ext_vector_type(8)));
-    const int l = threadIdx.x & 63, i = l & 15;
+    const int i = l & 15;
     // the transposing read: a lane names 4 columns of a row, and gets 4 rows of its column
-    const bf16* p = m + (8 * (l >> 4) + (i >> 2)) * row + c + 4 * (i & 3);
-    const S4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(p));
-    const S4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(p + 4 * row));
-    return __builtin_bit_cast(bf16x8, (S8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    const int r = 8 * (l >> 4) + (i >> 2), u = c / 4 + (i & 3);
+    const bf16* p = m + (r0 + r) * D;
+    const bf16* a = p + 4 * (u ^ lin_turn<bf16>(r));
+    const bf16* b = p + 4 * D + 4 * (u ^ lin_turn<bf16>(r + 4));
+    const S4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(a));
+    const S4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)(b));
+    return __builtin_bit_cast(bf16x8, (S8)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-__device__ __forceinline__ f32x8 lin_column8(const float* m, int row, int c) {
-    const int l = threadIdx.x & 63;
-    const float* p = m + 8 * (l >> 4) * row + c + (l & 15);
+template <int D> __device__ __forceinline__ f32x8 lin_column8(const float* m, int r0, int c, int l) {
+    const int r = 8 * (l >> 4), col = c + (l & 15);
     f32x8 x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = p[e * row];
+    for (int e = 0; e < 8; ++e) x[e] = m[(r0 + r + e) * D + 4 * ((col / 4) ^ lin_turn<float>(r + e)) + col % 4];
     return x;
+}
+
+// The lane.  ANEW: what is computed from it is not kept in registers from one
+// part of a chunk's work (or from one chunk) to the next.  The large kernels
+// have none left for it (spilling, widths of 128 took 1.4 times as long); the
+// others are better off with the addresses kept (widths of 64: 50 us against
+// 62 for 1024 tokens of 256 heads).
+template <bool ANEW> __device__ __forceinline__ int lin_lane() {
+    int l = threadIdx.x & 63;
+    if constexpr (ANEW) asm volatile("" : "+v"(l));
+    return l;
 }
 
 // One workgroup of 4 waves takes one key head of one entry, one segment of its
@@ -232,7 +269,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP3 = lin_parts<T>(3);   // what is added to the state: 24
     typedef typename Frag<T>::T F;
     typedef LinLds<T, DK, CW> S_;
-    constexpr int QP = S_::QP, KP = S_::KP, VP = S_::VP, PP = S_::PP, BATCH = S_::GATES / C;
+    constexpr int VD = S_::VD, PP = S_::PP, BATCH = S_::GATES / C;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     T* qs = reinterpret_cast<T*>(lds + S_::q);
     T* ks = reinterpret_cast<T*>(lds + S_::k);
@@ -318,10 +355,10 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
         int* bad = bads + (ci & 1);
         __syncthreads();   // the step before is done with what stands in LDS
         if constexpr (!STATE)
-            if (!SUM || g == 0) qv.template store<false>(qs, QP, rows, 0, a.dk, nullptr);
+            if (!SUM || g == 0) qv.template store<false, true>(qs, DK, rows, 0, a.dk, nullptr);
         if (SUM || g == 0) {
-            kv.template store<false>(ks, KP, rows, 0, a.dk, nullptr);
-            vv.template store<KIND == LIN_OUT>(vs, VP, rows, col0, a.dv, bad);
+            kv.template store<false, true>(ks, DK, rows, 0, a.dk, nullptr);
+            vv.template store<KIND == LIN_OUT, true>(vs, VD, rows, col0, a.dv, bad);
         }
         if constexpr (DOT)
             if (g == 0 && ci > 0) put_dots(start(ci - 1));
@@ -352,6 +389,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             // the pairs' weights: tiles of 16 queries by 16 keys, those that a step of 32 keys reads
 #pragma unroll
             for (int pi = 0; pi < (NT == 4 ? 3 : 1); ++pi) {
+                const int l = lin_lane<DK * CW >= 192>(), l16 = l & 15, lg = l >> 4;
                 const int p = wave + 4 * pi;
                 int qt = p < 4 ? p >> 1 : 2 + ((p - 4) >> 2), kt = p < 4 ? p & 1 : (p - 4) & 3;
                 if (REV) {
@@ -362,7 +400,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                 f32x4 w = f32x4{0.f, 0.f, 0.f, 0.f}, by;
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
-                    mma(w, lin_split8(ks + (16 * kt + l16) * KP + 32 * s, lg), lin_split8(qs + i * QP + 32 * s, lg));
+                    mma(w, lin_split8<DK>(ks, 16 * kt + l16, 32 * s, lg), lin_split8<DK>(qs, i, 32 * s, lg));
                 const double gi = gs[gate0 + i];
                 const double* gj = gs + gate0 + j0;
 #pragma unroll
@@ -378,6 +416,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             }
             // the far part, out of the state before the chunk
             if (!SUM || g == 0) {
+                const int l = lin_lane<DK * CW >= 192>(), l16 = l & 15, lg = l >> 4;
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -390,7 +429,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                         sp[w].set(__builtin_shufflevector(S[2 * s][w], S[2 * s + 1][w], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        const F qf = lin_split8(qs + (16 * i + l16) * QP + 32 * s, lg);
+                        const F qf = lin_split8<DK>(qs, 16 * i + l16, 32 * s, lg);
 #pragma unroll
                         for (int p = SP - 1; p >= 0; --p)
 #pragma unroll
@@ -426,11 +465,12 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
             }
             __syncthreads();
             // the chunk's own
+            const int l = lin_lane<DK * CW >= 192>(), l16 = l & 15, lg = l >> 4;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 F vf[CW];
 #pragma unroll
-                for (int w = 0; w < CW; ++w) vf[w] = lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w);
+                for (int w = 0; w < CW; ++w) vf[w] = lin_column8<VD>(vs, 32 * s, wcol + 16 * w, l);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (REV ? s < i / 2 : s > i / 2) continue;
@@ -477,6 +517,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
         }
         // the state behind the chunk: the values take the decays (and are split), the keys go in as they are
         if (SUM || g == a.G - 1) {
+            const int l = lin_lane<DK * CW >= 192>(), lg = l >> 4;
             float keep = 1.f;
             if (!SUM || g == 0) {
                 const double end = gs[gate0 + C - 1];
@@ -494,10 +535,10 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                     const f32x8 by = ld8(tail + gate0 + 32 * s + 8 * lg);
 #pragma unroll
                     for (int w = 0; w < CW; ++w)
-                        vp[w].set(lin_f32(lin_column8(vs + 32 * s * VP, VP, wcol + 16 * w)) * by);
+                        vp[w].set(lin_f32(lin_column8<VD>(vs, 32 * s, wcol + 16 * w, l)) * by);
 #pragma unroll
                     for (int m = 0; m < NM; ++m) {
-                        const F kf = lin_column8(ks + 32 * s * KP, KP, 16 * m);
+                        const F kf = lin_column8<DK>(ks, 32 * s, 16 * m, l);
 #pragma unroll
                         for (int p = VP3 - 1; p >= 0; --p)
 #pragma unroll
@@ -509,10 +550,10 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
                 const f32x8 by = ld8(tail + gate0 + 8 * lg);
                 F vf[CW];
 #pragma unroll
-                for (int w = 0; w < CW; ++w) vf[w] = lin_column8(vs, VP, wcol + 16 * w) * by;
+                for (int w = 0; w < CW; ++w) vf[w] = lin_column8<VD>(vs, 0, wcol + 16 * w, l) * by;
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    const F kf = lin_column8(ks, KP, 16 * m);
+                    const F kf = lin_column8<DK>(ks, 0, 16 * m, l);
 #pragma unroll
                     for (int w = 0; w < CW; ++w) {
                         f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -720,7 +761,7 @@ template <class T, int D, int C, int RP>
 __device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int rows, int cols, T* to) {
     LinTile<T, D, C> t;
     t.load(x + t0 * step, (unsigned)step, rows, 0, cols);
-    t.template store<false>(to, RP, rows, 0, cols, nullptr);
+    t.template store<false, false>(to, RP, rows, 0, cols, nullptr);
 }
 
 // dg of a chunk's tokens but for what passes the chunk, and the sums of fq
