@@ -96,8 +96,8 @@ tm_status tm_linear_attention(const void* q, long q_batch, long q_token, const v
                               tm_dtype dtype, void* workspace, void* stream);
 
 /* Workspace bytes of tm_linear_attention (backward == 0) or of its backward;
- * 256-byte aligned, holds no data between calls.  0 for sizes that the calls
- * refuse. */
+ * 256-byte aligned, holds no data between calls.  0 for calls that need none
+ * (the workspace may then be null), and for sizes that the calls refuse. */
 size_t tm_linear_workspace_bytes(int batch, int n_tokens, int heads, int kv_heads, int key_dim, int value_dim,
                                  int backward);
 

@@ -29,6 +29,8 @@
 // decay's sum over n tokens would lose n^1.5 roundings.
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/tm_layer.h"
 #include "tm_device.h"
 
@@ -247,7 +249,7 @@ template <int D> __device__ __forceinline__ f32x8 lin_column8(const float* m, in
 // The lane.  ANEW: what is computed from it is not kept in registers from one
 // part of a chunk's work (or from one chunk) to the next.  The large kernels
 // have none left for it (spilling, widths of 128 took 1.4 times as long); the
-// others are better off with the addresses kept (widths of 64: 50 us against
+// others are better off with the addresses kept (widths of 64: 57 us against
 // 62 for 1024 tokens of 256 heads).
 template <bool ANEW> __device__ __forceinline__ int lin_lane() {
     int l = threadIdx.x & 63;
@@ -617,13 +619,24 @@ template <class T, int DK, int CW> __global__ __launch_bounds__(256, 2) void lin
 
 // Single tokens and short drafts, token by token: 32 columns of a head's
 // state a workgroup, in its registers (4 columns and DK / 32 rows a thread).
-// Bound by reading and writing the state once.
+// Bound by reading and writing the state once; the tokens' rows are brought
+// into LDS together, and the waves' shares of the outputs meet there once for
+// all of them, so a draft pays the way to memory and the barriers once.
+template <class T> struct LinToken {   // LDS bytes of one token
+    static constexpr size_t bytes(int G, int dk) { return (size_t)(G + 1) * dk * sizeof(T) + 32 * 4 + 16 + (size_t)G * 512; }
+};
 template <class T, int DK>
-__global__ __launch_bounds__(256) void lin_token_kernel(LinArgs a) {
-    constexpr int R = DK / 32;
-    extern __shared__ float red[];   // [2][G][4 waves][32]
+__global__ __launch_bounds__(256) void lin_token_kernel(LinArgs a, int batch) {   // batch: tokens in LDS at a time
+    constexpr int R = DK / 32, VE = 16 / sizeof(T);
+    typedef T Vec __attribute__((ext_vector_type(VE)));
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int rows = (a.G + 1) * a.dk;                                   // queries, then the key
+    float* red = reinterpret_cast<float*>(lds);                          // [batch][G][4 waves][32]
+    float* vs = red + batch * a.G * 128;                                 // [batch][32]
+    float* keeps = vs + batch * 32;                                      // [batch], in 16 bytes each
+    T* qk = reinterpret_cast<T*>(keeps + 4 * batch);                     // [batch][rows]
     const int slab = blockIdx.x % a.slabs, bh = blockIdx.x / a.slabs, b = bh / a.Hk, h = bh % a.Hk;
-    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, wave = threadIdx.x >> 6, c = slab * 32 + 4 * cg;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, wave = threadIdx.x >> 6, c0 = slab * 32, c = c0 + 4 * cg;
     const bool on = c < a.dv;
     const int n = lin_tokens(a, b);
     f32x4 S[R];
@@ -634,50 +647,60 @@ __global__ __launch_bounds__(256) void lin_token_kernel(LinArgs a) {
         if (a.s_in && on && row < a.dk)
             S[i] = *reinterpret_cast<const f32x4*>(a.s_in + bh * a.s_in_bh + (long)row * a.dv + c);
     }
-    for (int t = 0; t < n; ++t) {
-        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + t * a.qt + (long)h * a.G * a.dk;
-        const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + t * a.kt + (long)h * a.dk;
-        const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + t * a.vt + (long)h * a.dv;
-        const float keep = expf(a.ld[a.per_token ? ((long)b * a.T + t) * a.Hk + h : h]);
-        f32x4 vv = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (on) {
-            struct __align__(4 * sizeof(T)) V4 { T e[4]; };
-            const V4 x = *reinterpret_cast<const V4*>(v + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vv[e] = (float)x.e[e];
+    for (int t0 = 0; t0 < n; t0 += batch) {
+        const int m = min(batch, n - t0), units = a.dk / VE;
+        if (t0 > 0) __syncthreads();
+        const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + t0 * a.qt + (long)h * a.G * a.dk;
+        const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + t0 * a.kt + (long)h * a.dk;
+        const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + t0 * a.vt + (long)h * a.dv + c0;
+        const int per = (a.G + 1) * units;
+        for (int i = threadIdx.x; i < m * per; i += 256) {
+            const int t = i / per, u = i % per;
+            const T* x = u < a.G * units ? q + t * a.qt + u * VE : k + t * a.kt + (u - a.G * units) * VE;
+            *reinterpret_cast<Vec*>(qk + t * rows + u * VE) = *reinterpret_cast<const Vec*>(x);
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = rg + 32 * i;
-            const float kr = row < a.dk ? (float)k[row] : 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][e] = fmaf(keep, S[i][e], kr * vv[e]);
+        for (int i = threadIdx.x; i < m * 32; i += 256) {
+            const int t = i >> 5, e = i & 31;
+            vs[i] = c0 + e < a.dv ? (float)v[t * a.vt + e] : 0.f;
         }
-        float* buf = red + (t & 1) * a.G * 128;
-        for (int g = 0; g < a.G; ++g) {
-            f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = threadIdx.x; t < m; t += 256)
+            keeps[4 * t] = expf(a.ld[a.per_token ? ((long)b * a.T + t0 + t) * a.Hk + h : h]);
+        __syncthreads();
+        for (int t = 0; t < m; ++t) {
+            const T* qr = qk + t * rows;
+            const T* kr = qr + a.G * a.dk;
+            const f32x4 vv = *reinterpret_cast<const f32x4*>(vs + t * 32 + 4 * cg);
+            const float keep = keeps[4 * t];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int row = rg + 32 * i;
-                if (row < a.dk) {
-                    const float qr = (float)q[(long)g * a.dk + row];
+                const float kv = row < a.dk ? (float)kr[row] : 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = fmaf(qr, S[i][e], y[e]);
-                }
+                for (int e = 0; e < 4; ++e) S[i][e] = fmaf(keep, S[i][e], kv * vv[e]);
             }
+            for (int g = 0; g < a.G; ++g) {
+                f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int m = 8; m < 64; m <<= 1)
+                for (int i = 0; i < R; ++i) {
+                    const int row = rg + 32 * i;
+                    const float qv = row < a.dk ? (float)qr[g * a.dk + row] : 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], m, 64);
-            if ((threadIdx.x & 63) < 8) *reinterpret_cast<f32x4*>(buf + (g * 4 + wave) * 32 + 4 * cg) = y;
+                    for (int e = 0; e < 4; ++e) y[e] = row < a.dk ? fmaf(qv, S[i][e], y[e]) : y[e];
+                }
+#pragma unroll
+                for (int s = 8; s < 64; s <<= 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], s, 64);
+                if ((threadIdx.x & 63) < 8) *reinterpret_cast<f32x4*>(red + ((t * a.G + g) * 4 + wave) * 32 + 4 * cg) = y;
+            }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < a.G * 32; i += 256) {
-            const int g = i >> 5, col = i & 31;
-            const float* p = buf + g * 128 + col;
+        for (int i = threadIdx.x; i < m * a.G * 32; i += 256) {
+            const int tg = i >> 5, col = i & 31, t = t0 + tg / a.G, g = tg % a.G;
+            const float* p = red + tg * 128 + col;
             const float y = ((p[0] + p[32]) + (p[64] + p[96])) * a.far_scale;
-            if (slab * 32 + col < a.dv)
-                reinterpret_cast<T*>(a.out)[(((long)b * a.T + t) * a.Hk * a.G + (long)h * a.G + g) * a.dv + slab * 32 + col] = (T)y;
+            if (c0 + col < a.dv)
+                reinterpret_cast<T*>(a.out)[(((long)b * a.T + t) * a.Hk * a.G + (long)h * a.G + g) * a.dv + c0 + col] = (T)y;
         }
     }
     if (a.s_out && on)
@@ -1043,14 +1066,21 @@ template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
     a.slabs = (a.dv + 31) / 32;
     const long blocks = (long)a.B * a.Hk * a.slabs;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
-    const size_t bytes = (size_t)a.G * 1024;
-    const dim3 grid((unsigned)blocks);
-    return timed_layer(st, [&] {
-        if (a.dk <= 64) launch_k((lin_token_kernel<T, 64>), grid, dim3(256), bytes, st, a);
-        else if (a.dk <= 128) launch_k((lin_token_kernel<T, 128>), grid, dim3(256), bytes, st, a);
-        else launch_k((lin_token_kernel<T, 256>), grid, dim3(256), bytes, st, a);
-        return hipGetLastError();
-    });
+    const size_t one = LinToken<T>::bytes(a.G, a.dk);
+    static_assert(LinToken<float>::bytes(64, 256) <= 160 * 1024, "LDS of a compute unit");
+    const int batch = (int)std::max<size_t>(1, std::min<size_t>(a.T, 40 * 1024 / one));
+    const size_t bytes = one * batch;
+    auto go = [&](auto kernel) {
+        if (bytes > 64 * 1024) {   // above the default dynamic LDS limit
+            const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            if (e != hipSuccess) return e;
+        }
+        return timed_layer(st, [&] {
+            launch_k(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, a, batch);
+            return hipGetLastError();
+        });
+    };
+    return a.dk <= 64 ? go(lin_token_kernel<T, 64>) : a.dk <= 128 ? go(lin_token_kernel<T, 128>) : go(lin_token_kernel<T, 256>);
 }
 
 // How a call is divided, and where its workspace holds what.
@@ -1062,6 +1092,7 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
     LinPlan p{};
+    if (B == 0 || T == 0) return p;
     const size_t bh = (size_t)B * Hk, cells = (size_t)dk * dv;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1083,7 +1114,7 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         p.h = take(bh * T * 4);
         p.sums = take(bh * ((T + 31) / 32) * 8);   // chunks of 32 tokens, or 64
         p.part = take(bh * p.nseg * 8);
-    } else if (T > 0 && B > 0) {
+    } else if (T > LIN_REC) {   // fewer tokens go token by token
         // the sequence is divided where its heads alone do not fill the chip
         const long cols = lin_columns(dk, dv), wgs = (long)bh * ((dv + cols - 1) / cols);
         long seg = wgs >= 256 || T <= 256 ? 1 : (512 + wgs - 1) / wgs;
@@ -1095,7 +1126,7 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
             p.gsum = take(bh * p.nseg * 8);
         }
     }
-    p.bytes = at < 256 ? 256 : at;
+    p.bytes = at;
     return p;
 }
 
@@ -1272,7 +1303,8 @@ tm_status tm_linear_attention(const void* q, long q_batch, long q_token, const v
     }
     if (!lin_tokens_ok(q, q_batch, q_token, batch, n_tokens) || !lin_tokens_ok(k, k_batch, k_token, batch, n_tokens) ||
         !lin_tokens_ok(v, v_batch, v_token, batch, n_tokens) || !out || (uintptr_t)out % 16 || !log_decay ||
-        (uintptr_t)log_decay % 4 || (uintptr_t)counts % 4 || !workspace || (uintptr_t)workspace % 256)
+        (uintptr_t)log_decay % 4 || (uintptr_t)counts % 4 || (uintptr_t)workspace % 256 ||
+        (!workspace && lin_plan(batch, n_tokens, kv_heads, key_dim, value_dim, false).bytes))
         return TM_ERR_INVALID;
     LinArgs a{};
     a.q = q; a.qb = q_batch; a.qt = q_token; a.k = k; a.kb = k_batch; a.kt = k_token; a.v = v; a.vb = v_batch; a.vt = v_token;

@@ -51,6 +51,13 @@ template <bool STREAM, class V> __device__ __forceinline__ void nput(V* p, V v) 
     }
 }
 
+// Workgroups from which a call's heads are divided no further: the sines and
+// cosines of a token are formed again for every division.  Forward, past the
+// caches: 2 x 8192 tokens of 40 heads of 128 take 78 us with 4096 (81 with
+// 2048, 88 with 16384); the gradients of 4 x 2047 tokens of 20 heads of 96
+// 37 us with 512 (48 with 256, 46 to 61 with 1024).
+constexpr int NORM_WGS = 1024, NORM_STREAM_WGS = 4096, NORM_BACK_WGS = 512;
+
 // A unit of a head vector.  Half layout: V pairs, elements c .. c + V - 1 and
 // r / 2 further on; interleaved: V / 2 pairs (one where V is 1); behind the
 // rotated elements V elements.
@@ -191,37 +198,48 @@ __global__ __launch_bounds__(256) void head_norm_kernel(NormArgs a, int lg) {
                 const int u = lane + i * lg, c = u < a.units ? element<V, HALF>(u, j, a) : -1;
                 w[i][j] = wp && c >= 0 ? wp[c] : 1.f;
             }
-#pragma unroll AHEAD
-        for (int h = from; h < to; ++h) {
-            float e[U][E], sum = 0.f;
+        for (int h = from; h < to; h += AHEAD) {   // AHEAD heads at a time: their loads are under way together
+            float e[AHEAD][U][E], sum[AHEAD];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int u = lane + i * lg;
-                if (u < a.units) {
-                    load_unit<T, V, HALF, STREAM>(x + (long)h * a.d, u, a, e[i]);
+            for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-                    for (int j = 0; j < E; ++j) sum += e[i][j] * e[i][j];
+                for (int i = 0; i < U; ++i) {
+                    const int u = lane + i * lg;
+                    if (u < a.units) load_unit<T, V, HALF, STREAM>(x + (long)min(h + k, to - 1) * a.d, u, a, e[k][i]);
                 }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                sum[k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (lane + i * lg < a.units)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) sum[k] += e[k][i][j] * e[k][i][j];
             }
-            for (int m = lg >> 1; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
-            const float r = 1.f / sqrtf(sum * inv_d + a.eps);
+            for (int m = lg >> 1; m > 0; m >>= 1)
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int u = lane + i * lg;
-                if (u < a.units) {
+                for (int k = 0; k < AHEAD; ++k) sum[k] += __shfl_xor(sum[k], m, 64);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) e[i][j] *= r * w[i][j];
-                    if (u < a.rot_units) turn<V, HALF, false>(e[i], cs[i], sn[i]);
-                    store_unit<T, V, HALF, STREAM>(y + (long)h * a.d, u, a, e[i]);
+            for (int k = 0; k < AHEAD; ++k) {
+                const float r = 1.f / sqrtf(sum[k] * inv_d + a.eps);
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int u = lane + i * lg;
+                    if (u < a.units && h + k < to) {
+#pragma unroll
+                        for (int j = 0; j < E; ++j) e[k][i][j] *= r * w[i][j];
+                        if (u < a.rot_units) turn<V, HALF, false>(e[k][i], cs[i], sn[i]);
+                        store_unit<T, V, HALF, STREAM>(y + (long)(h + k) * a.d, u, a, e[k][i]);
+                    }
                 }
             }
         }
     }
 }
 
-// The backward: a group of lanes takes all heads of a.tokens tokens, so that
-// the sums of dw stay in its registers; a workgroup adds its groups' sums
-// through LDS in their order and writes one partial sum.
+// The backward: a group of lanes takes some heads (blockIdx.y) of a.tokens
+// tokens, so that the sums of dw stay in its registers; a workgroup adds its
+// groups' sums through LDS in their order and writes one partial sum.
 template <class T, int V, bool HALF, int U, bool STREAM>
 __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int lg) {
     constexpr int E = Unit<V, HALF>::E, NP = Unit<V, HALF>::NP, AHEAD = U == 1 ? 2 : 1;
@@ -231,7 +249,8 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
     const long last = min(total, first + a.tokens);
     const float inv_d = 1.f / (float)a.d;
     for (int part = 0; part < (a.K ? 2 : 1); ++part) {   // queries, keys
-        const int from = part ? a.H : 0, to = part ? a.H + a.K : a.H;
+        const int h0 = blockIdx.y * a.hgroup, h1 = min(a.H + a.K, h0 + a.hgroup);
+        const int from = part ? max(h0, a.H) : h0, to = part ? h1 : min(h1, a.H);
         const float* wp = part ? a.wk : a.wq;
         float w[U][E], dw[U][E];
 #pragma unroll
@@ -242,7 +261,7 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
                 w[i][j] = wp && c >= 0 ? wp[c] : 1.f;
                 dw[i][j] = 0.f;
             }
-        for (long bt = first; bt < last; ++bt) {
+        for (long bt = first; bt < last && from < to; ++bt) {
             const int t = (int)(bt % a.T), b = (int)(bt / a.T);
             const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb + t * a.xt;
             const T* g = reinterpret_cast<const T*>(a.dy) + b * a.gb + t * a.gt;
@@ -251,39 +270,56 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
             float cs[U][NP], sn[U][NP];
 #pragma unroll
             for (int i = 0; i < U; ++i) angles<V, HALF>(lane + i * lg, p, a, cs[i], sn[i]);
-#pragma unroll AHEAD
-            for (int h = from; h < to; ++h) {
-                float e[U][E], n[U][E], sum = 0.f, dot = 0.f;
+            for (int h = from; h < to; h += AHEAD) {
+                float e[AHEAD][U][E], n[AHEAD][U][E], sum[AHEAD], dot[AHEAD];
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int u = lane + i * lg;
-                    if (u < a.units) {
-                        load_unit<T, V, HALF, STREAM>(x + (long)h * a.d, u, a, e[i]);
-                        load_unit<T, V, HALF, STREAM>(g + (long)h * a.d, u, a, n[i]);
-                        if (u < a.rot_units) turn<V, HALF, true>(n[i], cs[i], sn[i]);
+                for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            sum += e[i][j] * e[i][j];
-                            dot += e[i][j] * n[i][j] * w[i][j];
+                    for (int i = 0; i < U; ++i) {
+                        const int u = lane + i * lg;
+                        const long at = (long)min(h + k, to - 1) * a.d;
+                        if (u < a.units) {
+                            load_unit<T, V, HALF, STREAM>(x + at, u, a, e[k][i]);
+                            load_unit<T, V, HALF, STREAM>(g + at, u, a, n[k][i]);
+                        }
+                    }
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    sum[k] = dot[k] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int u = lane + i * lg;
+                        if (u < a.units) {
+                            if (u < a.rot_units) turn<V, HALF, true>(n[k][i], cs[i], sn[i]);
+#pragma unroll
+                            for (int j = 0; j < E; ++j) {
+                                sum[k] += e[k][i][j] * e[k][i][j];
+                                dot[k] += e[k][i][j] * n[k][i][j] * w[i][j];
+                            }
                         }
                     }
                 }
-                for (int m = lg >> 1; m > 0; m >>= 1) {
-                    sum += __shfl_xor(sum, m, 64);
-                    dot += __shfl_xor(dot, m, 64);
-                }
-                const float r = 1.f / sqrtf(sum * inv_d + a.eps), mean = dot * r * inv_d;
+                for (int m = lg >> 1; m > 0; m >>= 1)
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int u = lane + i * lg;
-                    if (u < a.units) {
+                    for (int k = 0; k < AHEAD; ++k) {
+                        sum[k] += __shfl_xor(sum[k], m, 64);
+                        dot[k] += __shfl_xor(dot[k], m, 64);
+                    }
 #pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            const float unit = e[i][j] * r;
-                            dw[i][j] += n[i][j] * unit;
-                            e[i][j] = r * (n[i][j] * w[i][j] - unit * mean);
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float r = 1.f / sqrtf(sum[k] * inv_d + a.eps), mean = dot[k] * r * inv_d;
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int u = lane + i * lg;
+                        if (u < a.units && h + k < to) {
+#pragma unroll
+                            for (int j = 0; j < E; ++j) {
+                                const float unit = e[k][i][j] * r;
+                                dw[i][j] += n[k][i][j] * unit;
+                                e[k][i][j] = r * (n[k][i][j] * w[i][j] - unit * mean);
+                            }
+                            store_unit<T, V, HALF, STREAM>(dx + (long)(h + k) * a.d, u, a, e[k][i]);
                         }
-                        store_unit<T, V, HALF, STREAM>(dx + (long)h * a.d, u, a, e[i]);
                     }
                 }
             }
@@ -300,26 +336,28 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
         for (int c = threadIdx.x; c < a.d; c += 256) {
             float s = 0.f;
             for (int k = 0; k < groups; ++k) s += red[k * a.d + c];
-            a.part[((long)blockIdx.x * 2 + part) * a.d + c] = s;
+            a.part[(((long)blockIdx.y * gridDim.x + blockIdx.x) * 2 + part) * a.d + c] = s;
         }
     }
 }
 
 // dw of queries (blockIdx.y 0) and keys (1): the workgroups' partial sums in
-// a fixed order, 16 elements a workgroup, 16 sums of each side by side.
-__global__ __launch_bounds__(256) void head_norm_dw_kernel(const float* part, int n, int d, float* dwq, float* dwk) {
-    __shared__ float red[256];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), k = threadIdx.x >> 4;
+// a fixed order, 8 elements a workgroup, 128 sums of each side by side.
+__global__ __launch_bounds__(1024) void head_norm_dw_kernel(const float* part, int n, int d, float* dwq, float* dwk) {
+    __shared__ float red[1024];
+    const int c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3;
     float* dw = blockIdx.y ? dwk : dwq;
     float s = 0.f;
     if (c < d && dw)
-        for (int i = k; i < n; i += 16) s += part[((long)i * 2 + blockIdx.y) * d + c];
+#pragma unroll 4
+        for (int i = k; i < n; i += 128) s += part[((long)i * 2 + blockIdx.y) * d + c];
     red[threadIdx.x] = s;
-    __syncthreads();
-    if (k == 0 && c < d && dw) {
-        for (int i = 1; i < 16; ++i) s += red[i * 16 + (threadIdx.x & 15)];
-        dw[c] = s;
+#pragma unroll
+    for (int m = 64; m > 0; m >>= 1) {
+        __syncthreads();
+        if (k < m) red[threadIdx.x] += red[threadIdx.x + 8 * m];
     }
+    if (k == 0 && c < d && dw) dw[c] = red[threadIdx.x];
 }
 
 __global__ void head_norm_zero_kernel(int d, float* dwq, float* dwk) {
@@ -336,7 +374,7 @@ static int pow2_up(int n) {
 }
 
 // Workgroups of the backward at most, each with a partial sum.
-constexpr int NORM_PARTS = 1024;
+constexpr int NORM_PARTS = 2048;
 
 template <class T, int V, bool HALF, int U>
 static hipError_t norm_launch(NormArgs a, int lg, bool back, int* parts, hipStream_t st) {
@@ -346,24 +384,29 @@ static hipError_t norm_launch(NormArgs a, int lg, bool back, int* parts, hipStre
                         tokens * (a.H + a.K) * a.d * (long)sizeof(T) * (back ? 3 : 2) > 256L << 20;
     if (back) {
         const long groups = (tokens + per - 1) / per;
-        a.tokens = (int)((groups + NORM_PARTS - 1) / NORM_PARTS);
+        a.tokens = (int)((groups + 1023) / 1024);
         const long blocks = (tokens + (long)per * a.tokens - 1) / ((long)per * a.tokens);
-        *parts = (int)blocks;
+        int parts_y = 1;
+        while (parts_y < a.H + a.K && blocks * parts_y < NORM_BACK_WGS) parts_y *= 2;   // at most NORM_PARTS with the last doubling
+        a.hgroup = (a.H + a.K + parts_y - 1) / parts_y;
+        parts_y = (a.H + a.K + a.hgroup - 1) / a.hgroup;
+        const dim3 grid((unsigned)blocks, (unsigned)parts_y);
+        *parts = (int)(blocks * parts_y);
         const size_t lds = (size_t)per * a.d * sizeof(float);
         if constexpr (V * sizeof(T) == 16) {
             if (stream) {
-                launch_k(head_norm_backward_kernel<T, V, HALF, U, true>, dim3((unsigned)blocks), dim3(256), lds, st, a, lg);
+                launch_k(head_norm_backward_kernel<T, V, HALF, U, true>, grid, dim3(256), lds, st, a, lg);
                 return hipGetLastError();
             }
         }
-        launch_k(head_norm_backward_kernel<T, V, HALF, U, false>, dim3((unsigned)blocks), dim3(256), lds, st, a, lg);
+        launch_k(head_norm_backward_kernel<T, V, HALF, U, false>, grid, dim3(256), lds, st, a, lg);
         return hipGetLastError();
     }
     const long blocks = (tokens + per - 1) / per;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
     const int heads = a.H + a.K;
     int groups = 1;
-    while (groups < heads && blocks * groups < (stream ? 16384 : 1024)) groups *= 2;
+    while (groups < heads && blocks * groups < (stream ? NORM_STREAM_WGS : NORM_WGS)) groups *= 2;
     a.hgroup = (heads + groups - 1) / groups;
     const dim3 grid((unsigned)blocks, (unsigned)((heads + a.hgroup - 1) / a.hgroup));
     if constexpr (V * sizeof(T) == 16) {
@@ -507,7 +550,7 @@ tm_status tm_head_norm_backward(const void* x, long x_batch, long x_token, const
     });
     if (e == hipSuccess && (dw_q || dwk))
         e = timed_layer(st, [&] {
-            launch_k(head_norm_dw_kernel, dim3((head_dim + 15) / 16, kv_heads ? 2 : 1), dim3(256), 0, st, a.part, parts,
+            launch_k(head_norm_dw_kernel, dim3((head_dim + 7) / 8, kv_heads ? 2 : 1), dim3(1024), 0, st, a.part, parts,
                      head_dim, dw_q, dwk);
             return hipGetLastError();
         });

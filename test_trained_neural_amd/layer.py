@@ -194,18 +194,19 @@ def tm_linear_attention(q, k, v, log_decay, out, scale, workspace, state_in=None
     if _elsewhere(index, stream):
         with _there(q.device, stream):
             return tm_linear_attention(q, k, v, log_decay, out, scale, workspace, state_in, state_out, counts)
-    T._blob("workspace", workspace, _linear_need(sizes, False))
-    _on(q.device, ("workspace", workspace))
+    _room(workspace, tm_linear_workspace_bytes(*sizes), q.device)
     rc = _lib().tm_linear_attention(*_tokens((("q", q), ("k", k), ("v", v)), dist), log_decay.data_ptr(), per_token,
                                     _at(counts), _at(state_in), _at(state_out), out.data_ptr(), scale, *sizes, dt,
-                                    workspace.data_ptr(), _raw_stream(index))
+                                    _at(workspace), _raw_stream(index))
     if rc:
         T._check("tm_linear_attention", rc)
 
 
-def _linear_need(sizes, backward):
-    """Workspace bytes of a call; 1 for sizes that it refuses."""
-    return _once(("linear_need", sizes, backward), lambda: tm_linear_workspace_bytes(*sizes, backward) or 1)
+def _room(workspace, need, device):
+    """A workspace holds what the call needs (None: where it needs nothing)."""
+    if need or workspace is not None:
+        T._blob("workspace", workspace, max(need, 1))
+        _on(device, ("workspace", workspace))
 
 
 def tm_linear_attention_backward(q, k, v, log_decay, dout, dq, dk, dv, scale, workspace, state_in=None,
@@ -226,12 +227,11 @@ def tm_linear_attention_backward(q, k, v, log_decay, dout, dq, dk, dv, scale, wo
         with _there(q.device, stream):
             return tm_linear_attention_backward(q, k, v, log_decay, dout, dq, dk, dv, scale, workspace, state_in,
                                                 dstate_out, dlog_decay, dstate_in, counts)
-    T._blob("workspace", workspace, _linear_need(sizes, True))
-    _on(q.device, ("workspace", workspace))
+    _room(workspace, tm_linear_workspace_bytes(*sizes, True), q.device)
     a = _tokens((("q", q), ("k", k), ("v", v), ("dout", dout)), dist)
     rc = _lib().tm_linear_attention_backward(*a[:9], log_decay.data_ptr(), per_token, _at(counts), _at(state_in),
                                              *a[9:], _at(dstate_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                             _at(dlog_decay), _at(dstate_in), scale, *sizes, dt, workspace.data_ptr(),
+                                             _at(dlog_decay), _at(dstate_in), scale, *sizes, dt, _at(workspace),
                                              _raw_stream(index))
     if rc:
         T._check("tm_linear_attention_backward", rc)
@@ -335,12 +335,13 @@ class HeadNorm:
         self.heads, self.kv_heads, self.w_q, self.w_k, self.eps, self.rotary = heads, kv_heads, w_q, w_k, eps, rotary
 
     def _rotation(self, positions):
+        """The rotation's part of a call: positions, freq, result_scale, layout."""
         r = self.rotary
         if r is None:   # positions are not read
-            return {}
+            return None, None, 1.0, TM_ROPE_HALF
         if positions is None:
             raise ValueError("positions are needed")
-        return {"positions": positions, "freq": r.freq, "result_scale": r.result_scale, "layout": r.layout}
+        return positions, r.freq, r.result_scale, r.layout
 
     def _weights(self):
         return self.w_q, self.w_k if self.kv_heads else None
@@ -351,8 +352,9 @@ class HeadNorm:
             with _there(x.device, stream):
                 return self(x, positions, out)
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        tm_head_norm(x, out, *self._weights(), self.heads, self.kv_heads, self.eps, **self._rotation(positions))
+            out = x.new_empty(x.shape)
+        tm_head_norm(x, out, self.w_q, self.w_k if self.kv_heads else None, self.heads, self.kv_heads, self.eps,
+                     *self._rotation(positions))
         return out
 
     def backward(self, x, dy, positions=None, dx=None, stream=None):
@@ -363,13 +365,13 @@ class HeadNorm:
             with _there(x.device, stream):
                 return self.backward(x, dy, positions, dx)
         if dx is None:
-            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+            dx = x.new_empty(x.shape)
         new = lambda: x.new_empty(x.shape[3], dtype=torch.float32)  # noqa: E731
         dw_q, dw_k = new(), new() if self.kv_heads else None
         ws = x.new_empty(tm_head_norm_workspace_bytes(*x.shape[:2], self.heads, self.kv_heads, x.shape[3]),
                          dtype=torch.uint8)
         tm_head_norm_backward(x, dy, dx, *self._weights(), dw_q, dw_k, self.heads, self.kv_heads, self.eps, ws,
-                              **self._rotation(positions))
+                              *self._rotation(positions))
         return dx, dw_q, dw_k
 
 
@@ -388,7 +390,7 @@ class LinearAttention:
         if kv_heads < 1 or not all(8 <= n <= 256 and n % 8 == 0 for n in (key_dim, value_dim)):
             raise ValueError("kv_heads must be positive, key_dim and value_dim multiples of 8 up to 256")
         self.kv_heads, self.key_dim, self.value_dim = kv_heads, key_dim, value_dim
-        self._scale = 1.0 / math.sqrt(key_dim)
+        self._scale, self._kind = 1.0 / math.sqrt(key_dim), ("linear", kv_heads, key_dim, value_dim)
 
     def init_state(self, batch, device="cuda"):
         return torch.zeros((batch, self.kv_heads, self.key_dim, self.value_dim), dtype=torch.float32, device=device)
@@ -410,15 +412,32 @@ class LinearAttention:
             _on(q.device, ("q", q))
             with _there(q.device, stream):
                 return self(q, k, v, log_decay, state, counts, scale, out, state_out)
-        sizes = self._sizes(q, k, v)
-        B, N, H, K, dk, dv = sizes
+        def check():
+            sizes = self._sizes(q, k, v)
+            B, N, H, K, dk, dv = sizes
+            dist, per_token, _, dt, index = _linear_geometry(
+                q, k, v, log_decay, counts, state, state_out, None, None, lambda z: (("out", out, (B, N, H, dv), q.dtype),))
+            return (dist[0], dist[1], dist[2], per_token, sizes, dt, index, (B, N, H, dv), (B, K, dk, dv),
+                    tm_linear_workspace_bytes(*sizes))
+
+        d_q, d_k, d_v, per_token, sizes, dt, index, shape, cells, need = _once(
+            (self._kind, _look(q), _look(k), _look(v), _look(log_decay), _look(state), _look(counts), _look(out),
+             _look(state_out)), check)
+        if _elsewhere(index, None):
+            with _there(q.device, None):
+                return self(q, k, v, log_decay, state, counts, scale, out, state_out)
         if out is None:
-            out = (torch.empty if counts is None else torch.zeros)((B, N, H, dv), dtype=q.dtype, device=q.device)
+            out = (q.new_empty if counts is None else q.new_zeros)(shape)
         if state_out is None:
-            state_out = torch.empty((B, K, dk, dv), dtype=torch.float32, device=q.device)
-        ws = torch.empty(_linear_need(sizes, False), dtype=torch.uint8, device=q.device)
-        tm_linear_attention(q, k, v, log_decay, out, self._scale if scale is None else scale, ws, state, state_out,
-                            counts)
+            state_out = log_decay.new_empty(cells)
+        ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        rc = _lib().tm_linear_attention(
+            _aligned("q", q.data_ptr()), *d_q, _aligned("k", k.data_ptr()), *d_k, _aligned("v", v.data_ptr()), *d_v,
+            log_decay.data_ptr(), per_token, _at(counts), _at(state), state_out.data_ptr(), out.data_ptr(),
+            self._scale if scale is None else scale, *sizes, dt,
+            _at(ws), _raw_stream(index))
+        if rc:
+            T._check("tm_linear_attention", rc)
         return out, state_out
 
     def backward(self, q, k, v, log_decay, dout, state=None, dstate=None, counts=None, scale=None, stream=None):
@@ -434,7 +453,8 @@ class LinearAttention:
         dq, dk, dv = (new(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
         dld = new(log_decay.shape, dtype=torch.float32, device=q.device)
         dstate_in = torch.empty((sizes[0],) + sizes[3:], dtype=torch.float32, device=q.device)
-        ws = torch.empty(_linear_need(sizes, True), dtype=torch.uint8, device=q.device)
+        need = tm_linear_workspace_bytes(*sizes, True)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         tm_linear_attention_backward(q, k, v, log_decay, dout, dq, dk, dv, self._scale if scale is None else scale, ws,
                                      state, dstate, dld, dstate_in, counts)
         return dq, dk, dv, dld, dstate_in

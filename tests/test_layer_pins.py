@@ -139,7 +139,7 @@ def test_head_norm_backward_refuses():
     assert f(*a) == T.TM_ERR_INVALID
 
 
-LIN = [P(0), 512, 128, P(0), 512, 128, P(0), 512, 128, P(0), 1, None, P(0), P(0), P(0), 1.0, 2, 4, 2, 2, 64, 64, T.TM_BF16, P(0), None]
+LIN = [P(0), 512, 128, P(0), 512, 128, P(0), 512, 128, P(0), 1, None, P(0), P(0), P(0), 1.0, 2, 4000, 2, 2, 64, 64, T.TM_BF16, P(0), None]
 
 
 @pytest.mark.parametrize("at,value", [
@@ -167,9 +167,10 @@ def test_linear_empty_calls_and_sizes():
     a = list(LIN)
     a[17], a[13] = 0, None
     assert L._lib().tm_linear_attention(*a) == T.TM_OK
-    for b, n in ((0, 0), (0, 5), (3, 0), (1, 1)):
-        assert T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64) == 256 and T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64, True) >= 256
-    assert T.tm_linear_workspace_bytes(2, 4, 2, 2, 64, 60) == 0 and T.tm_linear_workspace_bytes(2, 4, 3, 2, 64, 64) == 0
+    for b, n in ((0, 0), (0, 5), (3, 0), (1, 1), (5, 16)):
+        assert T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64) == 0
+        assert (T.tm_linear_workspace_bytes(b, n, 2, 2, 64, 64, True) > 0) == (b * n > 0)
+    assert T.tm_linear_workspace_bytes(2, 4000, 2, 2, 64, 60) == 0 and T.tm_linear_workspace_bytes(2, 4000, 3, 2, 64, 64) == 0
     assert 0 < T.tm_linear_workspace_bytes(2, 4096, 2, 2, 64, 64) < T.tm_linear_workspace_bytes(2, 4096, 2, 2, 64, 64, True)
 
 
