@@ -404,18 +404,14 @@ static hipError_t int8_quantize(const void* x, long x_row, signed char* codes, l
     });
 }
 
-template <class K> static hipError_t int8_lds(K kernel, size_t bytes) {
-    if (bytes <= 64 * 1024) return hipSuccess;   // the default dynamic LDS limit
-    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <class T, int BM, int BN, int WM, int WN> static hipError_t int8_tile(Int8Args g, hipStream_t st) {
     const long mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1L) / BN;
     if (mt * nt * (WM * WN) >= 1L << 26) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads
     g.mtiles = (int)mt;
     g.ntiles = (int)nt;
     const size_t bytes = 2 * (BM + BN) * 128;
-    const hipError_t e = int8_lds(int8_tile_kernel<T, BM, BN, WM, WN>, bytes);
+    static std::atomic<unsigned long long> done{0};
+    const hipError_t e = lds_limit((const void*)int8_tile_kernel<T, BM, BN, WM, WN>, bytes, done);
     if (e != hipSuccess) return e;
     return timed_layer(st, [&] {
         launch_k((int8_tile_kernel<T, BM, BN, WM, WN>), dim3((unsigned)(mt * nt)), dim3(WM * WN * 64), bytes, st, g);
@@ -428,7 +424,8 @@ template <class T, int MT, bool FUSED> static hipError_t int8_thin(const Int8Arg
     if (nb >= 1L << 23 || mb > 65535) return hipErrorInvalidValue;
     const size_t sums = 8 * MT * 16 * 17 * 4, codes = FUSED ? (size_t)g.M * ((g.code_row + 63) / 64 * 64 + 16) : 0;
     const size_t bytes = sums > codes ? sums : codes;
-    const hipError_t e = int8_lds(int8_thin_kernel<T, MT, FUSED>, bytes);
+    static std::atomic<unsigned long long> done{0};
+    const hipError_t e = lds_limit((const void*)int8_thin_kernel<T, MT, FUSED>, bytes, done);
     if (e != hipSuccess) return e;
     return timed_layer(st, [&] {
         launch_k((int8_thin_kernel<T, MT, FUSED>), dim3((unsigned)nb, (unsigned)mb), dim3(512), bytes, st, g);

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace tmk {
 
 // Event timing of launches (tm_timing_enable): while a timed call runs, its
@@ -533,6 +535,20 @@ template <class F> inline hipError_t timed_attn(hipStream_t st, F launch) {
 hipError_t timed_layer_call(hipStream_t st, hipError_t (*call)(void*), void* arg);
 template <class F> inline hipError_t timed_layer(hipStream_t st, F launch) {
     return timed_layer_call(st, [](void* f) { return (*static_cast<F*>(f))(); }, &launch);
+}
+
+// Dynamic LDS above the default limit of 64 KB: asked for once per kernel and
+// device (a bit of `done`, which belongs to the kernel).
+inline hipError_t lds_limit(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+    if (bytes <= 64 * 1024) return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 156 * 1024);   // and some static
+    if (e == hipSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ---- launchers (tm_project.hip) ----

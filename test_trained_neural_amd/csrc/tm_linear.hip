@@ -977,6 +977,8 @@ __global__ void lin_zero_kernel(float* p, int n) {
 // ---------------------------------------------------------------------------
 // launches
 
+#define LIN_TRY(x) do { const hipError_t e_ = (x); if (e_ != hipSuccess) return e_; } while (0)
+
 static int lin_width(int d) { return (d + 63) / 64 * 64; }
 
 template <class T, int DK, int CW, int KIND>
@@ -985,12 +987,9 @@ static hipError_t lin_run(LinArgs a, hipStream_t st) {
     const long blocks = (long)a.B * a.Hk * a.nseg * a.slabs;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
     constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
-    static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-    if (bytes > 64 * 1024) {   // above the default dynamic LDS limit
-        const hipError_t e = hipFuncSetAttribute((const void*)lin_kernel<T, DK, CW, KIND>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != hipSuccess) return e;
-    }
+    static_assert(bytes <= 156 * 1024, "LDS of a compute unit");
+    static std::atomic<unsigned long long> done{0};
+    LIN_TRY(lds_limit((const void*)lin_kernel<T, DK, CW, KIND>, bytes, done));
     return timed_layer(st, [&] {
         launch_k((lin_kernel<T, DK, CW, KIND>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
         return hipGetLastError();
@@ -1019,10 +1018,8 @@ template <class T, int DK, int CW, bool STATES> static hipError_t lin_many_run(L
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
     constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
     auto go = [&](auto kernel) {
-        if (bytes > 64 * 1024) {
-            const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-            if (e != hipSuccess) return e;
-        }
+        static std::atomic<unsigned long long> done{0};   // an instance of this function has one kernel
+        LIN_TRY(lds_limit((const void*)kernel, bytes, done));
         return timed_layer(st, [&] {
             launch_k(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, m);
             return hipGetLastError();
@@ -1045,12 +1042,9 @@ template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hip
     const long blocks = (long)a.B * a.Hk * a.chunks;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
     constexpr size_t bytes = 4 * sizeof(T) * C * (D + 16 / sizeof(T)) + 8 * 64 + 4 * 64;
-    static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-    if (bytes > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute((const void*)lin_pairs_kernel<T, D, C>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != hipSuccess) return e;
-    }
+    static_assert(bytes <= 156 * 1024, "LDS of a compute unit");
+    static std::atomic<unsigned long long> done{0};
+    LIN_TRY(lds_limit((const void*)lin_pairs_kernel<T, D, C>, bytes, done));
     return timed_layer(st, [&] {
         launch_k((lin_pairs_kernel<T, D, C>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
         return hipGetLastError();
@@ -1062,25 +1056,22 @@ template <class T> static hipError_t lin_pairs(const LinPairs& a, hipStream_t st
     return w >= 192 ? lin_pairs_run<T, 256, C>(a, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, st) : lin_pairs_run<T, 64, C>(a, st);
 }
 
-template <class T> static hipError_t lin_tokens_run(LinArgs a, hipStream_t st) {
+template <class T, int DK> static hipError_t lin_token_run(LinArgs a, hipStream_t st) {
     a.slabs = (a.dv + 31) / 32;
     const long blocks = (long)a.B * a.Hk * a.slabs;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
     const size_t one = LinToken<T>::bytes(a.G, a.dk);
-    static_assert(LinToken<float>::bytes(64, 256) <= 160 * 1024, "LDS of a compute unit");
+    static_assert(LinToken<float>::bytes(64, 256) <= 156 * 1024, "LDS of a compute unit");
     const int batch = (int)std::max<size_t>(1, std::min<size_t>(a.T, 40 * 1024 / one));
-    const size_t bytes = one * batch;
-    auto go = [&](auto kernel) {
-        if (bytes > 64 * 1024) {   // above the default dynamic LDS limit
-            const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-            if (e != hipSuccess) return e;
-        }
-        return timed_layer(st, [&] {
-            launch_k(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, a, batch);
-            return hipGetLastError();
-        });
-    };
-    return a.dk <= 64 ? go(lin_token_kernel<T, 64>) : a.dk <= 128 ? go(lin_token_kernel<T, 128>) : go(lin_token_kernel<T, 256>);
+    static std::atomic<unsigned long long> done{0};
+    LIN_TRY(lds_limit((const void*)lin_token_kernel<T, DK>, one * batch, done));
+    return timed_layer(st, [&] {
+        launch_k((lin_token_kernel<T, DK>), dim3((unsigned)blocks), dim3(256), one * batch, st, a, batch);
+        return hipGetLastError();
+    });
+}
+template <class T> static hipError_t lin_tokens_run(const LinArgs& a, hipStream_t st) {
+    return a.dk <= 64 ? lin_token_run<T, 64>(a, st) : a.dk <= 128 ? lin_token_run<T, 128>(a, st) : lin_token_run<T, 256>(a, st);
 }
 
 // How a call is divided, and where its workspace holds what.
@@ -1145,8 +1136,6 @@ static hipError_t lin_copy(const float* from, float* to, long n, hipStream_t st)
         return hipGetLastError();
     });
 }
-
-#define LIN_TRY(x) do { const hipError_t e_ = (x); if (e_ != hipSuccess) return e_; } while (0)
 
 template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, char* ws, hipStream_t st) {
     const long cells = (long)a.dk * a.dv;

@@ -326,13 +326,25 @@ class HeadNorm:
     """Norms of queries and keys for each head, with their rotary positions in
     the same pass: ``y = norm(x, positions)`` takes x
     [B][T][heads + kv_heads][d], a view of a projection's output for instance.
-    w_q, w_k: fp32 [d] (None: ones); rotary: a ``Rotary`` (None: no rotation, positions are not read).
-    ``backward(x, dy, positions)`` gives (dx, dw_q, dw_k) of the same call."""
+    w_q, w_k: fp32 [d] (None: ones; w_k is not read without key heads); rotary:
+    a ``Rotary`` (None: no rotation, positions are not read).
+    ``backward(x, dy, positions)`` gives (dx, dw_q, dw_k) of the same call.
+    The weights are read where they are at every call; other tensors in their
+    place need another ``HeadNorm``."""
 
     def __init__(self, heads, kv_heads=0, w_q=None, w_k=None, eps=1e-6, rotary=None):
         if heads < 1 or kv_heads < 0:
             raise ValueError("heads must be positive, kv_heads not negative")
+        w_k = w_k if kv_heads else None
+        d = next((w.shape[0] for w in (w_q, w_k) if w is not None), None)
+        for name, w in (("w_q", w_q), ("w_k", w_k)):
+            if w is not None:
+                _f32(w.device, (name, w, (d,)))
         self.heads, self.kv_heads, self.w_q, self.w_k, self.eps, self.rotary = heads, kv_heads, w_q, w_k, eps, rotary
+        # what a call's checks go by, beside its own tensors
+        self._kind = ("head_norm", heads, kv_heads, d, w_q is not None, w_k is not None,
+                      *(w.device for w in (w_q, w_k) if w is not None),
+                      None if rotary is None else (rotary.rot_dim, rotary.freq.device))
 
     def _rotation(self, positions):
         """The rotation's part of a call: positions, freq, result_scale, layout."""
@@ -343,18 +355,31 @@ class HeadNorm:
             raise ValueError("positions are needed")
         return positions, r.freq, r.result_scale, r.layout
 
-    def _weights(self):
-        return self.w_q, self.w_k if self.kv_heads else None
-
     def __call__(self, x, positions=None, out=None, stream=None):
         if stream is not None:
             _on(x.device, ("x", x))
             with _there(x.device, stream):
                 return self(x, positions, out)
+        positions, freq, result_scale, layout = self._rotation(positions)
+
+        def check():
+            y = x if out is None else out   # a new output is contiguous
+            dist, per_token, sizes, dt, index = _norm_geometry(x, y, self.w_q, self.w_k, positions, freq, self.heads,
+                                                               self.kv_heads)
+            B, N, H, d = x.shape
+            return dist[0], (N * H * d, H * d) if out is None else dist[1], per_token, sizes, dt, index
+
+        d_x, d_y, per_token, sizes, dt, index = _once((self._kind, _look(x), _look(positions), _look(out)), check)
+        if _elsewhere(index, None):
+            with _there(x.device, None):
+                return self(x, positions, out)
         if out is None:
             out = x.new_empty(x.shape)
-        tm_head_norm(x, out, self.w_q, self.w_k if self.kv_heads else None, self.heads, self.kv_heads, self.eps,
-                     *self._rotation(positions))
+        rc = _lib().tm_head_norm(x.data_ptr(), *d_x, out.data_ptr(), *d_y, _at(self.w_q), _at(self.w_k), self.eps,
+                                 _at(positions), per_token, _at(freq), result_scale, *sizes, layout, dt,
+                                 _raw_stream(index))
+        if rc:
+            T._check("tm_head_norm", rc)
         return out
 
     def backward(self, x, dy, positions=None, dx=None, stream=None):
@@ -370,7 +395,7 @@ class HeadNorm:
         dw_q, dw_k = new(), new() if self.kv_heads else None
         ws = x.new_empty(tm_head_norm_workspace_bytes(*x.shape[:2], self.heads, self.kv_heads, x.shape[3]),
                          dtype=torch.uint8)
-        tm_head_norm_backward(x, dy, dx, *self._weights(), dw_q, dw_k, self.heads, self.kv_heads, self.eps, ws,
+        tm_head_norm_backward(x, dy, dx, self.w_q, self.w_k, dw_q, dw_k, self.heads, self.kv_heads, self.eps, ws,
                               *self._rotation(positions))
         return dx, dw_q, dw_k
 
@@ -448,15 +473,29 @@ class LinearAttention:
             _on(q.device, ("q", q))
             with _there(q.device, stream):
                 return self.backward(q, k, v, log_decay, dout, state, dstate, counts, scale)
-        sizes = self._sizes(q, k, v)
-        new = torch.empty if counts is None else torch.zeros
-        dq, dk, dv = (new(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
-        dld = new(log_decay.shape, dtype=torch.float32, device=q.device)
-        dstate_in = torch.empty((sizes[0],) + sizes[3:], dtype=torch.float32, device=q.device)
-        need = tm_linear_workspace_bytes(*sizes, True)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        tm_linear_attention_backward(q, k, v, log_decay, dout, dq, dk, dv, self._scale if scale is None else scale, ws,
-                                     state, dstate, dld, dstate_in, counts)
+        def check():
+            sizes = self._sizes(q, k, v)
+            dist, per_token, _, dt, index = _linear_geometry(q, k, v, log_decay, counts, state, None, dout, dstate,
+                                                             lambda z: ())
+            return dist, per_token, sizes, dt, index, tm_linear_workspace_bytes(*sizes, True)
+
+        (d_q, d_k, d_v, d_o), per_token, sizes, dt, index, need = _once(
+            (self._kind, "backward", _look(q), _look(k), _look(v), _look(log_decay), _look(dout), _look(state),
+             _look(dstate), _look(counts)), check)
+        if _elsewhere(index, None):
+            with _there(q.device, None):
+                return self.backward(q, k, v, log_decay, dout, state, dstate, counts, scale)
+        new = torch.Tensor.new_empty if counts is None else torch.Tensor.new_zeros
+        dq, dk, dv, dld = (new(t, t.shape) for t in (q, k, v, log_decay))
+        dstate_in = log_decay.new_empty((sizes[0],) + sizes[3:])
+        ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        rc = _lib().tm_linear_attention_backward(
+            _aligned("q", q.data_ptr()), *d_q, _aligned("k", k.data_ptr()), *d_k, _aligned("v", v.data_ptr()), *d_v,
+            log_decay.data_ptr(), per_token, _at(counts), _at(state), _aligned("dout", dout.data_ptr()), *d_o, _at(dstate),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dld.data_ptr(), dstate_in.data_ptr(),
+            self._scale if scale is None else scale, *sizes, dt, _at(ws), _raw_stream(index))
+        if rc:
+            T._check("tm_linear_attention_backward", rc)
         return dq, dk, dv, dld, dstate_in
 
 
@@ -481,7 +520,9 @@ class Int8Linear:
         wide = _codes_of("codes", codes, scales, codes.shape[0], cols)
         if wide - cols >= 16:
             raise ValueError("codes of %d columns for cols %d" % (wide, cols))
+        _on(codes.device, ("scales", scales))
         self.codes, self.scales, self.cols, self.outs = codes, scales, cols, codes.shape[0]
+        self._kind = ("int8_linear", codes.shape, cols, codes.device)   # what a call's checks go by, beside x and out
 
     @property
     def shape(self):
@@ -492,20 +533,44 @@ class Int8Linear:
         return self.codes.device
 
     def __call__(self, x, out=None, stream=None):
+        """x [..][cols]; out: [..][outs], contiguous, or 2-d with contiguous
+        rows (x being 2-d then)."""
         if stream is not None:
             _on(x.device, ("x", x))
             with _there(x.device, stream):
                 return self(x, out)
-        if x.shape[-1] != self.cols:
-            raise ValueError("x has %d columns, the weight %d" % (x.shape[-1], self.cols))
-        rows = x if x.dim() == 2 else x.reshape(-1, self.cols)
+
+        def check():
+            _on(self.codes.device, ("x", x), ("out", out))
+            dt = T._dtype_code(x)
+            if x.dim() < 1 or x.shape[-1] != self.cols:
+                raise ValueError("x is %s, the weight has %d columns" % (tuple(x.shape), self.cols))
+            shape = x.shape[:-1] + (self.outs,)
+            rows = math.prod(x.shape[:-1])
+            x_row = _rows_of("x", x)[2] if x.dim() == 2 else self.cols
+            y_row = self.outs
+            if out is not None:
+                T._same(x.dtype, ("out", out))
+                T._shape("out", out, shape)
+                if out.dim() == 2:
+                    y_row = _rows_of("out", out)[2]
+                elif not out.is_contiguous():
+                    raise ValueError("out must be contiguous")
+            return (x.dim() != 2 and not x.is_contiguous(), shape, x_row, y_row, (rows, _int(self.outs), self.cols), dt,
+                    x.device.index, tm_int8_workspace_bytes(rows, self.cols))
+
+        copy, shape, x_row, y_row, sizes, dt, index, need = _once((self._kind, _look(x), _look(out)), check)
+        if _elsewhere(index, None):
+            with _there(x.device, None):
+                return self(x, out)
+        if copy:
+            x = x.contiguous()
         if out is None:
-            out = x.new_empty(x.shape[:-1] + (self.outs,))
-        elif out.dim() != 2:
-            T._shape("out", out, x.shape[:-1] + (self.outs,))
-            if not out.is_contiguous():
-                raise ValueError("out must be contiguous")
-        ws = x.new_empty(_once(("int8_need", rows.shape), lambda: tm_int8_workspace_bytes(*rows.shape) or 1),
-                         dtype=torch.uint8)
-        tm_int8_linear(rows, self.codes, self.scales, out if out.dim() == 2 else out.view(-1, self.outs), ws)
+            out = x.new_empty(shape)
+        ws = x.new_empty(need, dtype=torch.uint8)
+        codes = self.codes
+        rc = _lib().tm_int8_linear(x.data_ptr(), x_row, codes.data_ptr(), self.scales.data_ptr(), codes.shape[1],
+                                   out.data_ptr(), y_row, *sizes, dt, ws.data_ptr(), _raw_stream(index))
+        if rc:
+            T._check("tm_int8_linear", rc)
         return out
