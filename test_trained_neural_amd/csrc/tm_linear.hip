@@ -757,16 +757,21 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinScan states, LinScan g
     else lin_scan<true>(grads);
 }
 
-// <R, S> at the end of every segment.
-__global__ __launch_bounds__(256) void lin_flow_kernel(const float* S, const float* R, double* flow, int nseg,
-                                                       int slots, int cells) {
+// <R, S> at the end of a segment.
+struct LinFlow {
+    const float *S, *R;   // the borders' states and their gradients
+    double* flow;         // [batch * key heads][nseg]
+    int nseg, slots, cells;
+};
+__device__ __forceinline__ void lin_flow(const LinFlow& f, int block) {
     __shared__ double red[4];
-    const long bh = blockIdx.x / nseg;
-    const int seg = blockIdx.x % nseg;
-    const float* s = S + (bh * slots + seg + 1) * cells;
-    const float* r = R + (bh * slots + seg) * cells;
+    const long bh = block / f.nseg;
+    const int seg = block % f.nseg;
+    const float* s = f.S + (bh * f.slots + seg + 1) * f.cells;
+    const float* r = f.R + (bh * f.slots + seg) * f.cells;
     double d = 0.0;
-    for (int i = threadIdx.x * 4; i < cells; i += 1024) {
+#pragma unroll 4
+    for (int i = threadIdx.x * 4; i < f.cells; i += 1024) {
         const f32x4 x = *reinterpret_cast<const f32x4*>(s + i), y = *reinterpret_cast<const f32x4*>(r + i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) d = fma((double)x[e], (double)y[e], d);
@@ -775,7 +780,7 @@ __global__ __launch_bounds__(256) void lin_flow_kernel(const float* S, const flo
     for (int m = 32; m > 0; m >>= 1) d += __shfl_xor(d, m, 64);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = d;
     __syncthreads();
-    if (threadIdx.x == 0) flow[bh * nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
+    if (threadIdx.x == 0) f.flow[bh * f.nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 // Rows t0 .. of a token array into LDS, zeros behind the last and behind its
@@ -801,7 +806,8 @@ struct LinPairs {
     int per_token, B, T, Hk, G, dk, dv, chunks, slabs;
 };
 template <class T, int D, int C>
-__global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
+__global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, int flows) {
+    if ((int)blockIdx.x < flows) return lin_flow(f, blockIdx.x);   // a whole workgroup
     constexpr int PAD = 16 / sizeof(T), RP = D + PAD, NT = C / 16, NS = D / 32, XP = C + 1;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     T* qs = reinterpret_cast<T*>(lds);
@@ -812,7 +818,7 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a) {
     float* cross = reinterpret_cast<float*>(gs + 64);   // [64]
     float* X = reinterpret_cast<float*>(lds);           // [C][XP], in the operands' place once they are read
     static_assert(4 * C * XP <= 4 * (int)sizeof(T) * C * RP, "X fits in the operands' place");
-    const int chunk = blockIdx.x % a.chunks, bh = blockIdx.x / a.chunks, b = bh / a.Hk, h = bh % a.Hk;
+    const int block = blockIdx.x - flows, chunk = block % a.chunks, bh = block / a.chunks, b = bh / a.Hk, h = bh % a.Hk;
     const int n = a.counts ? min(max(a.counts[b], 0), a.T) : a.T, t0 = chunk * C;
     if (t0 >= n) return;
     const int rows = min(C, n - t0);
@@ -1037,23 +1043,23 @@ template <class T, bool STATES> static hipError_t lin_many(const LinMany& m, int
 }
 static int lin_many_columns(int wide) { return lin_width(wide) == 128 ? 128 : 64; }
 
-template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, hipStream_t st) {
+template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, const LinFlow& f, hipStream_t st) {
     a.chunks = (a.T + C - 1) / C;
-    const long blocks = (long)a.B * a.Hk * a.chunks;
+    const long flows = (long)a.B * a.Hk * f.nseg, blocks = flows + (long)a.B * a.Hk * a.chunks;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
     constexpr size_t bytes = 4 * sizeof(T) * C * (D + 16 / sizeof(T)) + 8 * 64 + 4 * 64;
     static_assert(bytes <= 156 * 1024, "LDS of a compute unit");
     static std::atomic<unsigned long long> done{0};
     LIN_TRY(lds_limit((const void*)lin_pairs_kernel<T, D, C>, bytes, done));
     return timed_layer(st, [&] {
-        launch_k((lin_pairs_kernel<T, D, C>), dim3((unsigned)blocks), dim3(256), bytes, st, a);
+        launch_k((lin_pairs_kernel<T, D, C>), dim3((unsigned)blocks), dim3(256), bytes, st, a, f, (int)flows);
         return hipGetLastError();
     });
 }
-template <class T> static hipError_t lin_pairs(const LinPairs& a, hipStream_t st) {
+template <class T> static hipError_t lin_pairs(const LinPairs& a, const LinFlow& f, hipStream_t st) {
     const int w = lin_width(a.dk > a.dv ? a.dk : a.dv);
     constexpr int C = lin_chunk<T>();
-    return w >= 192 ? lin_pairs_run<T, 256, C>(a, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, st) : lin_pairs_run<T, 64, C>(a, st);
+    return w >= 192 ? lin_pairs_run<T, 256, C>(a, f, st) : w == 128 ? lin_pairs_run<T, 128, C>(a, f, st) : lin_pairs_run<T, 64, C>(a, f, st);
 }
 
 template <class T, int DK> static hipError_t lin_token_run(LinArgs a, hipStream_t st) {
@@ -1227,16 +1233,12 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     LIN_TRY((lin_many<T, false>(LinMany{{w, y, x}, {}}, wide, st)));
     if (!g.dld) return hipSuccess;
     // the decays
-    LIN_TRY(timed_layer(st, [&] {
-        launch_k(lin_flow_kernel, dim3((unsigned)(bh * p.nseg)), dim3(256), 0, st, S, R, flow, p.nseg, slots, (int)cells);
-        return hipGetLastError();
-    }));
     float* h = reinterpret_cast<float*>(ws + p.h);
     double* part = reinterpret_cast<double*>(ws + p.part);
     float* sums = reinterpret_cast<float*>(ws + p.sums);
     LinPairs pairs{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
                scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_many_columns(wide) - 1) / lin_many_columns(wide)};
-    LIN_TRY(lin_pairs<T>(pairs, st));
+    LIN_TRY(lin_pairs<T>(pairs, LinFlow{S, R, flow, p.nseg, slots, (int)cells}, st));
     LIN_TRY(timed_layer(st, [&] {
         launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.counts, g.dld,
                  part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk<T>());

@@ -320,6 +320,17 @@ def tm_int8_linear(x, w, w_scales, y, workspace, stream=None):
         T._check("tm_int8_linear", rc)
 
 
+def _zeros_like(*ts):
+    """Contiguous tensors of zeros of the given ones' shapes and types, in one
+    piece of memory (one fill), each 16-byte aligned."""
+    at, places = 0, []
+    for t in ts:
+        places.append((at, at + T._nbytes(t)))
+        at = -(-places[-1][1] // 16) * 16
+    whole = ts[0].new_zeros(at, dtype=torch.uint8)
+    return [whole[a:b].view(t.dtype).view(t.shape) for t, (a, b) in zip(ts, places)]
+
+
 # ---------------------------------------------------------------------------
 
 class HeadNorm:
@@ -485,8 +496,10 @@ class LinearAttention:
         if _elsewhere(index, None):
             with _there(q.device, None):
                 return self.backward(q, k, v, log_decay, dout, state, dstate, counts, scale)
-        new = torch.Tensor.new_empty if counts is None else torch.Tensor.new_zeros
-        dq, dk, dv, dld = (new(t, t.shape) for t in (q, k, v, log_decay))
+        if counts is None:
+            dq, dk, dv, dld = (t.new_empty(t.shape) for t in (q, k, v, log_decay))
+        else:
+            dq, dk, dv, dld = _zeros_like(q, k, v, log_decay)
         dstate_in = log_decay.new_empty((sizes[0],) + sizes[3:])
         ws = q.new_empty(need, dtype=torch.uint8) if need else None
         rc = _lib().tm_linear_attention_backward(
