@@ -476,7 +476,7 @@ def mac_segment(mem, state, x, persistent, attention, w_kvq, conv, w_gate, gate_
     marshalling over the C calls).  x [B][S][D] (D = heads * dim; S a
     multiple of the chunk) is the segment's model vectors; ``attention`` is
     the caller's: window [B][P+2S][D] (x's dtype) -> y [B][S][D] for the
-    segment's positions, x's dtype (``WindowAttention`` is one).  The segment's queries (projections of x)
+    segment's positions, x's dtype (``WindowAttention`` and ``LinearWindow`` are).  The segment's queries (projections of x)
     read the memory before the segment is written; y is written (its keys,
     values and gates from the same projections) and read back through its
     queries to gate y.  Returns (out [B][S][D] fp32, state).  hist_x, hist_y:
@@ -583,7 +583,7 @@ from .attention import (TM_CACHE_BAD_ENTRY, TM_CACHE_BLOCK, TM_CACHE_FULL, TM_CA
                         tm_rotary, tm_rotary_frequencies)
 
 # a layer's operators beside the memory (include/tm_layer.h)
-from .layer import (HeadNorm, Int8Linear, LinearAttention, tm_head_norm, tm_head_norm_backward,  # noqa: E402,F401
-                    tm_head_norm_workspace_bytes, tm_int8_linear, tm_int8_matmul, tm_int8_quantize,
+from .layer import (HeadNorm, Int8Linear, LinearAttention, LinearWindow, tm_head_norm,  # noqa: E402,F401
+                    tm_head_norm_backward, tm_head_norm_workspace_bytes, tm_int8_linear, tm_int8_matmul, tm_int8_quantize,
                     tm_int8_workspace_bytes, tm_linear_attention, tm_linear_attention_backward,
                     tm_linear_workspace_bytes)

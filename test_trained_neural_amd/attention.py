@@ -454,6 +454,27 @@ class PagedCache:
         return int(f.value), int(n.value)
 
 
+def _product(x, w):
+    """x times a weight of PyTorch's Linear layout, or an ``Int8Linear``."""
+    return torch.nn.functional.linear(x, w) if isinstance(w, torch.Tensor) else w(x)
+
+
+def _layer_weights(w_qkv, w_out, heads, kv_heads, norm, dtype):
+    """(D, d, the vectors' type) of a layer's two projections, and their checks."""
+    D, d = w_out.shape[0], w_out.shape[1] // heads
+    for name, w, shape in (("w_out", w_out, (D, heads * d)), ("w_qkv", w_qkv, ((heads + 2 * kv_heads) * d, D))):
+        if tuple(w.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(w.shape)))
+    plain = [w for w in (w_qkv, w_out) if isinstance(w, torch.Tensor)]
+    dtype = dtype or (plain[0].dtype if plain else torch.bfloat16)
+    for w in plain:
+        T._same(dtype, ("the weights", w))
+    if norm is not None and (norm.heads, norm.kv_heads) != (heads, kv_heads):
+        raise ValueError("the norm is for %d and %d heads, the layer has %d and %d"
+                         % (norm.heads, norm.kv_heads, heads, kv_heads))
+    return D, d, dtype
+
+
 class WindowAttention:
     """The attention of ``mac_segment``'s window, for whole segments and for
     the single tokens that follow: grouped-query attention with rotary
@@ -461,7 +482,10 @@ class WindowAttention:
 
     w_qkv [(heads + 2 kv_heads) d][D] and w_out [D][heads d] (PyTorch's Linear
     layout, bf16 or fp32) project the window's vectors and the result; the
-    projections are plain products.  ``persistent`` [P][D] are the window's
+    projections are plain products, or 8-bit ones where a weight is an
+    ``Int8Linear`` (the vectors are then of ``dtype``, bf16 by default).
+    ``norm`` (a ``HeadNorm`` of these heads) norms queries and keys, with the
+    rotary positions it has in the same pass.  ``persistent`` [P][D] are the window's
     first rows, the same for every sequence and segment: their keys and
     values are written once, into a sequence of their own that each segment's
     sequences fork, so they share its pages.  ``batch`` sequences of up to
@@ -477,17 +501,19 @@ class WindowAttention:
     held are counted on the host, so these calls are not for capture into a
     graph (the cache's own are)."""
 
-    def __init__(self, w_qkv, w_out, heads, kv_heads, batch, max_tokens, persistent=None, rotary=None):
-        D, d = w_out.shape[0], w_out.shape[1] // heads
-        T._shape("w_out", w_out, (D, heads * d))
-        T._shape("w_qkv", w_qkv, ((heads + 2 * kv_heads) * d, D))
-        T._same(w_qkv.dtype, ("w_out", w_out), ("persistent", persistent))
+    def __init__(self, w_qkv, w_out, heads, kv_heads, batch, max_tokens, persistent=None, rotary=None, norm=None,
+                 dtype=None):
+        D, d, self.dtype = _layer_weights(w_qkv, w_out, heads, kv_heads, norm, dtype)
+        T._same(self.dtype, ("persistent", persistent))
+        if norm is not None and rotary is not None:
+            raise ValueError("with a norm, the rotary positions are the norm's")
         self.P = 0 if persistent is None else persistent.shape[0]
         T._shape("persistent", persistent, (self.P, D))
         if max_tokens < 1 or batch < 1:
             raise ValueError("batch and max_tokens must be positive")
         self.w_qkv, self.w_out, self.heads, self.kv_heads, self.head_dim = w_qkv, w_out, heads, kv_heads, d
         self.batch, self.max_tokens, self.rotary, self.persistent = batch, max_tokens, rotary, persistent
+        self.norm = norm
         dev = w_qkv.device
         up = lambda n: -(-n // TM_CACHE_PAGE)  # noqa: E731
         pages = up(self.P + max_tokens)
@@ -514,22 +540,25 @@ class WindowAttention:
         """Queries, keys (both rotated) and values of vectors that stand at
         ``start`` .. of their windows: views of one projection."""
         B, n, _ = x.shape
-        qkv = torch.nn.functional.linear(x, self.w_qkv).view(B, n, self.heads + 2 * self.kv_heads, self.head_dim)
+        qkv = _product(x, self.w_qkv).view(B, n, self.heads + 2 * self.kv_heads, self.head_dim)
         q_k = qkv[:, :, :self.heads + self.kv_heads]
-        if self.rotary is not None:
-            first = torch.full((B,), start, dtype=torch.int32, device=x.device)
-            self.rotary(q_k, first, out=q_k)
+        turn = self.rotary if self.norm is None else self.norm.rotary
+        first = None if turn is None else torch.full((B,), start, dtype=torch.int32, device=x.device)
+        if self.norm is not None:
+            self.norm(q_k, first, out=q_k)
+        elif turn is not None:
+            turn(q_k, first, out=q_k)
         return qkv[:, :, :self.heads], qkv[:, :, self.heads:self.heads + self.kv_heads], \
             qkv[:, :, self.heads + self.kv_heads:]
 
     def _read(self, q):
         y = self.cache.attend(self._slots, q, max_len=self._held)
-        return torch.nn.functional.linear(y.flatten(2), self.w_out)
+        return _product(y.flatten(2), self.w_out)
 
     def _room(self, x, n, held):
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("WindowAttention counts its tokens on the host: it cannot be captured into a graph")
-        T._same(self.w_qkv.dtype, ("the window", x))
+        T._same(self.dtype, ("the window", x))
         _on(self.cache.device, ("the window", x))
         if x.dim() != 3 or x.shape[0] != self.batch or x.shape[2] != self.w_qkv.shape[1]:
             raise ValueError("expected [%d][tokens][%d], got %s" % (self.batch, self.w_qkv.shape[1], tuple(x.shape)))

@@ -21,8 +21,8 @@ import math
 import torch
 
 import test_trained_neural_amd as T
-from .attention import (TM_ROPE_HALF, _aligned, _at, _elsewhere, _heads_of, _int, _list, _look, _on, _once, _raw_stream,
-                        _there)
+from .attention import (TM_ROPE_HALF, _aligned, _at, _elsewhere, _heads_of, _int, _layer_weights, _list, _look, _on, _once,
+                        _product, _raw_stream, _there)
 
 EXPORTED = ("tm_head_norm", "tm_head_norm_workspace_bytes", "tm_head_norm_backward", "tm_linear_attention",
             "tm_linear_workspace_bytes", "tm_linear_attention_backward", "tm_int8_quantize", "tm_int8_matmul",
@@ -587,3 +587,102 @@ class Int8Linear:
         if rc:
             T._check("tm_int8_linear", rc)
         return out
+
+
+class LinearWindow:
+    """Linear attention as the attention of ``mac_segment``'s window and of
+    the single tokens that follow, with a state in the place of
+    ``WindowAttention``'s cache: it does not grow with what was read.
+
+    w_qkv [(heads + 2 kv_heads) d][D], w_out [D][heads d], ``persistent``
+    [P][D], ``norm`` and ``dtype`` as ``WindowAttention``'s (the norm's rotary
+    positions count on from the window's first row).  What a token keeps of the
+    past: ``log_decay`` fp32 [kv_heads], or a gate, the logarithm of
+    sigmoid(x w_gate' + gate_bias), with w_gate [kv_heads][D] of the vectors'
+    type and gate_bias fp32 [kv_heads] (None: zeros).
+
+    ``attention(window)`` takes [B][P + 2 S][D] (its first P rows are
+    ``persistent``, whose state is kept) and returns the output [B][S][D] for
+    the segment's S rows; ``attention.token(x)`` takes the next vectors
+    [B][n][D] and returns theirs.  Nothing is recorded for gradients.  The
+    tokens are counted on the host: not for capture into a graph
+    (``LinearAttention`` itself is)."""
+
+    def __init__(self, w_qkv, w_out, heads, kv_heads, batch, log_decay=None, w_gate=None, gate_bias=None,
+                 persistent=None, norm=None, dtype=None):
+        D, d, self.dtype = _layer_weights(w_qkv, w_out, heads, kv_heads, norm, dtype)
+        T._same(self.dtype, ("persistent", persistent), ("w_gate", w_gate))
+        if (log_decay is None) == (w_gate is None):
+            raise ValueError("either log_decay or w_gate")
+        if batch < 1:
+            raise ValueError("batch must be positive")
+        dev = w_qkv.device
+        self.P = 0 if persistent is None else persistent.shape[0]
+        T._shape("persistent", persistent, (self.P, D))
+        T._shape("w_gate", w_gate, (kv_heads, D))
+        _f32(dev, ("log_decay", log_decay, (kv_heads,)), ("gate_bias", gate_bias, (kv_heads,)))
+        self.w_qkv, self.w_out, self.heads, self.kv_heads, self.head_dim, self.D = w_qkv, w_out, heads, kv_heads, d, D
+        self.log_decay, self.w_gate, self.gate_bias = log_decay, w_gate, gate_bias
+        self.batch, self.persistent, self.norm, self.device = batch, persistent, norm, dev
+        self.memory = LinearAttention(kv_heads, d)
+        self.refresh()
+
+    @torch.no_grad()
+    def refresh(self):
+        """Starts over with the weights and persistent rows as they are now."""
+        self.state = self._root = self.memory.init_state(self.batch, self.device)
+        self._held = 0
+        if self.P:
+            rows = self.persistent[None].expand(self.batch, -1, -1)
+            self._root = self._read(rows)[1]
+        self.state, self._held = self._root.clone(), self.P
+
+    def _read(self, x, out_state=None):
+        """(outputs before w_out, state) of vectors behind the held ones."""
+        B, n, _ = x.shape
+        qkv = _product(x, self.w_qkv).view(B, n, self.heads + 2 * self.kv_heads, self.head_dim)
+        q_k = qkv[:, :, :self.heads + self.kv_heads]
+        if self.norm is not None:
+            first = torch.full((B,), self._held, dtype=torch.int32, device=x.device)
+            self.norm(q_k, first, out=q_k)
+        g = self.log_decay
+        if g is None:
+            g = torch.nn.functional.linear(x, self.w_gate).float()
+            g = torch.nn.functional.logsigmoid(g if self.gate_bias is None else g + self.gate_bias)
+        return self.memory(qkv[:, :, :self.heads], qkv[:, :, self.heads:self.heads + self.kv_heads],
+                           qkv[:, :, self.heads + self.kv_heads:], g, state=self.state, state_out=out_state)
+
+    def _check(self, x):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("LinearWindow counts its tokens on the host: it cannot be captured into a graph")
+        T._same(self.dtype, ("the window", x))
+        _on(self.device, ("the window", x))
+        if x.dim() != 3 or x.shape[0] != self.batch or x.shape[2] != self.D:
+            raise ValueError("expected [%d][tokens][%d], got %s" % (self.batch, self.D, tuple(x.shape)))
+
+    @torch.no_grad()
+    def __call__(self, window):
+        self._check(window)
+        n = window.shape[1] - self.P
+        if n < 2 or n % 2:
+            raise ValueError("a window holds %d persistent rows and as many recalled as segment rows, got %d rows"
+                             % (self.P, window.shape[1]))
+        state, held = self.state, self._held
+        self.state, self._held = self._root, self.P
+        try:
+            y, self.state = self._read(window[:, self.P:])
+        except Exception:   # what was read before is still there
+            self.state, self._held = state, held
+            raise
+        self._held = self.P + n
+        return _product(y[:, n // 2:].flatten(2), self.w_out)
+
+    @torch.no_grad()
+    def token(self, x):
+        self._check(x)
+        n = x.shape[1]
+        if n < 1:
+            raise ValueError("no tokens")
+        y, _ = self._read(x, self.state)   # in place
+        self._held += n
+        return _product(y.flatten(2), self.w_out)
