@@ -783,15 +783,6 @@ __device__ __forceinline__ void lin_flow(const LinFlow& f, int block) {
     if (threadIdx.x == 0) f.flow[bh * f.nseg + seg] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// Rows t0 .. of a token array into LDS, zeros behind the last and behind its
-// columns.
-template <class T, int D, int C, int RP>
-__device__ __forceinline__ void lin_stage(const T* x, long step, int t0, int rows, int cols, T* to) {
-    LinTile<T, D, C> t;
-    t.load(x + t0 * step, (unsigned)step, rows, 0, cols);
-    t.template store<false, false>(to, RP, rows, 0, cols, nullptr);
-}
-
 // dg of a chunk's tokens but for what passes the chunk, and the sums of fq
 // and fk that this follows from.
 struct LinPairs {
@@ -801,23 +792,24 @@ struct LinPairs {
     const int* counts;
     const float *dotq, *dotk;   // fq, fk: [slabs][batch * key heads][T]
     float* h;                   // [batch * key heads][T]
-    float* sums;                // [batch * key heads][chunks][2]
+    double* sums;               // [batch * key heads][chunks][2]
     float scale;
     int per_token, B, T, Hk, G, dk, dv, chunks, slabs;
 };
+// All rows are read at once; queries and keys stand in LDS first, then
+// gradients and values in their place, so that four workgroups share a compute
+// unit (widths of 128) and hide each other's way to memory.
 template <class T, int D, int C>
 __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, int flows) {
     if ((int)blockIdx.x < flows) return lin_flow(f, blockIdx.x);   // a whole workgroup
     constexpr int PAD = 16 / sizeof(T), RP = D + PAD, NT = C / 16, NS = D / 32, XP = C + 1;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    T* qs = reinterpret_cast<T*>(lds);
-    T* ks = qs + C * RP;
-    T* vs = ks + C * RP;
-    T* ys = vs + C * RP;
-    double* gs = reinterpret_cast<double*>(ys + C * RP);
+    T* left = reinterpret_cast<T*>(lds);                // queries, then gradients
+    T* right = left + C * RP;                           // keys, then values
+    double* gs = reinterpret_cast<double*>(right + C * RP);
     float* cross = reinterpret_cast<float*>(gs + 64);   // [64]
     float* X = reinterpret_cast<float*>(lds);           // [C][XP], in the operands' place once they are read
-    static_assert(4 * C * XP <= 4 * (int)sizeof(T) * C * RP, "X fits in the operands' place");
+    static_assert(4 * C * XP <= 2 * (int)sizeof(T) * C * RP, "X fits in the operands' place");
     const int block = blockIdx.x - flows, chunk = block % a.chunks, bh = block / a.chunks, b = bh / a.Hk, h = bh % a.Hk;
     const int n = a.counts ? min(max(a.counts[b], 0), a.T) : a.T, t0 = chunk * C;
     if (t0 >= n) return;
@@ -833,40 +825,54 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, i
         }
         gs[lane] = g;
     }
-    const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb;
-    const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + (long)h * a.dk;
-    const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + (long)h * a.dv;
-    const T* y = reinterpret_cast<const T*>(a.dy) + b * a.gb;
-    lin_stage<T, D, C, RP>(k, a.kt, t0, rows, a.dk, ks);
-    lin_stage<T, D, C, RP>(v, a.vt, t0, rows, a.dv, vs);
+    const T* q = reinterpret_cast<const T*>(a.q) + b * a.qb + t0 * a.qt + (long)h * a.G * a.dk;
+    const T* k = reinterpret_cast<const T*>(a.k) + b * a.kb + t0 * a.kt + (long)h * a.dk;
+    const T* v = reinterpret_cast<const T*>(a.v) + b * a.vb + t0 * a.vt + (long)h * a.dv;
+    const T* y = reinterpret_cast<const T*>(a.dy) + b * a.gb + t0 * a.gt + (long)h * a.G * a.dv;
     float x[NT][4];
 #pragma unroll
     for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[kt][r] = 0.f;
     const int i = 16 * wave + l16;
+    LinTile<T, D, C> tq, tk, ty, tv;
     for (int g = 0; g < a.G; ++g) {
-        if (g > 0) __syncthreads();
-        lin_stage<T, D, C, RP>(q + (long)(h * a.G + g) * a.dk, a.qt, t0, rows, a.dk, qs);
-        lin_stage<T, D, C, RP>(y + (long)(h * a.G + g) * a.dv, a.gt, t0, rows, a.dv, ys);
-        __syncthreads();
+        tq.load(q + (long)g * a.dk, (unsigned)a.qt, rows, 0, a.dk);
+        tk.load(k, (unsigned)a.kt, rows, 0, a.dk);
+        ty.load(y + (long)g * a.dv, (unsigned)a.gt, rows, 0, a.dv);
+        tv.load(v, (unsigned)a.vt, rows, 0, a.dv);
+        f32x4 s[NT], p[NT];
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            __syncthreads();   // what stands in LDS is read
+            if (part == 0) {
+                tq.template store<false, false>(left, RP, rows, 0, a.dk, nullptr);
+                tk.template store<false, false>(right, RP, rows, 0, a.dk, nullptr);
+            } else {
+                ty.template store<false, false>(left, RP, rows, 0, a.dv, nullptr);
+                tv.template store<false, false>(right, RP, rows, 0, a.dv, nullptr);
+            }
+            __syncthreads();
+            f32x4* to = part ? p : s;
+#pragma unroll
+            for (int kt = 0; kt < NT; ++kt) {
+                to[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (kt <= wave && wave < NT)
+#pragma unroll
+                    for (int u = 0; u < NS; ++u)
+                        mma(to[kt], ld8(right + (16 * kt + l16) * RP + 32 * u + 8 * lg), ld8(left + i * RP + 32 * u + 8 * lg));
+            }
+        }
         if (wave < NT) {
             const double gi = gs[i];
 #pragma unroll
-            for (int kt = 0; kt < NT; ++kt) {
-                if (kt > wave) continue;
-                f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, p = s;
-#pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    mma(s, ld8(ks + (16 * kt + l16) * RP + 32 * u + 8 * lg), ld8(qs + i * RP + 32 * u + 8 * lg));
-                    mma(p, ld8(vs + (16 * kt + l16) * RP + 32 * u + 8 * lg), ld8(ys + i * RP + 32 * u + 8 * lg));
-                }
+            for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 16 * kt + 4 * lg + r;
-                    x[kt][r] += j < i ? s[r] * p[r] * (__builtin_amdgcn_exp2f((float)(gi - gs[j])) * a.scale) : 0.f;
+                    const float by = __builtin_amdgcn_exp2f((float)(gi - gs[j])) * a.scale;
+                    x[kt][r] += j < i ? s[kt][r] * p[kt][r] * by : 0.f;
                 }
-            }
         }
     }
     __syncthreads();
@@ -908,25 +914,25 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, i
     }
     __syncthreads();
     if (wave == 0) {
-        float fq = 0.f, fk = 0.f;
+        // 64 bits: what passes a chunk is the small difference of such sums, over all chunks of a segment
+        double fq = 0.0, fk = 0.0;
         const long to = (long)bh * a.T + t0 + lane, step = (long)a.B * a.Hk * a.T;
         if (lane < rows)
             for (int z = 0; z < a.slabs; ++z) {
-                fq += a.dotq[z * step + to];
-                fk += a.dotk[z * step + to];
+                fq += (double)a.dotq[z * step + to];
+                fk += (double)a.dotk[z * step + to];
             }
-        float from = fq, upto = fk;   // sums from this token on, and up to it
+        double from = fq, upto = fk;   // sums from this token on, and up to it
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
-            const float o = __shfl_down(from, m, 64), p = __shfl_up(upto, m, 64);
+            const double o = __shfl_down(from, m, 64), p = __shfl_up(upto, m, 64);
             if (lane + m < 64) from += o;
             if (lane >= m) upto += p;
         }
-        const float earlier = __shfl_up(upto, 1, 64);
-        if (lane < rows) a.h[to] = cross[lane] + (from + (lane ? earlier : 0.f));
-        const float all_k = __shfl(upto, 63, 64);
+        if (lane < rows) a.h[to] = (float)((double)cross[lane] + from + (upto - fk));
+        const double all_k = __shfl(upto, 63, 64);
         if (lane == 0) {
-            float* s = a.sums + ((long)bh * a.chunks + chunk) * 2;
+            double* s = a.sums + ((long)bh * a.chunks + chunk) * 2;
             s[0] = from;
             s[1] = all_k;
         }
@@ -935,7 +941,7 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, i
 
 // dg of a segment's tokens (per token), or their sum (into part): from the
 // segment's last chunk to its first, with what passes each.
-__global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const float* sums, const double* flow,
+__global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const double* sums, const double* flow,
                                                        const int* counts, float* dg, double* part, int per_token, int T,
                                                        int Hk, int nseg, int L, int C) {
     const int seg = blockIdx.x % nseg, bh = blockIdx.x / nseg, b = bh / Hk, kh = bh % Hk, lane = threadIdx.x;
@@ -944,9 +950,9 @@ __global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const flo
     double border = flow[(long)bh * nseg + seg], sum = 0.0;
     for (int c = (last - first + C - 1) / C - 1; c >= 0; --c) {
         const int t = first + c * C + lane;
-        const float* s = sums + ((long)bh * chunks + first / C + c) * 2;
-        const double through = border - (double)s[1];
-        border = through + (double)s[0];
+        const double* s = sums + ((long)bh * chunks + first / C + c) * 2;
+        const double through = border - s[1];
+        border = through + s[0];
         if (lane < C && t < last) {
             const double g = through + (double)h[(long)bh * T + t];
             if (per_token) dg[((long)b * T + t) * Hk + kh] = (float)g;
@@ -1047,7 +1053,7 @@ template <class T, int D, int C> static hipError_t lin_pairs_run(LinPairs a, con
     a.chunks = (a.T + C - 1) / C;
     const long flows = (long)a.B * a.Hk * f.nseg, blocks = flows + (long)a.B * a.Hk * a.chunks;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
-    constexpr size_t bytes = 4 * sizeof(T) * C * (D + 16 / sizeof(T)) + 8 * 64 + 4 * 64;
+    constexpr size_t bytes = 2 * sizeof(T) * C * (D + 16 / sizeof(T)) + 8 * 64 + 4 * 64;
     static_assert(bytes <= 156 * 1024, "LDS of a compute unit");
     static std::atomic<unsigned long long> done{0};
     LIN_TRY(lds_limit((const void*)lin_pairs_kernel<T, D, C>, bytes, done));
@@ -1109,7 +1115,7 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         p.dotq = take(bh * T * 4 * ((dk + 63) / 64));
         p.dotk = take(bh * T * 4 * ((dk + 63) / 64));
         p.h = take(bh * T * 4);
-        p.sums = take(bh * ((T + 31) / 32) * 8);   // chunks of 32 tokens, or 64
+        p.sums = take(bh * ((T + 31) / 32) * 16);   // chunks of 32 tokens, or 64
         p.part = take(bh * p.nseg * 8);
     } else if (T > LIN_REC) {   // fewer tokens go token by token
         // the sequence is divided where its heads alone do not fill the chip
@@ -1235,7 +1241,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     // the decays
     float* h = reinterpret_cast<float*>(ws + p.h);
     double* part = reinterpret_cast<double*>(ws + p.part);
-    float* sums = reinterpret_cast<float*>(ws + p.sums);
+    double* sums = reinterpret_cast<double*>(ws + p.sums);
     LinPairs pairs{a.q, a.k, a.v, g.dy, a.qb, a.qt, a.kb, a.kt, a.vb, a.vt, g.gb, g.gt, a.ld, a.counts, dotq, dotk, h, sums,
                scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_many_columns(wide) - 1) / lin_many_columns(wide)};
     LIN_TRY(lin_pairs<T>(pairs, LinFlow{S, R, flow, p.nseg, slots, (int)cells}, st));
