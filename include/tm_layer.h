@@ -79,13 +79,14 @@ tm_status tm_head_norm_backward(const void* x, long x_batch, long x_token, const
  * state_out: fp32 [batch][kv_heads][key_dim][value_dim] contiguous, 16-byte
  * aligned; state_in null: zeros; state_out null: not wanted; state_out may be
  * state_in.  An entry without tokens keeps its state.
- * key_dim, value_dim: multiples of 8, 8 .. 256; heads a multiple of kv_heads;
- * token arrays 16-byte aligned, distances multiples of 8 elements, those of
- * tokens below 2^23.
+ * key_dim, value_dim: multiples of 8, 8 .. 256; heads a multiple of kv_heads,
+ * at most 64 * kv_heads and 32768; n_tokens at most 2^30; token arrays
+ * 16-byte aligned, distances multiples of 8 elements, those of tokens below
+ * 2^23.
  * Products of bf16 calls are of bf16 operands with fp32 accumulation (the
  * pairs' weights within a chunk of tokens are rounded to bf16, the state is
- * read with 16 bits; what is added to it keeps 24), those of fp32 calls are
- * fp32.  Decays are summed in 64 bits, the state is fp32 throughout.
+ * read with 16 bits; what is added to it keeps 24), those of fp32 calls, and
+ * of calls of up to 16 tokens, are fp32.  Decays are summed in 64 bits, the state is fp32 throughout.
  * A non-finite key or value leaves the outputs of earlier tokens as they are;
  * those of its head from its token on, and its state, are not defined.
  * batch or n_tokens 0: state_out becomes state_in (batch 0: no-op). */
@@ -136,10 +137,10 @@ tm_status tm_int8_quantize(const void* x, long x_row, signed char* codes, long c
                            int cols, tm_dtype dtype, void* stream);
 
 /* y[m][n] = (sum_k a[m][k] w[n][k]) a_scales[m] w_scales[n], rounded once to
- * dtype: a [rows][code_row], w [outs][code_row] int8 (16-byte aligned,
- * code_row a multiple of 16 and at least cols; what stands behind cols must
- * be 0 in both), y rows y_row elements apart, aligned to its type.  The sum
- * is exact (32-bit integers); it takes a_scales, then w_scales, in 64
+ * dtype: a [rows][code_row], w [outs][code_row] int8 in -127 .. 127 (16-byte
+ * aligned, code_row a multiple of 16 and at least cols; what stands behind
+ * cols must be 0 in both), y rows y_row elements apart, aligned to its type.
+ * The sum is exact (32-bit integers); it takes a_scales, then w_scales, in 64
  * bits. */
 tm_status tm_int8_matmul(const signed char* a, const float* a_scales, const signed char* w, const float* w_scales,
                          long code_row, void* y, long y_row, long rows, int outs, int cols, tm_dtype dtype,

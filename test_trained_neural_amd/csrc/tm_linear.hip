@@ -1024,8 +1024,9 @@ template <class T, int DK, int CW, bool STATES> static hipError_t lin_many_run(L
     long blocks = 0;
     for (int i = 0; i < (STATES ? 2 : 3); ++i) {
         m.a[i].slabs = (m.a[i].dv + 64 * CW - 1) / (64 * CW);
-        m.blocks[i] = m.a[i].B * m.a[i].Hk * m.a[i].nseg * m.a[i].slabs;
-        blocks += (long)m.a[i].B * m.a[i].Hk * m.a[i].nseg * m.a[i].slabs;
+        const long own = (long)m.a[i].B * m.a[i].Hk * m.a[i].nseg * m.a[i].slabs;
+        m.blocks[i] = (int)own;   // refused below where it does not fit
+        blocks += own;
     }
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
     constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
@@ -1192,6 +1193,8 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
     const long cells = (long)dk * dv, bh = (long)a.B * a.Hk;
     const LinPlan p = lin_plan(a.B, a.T, a.Hk, dk, dv, true);
     const int slots = p.nseg + 1, wide = dk > dv ? dk : dv;
+    // the largest launches (three runs of up to four slabs, a chunk of 32 tokens or a segment each): before the first
+    if (bh * p.nseg * 12 >= 1L << 24 || bh * ((a.T + 31) / 32 + (long)p.nseg) >= 1L << 24) return hipErrorInvalidValue;
     a.nseg = p.nseg;
     a.L = p.L;
     float* S = reinterpret_cast<float*>(ws + p.states);
@@ -1258,7 +1261,7 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
 }
 
 static bool lin_sizes_ok(int B, int T, int H, int Hk, int dk, int dv) {
-    return B >= 0 && T >= 0 && T <= 1 << 30 && H > 0 && Hk > 0 && H % Hk == 0 && H / Hk <= 64 && Hk <= 65535 && dk >= 8 && dk <= 256 &&
+    return B >= 0 && T >= 0 && T <= 1 << 30 && H > 0 && Hk > 0 && H % Hk == 0 && H / Hk <= 64 && H <= 32768 && dk >= 8 && dk <= 256 &&
            dk % 8 == 0 && dv >= 8 && dv <= 256 && dv % 8 == 0 && (long)B * Hk < 1L << 24 &&
            (B == 0 || T <= (1L << 40) / ((long)B * H * 256));
 }

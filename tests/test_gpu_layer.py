@@ -282,6 +282,60 @@ def test_linear_attention_stepwise():
         within(st, want_s, size_s * e, "state of %d pieces" % (len(cuts) - 1))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513, 1025])
+def test_linear_attention_at_every_border(N, dtype):
+    """Lengths around the chunks', segments' and token path's borders, forward and backward; tokens first in memory,
+    keys and values shared by the batch, the same call twice bit for bit."""
+    B, H, K, dk, dv = 2, 2, 1, 16, 24
+    case = (dtype, B, N, H, K, dk, dv, True, False, True)
+    q, k, v, g, _, s, (Q, KK, V, G, S) = linear_case(case)
+    q = q.transpose(0, 1).contiguous().transpose(0, 1)       # [T][B] in memory
+    k, v = k[:1].expand(B, -1, -1, -1), v[:1].expand(B, -1, -1, -1)
+    KK, V = np.repeat(KK[:1], B, 0), np.repeat(V[:1], B, 0)
+    m = T.LinearAttention(K, dk, dv)
+    y, end = m(q, k, v, g, state=s)
+    scale = dk ** -0.5
+    want, want_s = O.linear(Q, KK, V, G, scale, S)
+    size, size_s = O.linear(*map(np.abs, (Q, KK, V)), G, scale, np.abs(S))
+    e, r, half = linear_error(case)
+    within(y, want, size * (e + r) + np.abs(want) * half, "y")
+    within(end, want_s, size_s * e, "state")
+    again = m(q, k, v, g, state=s)
+    assert torch.equal(again[0], y) and torch.equal(again[1], end)
+    dy, DY = normal((B, N, H, dv), 8, dtype)
+    got = m.backward(q, k, v, g, dy, state=s)
+    want = O.linear_backward(Q, KK, V, G, scale, S, DY, np.zeros_like(S))
+    size = O.linear_backward(*map(np.abs, (Q, KK, V)), G, scale, np.abs(S), np.abs(DY), np.zeros_like(S))
+    for n, name in enumerate(("dq", "dk", "dv")):
+        within(got[n], want[n], size[n] * (2 * e + r) + np.abs(want[n]) * half, name)
+    within(got[4], want[4], size[4] * 2 * e, "dstate")
+    assert np.linalg.norm(f64(got[3]) - want[3]) <= 1e-5 * np.linalg.norm(want[3])
+    again = m.backward(q, k, v, g, dy, state=s)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_linear_attention_wide_groups_and_far_rows():
+    """64 query heads on one key head, rows a megabyte apart, a state of its own for none."""
+    m = T.LinearAttention(1, 8)
+    big = torch.zeros(1, 40, (1 << 19) + 512, dtype=BF, device="cuda")
+    q = big[:, :, :512].unflatten(2, (64, 8))
+    x, Q = normal((1, 40, 64, 8), 1)
+    q.copy_(x)
+    (k, KK), (v, V) = normal((1, 40, 1, 8), 2), normal((1, 40, 1, 8), 3)
+    g = torch.full((1,), -0.1, device="cuda")
+    for n in (40, 7):
+        y, end = m(q[:, :n], k[:, :n], v[:, :n], g)
+        want, ws = O.linear(Q[:, :n], KK[:, :n], V[:, :n], f64(g), 8 ** -0.5, np.zeros((1, 1, 8, 8)))
+        size, _ = O.linear(*(np.abs(t[:, :n]) for t in (Q, KK, V)), f64(g), 8 ** -0.5, np.zeros((1, 1, 8, 8)))
+        within(y, want, size * 2.0 ** -7 + np.abs(want) * 2.0 ** -8, "y")
+        assert np.linalg.norm(f64(end) - ws) <= 1e-6 * np.linalg.norm(ws)
+    z = torch.zeros(0, 5, 1, 8, dtype=BF, device="cuda")
+    y, end = m(z, z, z, g)
+    assert y.shape == (0, 5, 1, 8) and end.shape == (0, 1, 8, 8)
+    assert not m.backward(z, z, z, g, z)[3].any()
+
+
 @pytest.mark.parametrize("T_", [9, 100, 600])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_linear_attention_non_finite(T_, dtype):

@@ -145,7 +145,8 @@ LIN = [P(0), 512, 128, P(0), 512, 128, P(0), 512, 128, P(0), 1, None, P(0), P(0)
 @pytest.mark.parametrize("at,value", [
     (22, 3), (0, None), (0, P(8)), (1, 4), (2, -8), (3, None), (6, P(2)), (9, None), (9, P(2)), (11, P(2)), (12, P(4)),
     (13, P(8)), (14, None), (14, P(8)), (15, math.inf), (16, -1), (17, -1), (18, 3), (18, 0), (18, 130), (19, 0), (20, 60),
-    (20, 264), (20, 0), (21, 4), (21, 512), (23, None), (23, P(16)), (17, (1 << 30) + 1)])
+    (20, 264), (20, 0), (21, 4), (21, 512), (23, None), (23, P(16)), (17, (1 << 30) + 1),
+    (2, 1 << 23), (18, 32770), (16, 1 << 23)])
 def test_linear_attention_refuses(at, value):
     a = list(LIN)
     a[at] = value
