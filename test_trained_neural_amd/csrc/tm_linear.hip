@@ -157,20 +157,20 @@ __device__ __forceinline__ bool lin_lost(bf16x8 x) {
 // first row; step: elements between rows (64 rows are less than 2^31 bytes
 // apart: an offset is 32 bits beside an address of the whole workgroup).
 template <class T, int D, int C> struct LinTile {
-    static constexpr int VE = 16 / sizeof(T), UNITS = D / VE, PER = 256 / UNITS, N = (C * UNITS + 255) / 256;
+    // rows of PER by N cover C; where they are more, or 256 threads are no whole
+    // rows (D 192), some rows are read and put down twice
+    static constexpr int VE = 16 / sizeof(T), UNITS = D / VE, PER = 256 / UNITS, N = (C + PER - 1) / PER;
+    static constexpr bool WHOLE = 256 % UNITS == 0 && C % PER == 0;
     typedef T Vec __attribute__((ext_vector_type(VE)));
     Vec v[N];
     __device__ __forceinline__ void load(const T* x, unsigned step, int rows, int c0, int cols) {
         const unsigned u = threadIdx.x % UNITS, c = c0 + u * VE < (unsigned)cols ? c0 + u * VE : 0u, r0 = threadIdx.x / UNITS;
         const char* at = reinterpret_cast<const char*>(x);
-        if (rows == C) {
+        if (WHOLE && rows == C) {
             const unsigned off = (r0 * step + c) * (unsigned)sizeof(T);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                // a tile of fewer rows than threads: the last are read again
-                const unsigned o = C * UNITS % 256 == 0 || r0 < (unsigned)C ? off : c * (unsigned)sizeof(T);
-                v[i] = *reinterpret_cast<const Vec*>(at + (unsigned long)(i * PER) * step * sizeof(T) + o);
-            }
+            for (int i = 0; i < N; ++i)
+                v[i] = *reinterpret_cast<const Vec*>(at + (unsigned long)(i * PER) * step * sizeof(T) + off);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -208,7 +208,7 @@ template <class T, int D, int C> struct LinTile {
         }
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (C * UNITS % 256 == 0 || r0 + i * PER < C) {
+            if (WHOLE || r0 + i * PER < C) {
                 const int r = r0 + i * PER;
                 if constexpr (!TURN) {
                     *reinterpret_cast<Vec*>(to + r * row + u * VE) = v[i];

@@ -315,6 +315,31 @@ def test_linear_attention_at_every_border(N, dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk", range(8, 257, 8))
+def test_linear_attention_at_every_width(dk, dtype):
+    """Every width of keys, with values of 264 less it, over whole and begun chunks, forward and backward."""
+    dv = 264 - dk
+    case = (dtype, 2, 70, 2, 1, dk, dv, True, False, True)
+    q, k, v, g, _, s, (Q, KK, V, G, S) = linear_case(case)
+    m = T.LinearAttention(1, dk, dv)
+    y, end = m(q, k, v, g, state=s)
+    scale = dk ** -0.5
+    want, want_s = O.linear(Q, KK, V, G, scale, S)
+    size, size_s = O.linear(*map(np.abs, (Q, KK, V)), G, scale, np.abs(S))
+    e, r, half = linear_error(case)
+    within(y, want, size * (e + r) + np.abs(want) * half, "y")
+    within(end, want_s, size_s * e, "state")
+    dy, DY = normal((2, 70, 2, dv), 8, dtype)
+    got = m.backward(q, k, v, g, dy, state=s)
+    want = O.linear_backward(Q, KK, V, G, scale, S, DY, np.zeros_like(S))
+    size = O.linear_backward(*map(np.abs, (Q, KK, V)), G, scale, np.abs(S), np.abs(DY), np.zeros_like(S))
+    for n, name in enumerate(("dq", "dk", "dv")):
+        within(got[n], want[n], size[n] * (2 * e + r) + np.abs(want[n]) * half, name)
+    within(got[4], want[4], size[4] * 2 * e, "dstate")
+    assert np.linalg.norm(f64(got[3]) - want[3]) <= 1e-5 * np.linalg.norm(want[3])
+
+
 def test_linear_attention_wide_groups_and_far_rows():
     """64 query heads on one key head, rows a megabyte apart, a state of its own for none."""
     m = T.LinearAttention(1, 8)
