@@ -31,24 +31,51 @@ __device__ __forceinline__ Int8Scale int8_scale(float m) {   // m: infinity wher
     s.scale = lost ? __builtin_nanf("") : m / 127.f;
     return s;
 }
-// max |x|, infinity if x is not finite
-__device__ __forceinline__ float int8_size(float m, float x) {
-    const float v = fabsf(x);
-    return v <= 3.402823466e38f ? fmaxf(m, v) : __builtin_inff();
-}
+// max |x| of a row's share, infinity where an element is not finite: as bits
+// without their sign, which are in the order of the values (bf16: two at a
+// time).
+template <class T> struct Int8Max;
+template <> struct Int8Max<float> {
+    unsigned m = 0;
+    __device__ __forceinline__ void add(float x) { m = max(m, __builtin_bit_cast(unsigned, x) & 0x7fffffffu); }
+    __device__ __forceinline__ void add(f32x4 v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add(v[e]);
+    }
+    __device__ __forceinline__ float get() const { return __builtin_bit_cast(float, min(m, 0x7f800000u)); }
+};
+template <> struct Int8Max<bf16> {
+    typedef unsigned short H2 __attribute__((ext_vector_type(2)));
+    typedef unsigned U4 __attribute__((ext_vector_type(4)));
+    H2 m = {0, 0};
+    __device__ __forceinline__ void two(unsigned w) { m = __builtin_elementwise_max(m, __builtin_bit_cast(H2, w & 0x7fff7fffu)); }
+    __device__ __forceinline__ void add(bf16 x) { two(__builtin_bit_cast(unsigned short, x)); }
+    __device__ __forceinline__ void add(bf16x8 v) {
+        const U4 u = __builtin_bit_cast(U4, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) two(u[e]);
+    }
+    __device__ __forceinline__ float get() const {
+        const unsigned h = max(m[0], m[1]);
+        return __builtin_bit_cast(float, min(h, 0x7f80u) << 16);
+    }
+};
+template <class T> struct Int8Vec;
+template <> struct Int8Vec<float> { typedef f32x4 V; };
+template <> struct Int8Vec<bf16> { typedef bf16x8 V; };
+
 // 4 values as the bytes of a word.  Added to 1.5 * 2^23 a quotient is rounded
 // to a whole number, to even at a half, which stands in the low bits.
 __device__ __forceinline__ unsigned int8_pack(const float* x, const Int8Scale& s) {
     constexpr float ONES = 12582912.f;
-    float v[4], far = 0.f;
+    float v[4], off[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float q = x[e] * s.by;
-        v[e] = q + ONES;
-        const float off = fabsf(q - (v[e] - ONES));
-        far = off < 0.4999f ? far : 1.f;   // also where q is not finite
+        v[e] = fmaf(x[e], s.by, ONES);
+        off[e] = fabsf(fmaf(x[e], s.by, -(v[e] - ONES)));   // from the whole number
     }
-    if (far != 0.f)
+    // next to a half; an infinite factor makes all of these infinite or NaN
+    if (!(fmaxf(fmaxf(off[0], off[1]), fmaxf(off[2], off[3])) < 0.4999f) || s.by == __builtin_inff())
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = 127.f * (x[e] * s.down) / s.top + ONES;
     const unsigned a = __builtin_bit_cast(unsigned, v[0]), b = __builtin_bit_cast(unsigned, v[1]),
@@ -57,19 +84,31 @@ __device__ __forceinline__ unsigned int8_pack(const float* x, const Int8Scale& s
     const unsigned ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
     return s.any ? (ab | cd << 16) : 0u;
 }
+// the codes of 16 bytes of a row
+__device__ __forceinline__ void int8_put_codes(signed char* c, f32x4 v, const Int8Scale& s) {
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<unsigned*>(c) = int8_pack(f, s);
+}
+__device__ __forceinline__ void int8_put_codes(signed char* c, bf16x8 v, const Int8Scale& s) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+    const uint2 w = {int8_pack(f, s), int8_pack(f + 4, s)};
+    *reinterpret_cast<uint2*>(c) = w;
+}
 
 // One row a workgroup.  VEC: rows allow loads of 16 bytes; up to 32 elements a
 // thread stay in registers between the maximum and the codes.
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* x, long x_row, signed char* codes, long code_row,
                                                             float* scales, int cols) {
+    typedef typename Int8Vec<T>::V Vec;
     constexpr int VE = 16 / sizeof(T), KEEP = 32 / VE;
-    struct __align__(16) Vec { T e[VE]; };
     __shared__ float red[4];
     const long row = blockIdx.x;
     const T* p = x + row * x_row;
     signed char* c = codes + row * code_row;
-    float m = 0.f;
+    Int8Max<T> top;
     Vec kept[KEEP];
     const int units = VEC ? cols / VE : 0;
     if constexpr (VEC) {
@@ -80,16 +119,11 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* x, long x_r
         }
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
-            if ((int)threadIdx.x + 256 * i < units)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) m = int8_size(m, (float)kept[i].e[e]);
-        for (int u = threadIdx.x + 256 * KEEP; u < units; u += 256) {
-            const Vec v = *reinterpret_cast<const Vec*>(p + (long)u * VE);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) m = int8_size(m, (float)v.e[e]);
-        }
+            if ((int)threadIdx.x + 256 * i < units) top.add(kept[i]);
+        for (int u = threadIdx.x + 256 * KEEP; u < units; u += 256) top.add(*reinterpret_cast<const Vec*>(p + (long)u * VE));
     }
-    for (int i = units * VE + threadIdx.x; i < cols; i += 256) m = int8_size(m, (float)p[i]);
+    for (int i = units * VE + threadIdx.x; i < cols; i += 256) top.add(p[i]);
+    float m = top.get();
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -97,21 +131,11 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const T* x, long x_r
     const Int8Scale s = int8_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
     if (threadIdx.x == 0) scales[row] = s.scale;
     if constexpr (VEC) {
-        auto put = [&](int u, const Vec& v) {
-            float f[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) f[e] = (float)v.e[e];
-            if constexpr (VE == 8) {
-                uint2 w = {int8_pack(f, s), int8_pack(f + 4, s)};
-                *reinterpret_cast<uint2*>(c + (long)u * 8) = w;
-            } else {
-                *reinterpret_cast<unsigned*>(c + (long)u * 4) = int8_pack(f, s);
-            }
-        };
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
-            if ((int)threadIdx.x + 256 * i < units) put(threadIdx.x + 256 * i, kept[i]);
-        for (int u = threadIdx.x + 256 * KEEP; u < units; u += 256) put(u, *reinterpret_cast<const Vec*>(p + (long)u * VE));
+            if ((int)threadIdx.x + 256 * i < units) int8_put_codes(c + (long)(threadIdx.x + 256 * i) * VE, kept[i], s);
+        for (int u = threadIdx.x + 256 * KEEP; u < units; u += 256)
+            int8_put_codes(c + (long)u * VE, *reinterpret_cast<const Vec*>(p + (long)u * VE), s);
     }
     // the rest of the row, and the zeros behind it, 4 columns at a time
     for (long i = units * VE + 4 * threadIdx.x; i < code_row; i += 1024) {
@@ -251,31 +275,40 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args g) {
     }
 }
 
-// Few rows of x: 16 rows of w by 16 MT rows of x a workgroup, the columns
+// Few rows of x: 16 NR rows of w by 16 MT rows of x a workgroup, the columns
 // divided among its 8 waves, whose sums meet in LDS.  Bound by reading w once.
 // FUSED (MT 1): the workgroup makes the rows' codes itself, in LDS, while its
 // first loads of w are under way: one launch, and the rows come from the L2.
-template <class T, int MT, bool FUSED>
-__global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
+// Every workgroup repeats that, so NR is 2 where 16 rows of w would make more
+// workgroups than there are compute units.
+template <class T, int MT, int NR, bool FUSED>
+__global__ __launch_bounds__(512, NR == 1 ? 4 : 2) void int8_thin_kernel(Int8Args g) {
     constexpr int AHEAD = 8;   // blocks of 64 columns in flight for a wave
-    extern __shared__ __attribute__((aligned(16))) signed char lds[];   // codes [M][stride] (FUSED); sums [8][MT][16][17]
+    extern __shared__ __attribute__((aligned(16))) signed char lds[];   // codes [M][stride] (FUSED); sums [8][MT][NR][16][17]
     __shared__ float sc[16];
     __shared__ float top[8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * 16 * NR;
     const long m0 = (long)blockIdx.y * 16 * MT;
     const int blocks = (int)((g.code_row + 63) / 64), per = (blocks + 7) / 8;
     const int b0 = wave * per, b1 = min(blocks, b0 + per);
     const int stride = blocks * 64 + 16;
-    const signed char* w = g.w + (long)min(n0 + l16, g.N - 1) * g.code_row + 16 * lg;
-    auto load_w = [&](int b) {
+    const signed char* w[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) w[r] = g.w + (long)min(n0 + 16 * r + l16, g.N - 1) * g.code_row + 16 * lg;
+    auto load_w = [&](int r, int b) {
         i32x4 v = i32x4{0, 0, 0, 0};
-        if (b < b1 && 64L * b + 16 * lg < g.code_row) v = *reinterpret_cast<const i32x4*>(w + 64L * b);
+        if (b < b1 && 64L * b + 16 * lg < g.code_row) v = *reinterpret_cast<const i32x4*>(w[r] + 64L * b);
         return v;
     };
-    i32x4 wv[AHEAD];
+    i32x4 wv[NR][AHEAD];
+    auto first_w = [&] {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) wv[i] = load_w(b0 + i);
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) wv[r][i] = load_w(r, b0 + i);
+    };
+    if constexpr (!FUSED) first_w();
     if constexpr (FUSED) {
         // threads of a row: all 512 for one row, 32 for 16
         const int M = (int)g.M;
@@ -284,27 +317,23 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
         const int row = threadIdx.x / lanes, at = threadIdx.x % lanes;
         const bool on = row < M;
         const T* x = reinterpret_cast<const T*>(g.x) + (on ? row : 0) * g.x_row;
+        typedef typename Int8Vec<T>::V Vec;
         constexpr int VE = 16 / sizeof(T), KEEP = 64 / VE;
-        struct __align__(16) Vec { T e[VE]; };
         const int units = g.xvec ? g.cols / VE : 0;
-        float m = 0.f;
+        Int8Max<T> most;
         Vec kept[KEEP];
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (on && at + i * lanes < units) kept[i] = *reinterpret_cast<const Vec*>(x + (long)(at + i * lanes) * VE);
+        first_w();   // behind the rows' loads, which are waited for first: loads come back in order
         if (on) {
 #pragma unroll
             for (int i = 0; i < KEEP; ++i)
-                if (at + i * lanes < units) kept[i] = *reinterpret_cast<const Vec*>(x + (long)(at + i * lanes) * VE);
-#pragma unroll
-            for (int i = 0; i < KEEP; ++i)
-                if (at + i * lanes < units)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) m = int8_size(m, (float)kept[i].e[e]);
-            for (int u = at + KEEP * lanes; u < units; u += lanes) {
-                const Vec v = *reinterpret_cast<const Vec*>(x + (long)u * VE);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) m = int8_size(m, (float)v.e[e]);
-            }
-            for (int i = units * VE + at; i < g.cols; i += lanes) m = int8_size(m, (float)x[i]);
+                if (at + i * lanes < units) most.add(kept[i]);
+            for (int u = at + KEEP * lanes; u < units; u += lanes) most.add(*reinterpret_cast<const Vec*>(x + (long)u * VE));
+            for (int i = units * VE + at; i < g.cols; i += lanes) most.add(x[i]);
         }
+        float m = most.get();
         for (int s = min(lanes, 64) >> 1; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
         if (lanes > 64) {   // a row's waves
             if (lane == 0) top[wave] = m;
@@ -317,22 +346,11 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
         if (on) {
             if (at == 0) sc[row] = s.scale;
             signed char* c = lds + row * stride;
-            auto put = [&](int u, const Vec& v) {
-                float f[VE];
-#pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] = (float)v.e[e];
-                if constexpr (VE == 8) {
-                    const uint2 w = {int8_pack(f, s), int8_pack(f + 4, s)};
-                    *reinterpret_cast<uint2*>(c + u * 8) = w;
-                } else {
-                    *reinterpret_cast<unsigned*>(c + u * 4) = int8_pack(f, s);
-                }
-            };
 #pragma unroll
             for (int i = 0; i < KEEP; ++i)
-                if (at + i * lanes < units) put(at + i * lanes, kept[i]);
+                if (at + i * lanes < units) int8_put_codes(c + (at + i * lanes) * VE, kept[i], s);
             for (int u = at + KEEP * lanes; u < units; u += lanes)
-                put(u, *reinterpret_cast<const Vec*>(x + (long)u * VE));
+                int8_put_codes(c + u * VE, *reinterpret_cast<const Vec*>(x + (long)u * VE), s);
             for (int i = units * VE + 4 * at; i < blocks * 64; i += 4 * lanes) {
                 float f[4];
 #pragma unroll
@@ -342,31 +360,34 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
         }
         __syncthreads();
     }
-    i32x4 acc[MT];
+    i32x4 acc[MT][NR];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) acc[i][r] = i32x4{0, 0, 0, 0};
     for (int b = b0; b < b1; b += AHEAD) {
-        i32x4 cur[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            cur[i] = wv[i];
-            wv[i] = load_w(b + AHEAD + i);
-        }
+            i32x4 cur[NR];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            if (b + i >= b1) break;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                i32x4 x = i32x4{0, 0, 0, 0};
-                if constexpr (FUSED) {
-                    x = *reinterpret_cast<const i32x4*>(lds + min(l16, (int)g.M - 1) * stride + 64 * (b + i) + 16 * lg);
-                } else {
-                    const long c = 64L * (b + i) + 16 * lg;
-                    if (c < g.code_row)
-                        x = *reinterpret_cast<const i32x4*>(g.a + min(m0 + 16 * t + l16, g.M - 1) * g.code_row + c);
-                }
-                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[i], x, acc[t], 0, 0, 0);
+            for (int r = 0; r < NR; ++r) {
+                cur[r] = wv[r][i];
+                wv[r][i] = load_w(r, b + AHEAD + i);
             }
+            if (b + i < b1)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    i32x4 x = i32x4{0, 0, 0, 0};
+                    if constexpr (FUSED) {
+                        x = *reinterpret_cast<const i32x4*>(lds + min(l16, (int)g.M - 1) * stride + 64 * (b + i) + 16 * lg);
+                    } else {
+                        const long c = 64L * (b + i) + 16 * lg;
+                        if (c < g.code_row)
+                            x = *reinterpret_cast<const i32x4*>(g.a + min(m0 + 16 * t + l16, g.M - 1) * g.code_row + c);
+                    }
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[r], x, acc[t][r], 0, 0, 0);
+                }
         }
     }
     __syncthreads();   // the codes are read
@@ -374,17 +395,19 @@ __global__ __launch_bounds__(512) void int8_thin_kernel(Int8Args g) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sums[((wave * MT + t) * 16 + l16) * 17 + 4 * lg + r] = acc[t][r];
+        for (int z = 0; z < NR; ++z)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[(((wave * MT + t) * NR + z) * 16 + l16) * 17 + 4 * lg + r] = acc[t][z][r];
     __syncthreads();
-    for (int i = threadIdx.x; i < MT * 256; i += 512) {
-        const int t = i >> 8, m = (i >> 4) & 15, n = i & 15;
+    for (int i = threadIdx.x; i < MT * NR * 256; i += 512) {
+        const int tz = i >> 8, t = tz / NR, m = (i >> 4) & 15, n = n0 + 16 * (tz % NR) + (i & 15);
         const long row = m0 + 16 * t + m;
         int s = 0;
 #pragma unroll
-        for (int z = 0; z < 8; ++z) s += sums[((z * MT + t) * 16 + m) * 17 + n];
-        if (row < g.M && n0 + n < g.N)
-            reinterpret_cast<T*>(g.y)[row * g.y_row + n0 + n] =
-                (T)((double)s * (double)(FUSED ? sc[m] : g.as[row]) * (double)g.wsc[n0 + n]);
+        for (int z = 0; z < 8; ++z) s += sums[((z * MT * NR + tz) * 16 + m) * 17 + (i & 15)];
+        if (row < g.M && n < g.N)
+            reinterpret_cast<T*>(g.y)[row * g.y_row + n] =
+                (T)((double)s * (double)(FUSED ? sc[m] : g.as[row]) * (double)g.wsc[n]);
     }
 }
 
@@ -419,18 +442,23 @@ template <class T, int BM, int BN, int WM, int WN> static hipError_t int8_tile(I
     });
 }
 
-template <class T, int MT, bool FUSED> static hipError_t int8_thin(const Int8Args& g, hipStream_t st) {
-    const long nb = (g.N + 15L) / 16, mb = (g.M + 16 * MT - 1) / (16 * MT);
+template <class T, int MT, int NR, bool FUSED> static hipError_t int8_thin_run(const Int8Args& g, hipStream_t st) {
+    const long nb = (g.N + 16L * NR - 1) / (16 * NR), mb = (g.M + 16 * MT - 1) / (16 * MT);
     if (nb >= 1L << 23 || mb > 65535) return hipErrorInvalidValue;
-    const size_t sums = 8 * MT * 16 * 17 * 4, codes = FUSED ? (size_t)g.M * ((g.code_row + 63) / 64 * 64 + 16) : 0;
+    const size_t sums = 8 * MT * NR * 16 * 17 * 4, codes = FUSED ? (size_t)g.M * ((g.code_row + 63) / 64 * 64 + 16) : 0;
     const size_t bytes = sums > codes ? sums : codes;
     static std::atomic<unsigned long long> done{0};
-    const hipError_t e = lds_limit((const void*)int8_thin_kernel<T, MT, FUSED>, bytes, done);
+    const hipError_t e = lds_limit((const void*)int8_thin_kernel<T, MT, NR, FUSED>, bytes, done);
     if (e != hipSuccess) return e;
     return timed_layer(st, [&] {
-        launch_k((int8_thin_kernel<T, MT, FUSED>), dim3((unsigned)nb, (unsigned)mb), dim3(512), bytes, st, g);
+        launch_k((int8_thin_kernel<T, MT, NR, FUSED>), dim3((unsigned)nb, (unsigned)mb), dim3(512), bytes, st, g);
         return hipGetLastError();
     });
+}
+template <class T, int MT, bool FUSED> static hipError_t int8_thin(const Int8Args& g, hipStream_t st) {
+    if constexpr (FUSED)
+        if (g.N > 16 * 256) return int8_thin_run<T, MT, 2, FUSED>(g, st);
+    return int8_thin_run<T, MT, 1, FUSED>(g, st);
 }
 
 // A call whose workgroups make the codes themselves.
