@@ -461,13 +461,20 @@ template <class T, int MT, bool FUSED> static hipError_t int8_thin(const Int8Arg
     return int8_thin_run<T, MT, 1, FUSED>(g, st);
 }
 
-// A call whose workgroups make the codes themselves.
+// A call whose workgroups make the codes themselves: as many rows as an
+// instruction takes, in half a compute unit's LDS (8 rows of 4096 to 6144: 11 us
+// a pass against 14 with the codes from a launch of their own).
 static bool int8_fused(long rows, long code_row) { return rows <= 16 && rows * ((code_row + 63) / 64 * 64 + 16) <= 72 * 1024; }
 
 template <class T> static hipError_t int8_matmul_t(const Int8Args& g, hipStream_t st) {
+    // Large tiles where they fill the chip, us by tiles of 256 / 128 / 64 / few rows:
+    //   4096 x 4096 -> 4096: 81 / 89 / 114 / 592;  2048 x 4096 -> 4096: 76 / 47 / 56 / 299;
+    //   4096 x 1024 -> 2048: 38 / 24 / 24 / 100;   1024 x 4096 -> 4096: 73 / 38 / 30 / 152;
+    //   256 x 4096 -> 4096: 70 / 34 / 17 / 41;     64 x 4096 -> 4096: 57 / 33 / 16 / 15;
+    //   300 x 1024 -> 1024: 36 / 18 / 8 / 8;       100 x 8192 -> 300: 106 / 54 / 25 / 21.
     auto tiles = [&](long b) { return (g.M + b - 1) / b * ((g.N + b - 1) / b); };
     if (tiles(256) >= 200) return int8_tile<T, 256, 256, 2, 4>(g, st);
-    if (tiles(128) >= 200) return int8_tile<T, 128, 128, 2, 2>(g, st);
+    if (tiles(128) >= 400) return int8_tile<T, 128, 128, 2, 2>(g, st);
     if (g.M > 64 && tiles(64) >= 128) return int8_tile<T, 64, 64, 2, 2>(g, st);
     if (g.M <= 16) return int8_thin<T, 1, false>(g, st);
     if (g.M <= 32) return int8_thin<T, 2, false>(g, st);

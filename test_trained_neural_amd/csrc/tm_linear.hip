@@ -37,7 +37,12 @@
 namespace tmk {
 
 constexpr double LOG2E = 1.4426950408889634074;
-constexpr int LIN_REC = 16;        // calls of up to as many tokens go token by token
+// Calls of up to as many tokens go token by token: us by tokens / by chunks
+// (widths of 128, 64 and 512 heads' states; widths of 64, 8 states), bf16
+// 2 tokens 8.3 / 12.1, 8 tokens 10.8 / 12.0, 28.9 / 22.0 and 8.4 / 7.6, 16
+// tokens 17.2 / 12.0, 45.5 / 22.2 and 12.9 / 7.6; fp32 8 tokens 9.7 / 14.1,
+// 27.4 / 26.9 and 7.5 / 7.4, 16 tokens 15.0 / 14.1, 42.7 / 27.3 and 11.3 / 7.4.
+template <class T> constexpr int lin_few() { return sizeof(T) == 4 ? 8 : 5; }
 constexpr int LIN_BACK_SEG = 256;  // tokens of a segment in the backward
 
 // What a chunk run does (see the table of roles above).
@@ -1118,11 +1123,18 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         p.h = take(bh * T * 4);
         p.sums = take(bh * ((T + 31) / 32) * 16);   // chunks of 32 tokens, or 64
         p.part = take(bh * p.nseg * 8);
-    } else if (T > LIN_REC) {   // fewer tokens go token by token
-        // the sequence is divided where its heads alone do not fill the chip
+    } else {
+        // The sequence is divided where its heads alone do not fill the chip, into
+        // segments of 64 tokens while those are few, else of 128 at least (us
+        // undivided / 256 / 128 / 64 tokens at least, bf16: 8 heads of 128, 512
+        // tokens 47 / 41 / 27 / 22, 4096 tokens 335 / 47 / 40 / 46; 64 heads of 128,
+        // 512 tokens 49 / 48 / 39 / 44; 2 heads of 64, 2048 tokens 90 / 24 / 19 / 18;
+        // fp32: 8 heads of 128, 1024 tokens 237 / 97 / 57 / 41).  Undivided: 256
+        // heads of 64, 2048 tokens 96 against 101; 8 heads of 128, 128 tokens 17.
         const long cols = lin_columns(dk, dv), wgs = (long)bh * ((dv + cols - 1) / cols);
-        long seg = wgs >= 256 || T <= 256 ? 1 : (512 + wgs - 1) / wgs;
-        seg = seg < (T + 255) / 256 ? seg : (T + 255) / 256;
+        const long least = wgs * ((T + 63) / 64) <= 256 ? 64 : 128;
+        long seg = wgs >= 256 || T <= 192 ? 1 : (512 + wgs - 1) / wgs;
+        seg = seg < (T + least - 1) / least ? seg : (T + least - 1) / least;
         p.L = (int)(((T + seg - 1) / seg + 63) / 64 * 64);
         p.nseg = (T + p.L - 1) / p.L;
         if (p.nseg > 1) {
@@ -1153,7 +1165,7 @@ static hipError_t lin_copy(const float* from, float* to, long n, hipStream_t st)
 template <class T> static hipError_t lin_forward(LinArgs a, float* state_out, char* ws, hipStream_t st) {
     const long cells = (long)a.dk * a.dv;
     a.s_in_bh = a.s_out_bh = cells;
-    if (a.T <= LIN_REC) {
+    if (a.T <= lin_few<T>()) {
         a.s_out = state_out;
         return lin_tokens_run<T>(a, st);
     }
