@@ -43,7 +43,11 @@ constexpr double LOG2E = 1.4426950408889634074;
 // tokens 17.2 / 12.0, 45.5 / 22.2 and 12.9 / 7.6; fp32 8 tokens 9.7 / 14.1,
 // 27.4 / 26.9 and 7.5 / 7.4, 16 tokens 15.0 / 14.1, 42.7 / 27.3 and 11.3 / 7.4.
 template <class T> constexpr int lin_few() { return sizeof(T) == 4 ? 8 : 5; }
-constexpr int LIN_BACK_SEG = 256;  // tokens of a segment in the backward
+// Tokens of a segment in the backward, at most. All gradients of 2 x 4096 tokens
+// of 16 heads of 128, segments of 64 / 256 / 512 tokens: 484 / 268 / 247 us, but at
+// 512 the gates' gradients, whose roundings grow with a segment, are 1.2e-6 of
+// their size from 64 bits instead of 8e-7.
+constexpr int LIN_BACK_SEG = 256;
 
 // What a chunk run does (see the table of roles above).
 enum { LIN_OUT, LIN_STATE, LIN_STATE_BACK, LIN_DQ, LIN_DK, LIN_DV };
@@ -802,8 +806,10 @@ struct LinPairs {
     int per_token, B, T, Hk, G, dk, dv, chunks, slabs;
 };
 // All rows are read at once; queries and keys stand in LDS first, then
-// gradients and values in their place, so that four workgroups share a compute
-// unit (widths of 128) and hide each other's way to memory.
+// gradients and values in their place: 36 KB at widths of 128, so that three
+// workgroups share a compute unit (their registers allow no fourth) and hide each
+// other's way to memory. 47 us for 2 x 4096 tokens of 16 heads of 128, bf16, with
+// the borders' flows; operands straight from memory, in rows of 64 bytes, 57 us.
 template <class T, int D, int C>
 __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, int flows) {
     if ((int)blockIdx.x < flows) return lin_flow(f, blockIdx.x);   // a whole workgroup
@@ -1110,7 +1116,8 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         return o;
     };
     if (back) {
-        // shorter segments where they would not fill the chip
+        // Halved while there are fewer segments than compute units: a segment is a
+        // workgroup's walk, one chunk after another.
         p.L = LIN_BACK_SEG;
         while (p.L > 64 && (long)bh * ((T + p.L - 1) / p.L) < 256) p.L /= 2;
         p.nseg = (T + p.L - 1) / p.L;
