@@ -83,10 +83,11 @@ tm_status tm_head_norm_backward(const void* x, long x_batch, long x_token, const
  * at most 64 * kv_heads and 32768; n_tokens at most 2^30; token arrays
  * 16-byte aligned, distances multiples of 8 elements, those of tokens below
  * 2^23.
- * Products of bf16 calls are of bf16 operands with fp32 accumulation (the
- * pairs' weights within a chunk of tokens are rounded to bf16, the state is
- * read with 16 bits; what is added to it keeps 24), those of fp32 calls, and
- * of bf16 calls of up to 5 tokens, are fp32.  Decays are summed in 64 bits, the state is fp32 throughout.
+ * Products of bf16 calls are of bf16 operands with fp32 accumulation: the
+ * pairs' weights within a chunk of tokens and the state before it keep 16 bits
+ * (two operands each), what is added to the state 24; the outputs' own rounding
+ * is coarser by 2^8.  Those of fp32 calls, and of bf16 calls of up to 5 tokens,
+ * are fp32.  Decays are summed in 64 bits, the state is fp32 throughout.
  * A non-finite key or value leaves the outputs of earlier tokens as they are;
  * those of its head from its token on, and its state, are not defined.
  * batch or n_tokens 0: state_out becomes state_in (batch 0: no-op). */

@@ -116,7 +116,11 @@ __device__ __forceinline__ f32x8 lin_f32(bf16x8 x) {   // a bf16's bits are an f
     return r;
 }
 
-// fp32 values as operands: one for fp32, N of 8 bits each for bf16.
+// fp32 values as operands: one for fp32, N of 8 bits each for bf16.  A pair's
+// weight and the state before a chunk take two: 16 bits of each, so that what
+// an output is off by is its own rounding to 8 (with weights of 8 bits outputs
+// were 0.0023 of their size from 64 bits, 0.0017 of it their own; the second
+// operand costs 1 to 3% of a call, 8% at widths of 64).
 template <class T, int N> struct Parts {
     typename Frag<T>::T p[N];
     __device__ __forceinline__ void set(f32x8 x) {
@@ -137,12 +141,15 @@ template <class T> constexpr int lin_parts(int n) { return sizeof(T) == 4 ? 1 : 
 // instructions the pairs of a chunk cost more than the state it saves).
 template <class T> constexpr int lin_chunk() { return sizeof(T) == 4 ? 32 : 64; }
 
-template <class T, int DK, int CW> struct LinLds {
-    static constexpr int C = lin_chunk<T>(), VD = 64 * CW, PP = C + 16 / sizeof(T);
-    static constexpr int GATES = 512;   // tokens whose decays are summed at a time
-    static constexpr size_t q = 0, k = q + sizeof(T) * C * DK, v = k + sizeof(T) * C * DK, p = v + sizeof(T) * C * VD,
-                            g = p + sizeof(T) * C * PP, head = g + 8 * GATES, tail = head + 4 * GATES,
-                            dot = tail + 4 * GATES, bad = dot + 4 * 4 * 64, bytes = bad + 16;
+// A run's LDS.  STATE: one that forms states alone, without queries and pairs.
+template <class T, int DK, int CW, bool STATE> struct LinLds {
+    static constexpr int C = lin_chunk<T>(), VD = 64 * CW, PP = C + 16 / sizeof(T), PARTS = lin_parts<T>(2);
+    // tokens whose decays are summed at a time (half as many where two workgroups would not fit a compute unit)
+    static constexpr int GATES = sizeof(T) == 2 && DK == 192 ? 256 : 512;
+    static constexpr size_t q = 0, k = q + (STATE ? 0 : sizeof(T) * C * DK), v = k + sizeof(T) * C * DK,
+                            p = v + sizeof(T) * C * VD, g = p + (STATE ? 0 : sizeof(T) * C * PP * PARTS),
+                            head = g + 8 * GATES, tail = head + 4 * GATES, dot = tail + 4 * GATES,
+                            bad = dot + 4 * 4 * 64, bytes = bad + 16;
 };
 
 // Whether 16 bytes hold a non-finite value: an exponent of ones.
@@ -279,7 +286,7 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
     // the state as an operand keeps 16 bits, 24 where its products enter the gradients of the decays
     constexpr int SP = lin_parts<T>(DOT ? 3 : 2), VP3 = lin_parts<T>(3);   // what is added to the state: 24
     typedef typename Frag<T>::T F;
-    typedef LinLds<T, DK, CW> S_;
+    typedef LinLds<T, DK, CW, STATE> S_;
     constexpr int VD = S_::VD, PP = S_::PP, BATCH = S_::GATES / C;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     T* qs = reinterpret_cast<T*>(lds + S_::q);
@@ -424,6 +431,11 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[r] = (T)w[r];
                 *reinterpret_cast<V4*>(ps + i * PP + 16 * kt + 4 * lg) = o;
+                if constexpr (S_::PARTS == 2) {   // what 8 bits leave of a weight, 8 bits of it
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[r] = (T)(w[r] - (float)o[r]);
+                    *reinterpret_cast<V4*>(ps + C * PP + i * PP + 16 * kt + 4 * lg) = o;
+                }
             }
             // the far part, out of the state before the chunk
             if (!SUM || g == 0) {
@@ -485,6 +497,11 @@ template <class T, int DK, int CW, int KIND> __device__ __forceinline__ void lin
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (REV ? s < i / 2 : s > i / 2) continue;
+                    if constexpr (S_::PARTS == 2) {
+                        const F rest = ld8(ps + C * PP + (16 * i + l16) * PP + 32 * s + 8 * lg);
+#pragma unroll
+                        for (int w = 0; w < CW; ++w) mma(O[i][w], vf[w], rest);
+                    }
                     const F pf = ld8(ps + (16 * i + l16) * PP + 32 * s + 8 * lg);
 #pragma unroll
                     for (int w = 0; w < CW; ++w) mma(O[i][w], vf[w], pf);
@@ -1009,7 +1026,7 @@ static hipError_t lin_run(LinArgs a, hipStream_t st) {
     a.slabs = (a.dv + 64 * CW - 1) / (64 * CW);
     const long blocks = (long)a.B * a.Hk * a.nseg * a.slabs;
     if (blocks >= 1L << 24) return hipErrorInvalidValue;   // a launch has fewer than 2^32 threads along an axis
-    constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
+    constexpr size_t bytes = LinLds<T, DK, CW, KIND == LIN_STATE>::bytes;
     static_assert(bytes <= 156 * 1024, "LDS of a compute unit");
     static std::atomic<unsigned long long> done{0};
     LIN_TRY(lds_limit((const void*)lin_kernel<T, DK, CW, KIND>, bytes, done));
@@ -1040,7 +1057,7 @@ template <class T, int DK, int CW, bool STATES> static hipError_t lin_many_run(L
         blocks += own;
     }
     if (blocks >= 1L << 24) return hipErrorInvalidValue;
-    constexpr size_t bytes = LinLds<T, DK, CW>::bytes;
+    constexpr size_t bytes = LinLds<T, DK, CW, STATES>::bytes;
     auto go = [&](auto kernel) {
         static std::atomic<unsigned long long> done{0};   // an instance of this function has one kernel
         LIN_TRY(lds_limit((const void*)kernel, bytes, done));
