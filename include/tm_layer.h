@@ -112,8 +112,9 @@ size_t tm_linear_workspace_bytes(int batch, int n_tokens, int heads, int kv_head
  * wanted) and dstate_in (fp32; null: not wanted).  dstate_in may be
  * dstate_out.  dk and dv are summed over the query heads of a key head, a
  * head's dlog_decay over batch and tokens, in an order that the call's sizes
- * fix.  The gradient of a decay of -inf is 0.  Gradients through non-finite
- * values are not defined.  batch 0: a head's dlog_decay becomes zero. */
+ * fix.  The gradient of a decay of -inf, or of -1000 and below, is 0.
+ * Gradients through non-finite values are not defined.  batch 0: a head's
+ * dlog_decay becomes zero. */
 tm_status tm_linear_attention_backward(const void* q, long q_batch, long q_token, const void* k, long k_batch,
                                        long k_token, const void* v, long v_batch, long v_token,
                                        const float* log_decay, int per_token, const int* counts,

@@ -72,8 +72,9 @@ __device__ __forceinline__ int lin_tokens(const LinArgs& a, int b) {
     return a.counts ? min(max(a.counts[b], 0), a.T) : a.T;
 }
 // log2 of what a token keeps: -inf as -1000 (NaN stays NaN)
+constexpr float LIN_DROPS = -1000.f;
 __device__ __forceinline__ double lin_gate(float g) {
-    return (double)(g < -1000.f ? -1000.f : g) * LOG2E;
+    return (double)(g < LIN_DROPS ? LIN_DROPS : g) * LOG2E;
 }
 
 // Rows in LDS, D elements long without gaps: the piece of 4 elements at column
@@ -968,10 +969,12 @@ __global__ __launch_bounds__(256) void lin_pairs_kernel(LinPairs a, LinFlow f, i
 }
 
 // dg of a segment's tokens (per token), or their sum (into part): from the
-// segment's last chunk to its first, with what passes each.
+// segment's last chunk to its first, with what passes each.  Nothing passes a
+// chunk with a token that drops what came before, and that token's dg is 0:
+// both are set, where the difference would leave a rounding of the flow.
 __global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const double* sums, const double* flow,
-                                                       const int* counts, float* dg, double* part, int per_token, int T,
-                                                       int Hk, int nseg, int L, int C) {
+                                                       const float* ld, const int* counts, float* dg, double* part,
+                                                       int per_token, int T, int Hk, int nseg, int L, int C) {
     const int seg = blockIdx.x % nseg, bh = blockIdx.x / nseg, b = bh / Hk, kh = bh % Hk, lane = threadIdx.x;
     const int n = counts ? min(max(counts[b], 0), T) : T, chunks = (T + C - 1) / C;
     const int first = seg * L, last = (int)min((long)n, (long)first + L);
@@ -979,11 +982,14 @@ __global__ __launch_bounds__(64) void lin_gates_kernel(const float* h, const dou
     for (int c = (last - first + C - 1) / C - 1; c >= 0; --c) {
         const int t = first + c * C + lane;
         const double* s = sums + ((long)bh * chunks + first / C + c) * 2;
-        const double through = border - s[1];
+        const bool on = lane < C && t < last;
+        const long at = ((long)b * T + t) * Hk + kh;
+        const bool drops = on && ld[per_token ? at : kh] <= LIN_DROPS;
+        const double through = __any(drops) ? 0.0 : border - s[1];
         border = through + s[0];
-        if (lane < C && t < last) {
-            const double g = through + (double)h[(long)bh * T + t];
-            if (per_token) dg[((long)b * T + t) * Hk + kh] = (float)g;
+        if (on) {
+            const double g = drops ? 0.0 : through + (double)h[(long)bh * T + t];
+            if (per_token) dg[at] = (float)g;
             sum += g;
         }
     }
@@ -1285,8 +1291,8 @@ template <class T> static hipError_t lin_backward(LinArgs a, const LinBack& g, c
                scale, a.per_token, a.B, a.T, a.Hk, a.G, dk, dv, 0, (dk + lin_many_columns(wide) - 1) / lin_many_columns(wide)};
     LIN_TRY(lin_pairs<T>(pairs, LinFlow{S, R, flow, p.nseg, slots, (int)cells}, st));
     LIN_TRY(timed_layer(st, [&] {
-        launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.counts, g.dld,
-                 part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk<T>());
+        launch_k(lin_gates_kernel, dim3((unsigned)(bh * p.nseg)), dim3(64), 0, st, h, sums, flow, a.ld, a.counts,
+                 g.dld, part, a.per_token, a.T, a.Hk, p.nseg, p.L, lin_chunk<T>());
         return hipGetLastError();
     }));
     if (a.per_token) return hipSuccess;

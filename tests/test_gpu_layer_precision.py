@@ -62,3 +62,35 @@ def test_linear_attention_of_single_pairs(n):
     size = O.linear_backward(*map(np.abs, (Q, KK, V)), f64(g), 0.125, np.abs(S), np.abs(DY), np.zeros_like(S))
     for i, name in enumerate(("dq", "dk", "dv")):
         within(got[i], want[i], size[i] * (2 * e + PARTS) + np.abs(want[i]) * half, name)
+
+
+# ---- the gradient of a decay that drops everything ----
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 40, 65, 700])
+def test_gradient_of_a_dropping_decay_is_zero(n, dtype):
+    """What a token keeps is exp(-inf) = 0 or, from -1000 on, counts as it: the derivative by its logarithm is 0, exactly,
+    for each token and summed for each head; the tokens beside it keep theirs."""
+    B, H, K, d = 2, 4, 2, 64
+    case = (dtype, B, n, H, K, d, d, True, False, True)
+    q, k, v, g, _, s, (Q, KK, V, _, S) = L.linear_case(case, wipes=False)
+    rng = np.random.default_rng(11)
+    drop = torch.from_numpy(rng.random((B, n, K)) < 0.05).to("cuda")
+    drop[:, n // 2] = True
+    g = g.clamp(min=-0.05)
+    g[drop] = -math.inf
+    g[:, n // 2, 1] = -1000.0
+    (dy, DY), (ds, DS) = normal(q.shape, 8, dtype), normal((B, K, d, d), 9, F32)
+    m = T.LinearAttention(K, d)
+    counts = [n, max(1, n - 9)]
+    got = m.backward(q, k, v, g, dy, state=s, dstate=ds, counts=ints(counts))[3]
+    assert not got[drop].any()
+    want = O.linear_backward(Q, KK, V, f64(g), d ** -0.5, S, DY, DS, counts)[3]
+    assert not want[f64(drop) > 0].any()
+    assert np.linalg.norm(f64(got) - want) <= 1e-5 * np.linalg.norm(want)
+    head = torch.tensor([-math.inf, -0.01], device="cuda")
+    got = m.backward(q, k, v, head, dy, state=s, dstate=ds, counts=ints(counts))[3]
+    want = O.linear_backward(Q, KK, V, f64(head), d ** -0.5, S, DY, DS, counts)[3]
+    assert got[0] == 0
+    # a sum over tokens whose errors may have one sign: sqrt(B n) times a token's 1e-5
+    assert abs(float(got[1]) - want[..., 1].sum()) <= 1e-5 * np.linalg.norm(want) * math.sqrt(B * n)
