@@ -455,8 +455,15 @@ class PagedCache:
 
 
 def _product(x, w):
-    """x times a weight of PyTorch's Linear layout, or an ``Int8Linear``."""
-    return torch.nn.functional.linear(x, w) if isinstance(w, torch.Tensor) else w(x)
+    """x times a weight of PyTorch's Linear layout, or an ``Int8Linear``.  The
+    rows are one matrix (copied where a view of more axes does not allow it):
+    of a view whose rows do not follow each other torch makes a batched product
+    with the weight as a transposed operand of batch distance 0, and in bf16
+    that has ended in a memory fault (an output's half of 2 x 1024 rows times
+    1024 x 1024)."""
+    if not isinstance(w, torch.Tensor):
+        return w(x)
+    return torch.nn.functional.linear(x.reshape(-1, x.shape[-1]), w).view(x.shape[:-1] + (w.shape[0],))
 
 
 def _layer_weights(w_qkv, w_out, heads, kv_heads, norm, dtype):

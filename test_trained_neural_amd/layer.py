@@ -647,7 +647,7 @@ class LinearWindow:
             self.norm(q_k, first, out=q_k)
         g = self.log_decay
         if g is None:
-            g = torch.nn.functional.linear(x, self.w_gate).float()
+            g = _product(x, self.w_gate).float()
             g = torch.nn.functional.logsigmoid(g if self.gate_bias is None else g + self.gate_bias)
         return self.memory(qkv[:, :, :self.heads], qkv[:, :, self.heads:self.heads + self.kv_heads],
                            qkv[:, :, self.heads + self.kv_heads:], g, state=self.state, state_out=out_state)
