@@ -589,6 +589,18 @@ class Int8Linear:
         return out
 
 
+def _logits(x, w):
+    """x [..][D] times w [heads][D], in fp32 from the product on: a logit
+    rounded to 8 bits is off by up to 2^-6 at 4, which the decays, summed over
+    thousands of tokens, keep.  bf16 rows are read as they are (a copy of them
+    in fp32 costs a window of 4 x 4096 rows of 4096 90 us of 960); for a single
+    head they are copied, since the library takes 16 ms for one column of such
+    a product."""
+    if x.dtype == torch.float32 or w.shape[0] == 1:
+        return _product(x.float(), w.float())
+    return torch.mm(x.reshape(-1, x.shape[-1]), w.t(), out_dtype=torch.float32).view(x.shape[:-1] + (w.shape[0],))
+
+
 class LinearWindow:
     """Linear attention as the attention of ``mac_segment``'s window and of
     the single tokens that follow, with a state in the place of
@@ -599,7 +611,8 @@ class LinearWindow:
     positions count on from the window's first row).  What a token keeps of the
     past: ``log_decay`` fp32 [kv_heads], or a gate, the logarithm of
     sigmoid(x w_gate' + gate_bias), with w_gate [kv_heads][D] of the vectors'
-    type and gate_bias fp32 [kv_heads] (None: zeros).
+    type and gate_bias fp32 [kv_heads] (None: zeros); the logits are formed in
+    fp32.
 
     ``attention(window)`` takes [B][P + 2 S][D] (its first P rows are
     ``persistent``, whose state is kept) and returns the output [B][S][D] for
@@ -647,7 +660,7 @@ class LinearWindow:
             self.norm(q_k, first, out=q_k)
         g = self.log_decay
         if g is None:
-            g = _product(x, self.w_gate).float()
+            g = _logits(x, self.w_gate)
             g = torch.nn.functional.logsigmoid(g if self.gate_bias is None else g + self.gate_bias)
         return self.memory(qkv[:, :, :self.heads], qkv[:, :, self.heads:self.heads + self.kv_heads],
                            qkv[:, :, self.heads + self.kv_heads:], g, state=self.state, state_out=out_state)

@@ -282,3 +282,31 @@ def test_timing_class():
     finally:
         T.tm_timing_enable(0)
     assert n == 1 and ms > 0
+
+
+@pytest.mark.parametrize("kv", [2, 1])
+@pytest.mark.parametrize("biased", [False, True])
+def test_linear_window_gates_in_fp32(biased, kv):
+    """A bf16 layer whose gates keep most of the state: log sigmoid of logits of 3 to 9, formed in fp32.  Queries, keys and
+    values are the layer's own (a projection rounded to bf16); the state is held to the roundings of its sums and to the
+    logits', a sum of D products: dz <= D 2^-24 sum |x w|, and d log sigmoid(z) <= exp(-z) dz."""
+    B, D, heads, d, n = 2, 64, 4, 64, 120
+    w, w_out, _ = weights(heads, kv, d, D, 0, BF, d)
+    wg = normal((kv, D), 93, BF)[0] / 8
+    wg[:, 0] = 4.0 if biased else 6.0
+    bias = torch.full((kv,), 2.0, device="cuda") if biased else None
+    at = T.LinearWindow(w, w_out, heads, kv, B, w_gate=wg, gate_bias=bias)
+    x, _ = normal((B, n, D), 7, BF)
+    x[:, :, 0] = 1.0
+    at.token(x)
+    qkv = torch.nn.functional.linear(x, w).view(B, n, heads + 2 * kv, d)
+    Q, KK, V = f64(qkv[:, :, :heads]), f64(qkv[:, :, heads:heads + kv]), f64(qkv[:, :, heads + kv:])
+    X, W = f64(x), f64(wg)
+    z = X @ W.T + (2.0 if biased else 0.0)
+    assert z.min() > 3 and z.max() < 9
+    off = np.exp(-z) * D * U * (np.abs(X) @ np.abs(W).T + 2.0) + 4 * U * np.log1p(np.exp(-z))
+    zero = np.zeros((B, kv, d, d))
+    g = -np.log1p(np.exp(-z))
+    want = O.linear(Q, KK, V, g, d ** -0.5, zero)[1]
+    size = O.linear(np.abs(Q), np.abs(KK), np.abs(V), g, d ** -0.5, zero)[1]
+    assert np.all(np.abs(f64(at.state) - want) <= size * ((n + 2 * d + 256) * U + off.sum(1)[:, :, None, None]))
