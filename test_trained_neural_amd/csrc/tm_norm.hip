@@ -160,8 +160,13 @@ __device__ __forceinline__ void turn(float* e, const float* cs, const float* sn)
         float& a = e[HALF ? j : 2 * j];
         float& b = e[HALF ? NP + j : 2 * j + 1];
         const float s = BACK ? -sn[j] : sn[j], a0 = a, b0 = b;
-        a = a0 * cs[j] - b0 * s;
-        b = a0 * s + b0 * cs[j];
+        if constexpr (BACK && V >= 4) {   // the units whose kernel has a second form, past the caches
+            a = fmaf(a0, cs[j], -(b0 * s));
+            b = fmaf(a0, s, b0 * cs[j]);
+        } else {
+            a = a0 * cs[j] - b0 * s;
+            b = a0 * s + b0 * cs[j];
+        }
     }
 }
 
@@ -239,7 +244,10 @@ __global__ __launch_bounds__(256) void head_norm_kernel(NormArgs a, int lg) {
 
 // The backward: a group of lanes takes some heads (blockIdx.y) of a.tokens
 // tokens, so that the sums of dw stay in its registers; a workgroup adds its
-// groups' sums through LDS in their order and writes one partial sum.
+// groups' sums through LDS in their order and writes one partial sum.  Its
+// sums of products are written as the multiply-adds they are: left to the
+// compiler, which of two products is rounded by itself differed between the
+// forms of one kernel, and with it a token's bits by the size of its call.
 template <class T, int V, bool HALF, int U, bool STREAM>
 __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int lg) {
     constexpr int E = Unit<V, HALF>::E, NP = Unit<V, HALF>::NP, AHEAD = U == 1 ? 2 : 1;
@@ -293,8 +301,8 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
                             if (u < a.rot_units) turn<V, HALF, true>(n[k][i], cs[i], sn[i]);
 #pragma unroll
                             for (int j = 0; j < E; ++j) {
-                                sum[k] += e[k][i][j] * e[k][i][j];
-                                dot[k] += e[k][i][j] * n[k][i][j] * w[i][j];
+                                sum[k] = fmaf(e[k][i][j], e[k][i][j], sum[k]);
+                                dot[k] = fmaf(e[k][i][j] * n[k][i][j], w[i][j], dot[k]);
                             }
                         }
                     }
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
                     }
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
-                    const float r = 1.f / sqrtf(sum[k] * inv_d + a.eps), mean = dot[k] * r * inv_d;
+                    const float r = 1.f / sqrtf(fmaf(sum[k], inv_d, a.eps)), mean = dot[k] * r * inv_d;
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
                         const int u = lane + i * lg;
@@ -315,8 +323,8 @@ __global__ __launch_bounds__(256) void head_norm_backward_kernel(NormArgs a, int
 #pragma unroll
                             for (int j = 0; j < E; ++j) {
                                 const float unit = e[k][i][j] * r;
-                                dw[i][j] += n[k][i][j] * unit;
-                                e[k][i][j] = r * (n[k][i][j] * w[i][j] - unit * mean);
+                                dw[i][j] = fmaf(n[k][i][j], unit, dw[i][j]);
+                                e[k][i][j] = r * fmaf(n[k][i][j], w[i][j], -(unit * mean));
                             }
                             store_unit<T, V, HALF, STREAM>(dx + (long)(h + k) * a.d, u, a, e[k][i]);
                         }
