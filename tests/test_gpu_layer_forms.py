@@ -19,6 +19,100 @@ def seeded(shape, seed, dtype):
     return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(dtype)
 
 
+# ---- products with 8-bit integers ----
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", [
+    (777, 1000, 1537), (1000, 130, 1100),      # tiles of 64: begun steps of columns, begun tiles on both sides
+    (2500, 200, 2700), (3300, 1040, 2048),     # of 128
+    (3700, 150, 3700), (8200, 640, 1700),      # of 256: bands of eight tiles and begun ones
+    (8, 8208, 4100), (3, 4112, 5001),          # rows coded by each workgroup, 32 rows of the weight each, many steps
+    (16, 9000, 4100), (30, 5000, 700), (64, 3001, 200), (100, 8192, 300)],   # few rows, their codes made beforehand
+    ids=lambda s: "x".join(map(str, s)))
+def test_int8_launch_forms(size, dtype):
+    """Bit for bit, with rows of the output that are an odd number of elements apart, and codes and product by themselves."""
+    L.test_int8_linear((dtype, *size))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_int8_rows_are_the_same_in_every_form(dtype):
+    """A row's result in tiles of 256, 128 and 64 and among few rows."""
+    w, x = seeded((3700, 150), 1, F32), seeded((3700, 150), 2, dtype)
+    lin = T.Int8Linear(w)
+    whole = lin(x)
+    for n in (1, 7, 16, 17, 33, 64, 65, 100, 700, 2500, 3699):
+        assert torch.equal(lin(x[:n]), whole[:n]), n
+        assert torch.equal(lin(x[-n:]), whole[-n:]), n
+
+
+# ---- linear attention: divided sequences of every width, long walks ----
+
+DIVIDED = [  # dtype, B, T, heads, kv_heads, dk, dv, per token, ragged, with a state
+    (BF, 1, 460, 4, 2, 128, 128, True, False, True), (BF, 2, 460, 2, 2, 160, 96, True, True, True),
+    (BF, 1, 333, 2, 1, 192, 192, False, False, True), (F32, 1, 460, 3, 1, 64, 96, True, True, True),
+    (F32, 2, 333, 2, 2, 128, 64, True, True, True), (F32, 1, 460, 2, 2, 96, 128, False, False, True),
+    (F32, 1, 333, 2, 1, 184, 72, True, False, True), (F32, 1, 333, 1, 1, 256, 136, True, False, True),
+    (BF, 1, 333, 1, 1, 232, 256, True, False, False),
+    (BF, 1, 2100, 8, 8, 128, 128, True, False, True), (F32, 1, 2100, 9, 9, 64, 128, True, False, True)]   # 128 tokens at least
+
+
+def linear_near(case, q, k, v, g, counts, s, host, entries, got):
+    """Outputs and states of some of the entries against the oracle."""
+    dtype, B, N, H, K, dk, dv = case[:7]
+    Q, KK, V, G, S = host
+    y, end = got
+    at = lambda x: x[entries] if x.ndim > 1 else x  # noqa: E731
+    n = None if counts is None else [counts[b] for b in entries]
+    scale = 1 / math.sqrt(dk)
+    want, want_s = O.linear(Q[entries], KK[entries], V[entries], at(G), scale, S[entries], n)
+    size, size_s = O.linear(*(np.abs(x[entries]) for x in (Q, KK, V)), at(G), scale, np.abs(S[entries]), n)
+    e, _, half = L.linear_error(case)
+    r = 2.0 ** -16 if dtype == BF else 0.0   # a pair's weight and the state in two parts
+    within(y[entries], want, size * (e + r) + np.abs(want) * half, "y")
+    within(end[entries], want_s, size_s * e, "state")
+
+
+@pytest.mark.parametrize("case", DIVIDED, ids=lambda c: "-".join(str(x) for x in c))
+def test_linear_attention_divided(case):
+    q, k, v, g, counts, s, host = L.linear_case(case)
+    m = T.LinearAttention(case[4], case[5], case[6])
+    got = m(q, k, v, g, state=s, counts=None if counts is None else ints(counts))
+    linear_near(case, q, k, v, g, counts, s, host, list(range(case[1])), got)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,N,H,K,d", [(16, 513, 16, 16, 16), (16, 1100, 32, 16, 16), (16, 1025, 16, 16, 8),   # undivided
+                                       (8, 2300, 32, 16, 8)])                                                  # four of 576
+def test_linear_attention_long_walks(B, N, H, K, d, dtype):
+    """A workgroup's walk over more than the 512 tokens whose decays are summed at a time, whole and ragged, with tokens
+    that drop the past around each such border."""
+    case = (dtype, B, N, H, K, d, d, True, False, True)
+    q, k, v, g, _, s, host = L.linear_case(case)
+    for t in (510, 511, 512, 513, 576, 1023, 1024, 1088):
+        if t < N:
+            g[t % B, t] = -math.inf
+            g[(t + 1) % B, t] = 0.0
+    host = (*host[:3], f64(g), host[4])
+    m = T.LinearAttention(K, d)
+    counts = [N - 37 * b if b % 3 else N for b in range(B)]
+    counts[1] = 512
+    entries = [0, 1, B // 2 + 1, B - 1]
+    for c in (None, counts):
+        got = m(q, k, v, g, state=s, counts=None if c is None else ints(c))
+        linear_near(case, q, k, v, g, c, s, host, entries, got)
+        if c is not None:
+            for b in range(B):
+                assert not got[0][b, c[b]:].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (192, 64), (64, 192), (256, 256)])
+def test_linear_attention_backward_of_several_segments(dk, dv, dtype):
+    """Gradients through several segments, their length halved or not, at the widths whose kernels differ."""
+    case = (dtype, 2, 300, 2, 1, dk, dv, True, True, True)
+    L.test_linear_attention_backward(case)
+
+
 # ---- head norms: several tokens a group of lanes, arrays past the caches ----
 
 @pytest.mark.parametrize("dtype,inter", [(F32, False), (F32, True), (BF, False)])
