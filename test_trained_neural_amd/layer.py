@@ -546,8 +546,9 @@ class Int8Linear:
         return self.codes.device
 
     def __call__(self, x, out=None, stream=None):
-        """x [..][cols]; out: [..][outs], contiguous, or 2-d with contiguous
-        rows (x being 2-d then)."""
+        """x [..][cols], any strides (copied where its rows are not contiguous,
+        or of more than two axes and not contiguous); out: [..][outs],
+        contiguous, or 2-d with contiguous rows (x being 2-d then)."""
         if stream is not None:
             _on(x.device, ("x", x))
             with _there(x.device, stream):
@@ -560,7 +561,8 @@ class Int8Linear:
                 raise ValueError("x is %s, the weight has %d columns" % (tuple(x.shape), self.cols))
             shape = x.shape[:-1] + (self.outs,)
             rows = math.prod(x.shape[:-1])
-            x_row = _rows_of("x", x)[2] if x.dim() == 2 else self.cols
+            rowwise = x.dim() == 2 and (self.cols <= 1 or x.stride(1) == 1)
+            x_row = _rows_of("x", x)[2] if rowwise else self.cols
             y_row = self.outs
             if out is not None:
                 T._same(x.dtype, ("out", out))
@@ -569,7 +571,7 @@ class Int8Linear:
                     y_row = _rows_of("out", out)[2]
                 elif not out.is_contiguous():
                     raise ValueError("out must be contiguous")
-            return (x.dim() != 2 and not x.is_contiguous(), shape, x_row, y_row, (rows, _int(self.outs), self.cols), dt,
+            return (not rowwise and not x.is_contiguous(), shape, x_row, y_row, (rows, _int(self.outs), self.cols), dt,
                     x.device.index, tm_int8_workspace_bytes(rows, self.cols))
 
         copy, shape, x_row, y_row, sizes, dt, index, need = _once((self._kind, _look(x), _look(out)), check)

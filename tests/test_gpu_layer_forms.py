@@ -45,6 +45,21 @@ def test_int8_rows_are_the_same_in_every_form(dtype):
         assert torch.equal(lin(x[-n:]), whole[-n:]), n
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_int8_takes_any_strides(dtype):
+    """Rows whose elements are apart, of two axes as of three; one row, one column, rows shared by all."""
+    lin = T.Int8Linear(seeded((40, 48), 1, F32))
+    x = seeded((48, 30), 2, dtype)
+    want = lin(x.t().contiguous())
+    assert torch.equal(lin(x.t()), want) and torch.equal(lin(x.t()[None])[0], want)
+    assert torch.equal(lin(x.t()[4:5]), want[4:5]) and torch.equal(lin(x[:, 4]), want[4])
+    out = torch.zeros(30, 41, dtype=dtype, device="cuda")
+    assert torch.equal(lin(x.t(), out=out[:, 1:]), want) and not out[:, 0].any()
+    assert torch.equal(lin(x.t()[:1].expand(5, -1)), want[:1].expand(5, -1))
+    one = T.Int8Linear(seeded((3, 1), 3, F32))
+    assert torch.equal(one(x[:, 5:6]), one(x[:, 5:6].contiguous()))
+
+
 # ---- linear attention: divided sequences of every width, long walks ----
 
 DIVIDED = [  # dtype, B, T, heads, kv_heads, dk, dv, per token, ragged, with a state
