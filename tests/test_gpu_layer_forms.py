@@ -128,6 +128,37 @@ def test_linear_attention_backward_of_several_segments(dk, dv, dtype):
     L.test_linear_attention_backward(case)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [4, 7, 90, 500])
+def test_linear_attention_grows_and_turns(N, dtype):
+    """Decays above 0 (the state grows), a negative scale, views of one projection and of a wider gradient, without a state."""
+    B, H, K, d = 2, 4, 2, 32
+    case = (dtype, B, N, H, K, d, d, True, False, False)
+    wide, _ = normal((B, N, H + 2 * K + 1, d), 21, dtype)
+    q, k, v = wide[:, :, :H], wide[:, :, H:H + K], wide[:, :, H + K:H + 2 * K]
+    Q, KK, V = f64(q), f64(k), f64(v)
+    g = seeded((B, N, K), 22, F32) * 0.3
+    dwide, _ = normal((B, N, H + 3, d), 23, dtype)
+    dy = dwide[:, :, 2:H + 2]
+    m, zero = T.LinearAttention(K, d), np.zeros((B, K, d, d))
+    y, end = m(q, k, v, g, scale=-0.3)
+    e, _, half = L.linear_error(case)
+    r = 2.0 ** -16 if dtype == BF else 0.0
+    want, want_s = O.linear(Q, KK, V, f64(g), -0.3, zero)
+    size, size_s = O.linear(*map(np.abs, (Q, KK, V)), f64(g), 0.3, zero)
+    within(y, want, size * (e + r) + np.abs(want) * half, "y")
+    within(end, want_s, size_s * e, "state")
+    got = m.backward(q, k, v, g, dy, scale=-0.3)
+    want = O.linear_backward(Q, KK, V, f64(g), -0.3, zero, f64(dy), zero)
+    size = O.linear_backward(*map(np.abs, (Q, KK, V)), f64(g), 0.3, zero, np.abs(f64(dy)), zero)
+    for n, name in enumerate(("dq", "dk", "dv")):
+        within(got[n], want[n], size[n] * (2 * e + r) + np.abs(want[n]) * half, name)
+    within(got[4], want[4], size[4] * 2 * e, "dstate")
+    assert np.linalg.norm(f64(got[3]) - want[3]) <= 1e-5 * np.linalg.norm(want[3])
+    same = m.backward(q.contiguous(), k.contiguous(), v.contiguous(), g, dy.contiguous(), scale=-0.3)
+    assert all(torch.equal(a, b) for a, b in zip(got, same))
+
+
 # ---- head norms: several tokens a group of lanes, arrays past the caches ----
 
 @pytest.mark.parametrize("dtype,inter", [(F32, False), (F32, True), (BF, False)])
@@ -164,3 +195,20 @@ def test_head_norm_past_the_caches(dtype, layout):
         want = sum(p[i].double() for p in parts)
         bound = 8 * U * math.sqrt(B * N * heads) * math.sqrt(B * N * heads)
         assert float((got.double() - want).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_head_norm_backward_into_views(dtype):
+    """dx as part of a projection's gradient, in the place of such a dy, and of such an x; what stands beside is left."""
+    H, K, d = 4, 2, 64
+    norm = T.HeadNorm(H, K, normal(d, 1, F32)[0], normal(d, 2, F32)[0], rotary=T.Rotary(d))
+    x, dy, pos = seeded((2, 9, H + 2 * K, d), 3, dtype), seeded((2, 9, H + 2 * K, d), 4, dtype), ints([5, 900])
+    cut = lambda t: t[:, :, :H + K]  # noqa: E731
+    want = norm.backward(cut(x).contiguous(), cut(dy).contiguous(), pos)
+    for place in ("own", "dy", "x"):
+        a, g, own = x.clone(), dy.clone(), torch.full_like(x, 7.0)
+        to = {"own": own, "dy": g, "x": a}[place]
+        beside = to[:, :, H + K:].clone()
+        got = norm.backward(cut(a), cut(g), pos, dx=cut(to))
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), place
+        assert torch.equal(to[:, :, H + K:], beside) and torch.equal(cut(to), want[0])

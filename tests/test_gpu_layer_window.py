@@ -310,3 +310,20 @@ def test_linear_window_gates_in_fp32(biased, kv):
     want = O.linear(Q, KK, V, g, d ** -0.5, zero)[1]
     size = O.linear(np.abs(Q), np.abs(KK), np.abs(V), g, d ** -0.5, zero)[1]
     assert np.all(np.abs(f64(at.state) - want) <= size * ((n + 2 * d + 256) * U + off.sum(1)[:, :, None, None]))
+
+
+@pytest.mark.parametrize("layer", ["linear", "window"])
+def test_bf16_layers_of_plain_weights(layer):
+    """Plain bf16 weights of 1024 x 1024, several sequences, persistent rows in front: windows and outputs that are views."""
+    B, S, D, heads, kv, d, P = 2, 512, 1024, 16, 4, 64, 16
+    w, w_out, pers = weights(heads, kv, d, D, P, BF, 3)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((B, 2 * S, D), generator=gen, device="cuda").to(BF)
+    window = torch.cat([pers[None].expand(B, P, D), x], dim=1)
+    make = lambda n: T.LinearWindow(w, w_out, heads, kv, n, log_decay=torch.full((kv,), -0.01, device="cuda"), persistent=pers) \
+        if layer == "linear" else T.WindowAttention(w, w_out, heads, kv, n, 2 * S, pers)  # noqa: E731
+    y = make(B)(window)
+    assert y.shape == (B, S, D) and torch.isfinite(y).all()
+    for b in range(B):   # a sequence by itself: its products' sums may be split otherwise, 8-bit roundings follow
+        one = make(1)(window[b:b + 1])
+        assert float((one[0].double() - y[b].double()).norm() / y[b].double().norm()) <= 4 * 2.0 ** -8
