@@ -39,14 +39,15 @@ namespace tmk {
 constexpr double LOG2E = 1.4426950408889634074;
 // Calls of up to as many tokens go token by token: us by tokens / by chunks
 // (widths of 128, 64 and 512 heads' states; widths of 64, 8 states), bf16
-// 2 tokens 8.3 / 12.1, 8 tokens 10.8 / 12.0, 28.9 / 22.0 and 8.4 / 7.6, 16
-// tokens 17.2 / 12.0, 45.5 / 22.2 and 12.9 / 7.6; fp32 8 tokens 9.7 / 14.1,
-// 27.4 / 26.9 and 7.5 / 7.4, 16 tokens 15.0 / 14.1, 42.7 / 27.3 and 11.3 / 7.4.
+// 2 tokens 7.3 / 12.3, 8 tokens 10.8 / 12.3, 28.4 / 22.3 and 8.4 / 7.9, 16
+// tokens 17.5 / 12.2, 44.4 / 22.3 and 12.8 / 7.8; fp32 8 tokens 9.8 / 14.0,
+// 27.3 / 27.0 and 7.5 / 7.4, 16 tokens 15.1 / 14.2, 43.6 / 27.0 and 11.3 / 7.4.
 template <class T> constexpr int lin_few() { return sizeof(T) == 4 ? 8 : 5; }
-// Tokens of a segment in the backward, at most. All gradients of 2 x 4096 tokens
-// of 16 heads of 128, segments of 64 / 256 / 512 tokens: 484 / 268 / 247 us, but at
-// 512 the gates' gradients, whose roundings grow with a segment, are 1.2e-6 of
-// their size from 64 bits instead of 8e-7.
+// Tokens of a segment in the backward, at most. All gradients, segments of 128 /
+// 256 / 512 tokens: 2 x 4096 tokens of 16 heads of 128 335 / 266 / 242 us (64:
+// 484), 2 x 2048 in fp32 317 / 293 / 284, 4 x 2048 tokens of 16 heads of 64 147 /
+// 124 / 124; but at 512 the gates' gradients, whose roundings grow with a segment,
+// are 1.05e-6 of their size from 64 bits instead of 7.4e-7.
 constexpr int LIN_BACK_SEG = 256;
 
 // What a chunk run does (see the table of roles above).
@@ -1157,10 +1158,11 @@ static LinPlan lin_plan(int B, int T, int Hk, int dk, int dv, bool back) {
         // The sequence is divided where its heads alone do not fill the chip, into
         // segments of 64 tokens while those are few, else of 128 at least (us
         // undivided / 256 / 128 / 64 tokens at least, bf16: 8 heads of 128, 512
-        // tokens 47 / 41 / 27 / 22, 4096 tokens 335 / 47 / 40 / 46; 64 heads of 128,
-        // 512 tokens 49 / 48 / 39 / 44; 2 heads of 64, 2048 tokens 90 / 24 / 19 / 18;
-        // fp32: 8 heads of 128, 1024 tokens 237 / 97 / 57 / 41).  Undivided: 256
-        // heads of 64, 2048 tokens 96 against 101; 8 heads of 128, 128 tokens 17.
+        // tokens 48 / 42 / 28 / 23, 4096 tokens 350 / 49 / 40 / 47; 64 heads of 128,
+        // 512 tokens 51 / 48 / 39 / 44; 2 heads of 64, 2048 tokens 98 / 26 / 19 / 18;
+        // fp32: 8 heads of 128, 1024 tokens 239 / 97 / 57 / 41).  Undivided: 256
+        // heads of 64, 2048 tokens 103 against 107 (512 tokens 30 against 41, fp32
+        // 2048 tokens 180 against 217); 8 heads of 128, 128 tokens 17.
         const long cols = lin_columns(dk, dv), wgs = (long)bh * ((dv + cols - 1) / cols);
         const long least = wgs * ((T + 63) / 64) <= 256 ? 64 : 128;
         long seg = wgs >= 256 || T <= 192 ? 1 : (512 + wgs - 1) / wgs;

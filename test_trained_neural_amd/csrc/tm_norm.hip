@@ -52,10 +52,14 @@ template <bool STREAM, class V> __device__ __forceinline__ void nput(V* p, V v) 
 }
 
 // Workgroups from which a call's heads are divided no further: the sines and
-// cosines of a token are formed again for every division.  Forward, past the
-// caches: 2 x 8192 tokens of 40 heads of 128 take 78 us with 4096 (81 with
-// 2048, 88 with 16384); the gradients of 4 x 2047 tokens of 20 heads of 96
-// 37 us with 512 (48 with 256, 46 to 61 with 1024).
+// cosines of a token are formed again for every division.  us with half as
+// many / these / twice as many.  Forward: 2048 tokens of 40 heads of 128 15.3 /
+// 15.5 / 16.7, of 20 heads of 96 in fp32 11.4 / 9.5 / 10.  Past the caches: 2 x
+// 8192 tokens of 40 heads of 128, interleaved pairs 80 / 77 / 89, half layout
+// 74 / 90 / 99, not rotated 86 / 83 / 94, 2 x 4096 in fp32 109 / 120 / 130.
+// Gradients: 4 x 2047 tokens of 20 heads of 96 47 / 36 / 45, 4 x 2048 in fp32
+// 92 / 92 / 129, of 20 heads of 128, interleaved, 41 / 41 / 37, 2 x 2048 tokens
+// of 10 heads of 256 33 / 31 / 45.
 constexpr int NORM_WGS = 1024, NORM_STREAM_WGS = 4096, NORM_BACK_WGS = 512;
 
 // A unit of a head vector.  Half layout: V pairs, elements c .. c + V - 1 and
